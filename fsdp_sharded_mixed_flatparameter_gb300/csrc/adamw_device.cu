@@ -18,6 +18,23 @@
 
 namespace zs {
 
+// The next step's count and scalars.
+__device__ __forceinline__ void advance(zero_adamw_device_state* __restrict__ state, double lr, double b1, double b2,
+                                        double eps, double wd) {
+  const int64_t t = state->step + 1;
+  const AdamScalars s = adam_scalars(lr, b1, b2, eps, wd, t);
+  state->scalars[0] = s.step_size;
+  state->scalars[1] = s.bc2_sqrt;
+  state->scalars[2] = s.decay;
+  state->scalars[3] = s.b1;
+  state->scalars[4] = s.omb1;
+  state->scalars[5] = s.b2;
+  state->scalars[6] = s.omb2;
+  state->scalars[7] = s.eps;
+  state->step = t;
+  state->apply = 1;
+}
+
 __global__ void adamw_prepare_kernel(const zero_adamw_hparams* __restrict__ hp,
                                      const zero_norm_result* __restrict__ clip,
                                      zero_adamw_device_state* __restrict__ state) {
@@ -33,18 +50,34 @@ __global__ void adamw_prepare_kernel(const zero_adamw_hparams* __restrict__ hp,
     state->apply = 0;
     return;
   }
-  const int64_t t = state->step + 1;
-  const AdamScalars s = adam_scalars(lr, b1, b2, eps, wd, t);
-  state->scalars[0] = s.step_size;
-  state->scalars[1] = s.bc2_sqrt;
-  state->scalars[2] = s.decay;
-  state->scalars[3] = s.b1;
-  state->scalars[4] = s.omb1;
-  state->scalars[5] = s.b2;
-  state->scalars[6] = s.omb2;
-  state->scalars[7] = s.eps;
-  state->step = t;
-  state->apply = 1;
+  advance(state, lr, b1, b2, eps, wd);
+}
+
+// The same for the parameter groups of a list, a thread each: every group
+// advances or none does.
+__global__ void __launch_bounds__(ZERO_LIST_MAX_GROUPS)
+    adamw_prepare_list_kernel(const zero_adamw_hparams* __restrict__ hp, int n_groups,
+                              const zero_norm_result* __restrict__ clip,
+                              zero_adamw_device_state* __restrict__ states) {
+  const int g = threadIdx.x;
+  const bool mine = g < n_groups;
+  double lr = 0.0, b1 = 0.0, b2 = 0.0, eps = 1.0, wd = 0.0;
+  if (mine) {
+    lr = hp[g].lr;
+    b1 = hp[g].beta1;
+    b2 = hp[g].beta2;
+    eps = hp[g].eps;
+    wd = hp[g].weight_decay;
+  }
+  const bool ok = adam_hparams_ok(lr, b1, b2, eps, wd);
+  const bool all_ok = __syncthreads_and(ok) != 0;
+  if (!mine) return;
+  states[g].status = ok ? ZERO_OK : ZERO_EINVAL;
+  if (!all_ok || (clip != nullptr && !clip->finite)) {
+    states[g].apply = 0;
+    return;
+  }
+  advance(&states[g], lr, b1, b2, eps, wd);
 }
 
 // The dynamic loss scale on the device (zero_loss_scale_update_device): the
@@ -98,6 +131,12 @@ zero_status launch_adamw_prepare(const zero_adamw_hparams* hp, const zero_norm_r
                                  zero_adamw_device_state* state, cudaStream_t st) {
   adamw_prepare_kernel<<<1, 32, 0, st>>>(hp, clip, state);
   return check_launch("adamw_prepare_kernel");
+}
+
+zero_status launch_adamw_prepare_list(const zero_adamw_hparams* hp, int n_groups, const zero_norm_result* clip,
+                                      zero_adamw_device_state* states, cudaStream_t st) {
+  adamw_prepare_list_kernel<<<1, ZERO_LIST_MAX_GROUPS, 0, st>>>(hp, n_groups, clip, states);
+  return check_launch("adamw_prepare_list_kernel");
 }
 
 }  // namespace zs

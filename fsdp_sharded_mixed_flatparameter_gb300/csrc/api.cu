@@ -323,6 +323,7 @@ zero_status zero_debug_errors(uint64_t* out, int32_t reset) {
   zero_status (*const readers[])(unsigned long long*, bool) = {
       zs::debug_read_adamw,          zs::debug_read_adamw_table,        zs::debug_read_adamw_table_acc,
       zs::debug_read_adamw_table_p4, zs::debug_read_adamw_table_p4_acc, zs::debug_read_adamw_device,
+      zs::debug_read_adamw_list,     zs::debug_read_adamw_table8,      zs::debug_read_state8,
       zs::debug_read_flatten,        zs::debug_read_sqnorm};
   uint64_t total = 0, first[3] = {0, 0, 0};
   for (auto rd : readers) {
@@ -416,6 +417,195 @@ zero_status zero_adamw_step_tensors_device(float* d_master, float* d_exp_avg, fl
   return zs::launch_adamw_table(d_master, d_exp_avg, d_exp_avg_sq, d_acc, d_table, n_tensors, grad_dtype,
                                 shard_start, grad_scale, d_grad_scale, d_param_lowp, lowp_dtype, n,
                                 zs::AdamScalars{}, d_state, d_clip, zs::as_stream(stream));
+}
+
+// ------------------------------------------------- 8-bit moments, tensor lists
+static zero_status check_state8(const char* who, const zero_state8* q, int64_t n) {
+  if (n < 0) return fail(ZERO_EINVAL, "%s: n %lld < 0", who, (long long)n);
+  if (q == nullptr) return fail(ZERO_EINVAL, "%s: NULL 8-bit state", who);
+  if (n > 0 && (q->exp_avg == nullptr || q->exp_avg_scale == nullptr || q->root == nullptr || q->root_scale == nullptr))
+    return fail(ZERO_EINVAL, "%s: NULL 8-bit state buffer", who);
+  if (!zs::aligned(q->exp_avg_scale, 4) || !zs::aligned(q->root_scale, 4))
+    return fail(ZERO_EINVAL, "%s: scales not 4-byte aligned", who);
+  return ZERO_OK;
+}
+
+zero_status zero_state8_pack(const float* d_exp_avg, const float* d_exp_avg_sq, int64_t n, const zero_state8* q,
+                             void* stream) {
+  const zero_status c = check_state8("zero_state8_pack", q, n);
+  if (c != ZERO_OK) return c;
+  if (n == 0) return ZERO_OK;
+  if (d_exp_avg == nullptr || d_exp_avg_sq == nullptr) return fail(ZERO_EINVAL, "zero_state8_pack: NULL buffer");
+  return zs::launch_state8_pack(d_exp_avg, d_exp_avg_sq, n, *q, zs::as_stream(stream));
+}
+
+zero_status zero_state8_unpack(const zero_state8* q, int64_t n, float* d_exp_avg, float* d_exp_avg_sq, void* stream) {
+  const zero_status c = check_state8("zero_state8_unpack", q, n);
+  if (c != ZERO_OK) return c;
+  if (n == 0) return ZERO_OK;
+  if (d_exp_avg == nullptr || d_exp_avg_sq == nullptr) return fail(ZERO_EINVAL, "zero_state8_unpack: NULL buffer");
+  return zs::launch_state8_unpack(*q, n, d_exp_avg, d_exp_avg_sq, zs::as_stream(stream));
+}
+
+static zero_status step8_tensors(const char* who, float* d_master, const zero_state8* q, const zero_tensor* d_table,
+                                 int32_t n_tensors, int64_t total, zero_dtype grad_dtype, int64_t shard_start,
+                                 float grad_scale, const float* d_grad_scale, const float* d_acc, void* d_param_lowp,
+                                 zero_dtype lowp_dtype, int64_t n, const zs::AdamScalars& s, int64_t step,
+                                 const zero_adamw_device_state* d_state, const zero_rounding* rounding,
+                                 const zero_norm_result* d_clip, void* stream) {
+  const zero_status c = check_state8(who, q, n);
+  if (c != ZERO_OK) return c;
+  if (n_tensors < 0 || (n_tensors > 0 && d_table == nullptr)) return fail(ZERO_EINVAL, "%s: bad table", who);
+  if (total < 0 || (n_tensors == 0 && total != 0)) return fail(ZERO_EINVAL, "%s: total does not fit the table", who);
+  if (shard_start < 0 || n > total - shard_start)
+    return fail(ZERO_EINVAL, "%s: [%lld, %lld) outside [0, %lld]", who, (long long)shard_start,
+                (long long)(shard_start + n), (long long)total);
+  if (!zs::valid_dtype(grad_dtype)) return fail(ZERO_EINVAL, "%s: bad grad_dtype %d", who, (int)grad_dtype);
+  if (!std::isfinite(grad_scale)) return fail(ZERO_EINVAL, "%s: non-finite grad_scale", who);
+  if (n > 0 && d_master == nullptr) return fail(ZERO_EINVAL, "%s: NULL master", who);
+  if (d_param_lowp != nullptr && lowp_dtype != ZERO_BF16 && lowp_dtype != ZERO_F16)
+    return fail(ZERO_EINVAL, "%s: lowp_dtype must be BF16 or F16", who);
+  if (n == 0) return ZERO_OK;
+  const zs::Table8Args a{d_master, *q, d_acc, d_table, n_tensors, grad_dtype, shard_start, n, grad_scale, d_grad_scale,
+                         d_param_lowp, lowp_dtype, d_state, rounding != nullptr,
+                         rounding != nullptr ? *rounding : zero_rounding{}, step, d_clip};
+  return zs::launch_adamw_table8(a, s, zs::as_stream(stream));
+}
+
+zero_status zero_adamw_step8_tensors(float* d_master, const zero_state8* q, const zero_tensor* d_table,
+                                     int32_t n_tensors, int64_t total, zero_dtype grad_dtype, int64_t shard_start,
+                                     float grad_scale, const float* d_grad_scale, const float* d_acc,
+                                     void* d_param_lowp, zero_dtype lowp_dtype, int64_t n,
+                                     const zero_adamw_hparams* hp, int64_t step, const zero_rounding* rounding,
+                                     const zero_norm_result* d_clip, void* stream) {
+  const char* who = "zero_adamw_step8_tensors";
+  zs::AdamScalars s;
+  const zero_status hs = adamw_scalars(who, hp, step, &s);
+  if (hs != ZERO_OK) return hs;
+  return step8_tensors(who, d_master, q, d_table, n_tensors, total, grad_dtype, shard_start, grad_scale, d_grad_scale,
+                       d_acc, d_param_lowp, lowp_dtype, n, s, step, nullptr, rounding, d_clip, stream);
+}
+
+zero_status zero_adamw_step8_tensors_device(float* d_master, const zero_state8* q, const zero_tensor* d_table,
+                                            int32_t n_tensors, int64_t total, zero_dtype grad_dtype,
+                                            int64_t shard_start, float grad_scale, const float* d_grad_scale,
+                                            const float* d_acc, void* d_param_lowp, zero_dtype lowp_dtype, int64_t n,
+                                            const zero_adamw_device_state* d_state, const zero_rounding* rounding,
+                                            const zero_norm_result* d_clip, void* stream) {
+  const char* who = "zero_adamw_step8_tensors_device";
+  const zero_status c = check_state(who, d_state);
+  if (c != ZERO_OK) return c;
+  return step8_tensors(who, d_master, q, d_table, n_tensors, total, grad_dtype, shard_start, grad_scale, d_grad_scale,
+                       d_acc, d_param_lowp, lowp_dtype, n, zs::AdamScalars{}, 0, d_state, rounding, d_clip,
+                       stream);
+}
+
+static zero_status check_groups(const char* who, int32_t n_groups) {
+  if (n_groups < 1 || n_groups > ZERO_LIST_MAX_GROUPS)
+    return fail(ZERO_EINVAL, "%s: %d groups, not 1 to %d", who, (int)n_groups, ZERO_LIST_MAX_GROUPS);
+  return ZERO_OK;
+}
+
+zero_status zero_list_chunks(const zero_list_tensor* list, int32_t n_tensors, int32_t n_groups, int32_t state_bits,
+                             zero_list_chunk* chunks, int64_t* n_chunks) {
+  const char* who = "zero_list_chunks";
+  if (n_chunks == nullptr) return fail(ZERO_EINVAL, "%s: NULL n_chunks", who);
+  if (n_tensors < 0 || (n_tensors > 0 && list == nullptr)) return fail(ZERO_EINVAL, "%s: bad list", who);
+  const zero_status g = check_groups(who, n_groups);
+  if (g != ZERO_OK) return g;
+  if (state_bits != 32 && state_bits != 8) return fail(ZERO_EINVAL, "%s: state_bits must be 32 or 8", who);
+  int64_t count = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const zero_list_tensor& t = list[i];
+    const int64_t k = t.numel / zs::kListChunk + (t.numel % zs::kListChunk != 0 ? 1 : 0);
+    if (t.numel < 0 || k > INT32_MAX) return fail(ZERO_EINVAL, "%s: numel[%d] = %lld", who, (int)i, (long long)t.numel);
+    if (t.group < 0 || t.group >= n_groups)
+      return fail(ZERO_EINVAL, "%s: group[%d] = %d of %d", who, (int)i, (int)t.group, (int)n_groups);
+    if (t.reserved != 0) return fail(ZERO_EINVAL, "%s: reserved[%d] != 0", who, (int)i);
+    if (t.numel > 0 && (t.master == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr))
+      return fail(ZERO_EINVAL, "%s: NULL buffer of tensor %d", who, (int)i);
+    const bool fits = state_bits == 32 ? t.exp_avg_scale == nullptr && t.root_scale == nullptr
+                                       : t.exp_avg_scale != nullptr && t.root_scale != nullptr;
+    if (t.numel > 0 && !fits)
+      return fail(ZERO_EINVAL, "%s: the scales of tensor %d do not fit %d-bit states", who, (int)i, (int)state_bits);
+    const uintptr_t sa = state_bits == 32 ? 4 : 1;
+    if (!zs::aligned(t.master, 4) || !zs::aligned(t.exp_avg, sa) || !zs::aligned(t.exp_avg_sq, sa) ||
+        !zs::aligned(t.exp_avg_scale, 4) || !zs::aligned(t.root_scale, 4) || !zs::aligned(t.lowp, 2))
+      return fail(ZERO_EINVAL, "%s: a buffer of tensor %d is not aligned to its elements", who, (int)i);
+    if (chunks != nullptr)
+      for (int64_t c = 0; c < k; ++c) chunks[count + c] = zero_list_chunk{i, static_cast<int32_t>(c)};
+    count += k;
+  }
+  *n_chunks = count;
+  return ZERO_OK;
+}
+
+// The checks and the launch that both forms of the list step share.
+static zero_status adamw_list(const char* who, const zs::ListArgs& a, const zs::ListScalars& s, int32_t n_groups,
+                              void* stream) {
+  if (a.n_tensors < 0 || a.n_chunks < 0) return fail(ZERO_EINVAL, "%s: n_tensors or n_chunks < 0", who);
+  if (a.n_chunks > 0 && (a.list == nullptr || a.chunks == nullptr || a.grads == nullptr || a.n_tensors == 0))
+    return fail(ZERO_EINVAL, "%s: NULL list, chunks or grads", who);
+  if (!zs::aligned(a.list, 8) || !zs::aligned(a.chunks, 8) || !zs::aligned(a.grads, 8))
+    return fail(ZERO_EINVAL, "%s: list, chunks or grads not 8-byte aligned", who);
+  const zero_status g = check_groups(who, n_groups);
+  if (g != ZERO_OK) return g;
+  if (a.state_bits != 32 && a.state_bits != 8) return fail(ZERO_EINVAL, "%s: state_bits must be 32 or 8", who);
+  if (a.stochastic && a.state_bits == 32)
+    return fail(ZERO_EINVAL, "%s: a rounding seed needs 8-bit states", who);
+  if (!zs::valid_dtype(a.grad_dtype)) return fail(ZERO_EINVAL, "%s: bad grad_dtype %d", who, a.grad_dtype);
+  if (a.lowp_dtype != ZERO_BF16 && a.lowp_dtype != ZERO_F16)
+    return fail(ZERO_EINVAL, "%s: lowp_dtype must be BF16 or F16", who);
+  if (!std::isfinite(a.gscale)) return fail(ZERO_EINVAL, "%s: non-finite grad_scale", who);
+  if (a.n_chunks == 0) return ZERO_OK;
+  return zs::launch_adamw_list(a, s, zs::as_stream(stream));
+}
+
+zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, const zero_list_chunk* d_chunks,
+                            int64_t n_chunks, int32_t state_bits, const zero_tensor* d_grads, zero_dtype grad_dtype,
+                            float grad_scale, const float* d_grad_scale, zero_dtype lowp_dtype,
+                            const zero_adamw_hparams* groups, int32_t n_groups, int64_t step,
+                            const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream) {
+  const char* who = "zero_adamw_list";
+  const zero_status g = check_groups(who, n_groups);
+  if (g != ZERO_OK) return g;
+  if (groups == nullptr) return fail(ZERO_EINVAL, "%s: NULL groups", who);
+  zs::ListScalars s{};
+  for (int32_t i = 0; i < n_groups; ++i) {
+    const zero_status hs = adamw_scalars(who, &groups[i], step, &s.s[i]);
+    if (hs != ZERO_OK) return hs;
+  }
+  const zs::ListArgs a{d_list, n_tensors, d_chunks, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
+                       lowp_dtype, nullptr, rounding != nullptr, rounding != nullptr ? *rounding : zero_rounding{},
+                       step, d_clip};
+  return adamw_list(who, a, s, n_groups, stream);
+}
+
+zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_tensors, const zero_list_chunk* d_chunks,
+                                   int64_t n_chunks, int32_t state_bits, const zero_tensor* d_grads,
+                                   zero_dtype grad_dtype, float grad_scale, const float* d_grad_scale,
+                                   zero_dtype lowp_dtype, const zero_adamw_device_state* d_states, int32_t n_groups,
+                                   const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream) {
+  const char* who = "zero_adamw_list_device";
+  const zero_status c = check_state(who, d_states);
+  if (c != ZERO_OK) return c;
+  const zs::ListArgs a{d_list, n_tensors, d_chunks, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
+                       lowp_dtype, d_states, rounding != nullptr, rounding != nullptr ? *rounding : zero_rounding{},
+                       0, d_clip};
+  return adamw_list(who, a, zs::ListScalars{}, n_groups, stream);
+}
+
+zero_status zero_adamw_prepare_list_device(const zero_adamw_hparams* d_hp, int32_t n_groups,
+                                           const zero_norm_result* d_clip, zero_adamw_device_state* d_states,
+                                           void* stream) {
+  const char* who = "zero_adamw_prepare_list_device";
+  const zero_status g = check_groups(who, n_groups);
+  if (g != ZERO_OK) return g;
+  if (d_hp == nullptr) return fail(ZERO_EINVAL, "%s: NULL d_hp", who);
+  if (!zs::aligned(d_hp, 8)) return fail(ZERO_EINVAL, "%s: d_hp not 8-byte aligned", who);
+  const zero_status c = check_state(who, d_states);
+  if (c != ZERO_OK) return c;
+  return zs::launch_adamw_prepare_list(d_hp, n_groups, d_clip, d_states, zs::as_stream(stream));
 }
 
 }  // extern "C"

@@ -49,6 +49,54 @@ AdamwTableInstance launch_adamw_table_acc;
 AdamwTableInstance launch_adamw_table_p4;
 AdamwTableInstance launch_adamw_table_p4_acc;
 
+// AdamW over a flat shard with 8-bit moments, grads through the table.
+struct Table8Args {
+  float* p;
+  zero_state8 q;
+  const float* acc;
+  const zero_tensor* table;
+  int n_tensors;
+  int grad_dtype;
+  int64_t shard_start, n;
+  float gscale;
+  const float* dscale;
+  void* lowp;
+  int lowp_dtype;
+  const zero_adamw_device_state* ds;
+  bool stochastic;
+  zero_rounding rounding;
+  int64_t step;
+  const zero_norm_result* clip;
+};
+zero_status launch_adamw_table8(const Table8Args& a, const AdamScalars& s, cudaStream_t st);
+
+// AdamW over a list of separate tensors.
+constexpr int kListChunk = ZERO_LIST_CHUNK;
+struct ListScalars {
+  AdamScalars s[ZERO_LIST_MAX_GROUPS];
+};
+struct ListArgs {
+  const zero_list_tensor* list;
+  int n_tensors;
+  const zero_list_chunk* chunks;
+  int64_t n_chunks;
+  int state_bits;
+  const zero_tensor* grads;
+  int grad_dtype;
+  float gscale;
+  const float* dscale;
+  int lowp_dtype;
+  const zero_adamw_device_state* ds;
+  bool stochastic;
+  zero_rounding rounding;
+  int64_t step;
+  const zero_norm_result* clip;
+};
+zero_status launch_adamw_list(const ListArgs& a, const ListScalars& s, cudaStream_t st);
+
+zero_status launch_state8_pack(const float* m, const float* v, int64_t n, const zero_state8& q, cudaStream_t st);
+zero_status launch_state8_unpack(const zero_state8& q, int64_t n, float* m, float* v, cudaStream_t st);
+
 // Debug builds (ZERO_DEBUG): each translation unit's violation record
 // {count, first site, first index, first block}; reset clears it.
 zero_status debug_read_adamw(unsigned long long* out, bool reset);
@@ -57,6 +105,9 @@ zero_status debug_read_adamw_table_acc(unsigned long long* out, bool reset);
 zero_status debug_read_adamw_table_p4(unsigned long long* out, bool reset);
 zero_status debug_read_adamw_table_p4_acc(unsigned long long* out, bool reset);
 zero_status debug_read_adamw_device(unsigned long long* out, bool reset);
+zero_status debug_read_adamw_list(unsigned long long* out, bool reset);
+zero_status debug_read_adamw_table8(unsigned long long* out, bool reset);
+zero_status debug_read_state8(unsigned long long* out, bool reset);
 zero_status debug_read_flatten(unsigned long long* out, bool reset);
 zero_status debug_read_sqnorm(unsigned long long* out, bool reset);
 zero_status launch_debug_selftest(long long index, cudaStream_t st);
@@ -69,6 +120,10 @@ zero_status launch_loss_scale_update(zero_loss_scale_state* state, int32_t accum
 // One thread: advance the device step state (see zero_adamw_prepare_device).
 zero_status launch_adamw_prepare(const zero_adamw_hparams* hp, const zero_norm_result* clip,
                                  zero_adamw_device_state* state, cudaStream_t st);
+
+// One block: the step states of n_groups parameter groups, all or none.
+zero_status launch_adamw_prepare_list(const zero_adamw_hparams* hp, int n_groups, const zero_norm_result* clip,
+                                      zero_adamw_device_state* states, cudaStream_t st);
 
 // `partials` (nullable): also write the norm tiles' partial sums of squares
 // of the values written (one binary64 per 32768 elements of dst / acc).

@@ -17,6 +17,10 @@ live on the device (zero_adamw_prepare_device), so flatten/accumulate plus
 and can be captured once in a ``torch.cuda.CUDAGraph`` and replayed as whole
 steps; the results are bit-identical to the host-counter steps.
 
+Moments in 8 bits (``state_bits=8``): exp_avg and the root of exp_avg_sq are
+held as e4m3 codes with a scale per 256 elements (zero_state8), 2 instead of 8
+bytes per parameter; every path above works the same.
+
 Grad range: for ZeRO-2/3 and FSDP the rank holds grads of its own shard
 only (``grad_range="shard"``, norm over the shard plus ``extra_sqnorm`` from
 the other ranks).  For ZeRO-1 every rank holds the whole averaged flat grad
@@ -34,18 +38,86 @@ import torch
 from . import zero_shard as zs
 
 
-class FlatShardAdamW:
+class GradTables:
+    """The device tables of grads lists, and the grad passes' scale arguments: what the
+    optimizers over a list of tensors share."""
+
+    def _init_tables(self, numels: Sequence[int], device) -> None:
+        self.numels = [int(n) for n in numels]
+        self.total = int(sum(self.numels))
+        self.device = torch.device(device)
+        self._registered = None
+        self._tables: Dict[tuple, Tuple[torch.Tensor, int]] = {}
+
+    def _table(self, grads: Sequence[Optional[torch.Tensor]]) -> torch.Tensor:
+        # keyed by address, size and contiguity, so a cached table is only reused for
+        # grads that passed the checks below when it was built
+        key = tuple(None if g is None else (g.data_ptr(), g.numel(), g.is_contiguous()) for g in grads)
+        hit = self._tables.get(key)
+        if hit is None:
+            if len(grads) != len(self.numels):
+                raise ValueError("one grad (or None) per parameter tensor is required")
+            for i, (g, n) in enumerate(zip(grads, self.numels)):
+                if g is not None and g.numel() != n:
+                    raise ValueError(f"grad {i} has {g.numel()} elements, expected {n}")
+            table, total = zs.zero_tensor_table(grads, self.numels)
+            assert total == self.total
+            hit = (zs.device_table(table, len(grads), self.device), total)
+            if len(self._tables) > 64:
+                self._tables.clear()
+            self._tables[key] = hit
+        return hit[0]
+
+    def device_table(self, grads: Sequence[Optional[torch.Tensor]]) -> Tuple[torch.Tensor, int, torch.dtype]:
+        """The FlatParameter table of a grads list in device memory (built once per list of
+        grad addresses and cached), with its tensor count and grad dtype.  Calling it before
+        a CUDA graph capture keeps the table's host-to-device copy out of the graph."""
+        return self._resolve(grads)
+
+    def register_grads(self, grads: Sequence[Optional[torch.Tensor]]) -> None:
+        """Fix the per-tensor grads once (e.g. views into one flat grad storage, as
+        FSDP's FlatParameter keeps them).  flatten() / step_tensors() called without
+        grads then reuse the device table and do no per-tensor host work, which
+        matters for lists of thousands of tensors."""
+        self._registered = (self._table(grads), len(grads), self._grad_dtype(grads))
+
+    @staticmethod
+    def _grad_dtype(grads) -> torch.dtype:
+        dts = {g.dtype for g in grads if g is not None}
+        if len(dts) > 1:
+            raise ValueError("all grads must share one dtype")
+        return dts.pop() if dts else torch.float32
+
+    def _resolve(self, grads):
+        if grads is None:
+            if self._registered is None:
+                raise ValueError("no grads given and none registered")
+            return self._registered
+        return self._table(grads), len(grads), self._grad_dtype(grads)
+
+    def _scale_args(self, scale, loss_scale):
+        """(host scale, device scale or None, non-finite flag) of a grad pass: with a
+        DeviceLossScale the kernels read its unscale factor and raise its flag."""
+        if loss_scale is None:
+            return float(scale), None, self.found_nonfinite
+        return 1.0, loss_scale.unscale, loss_scale.found_inf
+
+
+class FlatShardAdamW(GradTables):
     def __init__(self, numels: Sequence[int], *, world_size: int = 1, rank: int = 0, lr: float = 1e-4,
                  betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
                  max_norm: float = math.inf, lowp_dtype: Optional[torch.dtype] = torch.bfloat16,
                  grad_range: str = "shard", device="cuda", master: Optional[torch.Tensor] = None,
                  lowp_out: Optional[torch.Tensor] = None, grad_buffer: bool = True, capturable: bool = False,
-                 workspace: Optional[torch.Tensor] = None):
+                 workspace: Optional[torch.Tensor] = None, state_bits: int = 32,
+                 rounding_seed: Optional[int] = None):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 32 or 8")
+        if rounding_seed is not None and state_bits == 32:
+            raise ValueError("a rounding_seed needs state_bits=8")
         if grad_range not in ("shard", "full"):
             raise ValueError("grad_range must be 'shard' or 'full'")
-        self.device = torch.device(device)
-        self.numels = [int(n) for n in numels]
-        self.total = int(sum(self.numels))
+        self._init_tables(numels, device)
         self.world_size, self.rank = world_size, rank
         self.start, self.end = zs.zero_shard_range(self.total, world_size, rank)
         self.n = self.end - self.start
@@ -61,8 +133,15 @@ class FlatShardAdamW:
         if master.numel() != self.n or master.dtype != torch.float32:
             raise ValueError("master must be fp32 with the shard's size")
         self.master = master.to(dev).contiguous()
-        self.exp_avg = torch.zeros(self.n, dtype=torch.float32, device=dev)
-        self.exp_avg_sq = torch.zeros(self.n, dtype=torch.float32, device=dev)
+        # the moments: fp32, or 8 bits (state8; rounding_seed: None rounds them to nearest, an
+        # integer seeds stochastic rounding)
+        self.state_bits, self.rounding_seed = state_bits, rounding_seed
+        self.state8 = self.exp_avg = self.exp_avg_sq = None
+        if state_bits == 8:
+            self.state8 = zs.new_state8(self.n, dev)
+        else:
+            self.exp_avg = torch.zeros(self.n, dtype=torch.float32, device=dev)
+            self.exp_avg_sq = torch.zeros(self.n, dtype=torch.float32, device=dev)
         if lowp_out is not None:
             self.lowp = lowp_out  # e.g. the rank's slice of the full low-precision FlatParameter
         elif lowp_dtype is not None:
@@ -84,9 +163,10 @@ class FlatShardAdamW:
             self._dev_state = zs.new_adamw_device_state(dev)
         self._norm_ready = False  # the grad norm's tile partials are up to date in self.ws
         self._local_buf: Optional[torch.Tensor] = None
-        self._registered = None
-        self._tables: Dict[tuple, Tuple[torch.Tensor, int]] = {}
         self._flat_tables: Dict[tuple, torch.Tensor] = {}
+        self._grad_table: Optional[Tuple[int, torch.Tensor]] = None
+        if state_bits == 8 and grad_buffer and self.device.type == "cuda":
+            self._own_grad_table()  # here, not in a graph capture
 
     # ------------------------------------------------------- step counter
     @property
@@ -153,59 +233,6 @@ class FlatShardAdamW:
             self.weight_decay = weight_decay
 
     # ---------------------------------------------------------------- grads
-    def _table(self, grads: Sequence[Optional[torch.Tensor]]) -> torch.Tensor:
-        # keyed by address, size and contiguity, so a cached table is only reused for
-        # grads that passed the checks below when it was built
-        key = tuple(None if g is None else (g.data_ptr(), g.numel(), g.is_contiguous()) for g in grads)
-        hit = self._tables.get(key)
-        if hit is None:
-            if len(grads) != len(self.numels):
-                raise ValueError("one grad (or None) per parameter tensor is required")
-            for i, (g, n) in enumerate(zip(grads, self.numels)):
-                if g is not None and g.numel() != n:
-                    raise ValueError(f"grad {i} has {g.numel()} elements, expected {n}")
-            table, total = zs.zero_tensor_table(grads, self.numels)
-            assert total == self.total
-            hit = (zs.device_table(table, len(grads), self.device), total)
-            if len(self._tables) > 64:
-                self._tables.clear()
-            self._tables[key] = hit
-        return hit[0]
-
-    def device_table(self, grads: Sequence[Optional[torch.Tensor]]) -> Tuple[torch.Tensor, int, torch.dtype]:
-        """The FlatParameter table of a grads list in device memory (built once per list of
-        grad addresses and cached), with its tensor count and grad dtype.  Calling it before
-        a CUDA graph capture keeps the table's host-to-device copy out of the graph."""
-        return self._resolve(grads)
-
-    def register_grads(self, grads: Sequence[Optional[torch.Tensor]]) -> None:
-        """Fix the per-tensor grads once (e.g. views into one flat grad storage, as
-        FSDP's FlatParameter keeps them).  flatten() / step_tensors() called without
-        grads then reuse the device table and do no per-tensor host work, which
-        matters for lists of thousands of tensors."""
-        self._registered = (self._table(grads), len(grads), self._grad_dtype(grads))
-
-    @staticmethod
-    def _grad_dtype(grads) -> torch.dtype:
-        dts = {g.dtype for g in grads if g is not None}
-        if len(dts) > 1:
-            raise ValueError("all grads must share one dtype")
-        return dts.pop() if dts else torch.float32
-
-    def _resolve(self, grads):
-        if grads is None:
-            if self._registered is None:
-                raise ValueError("no grads given and none registered")
-            return self._registered
-        return self._table(grads), len(grads), self._grad_dtype(grads)
-
-    def _scale_args(self, scale, loss_scale):
-        """(host scale, device scale or None, non-finite flag) of a grad pass: with a
-        DeviceLossScale the kernels read its unscale factor and raise its flag."""
-        if loss_scale is None:
-            return float(scale), None, self.found_nonfinite
-        return 1.0, loss_scale.unscale, loss_scale.found_inf
-
     def flatten(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, accumulate: bool,
                 scale: float = 1.0, fuse_norm: bool = False, stream=None, loss_scale=None) -> None:
         """Flatten/cast per-tensor grads (or the registered ones) into the rank's flat
@@ -284,12 +311,42 @@ class FlatShardAdamW:
             self._norm_into(self.norm_buf, extra_sqnorm, self.max_norm, stream)
         if self.capturable:
             zs.zero_adamw_prepare_device(self._dev_hp, clip, self._dev_state, stream)
+        if self.state_bits == 8:
+            self._update_tables(self._own_grad_table(), 1, self.grad.numel(), torch.float32, self.start - self.glo, 1.0,
+                                None, None, clip, stream)
+        elif self.capturable:
             zs.zero_adamw_step_device(self.master, self.exp_avg, self.exp_avg_sq, self.shard_grad(), self.lowp,
                                       self._dev_state, clip, stream)
         else:
             zs.zero_adamw_step(self.master, self.exp_avg, self.exp_avg_sq, self.shard_grad(), self.lowp, self.lr,
                                self.betas[0], self.betas[1], self.eps, self.weight_decay, self._t + 1,
                                clip, stream)
+
+    def _own_grad_table(self) -> torch.Tensor:
+        """The one-entry table of the fp32 grad buffer (the 8-bit step reads every grad through a table)."""
+        if self.grad.numel() != self.ghi - self.glo:
+            raise ValueError("this step needs the grad buffer (grad_buffer=True)")
+        if self._grad_table is None or self._grad_table[0] != self.grad.data_ptr():
+            table = zs.device_table(zs.zero_tensor_table([self.grad])[0], 1, self.device)
+            self._grad_table = (self.grad.data_ptr(), table)
+        return self._grad_table[1]
+
+    def _update_tables(self, table, count: int, total: int, dt, shard_start: int, scale: float, d_scale, acc, clip,
+                       stream) -> None:
+        """Enqueue AdamW with the grads read through a tensor table (with capturable=True
+        after the prepare)."""
+        state = (self.state8,) if self.state_bits == 8 else (self.exp_avg, self.exp_avg_sq)
+        kw = dict(acc=acc, d_scale=d_scale)
+        if self.state_bits == 8:
+            kw.update(rounding_seed=self.rounding_seed, rounding_stream=self.start)  # the same draws on every path
+        if self.capturable:
+            call = zs.zero_adamw_step8_tensors_device if self.state_bits == 8 else zs.zero_adamw_step_tensors_device
+            call(self.master, *state, table, count, total, dt, shard_start, scale, self.lowp, self._dev_state, clip,
+                 stream, **kw)
+        else:
+            call = zs.zero_adamw_step8_tensors if self.state_bits == 8 else zs.zero_adamw_step_tensors
+            call(self.master, *state, table, count, total, dt, shard_start, scale, self.lowp, self.lr, self.betas[0],
+                 self.betas[1], self.eps, self.weight_decay, self._t + 1, clip, stream, **kw)
 
     def finish_step(self, stream=None, result: Optional[zs.NormResult] = None) -> zs.NormResult:
         """Read the step's grad norm (a device->host copy that waits for the step's
@@ -418,38 +475,37 @@ class FlatShardAdamW:
         acc = self.shard_grad() if accumulated else None
         if self.capturable:
             zs.zero_adamw_prepare_device(self._dev_hp, self.norm_buf, self._dev_state, stream)
-            zs.zero_adamw_step_tensors_device(self.master, self.exp_avg, self.exp_avg_sq, table, count, total,
-                                              dt, shard_start, sc, self.lowp, self._dev_state, self.norm_buf,
-                                              stream, acc=acc, d_scale=dsc)
-        else:
-            zs.zero_adamw_step_tensors(self.master, self.exp_avg, self.exp_avg_sq, table, count, total, dt,
-                                       shard_start, sc, self.lowp, self.lr, self.betas[0], self.betas[1],
-                                       self.eps, self.weight_decay, self._t + 1, self.norm_buf, stream, acc=acc,
-                                       d_scale=dsc)
+        self._update_tables(table, count, total, dt, shard_start, sc, dsc, acc, self.norm_buf, stream)
 
     # -------------------------------------------------------- checkpoint
     def state_dict(self) -> dict:
         """The rank's optimizer state on the host: step counter, fp32 master /
-        exp_avg / exp_avg_sq and the low-precision copy (a flat shard each)."""
-        sd = {"t": self.t, "start": self.start, "end": self.end, "master": self.master.cpu(),
-              "exp_avg": self.exp_avg.cpu(), "exp_avg_sq": self.exp_avg_sq.cpu()}
+        exp_avg / exp_avg_sq (or state8) and the low-precision copy (a flat shard each)."""
+        sd = {"t": self.t, "start": self.start, "end": self.end, "master": self.master.cpu()}
+        if self.state_bits == 8:
+            sd["state8"] = tuple(x.cpu() for x in self.state8)
+        else:
+            sd["exp_avg"], sd["exp_avg_sq"] = self.exp_avg.cpu(), self.exp_avg_sq.cpu()
         if self.lowp is not None:
             sd["lowp"] = self.lowp.cpu()
         return sd
 
     def load_state_dict(self, sd: dict) -> None:
+        """Restore a checkpoint of this shard; moments of the other width (fp32 / 8 bits) are
+        converted, 32-bit ones rounded to nearest."""
         if (sd["start"], sd["end"]) != (self.start, self.end):
             raise ValueError("state belongs to another shard")
         self.t = int(sd["t"])
         self.master.copy_(sd["master"])
-        self.exp_avg.copy_(sd["exp_avg"])
-        self.exp_avg_sq.copy_(sd["exp_avg_sq"])
+        zs.load_moments(sd, self.state8, self.exp_avg, self.exp_avg_sq, self.device)
         if self.lowp is not None and "lowp" in sd:
             self.lowp.copy_(sd["lowp"])
 
     def resident_bytes(self) -> int:
         """Device bytes this rank holds for the step (grad + state + low-precision copy)."""
-        b = 4 * (self.grad.numel() + 3 * self.n)  # grad is empty without a grad buffer
+        b = 4 * (self.grad.numel() + self.n)  # grad is empty without a grad buffer
+        moments = (self.exp_avg, self.exp_avg_sq) if self.state_bits == 32 else self.state8
+        b += sum(x.numel() * x.element_size() for x in moments)
         if self.lowp is not None:
             b += self.lowp.numel() * self.lowp.element_size()
         return b

@@ -54,6 +54,29 @@ class zero_adamw_device_state(ctypes.Structure):
                 ("scalars", ctypes.c_float * 8)]
 
 
+class zero_state8(ctypes.Structure):
+    _fields_ = [("exp_avg", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p), ("root", ctypes.c_void_p),
+                ("root_scale", ctypes.c_void_p)]
+
+
+class zero_rounding(ctypes.Structure):
+    _fields_ = [("seed", ctypes.c_uint64), ("stream", ctypes.c_int64)]
+
+
+class zero_list_tensor(ctypes.Structure):
+    _fields_ = [("master", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scale", ctypes.c_void_p), ("root_scale", ctypes.c_void_p), ("lowp", ctypes.c_void_p),
+                ("numel", ctypes.c_int64), ("group", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class zero_list_chunk(ctypes.Structure):
+    _fields_ = [("tensor", ctypes.c_int32), ("chunk", ctypes.c_int32)]
+
+
+STATE8_BLOCK = 256      # elements per scale of the 8-bit moments
+LIST_CHUNK = 2048       # elements per piece of a tensor list's work
+LIST_MAX_GROUPS = 64
+
 NORM_RESULT_BYTES = ctypes.sizeof(zero_norm_result)
 HPARAMS_BYTES = ctypes.sizeof(zero_adamw_hparams)
 DEVICE_STATE_BYTES = ctypes.sizeof(zero_adamw_device_state)
@@ -107,6 +130,18 @@ def lib() -> ctypes.CDLL:
     L.zero_adamw_step_device.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int, i64, vp, vp, vp]
     L.zero_adamw_step_tensors_device.argtypes = [vp, vp, vp, vp, i32, i64, ctypes.c_int, i64, f32, vp, vp, vp,
                                                  ctypes.c_int, i64, vp, vp, vp]
+    hpp, rdp, s8 = ctypes.POINTER(zero_adamw_hparams), ctypes.POINTER(zero_rounding), ctypes.POINTER(zero_state8)
+    ci = ctypes.c_int
+    L.zero_state8_pack.argtypes = [vp, vp, i64, s8, vp]
+    L.zero_state8_unpack.argtypes = [s8, i64, vp, vp, vp]
+    L.zero_adamw_step8_tensors.argtypes = [vp, s8, vp, i32, i64, ci, i64, f32, vp, vp, vp, ci, i64, hpp, i64, rdp,
+                                           vp, vp]
+    L.zero_adamw_step8_tensors_device.argtypes = [vp, s8, vp, i32, i64, ci, i64, f32, vp, vp, vp, ci, i64, vp, rdp,
+                                                  vp, vp]
+    L.zero_list_chunks.argtypes = [vp, i32, i32, i32, vp, ctypes.POINTER(i64)]
+    L.zero_adamw_list.argtypes = [vp, i32, vp, i64, i32, vp, ci, f32, vp, ci, hpp, i32, i64, rdp, vp, vp]
+    L.zero_adamw_list_device.argtypes = [vp, i32, vp, i64, i32, vp, ci, f32, vp, ci, vp, i32, rdp, vp, vp]
+    L.zero_adamw_prepare_list_device.argtypes = [vp, i32, vp, vp, vp]
     L.zero_status_string.argtypes = [ctypes.c_int]
     L.zero_status_string.restype = ctypes.c_char_p
     L.zero_last_error.argtypes = []
@@ -117,7 +152,9 @@ def lib() -> ctypes.CDLL:
                "zero_adamw_step", "zero_adamw_step_tensors", "zero_loss_scale_update", "zero_loss_scale_update_device",
                "zero_adamw_scalars",
                "zero_adamw_prepare_device", "zero_adamw_step_device", "zero_adamw_step_tensors_device",
-               "zero_debug_errors", "zero_debug_selftest"):
+               "zero_debug_errors", "zero_debug_selftest", "zero_state8_pack", "zero_state8_unpack",
+               "zero_adamw_step8_tensors", "zero_adamw_step8_tensors_device", "zero_list_chunks", "zero_adamw_list",
+               "zero_adamw_list_device", "zero_adamw_prepare_list_device"):
         getattr(L, nm).restype = ctypes.c_int
     _lib = L
     return L
@@ -485,6 +522,245 @@ def zero_adamw_step_tensors_device(master: torch.Tensor, exp_avg: torch.Tensor, 
         n_tensors, total, _DT[grad_dtype], shard_start, grad_scale, _dscale(d_scale),
         _dev(acc, "acc", torch.float32, allow_none=True), lp, lowp_dt, n, _state_arg(state),
         _dev(clip, "clip", allow_none=True), _stream(stream)))
+
+
+# ------------------------------------------------- 8-bit moments, tensor lists
+class State8(NamedTuple):
+    """The 8-bit moments of n elements: e4m3 codes (float8_e4m3fn, n) of exp_avg and of the
+    square root of exp_avg_sq, each with one fp32 power-of-two scale per 256 elements.
+    exp_avg = code x scale; exp_avg_sq = (code x scale)^2."""
+    exp_avg: torch.Tensor
+    exp_avg_scale: torch.Tensor
+    root: torch.Tensor
+    root_scale: torch.Tensor
+
+
+def state8_blocks(n: int) -> int:
+    """Scales of n elements: ceil(n / 256)."""
+    return -(-n // STATE8_BLOCK)
+
+
+def new_state8(n: int, device) -> State8:
+    """8-bit moments of n elements, all zero."""
+    b = state8_blocks(n)
+    codes = [torch.zeros(n, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.zeros(b, dtype=torch.float32, device=device) for _ in range(2)]
+    return State8(codes[0], scales[0], codes[1], scales[1])
+
+
+def _state8_arg(state: State8, n: int, who: str = "state8") -> zero_state8:
+    if not isinstance(state, tuple) or len(state) != 4:
+        raise ValueError(f"{who} must be a State8")
+    ptrs = []
+    for t, nm, dt, k in zip(state, State8._fields, (torch.float8_e4m3fn, torch.float32) * 2,
+                            (n, state8_blocks(n)) * 2):
+        ptrs.append(_dev(t, f"{who}.{nm}", dt))
+        if t.numel() != k:
+            raise ValueError(f"{who}.{nm} has {t.numel()} elements, expected {k}")
+    return zero_state8(*ptrs)
+
+
+def _rounding(rounding_seed: Optional[int], stream: int):
+    """NULL (round to nearest) or the 64-bit seed and the stream of stochastic rounding."""
+    if rounding_seed is None:
+        return None
+    return ctypes.byref(zero_rounding(int(rounding_seed) & 0xFFFFFFFFFFFFFFFF, int(stream)))
+
+
+def zero_state8_pack(exp_avg: torch.Tensor, exp_avg_sq: torch.Tensor, state8: State8, stream=None) -> None:
+    """fp32 moments into the 8-bit state, rounded to nearest."""
+    n = exp_avg.numel()
+    if exp_avg_sq.numel() != n:
+        raise ValueError("exp_avg_sq differs in size from exp_avg")
+    q = _state8_arg(state8, n)
+    _check(lib().zero_state8_pack(_dev(exp_avg, "exp_avg", torch.float32),
+                                  _dev(exp_avg_sq, "exp_avg_sq", torch.float32), n, ctypes.byref(q), _stream(stream)))
+
+
+def zero_state8_unpack(state8: State8, exp_avg: torch.Tensor, exp_avg_sq: torch.Tensor, stream=None) -> None:
+    """The fp32 moments that the 8-bit state stands for."""
+    n = exp_avg.numel()
+    if exp_avg_sq.numel() != n:
+        raise ValueError("exp_avg_sq differs in size from exp_avg")
+    q = _state8_arg(state8, n)
+    _check(lib().zero_state8_unpack(ctypes.byref(q), n, _dev(exp_avg, "exp_avg", torch.float32),
+                                    _dev(exp_avg_sq, "exp_avg_sq", torch.float32), _stream(stream)))
+
+
+def load_moments(sd: dict, state8: Optional[State8], exp_avg: Optional[torch.Tensor],
+                 exp_avg_sq: Optional[torch.Tensor], device) -> None:
+    """Copy a checkpoint's moments (fp32 exp_avg / exp_avg_sq, or state8) into an optimizer's,
+    converting where the widths differ, on the current stream."""
+    saved = sd.get("state8")
+    if saved is None and state8 is None:
+        exp_avg.copy_(sd["exp_avg"])
+        exp_avg_sq.copy_(sd["exp_avg_sq"])
+    elif saved is None:
+        zero_state8_pack(sd["exp_avg"].to(device), sd["exp_avg_sq"].to(device), state8)
+    elif state8 is None:
+        zero_state8_unpack(State8(*(x.to(device) for x in saved)), exp_avg, exp_avg_sq)
+    else:
+        for dst, src in zip(state8, saved):
+            dst.copy_(src)
+
+
+def _step8_common(master, state8, d_table, n_tensors, param_lowp, clip, acc):
+    n = master.numel()
+    q = _state8_arg(state8, n)
+    _check_acc(acc, n)
+    if n_tensors > 0 and d_table.numel() < n_tensors * TENSOR_ENTRY_BYTES:
+        raise ValueError("d_table holds fewer entries than n_tensors")
+    if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
+        raise ValueError("clip is smaller than zero_norm_result")
+    lp, lowp_dt = _lowp_arg(param_lowp, n)
+    return n, q, lp, lowp_dt
+
+
+def zero_adamw_step8_tensors(master: torch.Tensor, state8: State8, d_table: torch.Tensor, n_tensors: int, total: int,
+                             grad_dtype: torch.dtype, shard_start: int, grad_scale: float,
+                             param_lowp: Optional[torch.Tensor], lr: float, beta1: float, beta2: float, eps: float,
+                             weight_decay: float, step: int, clip: Optional[torch.Tensor] = None, stream=None,
+                             acc: Optional[torch.Tensor] = None, d_scale: Optional[torch.Tensor] = None,
+                             rounding_seed: Optional[int] = None, rounding_stream: Optional[int] = None) -> None:
+    """zero_adamw_step_tensors with the moments in 8 bits; rounding_seed: None rounds them to
+    nearest, an integer seeds stochastic rounding, whose stream is rounding_stream (default:
+    shard_start)."""
+    n, q, lp, lowp_dt = _step8_common(master, state8, d_table, n_tensors, param_lowp, clip, acc)
+    hp = zero_adamw_hparams(lr, beta1, beta2, eps, weight_decay)
+    _check(lib().zero_adamw_step8_tensors(
+        _dev(master, "master", torch.float32), ctypes.byref(q),
+        _dev(d_table, "d_table", torch.uint8, allow_none=n_tensors == 0), n_tensors, total, _DT[grad_dtype],
+        shard_start, grad_scale, _dscale(d_scale), _dev(acc, "acc", torch.float32, allow_none=True), lp, lowp_dt, n,
+        ctypes.byref(hp), step, _rounding(rounding_seed, shard_start if rounding_stream is None else rounding_stream),
+        _dev(clip, "clip", allow_none=True), _stream(stream)))
+
+
+def zero_adamw_step8_tensors_device(master: torch.Tensor, state8: State8, d_table: torch.Tensor, n_tensors: int,
+                                    total: int, grad_dtype: torch.dtype, shard_start: int, grad_scale: float,
+                                    param_lowp: Optional[torch.Tensor], state: torch.Tensor,
+                                    clip: Optional[torch.Tensor] = None, stream=None,
+                                    acc: Optional[torch.Tensor] = None, d_scale: Optional[torch.Tensor] = None,
+                                    rounding_seed: Optional[int] = None,
+                                    rounding_stream: Optional[int] = None) -> None:
+    """zero_adamw_step8_tensors with the scalars, step and skip decision of the device step state."""
+    n, q, lp, lowp_dt = _step8_common(master, state8, d_table, n_tensors, param_lowp, clip, acc)
+    _check(lib().zero_adamw_step8_tensors_device(
+        _dev(master, "master", torch.float32), ctypes.byref(q),
+        _dev(d_table, "d_table", torch.uint8, allow_none=n_tensors == 0), n_tensors, total, _DT[grad_dtype],
+        shard_start, grad_scale, _dscale(d_scale), _dev(acc, "acc", torch.float32, allow_none=True), lp, lowp_dt, n,
+        _state_arg(state), _rounding(rounding_seed, shard_start if rounding_stream is None else rounding_stream),
+        _dev(clip, "clip", allow_none=True), _stream(stream)))
+
+
+class TensorList(NamedTuple):
+    """A list of tensors prepared for zero_adamw_list: the device copies of its entries and
+    of its chunks.  It holds addresses: keep the tensors alive."""
+    entries: torch.Tensor   # uint8, 64 bytes per tensor
+    chunks: torch.Tensor    # int32 [n_chunks, 2]
+    numels: Tuple[int, ...]
+    state_bits: int
+    n_groups: int
+    lowp_dtype: Optional[torch.dtype]
+
+
+def zero_tensor_list(masters: Sequence[torch.Tensor], states: Sequence[tuple],
+                     lowp: Optional[Sequence[Optional[torch.Tensor]]] = None, group_of: Optional[Sequence[int]] = None,
+                     n_groups: int = 1, state_bits: int = 32) -> TensorList:
+    """Check a list and copy it to the device.  states[i]: (exp_avg, exp_avg_sq), fp32, or
+    with state_bits=8 a State8; lowp[i]: None or a bf16/f16 copy (one dtype for the list)."""
+    n = len(masters)
+    if n == 0:
+        raise ValueError("an empty tensor list")
+    lowp = [None] * n if lowp is None else list(lowp)
+    group_of = [0] * n if group_of is None else [int(g) for g in group_of]
+    if len(states) != n or len(lowp) != n or len(group_of) != n:
+        raise ValueError("masters, states, lowp and group_of differ in length")
+    if state_bits not in (8, 32):
+        raise ValueError("state_bits must be 32 or 8")
+    dts = {t.dtype for t in lowp if t is not None}
+    if len(dts) > 1 or not dts <= {torch.bfloat16, torch.float16}:
+        raise ValueError("low-precision copies must be all bf16 or all f16")
+    entries = (zero_list_tensor * n)()
+    for i, (p, st, lp) in enumerate(zip(masters, states, lowp)):
+        k = p.numel()
+        e = entries[i]
+        e.master = _dev(p, f"masters[{i}]", torch.float32)
+        if state_bits == 8:
+            q = _state8_arg(st, k, f"states[{i}]")
+            e.exp_avg, e.exp_avg_scale, e.exp_avg_sq, e.root_scale = q.exp_avg, q.exp_avg_scale, q.root, q.root_scale
+        else:
+            for t in st:
+                if t.numel() != k:
+                    raise ValueError(f"states[{i}] differs in size from masters[{i}]")
+            e.exp_avg = _dev(st[0], f"states[{i}].exp_avg", torch.float32)
+            e.exp_avg_sq = _dev(st[1], f"states[{i}].exp_avg_sq", torch.float32)
+        if lp is not None:
+            if lp.numel() != k:
+                raise ValueError(f"lowp[{i}] differs in size from masters[{i}]")
+            e.lowp = _dev(lp, f"lowp[{i}]")
+        e.numel, e.group = k, group_of[i]
+        if p.device != masters[0].device or any(t.device != p.device for t in (*st, *([] if lp is None else [lp]))):
+            raise ValueError(f"tensor {i} is not on one device with the list")
+    count = ctypes.c_int64()
+    _check(lib().zero_list_chunks(entries, n, n_groups, state_bits, None, ctypes.byref(count)))
+    chunks = np.zeros((count.value, 2), dtype=np.int32)
+    _check(lib().zero_list_chunks(entries, n, n_groups, state_bits, ctypes.c_void_p(chunks.ctypes.data),
+                                  ctypes.byref(count)))
+    dev = masters[0].device
+    raw = torch.frombuffer(bytearray(bytes(memoryview(entries))), dtype=torch.uint8)
+    return TensorList(raw.to(dev), torch.from_numpy(chunks).to(dev), tuple(p.numel() for p in masters), state_bits,
+                      n_groups, dts.pop() if dts else None)
+
+
+def _list_args(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float, d_scale):
+    if d_grads.numel() < len(tl.numels) * TENSOR_ENTRY_BYTES:
+        raise ValueError("d_grads holds fewer entries than the list")
+    return (_dev(tl.entries, "entries"), len(tl.numels), _dev(tl.chunks, "chunks", torch.int32), tl.chunks.shape[0],
+            tl.state_bits, _dev(d_grads, "d_grads", torch.uint8), _DT[grad_dtype], grad_scale, _dscale(d_scale),
+            ZERO_BF16 if tl.lowp_dtype is None else _DT[tl.lowp_dtype])
+
+
+def zero_adamw_list(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float,
+                    groups: Sequence[Tuple[float, float, float, float, float]], step: int,
+                    clip: Optional[torch.Tensor] = None, stream=None, d_scale: Optional[torch.Tensor] = None,
+                    rounding_seed: Optional[int] = None, rounding_stream: int = 0) -> None:
+    """One AdamW step over every tensor of a list.  d_grads: the device table of the grads
+    (zero_tensor_table + device_table, in list order); groups: (lr, beta1, beta2, eps,
+    weight_decay) of each parameter group."""
+    if len(groups) != tl.n_groups:
+        raise ValueError(f"{len(groups)} groups given, the list has {tl.n_groups}")
+    if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
+        raise ValueError("clip is smaller than zero_norm_result")
+    hp = (zero_adamw_hparams * len(groups))(*[zero_adamw_hparams(*g) for g in groups])
+    _check(lib().zero_adamw_list(*_list_args(tl, d_grads, grad_dtype, grad_scale, d_scale), hp, len(groups), step,
+                                 _rounding(rounding_seed, rounding_stream), _dev(clip, "clip", allow_none=True), _stream(stream)))
+
+
+def zero_adamw_list_device(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float,
+                           states: torch.Tensor, clip: Optional[torch.Tensor] = None, stream=None,
+                           d_scale: Optional[torch.Tensor] = None, rounding_seed: Optional[int] = None,
+                           rounding_stream: int = 0) -> None:
+    """zero_adamw_list with the groups' scalars, step and skip decision from device step states."""
+    if states.numel() * states.element_size() < tl.n_groups * DEVICE_STATE_BYTES:
+        raise ValueError("states is smaller than one zero_adamw_device_state per group")
+    if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
+        raise ValueError("clip is smaller than zero_norm_result")
+    _check(lib().zero_adamw_list_device(*_list_args(tl, d_grads, grad_dtype, grad_scale, d_scale),
+                                        _dev(states, "states"), tl.n_groups, _rounding(rounding_seed, rounding_stream),
+                                        _dev(clip, "clip", allow_none=True), _stream(stream)))
+
+
+def zero_adamw_prepare_list_device(d_hp: torch.Tensor, n_groups: int, clip: Optional[torch.Tensor],
+                                   states: torch.Tensor, stream=None) -> None:
+    """Advance every group's device step state for the next step (all or none)."""
+    if d_hp.numel() * d_hp.element_size() < n_groups * HPARAMS_BYTES:
+        raise ValueError("d_hp is smaller than one zero_adamw_hparams per group")
+    if states.numel() * states.element_size() < n_groups * DEVICE_STATE_BYTES:
+        raise ValueError("states is smaller than one zero_adamw_device_state per group")
+    if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
+        raise ValueError("clip is smaller than zero_norm_result")
+    _check(lib().zero_adamw_prepare_list_device(_dev(d_hp, "d_hp"), n_groups, _dev(clip, "clip", allow_none=True),
+                                                _dev(states, "states"), _stream(stream)))
 
 
 # ------------------------------------------------------------ debug builds

@@ -14,7 +14,9 @@
  * zero_grad_sqnorm_finalize / _combine (the norm from fused partials and from
  * the ranks' sums), the loss-scale updates (host and device), the AdamW
  * variants that read the grads through the tensor table or take their
- * scalars from a device step state (graph-capturable steps), and
+ * scalars from a device step state (graph-capturable steps), the step with
+ * moments in 8 bits (zero_adamw_step8_tensors, zero_state8_pack / _unpack),
+ * the step over many separate tensors (zero_adamw_list), and
  * zero_grad_sqnorm_noalloc.
  *
  * Sources: the ZeRO page (ai6s.net, "cann-recipes-train" ZeRO-1/2/3 on
@@ -495,6 +497,180 @@ zero_status zero_adamw_step_tensors_device(float* d_master, float* d_exp_avg, fl
                                            zero_dtype lowp_dtype, int64_t n,
                                            const zero_adamw_device_state* d_state,
                                            const zero_norm_result* d_clip, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Moments in 8 bits, and AdamW over many separate tensors.  No counterpart
+ * on the source pages (their ledger counts 12 bytes of fp32 state per
+ * parameter; here 4 + 2): the update is zero_adamw_step's.
+ *
+ * The 8-bit format.  Per block of 256 consecutive elements of a shard (or of
+ * a tensor; the last block may be short), exp_avg is held as e4m3 codes c and
+ * one power of two S, exp_avg = c * S; likewise the square root of
+ * exp_avg_sq, exp_avg_sq = (c * S)^2 rounded to binary32.  S is the least
+ * power of two >= 2^-126 with max|x| <= 448 S over the block, so x / S and
+ * c * S are exact and the code's rounding is the only one:
+ *   nearest     c = x / S rounded to nearest even on the e4m3 grid;
+ *   stochastic  |c| = floor((floor(128 |x/S| / u) + k) / 128) u, u the grid's
+ *               spacing at |x/S| and k in [0, 128) drawn for the element.
+ * A root above zero is raised to the grid's least value 2^-9 first, so it
+ * never becomes zero.  A block whose max|x| is not finite (or >= 2^126) has
+ * S = NaN: all its elements read back as NaN.  Codes of zero with scales of
+ * zero (fresh memory) are zero moments.
+ * The draws are functions of (seed, step, stream, element): with
+ * H the 32-bit PCG permutation RXS-M-XS, h = H(lo32 seed), h = H(hi32 seed ^
+ * h), h = H(lo32 step ^ h), h = H(stream ^ h), and i the index of a pair of
+ * elements 2i, 2i + 1: h = H(hi32 i ^ h), w = H(lo32 i ^ h).  The low half
+ * of w is the even element's, the high half the odd one's; of each, bits 0..6
+ * round exp_avg, bits 7..13 the root.  stream: the low 32 bits of
+ * zero_rounding.stream, for a list of that plus the tensor's number.
+ * --------------------------------------------------------------------- */
+#define ZERO_STATE8_BLOCK 256
+
+/* The 8-bit moments of n elements (device memory): n codes and
+ * ceil(n / 256) scales each. */
+typedef struct zero_state8 {
+  uint8_t* exp_avg;      /* e4m3 codes */
+  float* exp_avg_scale;  /* powers of two */
+  uint8_t* root;         /* e4m3 codes of sqrt(exp_avg_sq) */
+  float* root_scale;
+} zero_state8;
+
+/* Stochastic rounding's draws (see above). */
+typedef struct zero_rounding {
+  uint64_t seed;
+  int64_t stream; /* its low 32 bits: ranks, or lists, that share a seed take different streams */
+} zero_rounding;
+
+/* zero_state8_pack -- device.
+ * The fp32 moments d_exp_avg, d_exp_avg_sq (n elements) into q, rounded to
+ * nearest.  A negative exp_avg_sq makes its block NaN.
+ * Errors: ZERO_EINVAL for n < 0, NULL q, or NULL buffers with n > 0. */
+zero_status zero_state8_pack(const float* d_exp_avg, const float* d_exp_avg_sq, int64_t n, const zero_state8* q,
+                             void* stream);
+
+/* zero_state8_unpack -- device.
+ * The values q stands for: d_exp_avg = c S, d_exp_avg_sq = fl((c S)^2).
+ * Packing what was unpacked gives the same values again.
+ * Errors: as zero_state8_pack. */
+zero_status zero_state8_unpack(const zero_state8* q, int64_t n, float* d_exp_avg, float* d_exp_avg_sq, void* stream);
+
+/* zero_adamw_step8_tensors -- device.
+ * zero_adamw_step_tensors with the moments in 8 bits: the rank's flat shard
+ * [shard_start, shard_start + n), the grads fl(grad_scale * x) read through
+ * the table (a flat grad is a table of one tensor), optionally added to
+ * d_acc.  Per element, with m = c S of exp_avg and r = c S of the root:
+ *   g = grad * coef;  p = p * (1 - lr*wd)
+ *   m = fma(1-beta1, g, m*beta1)
+ *   v = fma((1-beta2)*g, g, (r*r)*beta2);  r = sqrt(v)
+ *   p = p - (lr / (1-beta1^t)) * (m / fma(r, 1 / sqrt(1-beta2^t), eps))
+ * each operation rounded to nearest in binary32; p and lowp use these m and
+ * r, which are rounded to 8 bits only when they are stored in q.
+ * rounding: NULL rounds to nearest, else (host memory) the seed and stream of
+ * stochastic rounding.
+ * 16 bytes per parameter with 16-bit grads and copy, where the fp32 state
+ * takes 28.  Any element alignment is accepted; the fast path needs master
+ * and d_acc 32-byte and the codes 8-byte aligned.
+ * Errors: those of zero_adamw_step_tensors, and NULL q or NULL q buffers
+ * with n > 0. */
+zero_status zero_adamw_step8_tensors(float* d_master, const zero_state8* q, const zero_tensor* d_table,
+                                     int32_t n_tensors, int64_t total, zero_dtype grad_dtype, int64_t shard_start,
+                                     float grad_scale, const float* d_grad_scale, const float* d_acc,
+                                     void* d_param_lowp, zero_dtype lowp_dtype, int64_t n,
+                                     const zero_adamw_hparams* hp, int64_t step, const zero_rounding* rounding,
+                                     const zero_norm_result* d_clip, void* stream);
+
+/* zero_adamw_step8_tensors_device -- device.
+ * zero_adamw_step8_tensors with the scalars, the step of the draws and the
+ * skip decision from d_state, as zero_adamw_step_device. */
+zero_status zero_adamw_step8_tensors_device(float* d_master, const zero_state8* q, const zero_tensor* d_table,
+                                            int32_t n_tensors, int64_t total, zero_dtype grad_dtype,
+                                            int64_t shard_start, float grad_scale, const float* d_grad_scale,
+                                            const float* d_acc, void* d_param_lowp, zero_dtype lowp_dtype, int64_t n,
+                                            const zero_adamw_device_state* d_state, const zero_rounding* rounding,
+                                            const zero_norm_result* d_clip, void* stream);
+
+/* One tensor of a list (64 bytes).  master: fp32.  exp_avg, exp_avg_sq: fp32
+ * with the scale pointers NULL, or (8 bits) e4m3 codes of exp_avg and of
+ * exp_avg_sq's root with their scales.  lowp: NULL, or the low-precision
+ * copy.  Each buffer is contiguous with numel elements (scales:
+ * ceil(numel / 256)), at any element alignment; the fast path needs fp32
+ * buffers 32-byte, codes 8-byte, 16-bit buffers 16-byte aligned. */
+typedef struct zero_list_tensor {
+  float* master;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* root_scale;
+  void* lowp;
+  int64_t numel;
+  int32_t group;    /* parameter group, in [0, n_groups) */
+  int32_t reserved; /* 0 */
+} zero_list_tensor;
+
+/* One piece of work of a list: elements [2048 chunk, 2048 (chunk + 1)) of a tensor. */
+typedef struct zero_list_chunk {
+  int32_t tensor;
+  int32_t chunk;
+} zero_list_chunk;
+
+#define ZERO_LIST_CHUNK 2048
+#define ZERO_LIST_MAX_GROUPS 64
+
+/* zero_list_chunks -- host only.
+ * Checks a list (state_bits 32 or 8, groups in [0, n_groups), no NULL where
+ * numel > 0, numel >= 0 and below 2^31 chunks, reserved 0) and counts its
+ * chunks into *n_chunks; with chunks != NULL also fills chunks[0 .. *n_chunks)
+ * in list order.  The caller copies the list and the chunks to device memory
+ * for zero_adamw_list.
+ * Errors: ZERO_EINVAL for a bad list, n_tensors < 0, n_groups outside
+ * [1, 64], state_bits other than 32 and 8, or NULL n_chunks. */
+zero_status zero_list_chunks(const zero_list_tensor* list, int32_t n_tensors, int32_t n_groups, int32_t state_bits,
+                             zero_list_chunk* chunks, int64_t* n_chunks);
+
+/* zero_adamw_list -- device.
+ * One AdamW step over every tensor of a list, each with its group's
+ * hyper-parameters and the grad d_grads[i].ptr (NULL: reads as zeros, as in
+ * zero_flatten_cast; numel and flat_offset are not used, so the table of a
+ * grad-norm pass serves here too).  Tensor by tensor the result is
+ * zero_adamw_step's on fl(grad_scale * x), bit for bit (state_bits 32), or
+ * zero_adamw_step8_tensors' with stream + tensor number as the stream
+ * (state_bits 8).  One launch, whatever the number of tensors.
+ * d_list, d_chunks: device copies of a list that zero_list_chunks accepted
+ *   and of its chunks.  Their contents cannot be checked on the host: a list
+ *   that differs from the checked one is the caller's error.
+ * groups: host, n_groups hyper-parameters; step t >= 1 is the same for all.
+ * rounding: as for zero_adamw_step8_tensors; must be NULL with 32 bits.
+ * d_clip, d_grad_scale, lowp_dtype: as for zero_adamw_step_tensors.
+ * Errors: ZERO_EINVAL for n_tensors < 0, n_chunks < 0, NULL d_list, d_chunks
+ * or d_grads with n_chunks > 0, n_groups outside [1, 64], bad
+ * hyper-parameters of any group, step < 1, a bad dtype, state_bits or
+ * rounding, or a non-finite grad_scale. */
+zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, const zero_list_chunk* d_chunks,
+                            int64_t n_chunks, int32_t state_bits, const zero_tensor* d_grads, zero_dtype grad_dtype,
+                            float grad_scale, const float* d_grad_scale, zero_dtype lowp_dtype,
+                            const zero_adamw_hparams* groups, int32_t n_groups, int64_t step,
+                            const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream);
+
+/* zero_adamw_list_device -- device.
+ * zero_adamw_list with the scalars, the step of the draws and the skip
+ * decision from d_states[n_groups], as the last
+ * zero_adamw_prepare_list_device on the stream left them. */
+zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_tensors, const zero_list_chunk* d_chunks,
+                                   int64_t n_chunks, int32_t state_bits, const zero_tensor* d_grads,
+                                   zero_dtype grad_dtype, float grad_scale, const float* d_grad_scale,
+                                   zero_dtype lowp_dtype, const zero_adamw_device_state* d_states, int32_t n_groups,
+                                   const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream);
+
+/* zero_adamw_prepare_list_device -- device (one block).
+ * zero_adamw_prepare_device for n_groups groups at once: d_hp[g] and
+ * d_states[g].  All groups step or none does: when d_clip's norm is not
+ * finite, or any group's hyper-parameters are out of range (that group's
+ * status becomes ZERO_EINVAL), every apply is 0 and every step stays.
+ * Errors: ZERO_EINVAL for n_groups outside [1, 64], NULL or misaligned d_hp
+ * or d_states. */
+zero_status zero_adamw_prepare_list_device(const zero_adamw_hparams* d_hp, int32_t n_groups,
+                                           const zero_norm_result* d_clip, zero_adamw_device_state* d_states,
+                                           void* stream);
 
 /* ---------------------------------------------------------------------
  * Debug builds.  No counterpart on the source pages.  Built with
