@@ -1,0 +1,78 @@
+// adamw_list8.cu -- AdamW over many separate tensors in one launch, with the
+// moments in 8 bits (state8.cuh).  The work split is adamw_list.cu's: a block
+// per chunk of 1024 elements, a warp per 256, which here is one scale.
+#include "common.cuh"
+#include "kernels.h"
+#include "list.cuh"
+
+namespace zs {
+
+template <int DT, bool SR, bool VEC>
+__device__ __forceinline__ void list8_block(const zero_list_tensor& t, const void* grad, int64_t k, int64_t rest,
+                                            float gscale, float coef, const AdamScalars& s, int lowp_dtype,
+                                            uint32_t key) {
+  const int left = static_cast<int>(rest < kBlock8 ? rest : kBlock8);
+  float p[8], g[8];
+  float* const pk = t.master + k;
+  uint8_t* const qm = static_cast<uint8_t*>(t.exp_avg) + k;
+  uint8_t* const qr = static_cast<uint8_t*>(t.exp_avg_sq) + k;
+  float* const ms = t.exp_avg_scale + k / kBlock8;
+  float* const rs = t.root_scale + k / kBlock8;
+  load_block_f32<VEC>(pk, left, p);
+  const uint2 cm = load_codes<VEC>(qm, left), cr = load_codes<VEC>(qr, left);
+  const float sm = *ms, sr = *rs;
+  load_block_grad<DT, VEC>(grad, k, rest, gscale, g);
+  update_block<VEC, SR>(pk, qm, qr, ms, rs, t.lowp == nullptr ? nullptr : static_cast<unsigned short*>(t.lowp) + k,
+                        lowp_dtype, left, p, g, cm, cr, sm, sr, coef, s, key, k >> 1);
+}
+
+template <int DT, bool SR>
+__global__ void __launch_bounds__(kListThreads, 10)
+    adamw_list8_kernel(const zero_list_tensor* __restrict__ list, int n_tensors,
+                       const int32_t* __restrict__ first_chunk, const zero_tensor* __restrict__ grads, float gscale,
+                       const float* __restrict__ dscale, int lowp_dtype, const __grid_constant__ ListScalars hs,
+                       const zero_adamw_device_state* __restrict__ ds, RoundingBase rnd,
+                       const zero_norm_result* __restrict__ clip) {
+  const int tensor = find_chunk_tensor(first_chunk, n_tensors, blockIdx.x);
+  const int chunk = blockIdx.x - __ldg(first_chunk + tensor);
+  const zero_list_tensor t = list[tensor];
+  const void* grad = grads[tensor].ptr;
+  if (!ZS_CHECK(chunk >= 0 && chunk < (t.numel + kListChunk - 1) / kListChunk, 90, blockIdx.x)) return;
+  float coef = 1.0f;
+  if (clip != nullptr) {
+    if (!clip->finite) return;  // non-finite grad norm: the step is skipped
+    coef = clip->clip_coef;
+  }
+  if (dscale != nullptr) gscale = *dscale;
+  const int64_t k = static_cast<int64_t>(chunk) * kListChunk + kBlock8 * (threadIdx.x >> 5);
+  const int64_t left = t.numel - k;
+  if (left <= 0) return;
+  AdamScalars s;
+  if (!group_scalars(hs, ds, t.group, s)) return;
+  uint32_t key = 0u;
+  if (SR) key = rounding_key(rnd, ds, tensor, k >> 1);
+  if (left >= kBlock8 && aligned(t.master, 32) && aligned(t.exp_avg, 8) && aligned(t.exp_avg_sq, 8))
+    list8_block<DT, SR, true>(t, grad, k, left, gscale, coef, s, lowp_dtype, key);
+  else
+    list8_block<DT, SR, false>(t, grad, k, left, gscale, coef, s, lowp_dtype,
+                               key);
+}
+
+template <int DT, bool SR>
+static zero_status launch_list8_t(const ListArgs& a, const ListScalars& hs, cudaStream_t st) {
+  adamw_list8_kernel<DT, SR><<<static_cast<unsigned>(a.n_chunks), kListThreads, 0, st>>>(
+      a.list, a.n_tensors, a.first_chunk, a.grads, a.gscale, a.dscale, a.lowp_dtype, hs, a.ds, a.rounding, a.clip);
+  return check_launch("adamw_list8_kernel");
+}
+
+ZS_DEBUG_UNIT(adamw_list8)
+
+zero_status launch_adamw_list8(const ListArgs& a, const ListScalars& hs, cudaStream_t st) {
+  if (a.grad_dtype == ZERO_F32)
+    return a.stochastic ? launch_list8_t<ZERO_F32, true>(a, hs, st) : launch_list8_t<ZERO_F32, false>(a, hs, st);
+  if (a.grad_dtype == ZERO_BF16)
+    return a.stochastic ? launch_list8_t<ZERO_BF16, true>(a, hs, st) : launch_list8_t<ZERO_BF16, false>(a, hs, st);
+  return a.stochastic ? launch_list8_t<ZERO_F16, true>(a, hs, st) : launch_list8_t<ZERO_F16, false>(a, hs, st);
+}
+
+}  // namespace zs

@@ -8,6 +8,7 @@
 #include "adam_scalars.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "rounding.cuh"
 
 namespace zs {
 
@@ -323,7 +324,8 @@ zero_status zero_debug_errors(uint64_t* out, int32_t reset) {
   zero_status (*const readers[])(unsigned long long*, bool) = {
       zs::debug_read_adamw,          zs::debug_read_adamw_table,        zs::debug_read_adamw_table_acc,
       zs::debug_read_adamw_table_p4, zs::debug_read_adamw_table_p4_acc, zs::debug_read_adamw_device,
-      zs::debug_read_adamw_list,     zs::debug_read_adamw_table8,      zs::debug_read_state8,
+      zs::debug_read_adamw_list,     zs::debug_read_adamw_list8,       zs::debug_read_adamw_table8,
+      zs::debug_read_state8,
       zs::debug_read_flatten,        zs::debug_read_sqnorm};
   uint64_t total = 0, first[3] = {0, 0, 0};
   for (auto rd : readers) {
@@ -463,12 +465,13 @@ static zero_status step8_tensors(const char* who, float* d_master, const zero_st
   if (!zs::valid_dtype(grad_dtype)) return fail(ZERO_EINVAL, "%s: bad grad_dtype %d", who, (int)grad_dtype);
   if (!std::isfinite(grad_scale)) return fail(ZERO_EINVAL, "%s: non-finite grad_scale", who);
   if (n > 0 && d_master == nullptr) return fail(ZERO_EINVAL, "%s: NULL master", who);
+  if (n / 2048 >= INT32_MAX) return fail(ZERO_EINVAL, "%s: n %lld exceeds 2^42", who, (long long)n);
   if (d_param_lowp != nullptr && lowp_dtype != ZERO_BF16 && lowp_dtype != ZERO_F16)
     return fail(ZERO_EINVAL, "%s: lowp_dtype must be BF16 or F16", who);
   if (n == 0) return ZERO_OK;
   const zs::Table8Args a{d_master, *q, d_acc, d_table, n_tensors, grad_dtype, shard_start, n, grad_scale, d_grad_scale,
                          d_param_lowp, lowp_dtype, d_state, rounding != nullptr,
-                         rounding != nullptr ? *rounding : zero_rounding{}, step, d_clip};
+                         zs::rounding_base(rounding, d_state == nullptr ? &step : nullptr), d_clip};
   return zs::launch_adamw_table8(a, s, zs::as_stream(stream));
 }
 
@@ -507,9 +510,8 @@ static zero_status check_groups(const char* who, int32_t n_groups) {
 }
 
 zero_status zero_list_chunks(const zero_list_tensor* list, int32_t n_tensors, int32_t n_groups, int32_t state_bits,
-                             zero_list_chunk* chunks, int64_t* n_chunks) {
+                             int32_t* first_chunk, int32_t* n_chunks) {
   const char* who = "zero_list_chunks";
-  if (n_chunks == nullptr) return fail(ZERO_EINVAL, "%s: NULL n_chunks", who);
   if (n_tensors < 0 || (n_tensors > 0 && list == nullptr)) return fail(ZERO_EINVAL, "%s: bad list", who);
   const zero_status g = check_groups(who, n_groups);
   if (g != ZERO_OK) return g;
@@ -517,8 +519,7 @@ zero_status zero_list_chunks(const zero_list_tensor* list, int32_t n_tensors, in
   int64_t count = 0;
   for (int32_t i = 0; i < n_tensors; ++i) {
     const zero_list_tensor& t = list[i];
-    const int64_t k = t.numel / zs::kListChunk + (t.numel % zs::kListChunk != 0 ? 1 : 0);
-    if (t.numel < 0 || k > INT32_MAX) return fail(ZERO_EINVAL, "%s: numel[%d] = %lld", who, (int)i, (long long)t.numel);
+    if (t.numel < 0) return fail(ZERO_EINVAL, "%s: numel[%d] = %lld < 0", who, (int)i, (long long)t.numel);
     if (t.group < 0 || t.group >= n_groups)
       return fail(ZERO_EINVAL, "%s: group[%d] = %d of %d", who, (int)i, (int)t.group, (int)n_groups);
     if (t.reserved != 0) return fail(ZERO_EINVAL, "%s: reserved[%d] != 0", who, (int)i);
@@ -532,11 +533,12 @@ zero_status zero_list_chunks(const zero_list_tensor* list, int32_t n_tensors, in
     if (!zs::aligned(t.master, 4) || !zs::aligned(t.exp_avg, sa) || !zs::aligned(t.exp_avg_sq, sa) ||
         !zs::aligned(t.exp_avg_scale, 4) || !zs::aligned(t.root_scale, 4) || !zs::aligned(t.lowp, 2))
       return fail(ZERO_EINVAL, "%s: a buffer of tensor %d is not aligned to its elements", who, (int)i);
-    if (chunks != nullptr)
-      for (int64_t c = 0; c < k; ++c) chunks[count + c] = zero_list_chunk{i, static_cast<int32_t>(c)};
-    count += k;
+    if (first_chunk != nullptr) first_chunk[i] = static_cast<int32_t>(count);
+    count += t.numel / zs::kListChunk + (t.numel % zs::kListChunk != 0 ? 1 : 0);
+    if (count > INT32_MAX) return fail(ZERO_EINVAL, "%s: 2^31 chunks or more up to tensor %d", who, (int)i);
   }
-  *n_chunks = count;
+  if (first_chunk != nullptr) first_chunk[n_tensors] = static_cast<int32_t>(count);
+  if (n_chunks != nullptr) *n_chunks = static_cast<int32_t>(count);
   return ZERO_OK;
 }
 
@@ -544,10 +546,10 @@ zero_status zero_list_chunks(const zero_list_tensor* list, int32_t n_tensors, in
 static zero_status adamw_list(const char* who, const zs::ListArgs& a, const zs::ListScalars& s, int32_t n_groups,
                               void* stream) {
   if (a.n_tensors < 0 || a.n_chunks < 0) return fail(ZERO_EINVAL, "%s: n_tensors or n_chunks < 0", who);
-  if (a.n_chunks > 0 && (a.list == nullptr || a.chunks == nullptr || a.grads == nullptr || a.n_tensors == 0))
-    return fail(ZERO_EINVAL, "%s: NULL list, chunks or grads", who);
-  if (!zs::aligned(a.list, 8) || !zs::aligned(a.chunks, 8) || !zs::aligned(a.grads, 8))
-    return fail(ZERO_EINVAL, "%s: list, chunks or grads not 8-byte aligned", who);
+  if (a.n_chunks > 0 && (a.list == nullptr || a.first_chunk == nullptr || a.grads == nullptr || a.n_tensors == 0))
+    return fail(ZERO_EINVAL, "%s: NULL list, first_chunk or grads", who);
+  if (!zs::aligned(a.list, 8) || !zs::aligned(a.first_chunk, 4) || !zs::aligned(a.grads, 8))
+    return fail(ZERO_EINVAL, "%s: list, first_chunk or grads not aligned", who);
   const zero_status g = check_groups(who, n_groups);
   if (g != ZERO_OK) return g;
   if (a.state_bits != 32 && a.state_bits != 8) return fail(ZERO_EINVAL, "%s: state_bits must be 32 or 8", who);
@@ -561,8 +563,8 @@ static zero_status adamw_list(const char* who, const zs::ListArgs& a, const zs::
   return zs::launch_adamw_list(a, s, zs::as_stream(stream));
 }
 
-zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, const zero_list_chunk* d_chunks,
-                            int64_t n_chunks, int32_t state_bits, const zero_tensor* d_grads, zero_dtype grad_dtype,
+zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, const int32_t* d_first_chunk,
+                            int32_t n_chunks, int32_t state_bits, const zero_tensor* d_grads, zero_dtype grad_dtype,
                             float grad_scale, const float* d_grad_scale, zero_dtype lowp_dtype,
                             const zero_adamw_hparams* groups, int32_t n_groups, int64_t step,
                             const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream) {
@@ -575,23 +577,21 @@ zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, c
     const zero_status hs = adamw_scalars(who, &groups[i], step, &s.s[i]);
     if (hs != ZERO_OK) return hs;
   }
-  const zs::ListArgs a{d_list, n_tensors, d_chunks, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
-                       lowp_dtype, nullptr, rounding != nullptr, rounding != nullptr ? *rounding : zero_rounding{},
-                       step, d_clip};
+  const zs::ListArgs a{d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
+                       lowp_dtype, nullptr, rounding != nullptr, zs::rounding_base(rounding, &step), d_clip};
   return adamw_list(who, a, s, n_groups, stream);
 }
 
-zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_tensors, const zero_list_chunk* d_chunks,
-                                   int64_t n_chunks, int32_t state_bits, const zero_tensor* d_grads,
+zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_tensors, const int32_t* d_first_chunk,
+                                   int32_t n_chunks, int32_t state_bits, const zero_tensor* d_grads,
                                    zero_dtype grad_dtype, float grad_scale, const float* d_grad_scale,
                                    zero_dtype lowp_dtype, const zero_adamw_device_state* d_states, int32_t n_groups,
                                    const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream) {
   const char* who = "zero_adamw_list_device";
   const zero_status c = check_state(who, d_states);
   if (c != ZERO_OK) return c;
-  const zs::ListArgs a{d_list, n_tensors, d_chunks, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
-                       lowp_dtype, d_states, rounding != nullptr, rounding != nullptr ? *rounding : zero_rounding{},
-                       0, d_clip};
+  const zs::ListArgs a{d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
+                       lowp_dtype, d_states, rounding != nullptr, zs::rounding_base(rounding, nullptr), d_clip};
   return adamw_list(who, a, zs::ListScalars{}, n_groups, stream);
 }
 

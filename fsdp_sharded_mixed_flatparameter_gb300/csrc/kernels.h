@@ -49,6 +49,13 @@ AdamwTableInstance launch_adamw_table_acc;
 AdamwTableInstance launch_adamw_table_p4;
 AdamwTableInstance launch_adamw_table_p4_acc;
 
+// Stochastic rounding's draws, as far as the launch knows them: the hash of the
+// seed and (unless the step is on the device) of the step, and the stream.
+struct RoundingBase {
+  uint32_t hash;
+  uint32_t stream;
+};
+
 // AdamW over a flat shard with 8-bit moments, grads through the table.
 struct Table8Args {
   float* p;
@@ -64,22 +71,22 @@ struct Table8Args {
   int lowp_dtype;
   const zero_adamw_device_state* ds;
   bool stochastic;
-  zero_rounding rounding;
-  int64_t step;
+  RoundingBase rounding;
   const zero_norm_result* clip;
 };
 zero_status launch_adamw_table8(const Table8Args& a, const AdamScalars& s, cudaStream_t st);
 
 // AdamW over a list of separate tensors.
 constexpr int kListChunk = ZERO_LIST_CHUNK;
+constexpr int kListThreads = kListChunk / 8;
 struct ListScalars {
   AdamScalars s[ZERO_LIST_MAX_GROUPS];
 };
 struct ListArgs {
   const zero_list_tensor* list;
   int n_tensors;
-  const zero_list_chunk* chunks;
-  int64_t n_chunks;
+  const int32_t* first_chunk;
+  int32_t n_chunks;
   int state_bits;
   const zero_tensor* grads;
   int grad_dtype;
@@ -88,11 +95,11 @@ struct ListArgs {
   int lowp_dtype;
   const zero_adamw_device_state* ds;
   bool stochastic;
-  zero_rounding rounding;
-  int64_t step;
+  RoundingBase rounding;
   const zero_norm_result* clip;
 };
 zero_status launch_adamw_list(const ListArgs& a, const ListScalars& s, cudaStream_t st);
+zero_status launch_adamw_list8(const ListArgs& a, const ListScalars& s, cudaStream_t st);
 
 zero_status launch_state8_pack(const float* m, const float* v, int64_t n, const zero_state8& q, cudaStream_t st);
 zero_status launch_state8_unpack(const zero_state8& q, int64_t n, float* m, float* v, cudaStream_t st);
@@ -106,6 +113,7 @@ zero_status debug_read_adamw_table_p4(unsigned long long* out, bool reset);
 zero_status debug_read_adamw_table_p4_acc(unsigned long long* out, bool reset);
 zero_status debug_read_adamw_device(unsigned long long* out, bool reset);
 zero_status debug_read_adamw_list(unsigned long long* out, bool reset);
+zero_status debug_read_adamw_list8(unsigned long long* out, bool reset);
 zero_status debug_read_adamw_table8(unsigned long long* out, bool reset);
 zero_status debug_read_state8(unsigned long long* out, bool reset);
 zero_status debug_read_flatten(unsigned long long* out, bool reset);

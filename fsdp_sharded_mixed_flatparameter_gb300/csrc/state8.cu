@@ -8,32 +8,68 @@
 
 namespace zs {
 
+template <bool VEC>
+__device__ __forceinline__ void pack_block(const float* __restrict__ m, const float* __restrict__ v,
+                                           const zero_state8& q, int64_t b, int left) {
+  const int64_t k = b * kBlock8;
+  if (!ZS_CHECK(left > 0 && (!VEC || (aligned(m + k, 32) && aligned(v + k, 32) && aligned(q.exp_avg + k, 8) &&
+                                      aligned(q.root + k, 8))),
+                80, k))
+    return;
+  float x[8], r[8];
+  load_block_f32<VEC>(m + k, left, x);
+  load_block_f32<VEC>(v + k, left, r);
+  F2 xm[4], xr[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    xm[i] = pair(x[2 * i], x[2 * i + 1]);
+    xr[i] = pair(__fsqrt_rn(r[2 * i]), __fsqrt_rn(r[2 * i + 1]));
+  }
+  uint2 cm, cr;
+  float sm, sr;
+  encode_block<VEC, false>(xm, xr, warp_amax(xm), warp_amax(xr), 0u, 0, cm, cr, sm, sr);
+  store_codes<VEC>(q.exp_avg + k, left, cm);
+  store_codes<VEC>(q.root + k, left, cr);
+  if ((threadIdx.x & 31) == 0) {
+    q.exp_avg_scale[b] = sm;
+    q.root_scale[b] = sr;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void unpack_block(const zero_state8& q, float* __restrict__ m, float* __restrict__ v,
+                                             int64_t b, int left) {
+  const int64_t k = b * kBlock8;
+  if (!ZS_CHECK(left > 0 && (!VEC || (aligned(m + k, 32) && aligned(v + k, 32) && aligned(q.exp_avg + k, 8) &&
+                                      aligned(q.root + k, 8))),
+                81, k))
+    return;
+  const uint2 cm = load_codes<VEC>(q.exp_avg + k, left), cr = load_codes<VEC>(q.root + k, left);
+  F2 xm[4], xr[4];
+  float x[8], r[8];
+  const float sm = q.exp_avg_scale[b], sr = q.root_scale[b];
+  decode8(cm, xm);
+  decode8(cr, xr);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const F2 y = mul2(xr[i], both(sr));
+    unpair(mul2(xm[i], both(sm)), x[2 * i], x[2 * i + 1]);
+    unpair(mul2(y, y), r[2 * i], r[2 * i + 1]);
+  }
+  store_block_f32<VEC>(m + k, left, x);
+  store_block_f32<VEC>(v + k, left, r);
+}
+
 __global__ void __launch_bounds__(256)
     state8_pack_kernel(const float* __restrict__ m, const float* __restrict__ v, int64_t n, zero_state8 q, bool vec) {
   const int64_t nb = (n + kBlock8 - 1) / kBlock8;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
   for (int64_t b = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); b < nb; b += stride) {
-    const int64_t k = b * kBlock8;
-    const int left = static_cast<int>(n - k < kBlock8 ? n - k : kBlock8);
-    const bool w = vec && left == kBlock8;
-    if (!ZS_CHECK(left > 0 && (!w || (aligned(m + k, 32) && aligned(v + k, 32) && aligned(q.exp_avg + k, 8) &&
-                                      aligned(q.root + k, 8))),
-                  80, k))
-      continue;
-    float x[8], r[8];
-    load_block_f32(m + k, w, left, x);
-    load_block_f32(v + k, w, left, r);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = __fsqrt_rn(r[j]);
-    uint32_t cm[2], cr[2];
-    float sm, sr;
-    encode_block<false>(x, r, w, 0u, 0, cm, cr, sm, sr);
-    store_codes(q.exp_avg + k, w, left, cm);
-    store_codes(q.root + k, w, left, cr);
-    if ((threadIdx.x & 31) == 0) {
-      q.exp_avg_scale[b] = sm;
-      q.root_scale[b] = sr;
-    }
+    const int64_t left = n - b * kBlock8;
+    if (vec && left >= kBlock8)
+      pack_block<true>(m, v, q, b, kBlock8);
+    else
+      pack_block<false>(m, v, q, b, static_cast<int>(left < kBlock8 ? left : kBlock8));
   }
 }
 
@@ -42,23 +78,11 @@ __global__ void __launch_bounds__(256)
   const int64_t nb = (n + kBlock8 - 1) / kBlock8;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
   for (int64_t b = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); b < nb; b += stride) {
-    const int64_t k = b * kBlock8;
-    const int left = static_cast<int>(n - k < kBlock8 ? n - k : kBlock8);
-    const bool w = vec && left == kBlock8;
-    if (!ZS_CHECK(left > 0 && (!w || (aligned(m + k, 32) && aligned(v + k, 32) && aligned(q.exp_avg + k, 8) &&
-                                      aligned(q.root + k, 8))),
-                  81, k))
-      continue;
-    uint32_t cm[2], cr[2];
-    load_codes(q.exp_avg + k, w, left, cm);
-    load_codes(q.root + k, w, left, cr);
-    float x[8], r[8];
-    decode8(cm, q.exp_avg_scale[b], x);
-    decode8(cr, q.root_scale[b], r);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = __fmul_rn(r[j], r[j]);
-    store_block_f32(m + k, w, left, x);
-    store_block_f32(v + k, w, left, r);
+    const int64_t left = n - b * kBlock8;
+    if (vec && left >= kBlock8)
+      unpack_block<true>(q, m, v, b, kBlock8);
+    else
+      unpack_block<false>(q, m, v, b, static_cast<int>(left < kBlock8 ? left : kBlock8));
   }
 }
 

@@ -31,28 +31,75 @@
 
 #include "adam.cuh"
 #include "common.cuh"
+#include "rounding.cuh"
 
 namespace zs {
 
 constexpr int kBlock8 = 256;  // elements per scale: one warp, 8 elements per lane
 
+// ------------------------------------------------------------------ pairs
+// Two binary32 values in one 64-bit register pair: sm_100's packed
+// arithmetic does both in one instruction, each rounded as alone.  The update
+// is bound by instructions before it is bound by the arithmetic units, so
+// everything that can be is done in pairs.
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ void unpair(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Hardware root and reciprocal (relative error at most 2^-23 each, subnormal
+// arguments and results as zero).
+__device__ __forceinline__ float root_approx(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // ------------------------------------------------------------------ codes
-// 4 e4m3 codes (byte i = element i), widened exactly.
-__device__ __forceinline__ void decode4(uint32_t c, float* x) {
-  uint32_t a, b;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-      : "=r"(a), "=r"(b)
+// 4 e4m3 codes (byte i = element i) as two pairs, widened exactly.
+__device__ __forceinline__ void decode4(uint32_t c, F2& a, F2& b) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(c));
-  const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
-  const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  x[0] = fa.x;
-  x[1] = fa.y;
-  x[2] = fb.x;
-  x[3] = fb.y;
+  const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  a = pair(fa.x, fa.y);
+  b = pair(fb.x, fb.y);
 }
 
 // 4 values (|x| <= 448) to the nearest codes.
-__device__ __forceinline__ uint32_t encode4_nearest(float x0, float x1, float x2, float x3) {
+__device__ __forceinline__ uint32_t encode4_nearest(F2 a, F2 b) {
+  float x0, x1, x2, x3;
+  unpair(a, x0, x1);
+  unpair(b, x2, x3);
   uint32_t r;
   asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
       : "=r"(r)
@@ -65,7 +112,9 @@ __device__ __forceinline__ uint32_t encode4_nearest(float x0, float x1, float x2
 // (normal from 2^-14, below it spaced evenly) and 7 more fraction bits, so
 // truncating to binary16 gives floor(128 |x| / u), adding the element's 7
 // random bits (one per half of k) and dropping 7 gives the code.
-__device__ __forceinline__ uint32_t encode2_stochastic(float x0, float x1, uint32_t k) {
+__device__ __forceinline__ uint32_t encode2_stochastic(F2 x, uint32_t k) {
+  float x0, x1;
+  unpair(x, x0, x1);
   uint32_t h;
   asm("cvt.rz.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(x0), "f"(x1));
   const uint32_t mag = (h & 0x7fff7fffu) + (k & 0x007f007fu);
@@ -90,184 +139,246 @@ __device__ __forceinline__ void block_scale(uint32_t amax, float& s, float& inv)
 }
 
 // --------------------------------------------------------------- rounding
-// The 32-bit PCG permutation (O'Neill, RXS-M-XS 32) as a hash.
-__host__ __device__ __forceinline__ uint32_t pcg_hash(uint32_t x) {
-  x = x * 747796405u + 2891336453u;
-  x = ((x >> ((x >> 28) + 4u)) ^ x) * 277803737u;
-  return (x >> 22) ^ x;
-}
-
-// The key of one block's draws: the word of pair i (elements 2i, 2i + 1) is
-// pcg_hash(low 32 bits of i ^ key); of each half of it bits 0..6 round
-// exp_avg and bits 7..13 the root.  `pair`: any pair of the block
-// (a block never crosses a multiple of 2^32 pairs).
-__device__ __forceinline__ uint32_t rounding_key(uint64_t seed, int64_t step, uint32_t stream, int64_t pair) {
-  uint32_t h = pcg_hash(static_cast<uint32_t>(seed));
-  h = pcg_hash(static_cast<uint32_t>(seed >> 32) ^ h);
-  h = pcg_hash(static_cast<uint32_t>(step) ^ h);
-  h = pcg_hash(stream ^ h);
+// The key of one block's draws (pcg_hash: rounding.cuh): the word of pair i
+// (elements 2i, 2i + 1) is pcg_hash(low 32 bits of i ^ key); of each half of it
+// bits 0..6 round exp_avg and bits 7..13 the root.  The launch has hashed the
+// seed and the step; a step on the device (ds) is hashed here.  `pair`: any
+// pair of the block (a block never crosses a multiple of 2^32 pairs).
+__device__ __forceinline__ uint32_t rounding_key(const RoundingBase& rnd, const zero_adamw_device_state* ds,
+                                                 uint32_t tensor, int64_t pair) {
+  uint32_t h = rnd.hash;
+  if (ds != nullptr) h = pcg_hash(static_cast<uint32_t>(ds->step) ^ h);
+  h = pcg_hash((rnd.stream + tensor) ^ h);
   return pcg_hash(static_cast<uint32_t>(pair >> 32) ^ h);
 }
 
 // ----------------------------------------------------------------- update
-// adam_update of adam.cuh on decoded moments: m, and r = sqrt(v) in place of
-// v.  The moments' operations and roundings are the same; the denominator
-// is sqrt(v) times fl(1 / sqrt(1 - beta2^t)) plus eps in one fma, where the
-// 32-bit update divides: an IEEE division is about a dozen instructions,
-// and with 16 instead of 30 bytes per element the update is near the issue
-// limit, not only the bandwidth's.
-__device__ __forceinline__ void adam_update8(float& p, float& m, float& r, float g, float coef, const AdamScalars& s,
-                                             float inv_bc2_sqrt) {
-  g = __fmul_rn(g, coef);
-  p = __fmul_rn(p, s.decay);
-  m = __fmaf_rn(s.omb1, g, __fmul_rn(m, s.b1));
-  const float v = __fmaf_rn(__fmul_rn(s.omb2, g), g, __fmul_rn(__fmul_rn(r, r), s.b2));
-  r = __fsqrt_rn(v);
-  const float u = __fdiv_rn(m, __fmaf_rn(r, inv_bc2_sqrt, s.eps));
-  p = __fsub_rn(p, __fmul_rn(s.step_size, u));
+// The update's factors for one block, each twice.  The decoded moments enter
+// only as m beta1 = c (S beta1) and v beta2 = c^2 (S^2 beta2), which with S a
+// power of two are the same numbers as fl(m beta1) and fl(fl(r^2) beta2).
+struct Factors8 {
+  F2 coef, decay, mb1, omb1, vb2, omb2, inv_bc2, eps, step;
+};
+
+__device__ __forceinline__ Factors8 factors8(const AdamScalars& s, float sm, float sr, float coef) {
+  Factors8 f;
+  f.coef = both(coef);
+  f.decay = both(s.decay);
+  f.mb1 = both(__fmul_rn(sm, s.b1));
+  f.omb1 = both(s.omb1);
+  f.vb2 = both(__fmul_rn(__fmul_rn(sr, sr), s.b2));
+  f.omb2 = both(s.omb2);
+  f.inv_bc2 = both(__frcp_rn(s.bc2_sqrt));
+  f.eps = both(fmaxf(s.eps, 0x1p-126f));  // the reciprocal's argument stays normal
+  f.step = both(-s.step_size);
+  return f;
+}
+
+// The 32-bit update (adam.cuh) on two elements whose moments come as codes:
+// cm, cr (the codes' values) in, m and v out.  m and v are what the 32-bit
+// update gives for the decoded moments, bit for bit.  The parameter's change
+// is step m / (sqrt(v) / sqrt(1 - beta2^t) + eps) with the hardware root and
+// reciprocal, within 8 ulp of itself: correctly rounded division and root
+// are some 25 instructions and two branches an element, together as much as
+// all the rest, for digits far below the 3 bits that the moments keep.
+// Returns r = sqrt(v).
+__device__ __forceinline__ F2 adam_update8(F2& p, F2& cm, F2& cr, F2 g, const Factors8& f) {
+  g = mul2(g, f.coef);
+  const F2 m = fma2(f.omb1, g, mul2(cm, f.mb1));
+  const F2 v = fma2(mul2(f.omb2, g), g, mul2(mul2(cr, cr), f.vb2));
+  float v0, v1, d0, d1;
+  unpair(v, v0, v1);
+  const F2 r = pair(root_approx(v0), root_approx(v1));
+  unpair(fma2(r, f.inv_bc2, f.eps), d0, d1);
+  const F2 u = mul2(m, pair(reciprocal_approx(d0), reciprocal_approx(d1)));
+  p = fma2(f.step, u, mul2(p, f.decay));
+  cm = m;
+  cr = v;
+  return r;
 }
 
 // ------------------------------------------------------------- one block
-// A warp holds one block of 256 elements, 8 per lane: in vector order lane l
-// has elements 8l .. 8l + 7, in element order l, l + 32, ..., l + 224 (tails
-// and unaligned buffers; absent elements are zeros).
-__device__ __forceinline__ int elem_of(bool vec, int lane, int j) { return vec ? 8 * lane + j : lane + 32 * j; }
-
-__device__ __forceinline__ uint32_t warp_amax(const float (&x)[8]) {
-  uint32_t a = 0u;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(x[j]) & 0x7fffffffu);
-  return __reduce_max_sync(0xffffffffu, a);
+// A warp holds one block of 256 elements, 8 per lane.  VEC: lane l has
+// elements 8l .. 8l + 7 of a full block in aligned buffers; else it has
+// elements l, l + 32, ..., l + 224, those from `left` on absent (zeros): tails
+// and unaligned buffers.  The two are separate instantiations: one code for
+// both, with the order as a variable, took 101 registers instead of 64.
+template <bool VEC>
+__device__ __forceinline__ int elem_of(int j) {
+  const int lane = threadIdx.x & 31;
+  return VEC ? 8 * lane + j : lane + 32 * j;
 }
 
-// Codes of the warp's block (c[0], c[1]: this lane's 8 elements, byte j of
-// the pair = element j), and its scales.  Every lane must call it.
-// `pair0`: the index of the block's first pair.
-template <bool SR>
-__device__ __forceinline__ void encode_block(const float (&m)[8], const float (&r)[8], bool vec, uint32_t key,
-                                             int64_t pair0, uint32_t (&cm)[2], uint32_t (&cr)[2], float& sm,
+// max|x| over the warp's block, as bits (NaN is the largest).
+__device__ __forceinline__ uint32_t warp_amax(const F2 (&x)[4]) {
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x0, x1;
+    unpair(x[i], x0, x1);
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(x0), "f"(x1));
+  }
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(a));
+}
+
+// Codes of the warp's block (byte j of the pair = this lane's element j) and
+// its scales, from m, r = sqrt(v) and the block's max|m|, max r as bits.
+// Every lane must call it.  `pair0`: the block's first pair.
+template <bool VEC, bool SR>
+__device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4], uint32_t amax_m, uint32_t amax_r,
+                                             uint32_t key, int64_t pair0, uint2& cm, uint2& cr, float& sm,
                                              float& sr) {
-  const int lane = threadIdx.x & 31;
   float im, ir;
-  block_scale(warp_amax(m), sm, im);
-  block_scale(warp_amax(r), sr, ir);
+  block_scale(amax_m, sm, im);
+  block_scale(amax_r, sr, ir);
   if (SR) {  // 1/S >= 2^-118 in a finite block: 2^-8 of it is still normal
     im *= 0x1p-8f;
     ir *= 0x1p-8f;
   }
   const float least = SR ? 0x1p-17f : 0x1p-9f;  // the smallest code's value
-  float x[8], y[8];
+  F2 x[4], y[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    x[j] = __fmul_rn(m[j], im);
-    y[j] = __fmul_rn(r[j], ir);
-    if (r[j] > 0.0f) y[j] = fmaxf(y[j], least);
+  for (int i = 0; i < 4; ++i) {
+    x[i] = mul2(m[i], both(im));
+    y[i] = mul2(r[i], both(ir));
+    float y0, y1, r0, r1;
+    unpair(y[i], y0, y1);
+    unpair(r[i], r0, r1);
+    if (r0 > 0.0f) y0 = fmaxf(y0, least);
+    if (r1 > 0.0f) y1 = fmaxf(y1, least);
+    y[i] = pair(y0, y1);
   }
   if (!SR) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      cm[h] = encode4_nearest(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
-      cr[h] = encode4_nearest(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
-    }
+    cm = make_uint2(encode4_nearest(x[0], x[1]), encode4_nearest(x[2], x[3]));
+    cr = make_uint2(encode4_nearest(y[0], y[1]), encode4_nearest(y[2], y[3]));
   } else {
+    const int lane = threadIdx.x & 31;
     uint32_t um[4], ur[4];
     const uint32_t p0 = static_cast<uint32_t>(pair0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t w;
-      if (vec) {
+      if (VEC) {
         w = pcg_hash((p0 + 4u * lane + i) ^ key);
       } else {  // elements lane + 64 i and lane + 64 i + 32: the same half of two words
         const uint32_t a = pcg_hash((p0 + 32u * i + (lane >> 1)) ^ key);
         const uint32_t b = pcg_hash((p0 + 32u * i + 16u + (lane >> 1)) ^ key);
         w = __byte_perm(a, b, (lane & 1) ? 0x7632 : 0x5410);
       }
-      um[i] = encode2_stochastic(x[2 * i], x[2 * i + 1], w);
-      ur[i] = encode2_stochastic(y[2 * i], y[2 * i + 1], w >> 7);
+      um[i] = encode2_stochastic(x[i], w);
+      ur[i] = encode2_stochastic(y[i], w >> 7);
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      cm[h] = __byte_perm(um[2 * h], um[2 * h + 1], 0x6420);
-      cr[h] = __byte_perm(ur[2 * h], ur[2 * h + 1], 0x6420);
-    }
+    cm = make_uint2(__byte_perm(um[0], um[1], 0x6420), __byte_perm(um[2], um[3], 0x6420));
+    cr = make_uint2(__byte_perm(ur[0], ur[1], 0x6420), __byte_perm(ur[2], ur[3], 0x6420));
   }
 }
 
-// 8 codes of one lane as floats.
-__device__ __forceinline__ void decode8(const uint32_t (&c)[2], float s, float (&x)[8]) {
-  decode4(c[0], x);
-  decode4(c[1], x + 4);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], s);
+// The values of one lane's 8 codes.
+__device__ __forceinline__ void decode8(uint2 c, F2 (&x)[4]) {
+  decode4(c.x, x[0], x[1]);
+  decode4(c.y, x[2], x[3]);
 }
 
-// This lane's codes of the block at `p` (its first element; `left` elements
-// remain from there): one 8-byte load, or bytes in element order.
-__device__ __forceinline__ void load_codes(const uint8_t* p, bool vec, int left, uint32_t (&c)[2]) {
-  const int lane = threadIdx.x & 31;
-  if (vec) {
-    asm volatile("ld.global.cs.v2.u32 {%0,%1}, [%2];" : "=r"(c[0]), "=r"(c[1]) : "l"(p + 8 * lane));
-  } else {
-    c[0] = c[1] = 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (lane + 32 * j < left) c[j >> 2] |= static_cast<uint32_t>(p[lane + 32 * j]) << (8 * (j & 3));
-  }
-}
-
-__device__ __forceinline__ void store_codes(uint8_t* p, bool vec, int left, const uint32_t (&c)[2]) {
-  const int lane = threadIdx.x & 31;
-  if (vec) {
-    asm volatile("st.global.cs.v2.u32 [%0], {%1,%2};" ::"l"(p + 8 * lane), "r"(c[0]), "r"(c[1]) : "memory");
+// This lane's codes of the block that starts at `p`.
+template <bool VEC>
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int left) {
+  uint2 c = make_uint2(0u, 0u);
+  if (VEC) {
+    asm volatile("ld.global.cs.v2.u32 {%0,%1}, [%2];" : "=r"(c.x), "=r"(c.y) : "l"(p + elem_of<VEC>(0)));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (lane + 32 * j < left) p[lane + 32 * j] = static_cast<uint8_t>(c[j >> 2] >> (8 * (j & 3)));
+      if (elem_of<VEC>(j) < left) (j < 4 ? c.x : c.y) |= static_cast<uint32_t>(p[elem_of<VEC>(j)]) << (8 * (j & 3));
   }
+  return c;
 }
 
-// This lane's 8 binary32 values of a block, zeros beyond `left`.
-__device__ __forceinline__ void load_block_f32(const float* p, bool vec, int left, float (&x)[8]) {
-  const int lane = threadIdx.x & 31;
-  if (vec) {
-    ld8_rw(p + 8 * lane, x);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = (lane + 32 * j < left) ? p[lane + 32 * j] : 0.0f;
-  }
-}
-
-__device__ __forceinline__ void store_block_f32(float* p, bool vec, int left, const float (&x)[8]) {
-  const int lane = threadIdx.x & 31;
-  if (vec) {
-    st8(p + 8 * lane, x);
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t* p, int left, uint2 c) {
+  if (VEC) {
+    asm volatile("st.global.cs.v2.u32 [%0], {%1,%2};" ::"l"(p + elem_of<VEC>(0)), "r"(c.x), "r"(c.y) : "memory");
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (lane + 32 * j < left) p[lane + 32 * j] = x[j];
+      if (elem_of<VEC>(j) < left) p[elem_of<VEC>(j)] = static_cast<uint8_t>((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
   }
 }
 
-// The low-precision copy of a block's new parameters (lowp_dtype BF16 or
-// F16; in vector order the address of each lane's 8 values is as aligned as
-// the copy's start: 16, 8, 4 or 2 bytes).
-__device__ __forceinline__ void store_block_lowp(void* lowp, int lowp_dtype, bool vec, int left,
-                                                 const float (&x)[8]) {
-  const int lane = threadIdx.x & 31;
+// This lane's 8 binary32 values of the block that starts at `p`.
+template <bool VEC>
+__device__ __forceinline__ void load_block_f32(const float* p, int left, float (&x)[8]) {
+  if (VEC) {
+    ld8_rw(p + elem_of<VEC>(0), x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = (elem_of<VEC>(j) < left) ? p[elem_of<VEC>(j)] : 0.0f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_block_f32(float* p, int left, const float (&x)[8]) {
+  if (VEC) {
+    st8(p + elem_of<VEC>(0), x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (elem_of<VEC>(j) < left) p[elem_of<VEC>(j)] = x[j];
+  }
+}
+
+// The low-precision copy of a block's new parameters (BF16 or F16, at any
+// 2-byte alignment).
+template <bool VEC>
+__device__ __forceinline__ void store_block_lowp(void* lowp, int lowp_dtype, int left, const float (&x)[8]) {
   uint32_t w[4];
+  if (lowp_dtype == ZERO_BF16) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = (lowp_dtype == ZERO_BF16) ? pack2_rn<ZERO_BF16>(x[2 * i], x[2 * i + 1])
-                                     : pack2_rn<ZERO_F16>(x[2 * i], x[2 * i + 1]);
-  unsigned short* d = static_cast<unsigned short*>(lowp);
-  if (vec && aligned(lowp, 16)) {
-    st16(d + 8 * lane, make_uint4(w[0], w[1], w[2], w[3]));
+    for (int i = 0; i < 4; ++i) w[i] = pack2_rn<ZERO_BF16>(x[2 * i], x[2 * i + 1]);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = elem_of(vec, lane, j);
-      if (vec || e < left) d[e] = static_cast<unsigned short>((j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu);
-    }
+    for (int i = 0; i < 4; ++i) w[i] = pack2_rn<ZERO_F16>(x[2 * i], x[2 * i + 1]);
+  }
+  unsigned short* d = static_cast<unsigned short*>(lowp);
+  if (VEC && aligned(lowp, 16)) {
+    st16(d + elem_of<VEC>(0), make_uint4(w[0], w[1], w[2], w[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (VEC || elem_of<VEC>(j) < left)
+        d[elem_of<VEC>(j)] = static_cast<unsigned short>((j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu);
+  }
+}
+
+// The update of one block whose codes, scales and grads (fl(scale x), summed)
+// are in registers, and its stores.  The root's scale comes from the
+// correctly rounded root of the block's largest exp_avg_sq, so it does not
+// depend on the hardware root's last bit.
+template <bool VEC, bool SR>
+__device__ __forceinline__ void update_block(float* p, uint8_t* qm, uint8_t* qr, float* ms, float* rs,
+                                             unsigned short* lowp, int lowp_dtype, int left, const float (&x)[8],
+                                             const float (&g)[8], uint2 cm, uint2 cr, float sm, float sr, float coef,
+                                             const AdamScalars& s, uint32_t key, int64_t pair0) {
+  const Factors8 f = factors8(s, sm, sr, coef);
+  F2 m[4], v[4], r[4];
+  float y[8];
+  decode8(cm, m);
+  decode8(cr, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    F2 w = pair(x[2 * i], x[2 * i + 1]);
+    r[i] = adam_update8(w, m[i], v[i], pair(g[2 * i], g[2 * i + 1]), f);
+    unpair(w, y[2 * i], y[2 * i + 1]);
+  }
+  const uint32_t amax_m = warp_amax(m);
+  const uint32_t amax_r = __float_as_uint(__fsqrt_rn(__uint_as_float(warp_amax(v))));
+  store_block_f32<VEC>(p, left, y);
+  if (lowp != nullptr) store_block_lowp<VEC>(lowp, lowp_dtype, left, y);
+  encode_block<VEC, SR>(m, r, amax_m, amax_r, key, pair0, cm, cr, sm, sr);
+  store_codes<VEC>(qm, left, cm);
+  store_codes<VEC>(qr, left, cr);
+  if ((threadIdx.x & 31) == 0) {
+    *ms = sm;
+    *rs = sr;
   }
 }
 

@@ -58,6 +58,7 @@ class TensorListAdamW(GradTables):
                                  float(h["weight_decay"])])
         if not 1 <= len(self._groups) <= zs.LIST_MAX_GROUPS:
             raise ValueError(f"1 to {zs.LIST_MAX_GROUPS} groups")
+        self._hp = zs.list_groups(self._groups)
         numels = [p.numel() for p in self.masters]
         self._init_tables(numels, self.device)
         self.offsets, total = [], 0
@@ -117,6 +118,7 @@ class TensorListAdamW(GradTables):
         h = {**self.group(i), **hp}
         self._groups[i] = [float(h["lr"]), float(h["betas"][0]), float(h["betas"][1]), float(h["eps"]),
                            float(h["weight_decay"])]
+        self._hp = zs.list_groups(self._groups)
         if self.capturable:
             i %= len(self._groups)
             zs.device_hparams(*self._groups[i], self.device,
@@ -143,7 +145,7 @@ class TensorListAdamW(GradTables):
             zs.zero_adamw_list_device(self._list, table, dt, sc, self._dev_states, clip, stream, d_scale=dsc,
                                       rounding_seed=self.rounding_seed)
         else:
-            zs.zero_adamw_list(self._list, table, dt, sc, self._groups, self._t + 1, clip, stream, d_scale=dsc,
+            zs.zero_adamw_list(self._list, table, dt, sc, self._hp, self._t + 1, clip, stream, d_scale=dsc,
                                rounding_seed=self.rounding_seed)
 
     def finish_step(self, stream=None, norm_result: Optional[torch.Tensor] = None) -> zs.NormResult:

@@ -69,12 +69,8 @@ class zero_list_tensor(ctypes.Structure):
                 ("numel", ctypes.c_int64), ("group", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-class zero_list_chunk(ctypes.Structure):
-    _fields_ = [("tensor", ctypes.c_int32), ("chunk", ctypes.c_int32)]
-
-
 STATE8_BLOCK = 256      # elements per scale of the 8-bit moments
-LIST_CHUNK = 2048       # elements per piece of a tensor list's work
+LIST_CHUNK = 1024       # elements per piece of a tensor list's work
 LIST_MAX_GROUPS = 64
 
 NORM_RESULT_BYTES = ctypes.sizeof(zero_norm_result)
@@ -138,9 +134,9 @@ def lib() -> ctypes.CDLL:
                                            vp, vp]
     L.zero_adamw_step8_tensors_device.argtypes = [vp, s8, vp, i32, i64, ci, i64, f32, vp, vp, vp, ci, i64, vp, rdp,
                                                   vp, vp]
-    L.zero_list_chunks.argtypes = [vp, i32, i32, i32, vp, ctypes.POINTER(i64)]
-    L.zero_adamw_list.argtypes = [vp, i32, vp, i64, i32, vp, ci, f32, vp, ci, hpp, i32, i64, rdp, vp, vp]
-    L.zero_adamw_list_device.argtypes = [vp, i32, vp, i64, i32, vp, ci, f32, vp, ci, vp, i32, rdp, vp, vp]
+    L.zero_list_chunks.argtypes = [vp, i32, i32, i32, vp, ctypes.POINTER(i32)]
+    L.zero_adamw_list.argtypes = [vp, i32, vp, i32, i32, vp, ci, f32, vp, ci, hpp, i32, i64, rdp, vp, vp]
+    L.zero_adamw_list_device.argtypes = [vp, i32, vp, i32, i32, vp, ci, f32, vp, ci, vp, i32, rdp, vp, vp]
     L.zero_adamw_prepare_list_device.argtypes = [vp, i32, vp, vp, vp]
     L.zero_status_string.argtypes = [ctypes.c_int]
     L.zero_status_string.restype = ctypes.c_char_p
@@ -177,7 +173,7 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, allow_none: bool = Fa
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _grad_ptr(t: torch.Tensor, name: str) -> int:
@@ -197,12 +193,12 @@ def _grad_ptr(t: torch.Tensor, name: str) -> int:
     raise ValueError(f"{name} must be a CUDA tensor or a pinned host tensor")
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+def _stream(stream) -> int:
+    if stream is None:  # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 # ------------------------------------------------------------------ host only
@@ -551,13 +547,15 @@ def new_state8(n: int, device) -> State8:
 def _state8_arg(state: State8, n: int, who: str = "state8") -> zero_state8:
     if not isinstance(state, tuple) or len(state) != 4:
         raise ValueError(f"{who} must be a State8")
-    ptrs = []
-    for t, nm, dt, k in zip(state, State8._fields, (torch.float8_e4m3fn, torch.float32) * 2,
-                            (n, state8_blocks(n)) * 2):
-        ptrs.append(_dev(t, f"{who}.{nm}", dt))
-        if t.numel() != k:
-            raise ValueError(f"{who}.{nm} has {t.numel()} elements, expected {k}")
-    return zero_state8(*ptrs)
+    m, ms, r, rs = state
+    q = zero_state8(_dev(m, f"{who}.exp_avg", torch.float8_e4m3fn), _dev(ms, f"{who}.exp_avg_scale", torch.float32),
+                    _dev(r, f"{who}.root", torch.float8_e4m3fn), _dev(rs, f"{who}.root_scale", torch.float32))
+    b = -(-n // STATE8_BLOCK)
+    if m.numel() != n or r.numel() != n or ms.numel() != b or rs.numel() != b:
+        for t, nm, k in zip(state, State8._fields, (n, b, n, b)):
+            if t.numel() != k:
+                raise ValueError(f"{who}.{nm} has {t.numel()} elements, expected {k}")
+    return q
 
 
 def _rounding(rounding_seed: Optional[int], stream: int):
@@ -654,9 +652,10 @@ def zero_adamw_step8_tensors_device(master: torch.Tensor, state8: State8, d_tabl
 
 class TensorList(NamedTuple):
     """A list of tensors prepared for zero_adamw_list: the device copies of its entries and
-    of its chunks.  It holds addresses: keep the tensors alive."""
-    entries: torch.Tensor   # uint8, 64 bytes per tensor
-    chunks: torch.Tensor    # int32 [n_chunks, 2]
+    of the tensors' first chunks.  It holds addresses: keep the tensors alive."""
+    entries: torch.Tensor      # uint8, 64 bytes per tensor
+    first_chunk: torch.Tensor  # int32, one per tensor and their count
+    n_chunks: int
     numels: Tuple[int, ...]
     state_bits: int
     n_groups: int
@@ -701,23 +700,25 @@ def zero_tensor_list(masters: Sequence[torch.Tensor], states: Sequence[tuple],
         e.numel, e.group = k, group_of[i]
         if p.device != masters[0].device or any(t.device != p.device for t in (*st, *([] if lp is None else [lp]))):
             raise ValueError(f"tensor {i} is not on one device with the list")
-    count = ctypes.c_int64()
-    _check(lib().zero_list_chunks(entries, n, n_groups, state_bits, None, ctypes.byref(count)))
-    chunks = np.zeros((count.value, 2), dtype=np.int32)
-    _check(lib().zero_list_chunks(entries, n, n_groups, state_bits, ctypes.c_void_p(chunks.ctypes.data),
-                                  ctypes.byref(count)))
+    first = np.zeros(n + 1, dtype=np.int32)
+    _check(lib().zero_list_chunks(entries, n, n_groups, state_bits, ctypes.c_void_p(first.ctypes.data), None))
     dev = masters[0].device
     raw = torch.frombuffer(bytearray(bytes(memoryview(entries))), dtype=torch.uint8)
-    return TensorList(raw.to(dev), torch.from_numpy(chunks).to(dev), tuple(p.numel() for p in masters), state_bits,
+    return TensorList(raw.to(dev), torch.from_numpy(first).to(dev), int(first[-1]), tuple(p.numel() for p in masters), state_bits,
                       n_groups, dts.pop() if dts else None)
 
 
 def _list_args(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float, d_scale):
     if d_grads.numel() < len(tl.numels) * TENSOR_ENTRY_BYTES:
         raise ValueError("d_grads holds fewer entries than the list")
-    return (_dev(tl.entries, "entries"), len(tl.numels), _dev(tl.chunks, "chunks", torch.int32), tl.chunks.shape[0],
-            tl.state_bits, _dev(d_grads, "d_grads", torch.uint8), _DT[grad_dtype], grad_scale, _dscale(d_scale),
-            ZERO_BF16 if tl.lowp_dtype is None else _DT[tl.lowp_dtype])
+    return (tl.entries.data_ptr(), len(tl.numels), tl.first_chunk.data_ptr(), tl.n_chunks, tl.state_bits,
+            _dev(d_grads, "d_grads", torch.uint8), _DT[grad_dtype], grad_scale,
+            None if d_scale is None else _dscale(d_scale), ZERO_BF16 if tl.lowp_dtype is None else _DT[tl.lowp_dtype])
+
+
+def list_groups(groups: Sequence[Tuple[float, float, float, float, float]]):
+    """(lr, beta1, beta2, eps, weight_decay) of each group as zero_adamw_list takes them."""
+    return (zero_adamw_hparams * len(groups))(*[zero_adamw_hparams(*g) for g in groups])
 
 
 def zero_adamw_list(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float,
@@ -726,12 +727,12 @@ def zero_adamw_list(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dty
                     rounding_seed: Optional[int] = None, rounding_stream: int = 0) -> None:
     """One AdamW step over every tensor of a list.  d_grads: the device table of the grads
     (zero_tensor_table + device_table, in list order); groups: (lr, beta1, beta2, eps,
-    weight_decay) of each parameter group."""
+    weight_decay) of each parameter group, or list_groups() of them made once."""
     if len(groups) != tl.n_groups:
         raise ValueError(f"{len(groups)} groups given, the list has {tl.n_groups}")
     if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
         raise ValueError("clip is smaller than zero_norm_result")
-    hp = (zero_adamw_hparams * len(groups))(*[zero_adamw_hparams(*g) for g in groups])
+    hp = groups if isinstance(groups, ctypes.Array) else list_groups(groups)
     _check(lib().zero_adamw_list(*_list_args(tl, d_grads, grad_dtype, grad_scale, d_scale), hp, len(groups), step,
                                  _rounding(rounding_seed, rounding_stream), _dev(clip, "clip", allow_none=True), _stream(stream)))
 

@@ -559,12 +559,15 @@ zero_status zero_state8_unpack(const zero_state8* q, int64_t n, float* d_exp_avg
  * [shard_start, shard_start + n), the grads fl(grad_scale * x) read through
  * the table (a flat grad is a table of one tensor), optionally added to
  * d_acc.  Per element, with m = c S of exp_avg and r = c S of the root:
- *   g = grad * coef;  p = p * (1 - lr*wd)
+ *   g = grad * coef
  *   m = fma(1-beta1, g, m*beta1)
- *   v = fma((1-beta2)*g, g, (r*r)*beta2);  r = sqrt(v)
- *   p = p - (lr / (1-beta1^t)) * (m / fma(r, 1 / sqrt(1-beta2^t), eps))
- * each operation rounded to nearest in binary32; p and lowp use these m and
- * r, which are rounded to 8 bits only when they are stored in q.
+ *   v = fma((1-beta2)*g, g, (r*r)*beta2)
+ *   p = fma(-lr / (1-beta1^t), m / (sqrt(v) / sqrt(1-beta2^t) + eps), p * (1 - lr*wd))
+ * m and v are those of zero_adamw_step for the decoded moments, bit for bit
+ * (each operation rounded to nearest in binary32); the quotient is formed
+ * with the hardware's root and reciprocal and is within 8 ulp.  p and lowp
+ * use these m and v, which are rounded to 8 bits only when they are stored in
+ * q.  An exp_avg_sq below the normal range (2^-126) counts as zero.
  * rounding: NULL rounds to nearest, else (host memory) the seed and stream of
  * stochastic rounding.
  * 16 bytes per parameter with 16-bit grads and copy, where the fp32 state
@@ -607,25 +610,20 @@ typedef struct zero_list_tensor {
   int32_t reserved; /* 0 */
 } zero_list_tensor;
 
-/* One piece of work of a list: elements [2048 chunk, 2048 (chunk + 1)) of a tensor. */
-typedef struct zero_list_chunk {
-  int32_t tensor;
-  int32_t chunk;
-} zero_list_chunk;
-
-#define ZERO_LIST_CHUNK 2048
+#define ZERO_LIST_CHUNK 1024
 #define ZERO_LIST_MAX_GROUPS 64
 
 /* zero_list_chunks -- host only.
- * Checks a list (state_bits 32 or 8, groups in [0, n_groups), no NULL where
- * numel > 0, numel >= 0 and below 2^31 chunks, reserved 0) and counts its
- * chunks into *n_chunks; with chunks != NULL also fills chunks[0 .. *n_chunks)
- * in list order.  The caller copies the list and the chunks to device memory
- * for zero_adamw_list.
+ * A list's work is cut into chunks of 1024 elements, none across two tensors,
+ * numbered in list order.  Checks a list (state_bits 32 or 8, groups in
+ * [0, n_groups), no NULL where numel > 0, numel >= 0, fewer than 2^31 chunks,
+ * reserved 0) and, with first_chunk != NULL, fills first_chunk[0 .. n_tensors]
+ * with the number of each tensor's first chunk, then their count.  The caller
+ * copies the list and first_chunk to device memory for zero_adamw_list.
  * Errors: ZERO_EINVAL for a bad list, n_tensors < 0, n_groups outside
- * [1, 64], state_bits other than 32 and 8, or NULL n_chunks. */
+ * [1, 64], or state_bits other than 32 and 8. */
 zero_status zero_list_chunks(const zero_list_tensor* list, int32_t n_tensors, int32_t n_groups, int32_t state_bits,
-                             zero_list_chunk* chunks, int64_t* n_chunks);
+                             int32_t* first_chunk, int32_t* n_chunks);
 
 /* zero_adamw_list -- device.
  * One AdamW step over every tensor of a list, each with its group's
@@ -635,18 +633,18 @@ zero_status zero_list_chunks(const zero_list_tensor* list, int32_t n_tensors, in
  * zero_adamw_step's on fl(grad_scale * x), bit for bit (state_bits 32), or
  * zero_adamw_step8_tensors' with stream + tensor number as the stream
  * (state_bits 8).  One launch, whatever the number of tensors.
- * d_list, d_chunks: device copies of a list that zero_list_chunks accepted
- *   and of its chunks.  Their contents cannot be checked on the host: a list
+ * d_list, d_first_chunk, n_chunks: device copies of a list that
+ *   zero_list_chunks accepted and of its first_chunk, and their count.  Their contents cannot be checked on the host: a list
  *   that differs from the checked one is the caller's error.
  * groups: host, n_groups hyper-parameters; step t >= 1 is the same for all.
  * rounding: as for zero_adamw_step8_tensors; must be NULL with 32 bits.
  * d_clip, d_grad_scale, lowp_dtype: as for zero_adamw_step_tensors.
- * Errors: ZERO_EINVAL for n_tensors < 0, n_chunks < 0, NULL d_list, d_chunks
- * or d_grads with n_chunks > 0, n_groups outside [1, 64], bad
+ * Errors: ZERO_EINVAL for n_tensors < 0, n_chunks < 0, NULL d_list,
+ * d_first_chunk or d_grads with n_chunks > 0, n_groups outside [1, 64], bad
  * hyper-parameters of any group, step < 1, a bad dtype, state_bits or
  * rounding, or a non-finite grad_scale. */
-zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, const zero_list_chunk* d_chunks,
-                            int64_t n_chunks, int32_t state_bits, const zero_tensor* d_grads, zero_dtype grad_dtype,
+zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, const int32_t* d_first_chunk,
+                            int32_t n_chunks, int32_t state_bits, const zero_tensor* d_grads, zero_dtype grad_dtype,
                             float grad_scale, const float* d_grad_scale, zero_dtype lowp_dtype,
                             const zero_adamw_hparams* groups, int32_t n_groups, int64_t step,
                             const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream);
@@ -655,8 +653,8 @@ zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, c
  * zero_adamw_list with the scalars, the step of the draws and the skip
  * decision from d_states[n_groups], as the last
  * zero_adamw_prepare_list_device on the stream left them. */
-zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_tensors, const zero_list_chunk* d_chunks,
-                                   int64_t n_chunks, int32_t state_bits, const zero_tensor* d_grads,
+zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_tensors, const int32_t* d_first_chunk,
+                                   int32_t n_chunks, int32_t state_bits, const zero_tensor* d_grads,
                                    zero_dtype grad_dtype, float grad_scale, const float* d_grad_scale,
                                    zero_dtype lowp_dtype, const zero_adamw_device_state* d_states, int32_t n_groups,
                                    const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream);

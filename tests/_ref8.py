@@ -102,24 +102,28 @@ def grad(x, scale=1.0, acc=None, coef=1.0):
     return g * coef, (err + EPS * np.abs(g)) * abs(coef)
 
 
-def step(p, m, v, g, g_err, *, lr, b1, b2, eps, wd, t):
-    """One AdamW step: {name: (value, bound)} for p, m and r = sqrt(v)."""
+def step(p, m, v, g, g_err, *, lr, b1, b2, eps, wd, t, root=1, div=1):
+    """One AdamW step: {name: (value, bound)} for p, m and r = sqrt(v).  root, div: the errors of the
+    square root and of the division in EPS (1: correctly rounded; the 8-bit update's hardware root
+    and reciprocal: 2 and, with its product, 3)."""
     alpha, bc2 = lr / (1 - b1 ** t), math.sqrt(1 - b2 ** t)
     m1 = b1 * m + (1 - b1) * g
     m_err = EPS * (2 * np.abs(b1 * m) + np.abs((1 - b1) * g) + np.abs(m1)) + (1 - b1) * g_err
     v1 = b2 * v + (1 - b2) * g * g
-    # v is itself a rounded square of the root (8 bits) or exact (32): 1; constant and product: 2
-    v_err = EPS * (3 * b2 * v + 2 * (1 - b2) * g * g + v1) + (1 - b2) * 2 * np.abs(g) * g_err
+    # beta2: constant and product; the decoded v is the square of the root, exact in the update; 1 - beta2: constant, product
+    v_err = EPS * (2 * b2 * v + 2 * (1 - b2) * g * g + v1) + (1 - b2) * 2 * np.abs(g) * g_err
     r1 = np.sqrt(v1)
     with np.errstate(divide="ignore", invalid="ignore"):
-        r_err = np.where(v1 > 0, v_err / np.maximum(r1, 1e-300), 0.0) + EPS * r1
+        r_err = np.where(v1 > 0, v_err / (2 * np.maximum(r1, 1e-300)), 0.0)
     d = r1 / bc2 + eps
-    d_err = r_err / bc2 + EPS * (2 * r1 / bc2 + eps + d)
+    # sqrt(1 - beta2^t): constant and division, or its reciprocal's two roundings
+    d_err = (r_err + root * EPS * r1) / bc2 + EPS * (2 * r1 / bc2 + eps + d)
     u = m1 / d
-    u_err = m_err / d + np.abs(u) * (d_err / d + EPS)
+    u_err = m_err / d + np.abs(u) * (d_err / d + div * EPS)
     p1 = p * (1 - lr * wd) - alpha * u
     p_err = EPS * (2 * np.abs(p) + 2 * np.abs(alpha * u) + np.abs(p1)) + alpha * u_err
-    return {"p": (p1, 1.1 * p_err + TINY), "m": (m1, 1.1 * m_err + TINY), "r": (r1, 1.1 * r_err + TINY)}
+    return {"p": (p1, 1.1 * p_err + TINY), "m": (m1, 1.1 * m_err + TINY), "r": (r1, 1.1 * (r_err + root * EPS * r1) + TINY),
+            "v": (v1, 1.1 * v_err + TINY)}
 
 
 def check_codes(codes, scales, value, bound, *, k=None, floor=False, name=""):

@@ -63,7 +63,7 @@ def f64(t):
 def check_step(p0, old, g, g_err, p1, lowp, new, *, hp=HP, t=3, seed=None, stream=0):
     """Master, copy and 8-bit state of one step against the formulas."""
     m0, r0 = R.values(old[0], old[1]), R.values(old[2], old[3])
-    out = R.step(p0, m0, r0 * r0, g, g_err, t=t, **hp)
+    out = R.step(p0, m0, r0 * r0, g, g_err, t=t, root=2, div=3, **hp)
     R.check_close(f64(p1), *out["p"], "master")
     km = kr = None
     if seed is not None:
@@ -240,7 +240,7 @@ def test_fresh_state_first_step_is_sign_descent():
     q, p = pkg.new_state8(n, "cuda"), torch.zeros(n, device="cuda")
     x = torch.linspace(-1, 1, n, device="cuda") * 1e-3
     shard_call(p, q, x, step=1)
-    # p = -lr g / (|g| + eps): the moments enter before they are rounded to 8 bits
+    # p = -lr g / (|g| + eps): the moments enter before they are rounded to 8 bits; a dozen roundings, root and reciprocal
     want = -HP["lr"] * f64(x) / (np.abs(f64(x)) + HP["eps"])
     np.testing.assert_allclose(f64(p), want, rtol=32 * R.EPS)
 
@@ -479,7 +479,7 @@ def test_indices_past_2_to_31():
     assert float(p[:tail.start].abs().max()) == 0.0
     new = zs.State8(q.exp_avg[tail], q.exp_avg_scale[sb], q.root[tail], q.root_scale[sb])
     gr, err = R.grad(f64(x[tail]))
-    out = R.step(p0, R.values(oldh[0], oldh[1]), R.values(oldh[2], oldh[3]) ** 2, gr, err, t=3, **HP)
+    out = R.step(p0, R.values(oldh[0], oldh[1]), R.values(oldh[2], oldh[3]) ** 2, gr, err, t=3, root=2, div=3, **HP)
     R.check_close(f64(p[tail]), *out["p"], "master")
     km, kr = R.draws(21, 3, 0, m, first=tail.start)
     h = host(new)

@@ -22,16 +22,15 @@ def entry(numel, bits=32, **kw):
 
 
 def chunks_of(entries, n_groups=1, bits=32, fill=True):
+    """(status, first_chunk) of a list."""
     arr = (zs.zero_list_tensor * max(len(entries), 1))(*entries)
-    count = ctypes.c_int64(-1)
-    st = zs.lib().zero_list_chunks(arr, len(entries), n_groups, bits, None, ctypes.byref(count))
-    if st != zs.ZERO_OK:
-        return st, None
-    out = np.full((count.value + 1, 2), -7, dtype=np.int32)
-    if fill:
-        assert zs.lib().zero_list_chunks(arr, len(entries), n_groups, bits, ctypes.c_void_p(out.ctypes.data),
-                                         ctypes.byref(count)) == zs.ZERO_OK
-        assert (out[-1] == -7).all()
+    count = ctypes.c_int32(-1)
+    out = np.full(len(entries) + 2, -7, dtype=np.int32)
+    st = zs.lib().zero_list_chunks(arr, len(entries), n_groups, bits, ctypes.c_void_p(out.ctypes.data) if fill else None,
+                                   ctypes.byref(count))
+    assert out[-1] == -7
+    if st == zs.ZERO_OK and fill:
+        assert count.value == out[-2]
     return st, out[:-1]
 
 
@@ -77,20 +76,20 @@ def test_reference_step_is_torch_adamw():
 
 # ------------------------------------------------------------------ chunks
 def test_chunks_follow_the_tensors():
-    sizes = [0, 1, 2047, 2048, 2049, 0, 10000]
+    sizes = [0, 1, zs.LIST_CHUNK - 1, zs.LIST_CHUNK, zs.LIST_CHUNK + 1, 0, 10000]
     st, c = chunks_of([entry(n) for n in sizes])
-    want = [(i, k) for i, n in enumerate(sizes) for k in range(-(-n // 2048))]
-    assert st == zs.ZERO_OK and [tuple(r) for r in c.tolist()] == want
+    assert st == zs.ZERO_OK and c.tolist() == np.cumsum([0] + [-(-n // zs.LIST_CHUNK) for n in sizes]).tolist()
     st, c = chunks_of([])
-    assert st == zs.ZERO_OK and len(c) == 0
+    assert st == zs.ZERO_OK and c.tolist() == [0]
     st, c = chunks_of([zs.zero_list_tensor(numel=0)], bits=8)  # nothing to point at
-    assert st == zs.ZERO_OK and len(c) == 0
+    assert st == zs.ZERO_OK and c.tolist() == [0, 0]
 
 
 @pytest.mark.parametrize("bad", [
     [entry(-1)], [entry(5, group=1)], [entry(5, group=-1)], [entry(5, reserved=1)], [entry(5, master=None)],
     [entry(5, exp_avg=None)], [entry(5, exp_avg_sq=None)], [entry(5, exp_avg_scale=FAKE)], [entry(5, root_scale=FAKE)],
     [entry(5, master=FAKE + 2)], [entry(5, exp_avg=FAKE + 1)], [entry(5, lowp=FAKE + 1)], [entry(1 << 43)],
+    [entry(1 << 41), entry(1 << 41)],
 ])
 def test_bad_lists_are_refused(bad):
     assert chunks_of(bad, fill=False)[0] == zs.ZERO_EINVAL
@@ -106,24 +105,24 @@ def test_bad_8bit_lists_and_arguments_are_refused():
     assert chunks_of(ok, bits=16)[0] == zs.ZERO_EINVAL
     for groups in (0, 65):
         assert chunks_of(ok, n_groups=groups, bits=8)[0] == zs.ZERO_EINVAL
-    assert zs.lib().zero_list_chunks(None, 1, 1, 32, None, ctypes.byref(ctypes.c_int64())) == zs.ZERO_EINVAL
-    assert zs.lib().zero_list_chunks(None, -1, 1, 32, None, ctypes.byref(ctypes.c_int64())) == zs.ZERO_EINVAL
-    assert zs.lib().zero_list_chunks(None, 0, 1, 32, None, None) == zs.ZERO_EINVAL
+    assert zs.lib().zero_list_chunks(None, 1, 1, 32, None, None) == zs.ZERO_EINVAL
+    assert zs.lib().zero_list_chunks(None, -1, 1, 32, None, None) == zs.ZERO_EINVAL
+    assert zs.lib().zero_list_chunks(None, 0, 1, 32, None, None) == zs.ZERO_OK
 
 
 # ---------------------------------------------------------------- refusals
 def call_list(**kw):
     hp = kw.pop("hp", HP)
-    a = dict(list=FAKE, n_tensors=1, chunks=FAKE, n_chunks=1, bits=8, grads=FAKE, dt=0, scale=1.0, dscale=None, lowp=1,
+    a = dict(list=FAKE, n_tensors=1, first=FAKE, n_chunks=1, bits=8, grads=FAKE, dt=0, scale=1.0, dscale=None, lowp=1,
              groups=ctypes.byref(hp) if hp is not None else None, n_groups=1, step=1, seed=None, clip=None, stream=None)
     a.update(kw)
     return zs.lib().zero_adamw_list(*a.values())
 
 
 @pytest.mark.parametrize("bad", [
-    dict(list=None), dict(chunks=None), dict(grads=None), dict(n_tensors=0), dict(n_tensors=-1), dict(n_chunks=-1),
+    dict(list=None), dict(first=None), dict(grads=None), dict(n_tensors=0), dict(n_tensors=-1), dict(n_chunks=-1),
     dict(bits=4), dict(dt=3), dict(scale=float("nan")), dict(lowp=0), dict(hp=None), dict(n_groups=0),
-    dict(n_groups=65), dict(step=0), dict(list=FAKE + 4), dict(chunks=FAKE + 4), dict(grads=FAKE + 4),
+    dict(n_groups=65), dict(step=0), dict(list=FAKE + 4), dict(first=FAKE + 2), dict(grads=FAKE + 4),
     dict(bits=32, seed=ctypes.byref(zs.zero_rounding(1, 0))), dict(hp=zs.zero_adamw_hparams(-1, 0.9, 0.9, 1e-8, 0)),
     dict(hp=zs.zero_adamw_hparams(1e-3, 1.0, 0.9, 1e-8, 0)), dict(hp=zs.zero_adamw_hparams(1e-3, 0.9, 0.9, 0, 0)),
 ])
@@ -132,14 +131,14 @@ def test_list_step_refuses(bad):
 
 
 def test_list_step_of_nothing_is_a_no_op():
-    assert call_list(n_chunks=0, list=None, chunks=None, grads=None, n_tensors=0) == zs.ZERO_OK
+    assert call_list(n_chunks=0, list=None, first=None, grads=None, n_tensors=0) == zs.ZERO_OK
 
 
 def test_list_device_forms_refuse():
     L = zs.lib()
 
     def dev(states=FAKE, n_groups=1, **kw):
-        a = dict(list=FAKE, n_tensors=1, chunks=FAKE, n_chunks=1, bits=8, grads=FAKE, dt=0, scale=1.0, dscale=None,
+        a = dict(list=FAKE, n_tensors=1, first=FAKE, n_chunks=1, bits=8, grads=FAKE, dt=0, scale=1.0, dscale=None,
                  lowp=1, states=states, n_groups=n_groups, seed=None, clip=None, stream=None)
         a.update(kw)
         return L.zero_adamw_list_device(*a.values())
