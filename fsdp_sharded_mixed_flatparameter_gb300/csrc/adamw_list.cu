@@ -33,12 +33,12 @@ __device__ __forceinline__ void list_block(const zero_list_tensor& t, const void
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kListThreads, 8)
+__global__ void __launch_bounds__(kListThreads, 10)
     adamw_list_kernel(const zero_list_tensor* __restrict__ list, int n_tensors,
                       const int32_t* __restrict__ first_chunk, const zero_tensor* __restrict__ grads, float gscale,
                       const float* __restrict__ dscale, int lowp_dtype, const __grid_constant__ ListScalars hs,
                       const zero_adamw_device_state* __restrict__ ds, const zero_norm_result* __restrict__ clip) {
-  const int tensor = find_chunk_tensor(first_chunk, n_tensors, blockIdx.x);
+  const int tensor = block_tensor(first_chunk, n_tensors, blockIdx.x);
   const int chunk = blockIdx.x - __ldg(first_chunk + tensor);
   const zero_list_tensor t = list[tensor];
   const void* grad = grads[tensor].ptr;

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kListThreads, 10)
                        const float* __restrict__ dscale, int lowp_dtype, const __grid_constant__ ListScalars hs,
                        const zero_adamw_device_state* __restrict__ ds, RoundingBase rnd,
                        const zero_norm_result* __restrict__ clip) {
-  const int tensor = find_chunk_tensor(first_chunk, n_tensors, blockIdx.x);
+  const int tensor = block_tensor(first_chunk, n_tensors, blockIdx.x);
   const int chunk = blockIdx.x - __ldg(first_chunk + tensor);
   const zero_list_tensor t = list[tensor];
   const void* grad = grads[tensor].ptr;

@@ -28,6 +28,19 @@ __device__ __forceinline__ int find_chunk_tensor(const int32_t* __restrict__ fir
   return lo;
 }
 
+// Found by one warp for the block; every thread must call it.  (Each warp for
+// itself: 30 instructions times four, 4566 against 4535 us for 1.88e9 elements
+// in 8 bits.)
+__device__ __forceinline__ int block_tensor(const int32_t* __restrict__ first, int n, int c) {
+  __shared__ int found;
+  if (threadIdx.x < 32) {
+    const int ti = find_chunk_tensor(first, n, c);
+    if (threadIdx.x == 0) found = ti;
+  }
+  __syncthreads();
+  return found;
+}
+
 // The scalars of a tensor's group: the launch's, or those of the device step
 // states; false: the prepared step is skipped.
 __device__ __forceinline__ bool group_scalars(const ListScalars& hs, const zero_adamw_device_state* ds, int g,

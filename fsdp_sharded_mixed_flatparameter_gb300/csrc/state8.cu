@@ -60,7 +60,7 @@ __device__ __forceinline__ void unpack_block(const zero_state8& q, float* __rest
   store_block_f32<VEC>(v + k, left, r);
 }
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 6)
     state8_pack_kernel(const float* __restrict__ m, const float* __restrict__ v, int64_t n, zero_state8 q, bool vec) {
   const int64_t nb = (n + kBlock8 - 1) / kBlock8;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 6)
     state8_unpack_kernel(zero_state8 q, int64_t n, float* __restrict__ m, float* __restrict__ v, bool vec) {
   const int64_t nb = (n + kBlock8 - 1) / kBlock8;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;

@@ -107,18 +107,25 @@ __device__ __forceinline__ uint32_t encode4_nearest(F2 a, F2 b) {
   return r;
 }
 
-// Two values, already scaled by 2^-8 (|x| <= 448 / 256), to codes in the low
-// bytes of the result's halves.  binary16 has e4m3's exponents moved by 8
-// (normal from 2^-14, below it spaced evenly) and 7 more fraction bits, so
-// truncating to binary16 gives floor(128 |x| / u), adding the element's 7
-// random bits (one per half of k) and dropping 7 gives the code.
-__device__ __forceinline__ uint32_t encode2_stochastic(F2 x, uint32_t k) {
-  float x0, x1;
-  unpair(x, x0, x1);
-  uint32_t h;
-  asm("cvt.rz.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(x0), "f"(x1));
-  const uint32_t mag = (h & 0x7fff7fffu) + (k & 0x007f007fu);
-  return ((mag >> 7) & 0x007f007fu) | ((h >> 8) & 0x00800080u);
+// 4 values, already scaled by 2^-8 (|x| <= 448 / 256), to codes by stochastic
+// rounding; k0, k1: twice the elements' 7-bit numbers, in the halves of a word
+// for each pair.  binary16 has e4m3's exponents moved by 8 (normal from
+// 2^-14, below it spaced evenly) and 7 more fraction bits: truncated to
+// binary16 a value is floor(128 |x| / u), adding the number carries into the
+// code, and doubled (the sign bit is taken out, |x| < 2 leaves bit 14 free)
+// the code fills the upper byte of each half, where one byte permutation
+// collects four.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t encode4_stochastic(F2 a, F2 b, uint32_t k0, uint32_t k1) {
+  float x0, x1, x2, x3;
+  unpair(a, x0, x1);
+  unpair(b, x2, x3);
+  uint32_t h0, h1;
+  asm("cvt.rz.f16x2.f32 %0, %2, %1;" : "=r"(h0) : "f"(x0), "f"(x1));
+  asm("cvt.rz.f16x2.f32 %0, %2, %1;" : "=r"(h1) : "f"(x2), "f"(x3));
+  if (!SIGNED) return __byte_perm(2u * h0 + k0, 2u * h1 + k1, 0x7531);
+  const uint32_t c = __byte_perm(2u * (h0 & 0x7fff7fffu) + k0, 2u * (h1 & 0x7fff7fffu) + k1, 0x7531);
+  return c | (__byte_perm(h0, h1, 0x7531) & 0x80808080u);
 }
 
 // ------------------------------------------------------------------ scale
@@ -253,7 +260,7 @@ __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4],
     cr = make_uint2(encode4_nearest(y[0], y[1]), encode4_nearest(y[2], y[3]));
   } else {
     const int lane = threadIdx.x & 31;
-    uint32_t um[4], ur[4];
+    uint32_t km[4], kr[4];
     const uint32_t p0 = static_cast<uint32_t>(pair0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -265,11 +272,13 @@ __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4],
         const uint32_t b = pcg_hash((p0 + 32u * i + 16u + (lane >> 1)) ^ key);
         w = __byte_perm(a, b, (lane & 1) ? 0x7632 : 0x5410);
       }
-      um[i] = encode2_stochastic(x[i], w);
-      ur[i] = encode2_stochastic(y[i], w >> 7);
+      km[i] = (w << 1) & 0x00fe00feu;
+      kr[i] = (w >> 6) & 0x00fe00feu;
     }
-    cm = make_uint2(__byte_perm(um[0], um[1], 0x6420), __byte_perm(um[2], um[3], 0x6420));
-    cr = make_uint2(__byte_perm(ur[0], ur[1], 0x6420), __byte_perm(ur[2], ur[3], 0x6420));
+    cm = make_uint2(encode4_stochastic<true>(x[0], x[1], km[0], km[1]),
+                    encode4_stochastic<true>(x[2], x[3], km[2], km[3]));
+    cr = make_uint2(encode4_stochastic<false>(y[0], y[1], kr[0], kr[1]),
+                    encode4_stochastic<false>(y[2], y[3], kr[2], kr[3]));
   }
 }
 

@@ -13,6 +13,7 @@ from __future__ import annotations
 import math
 from typing import List, Optional, Sequence, Tuple
 
+import numpy as np
 import torch
 
 from . import zero_shard as zs
@@ -59,20 +60,24 @@ class TensorListAdamW(GradTables):
         if not 1 <= len(self._groups) <= zs.LIST_MAX_GROUPS:
             raise ValueError(f"1 to {zs.LIST_MAX_GROUPS} groups")
         self._hp = zs.list_groups(self._groups)
-        numels = [p.numel() for p in self.masters]
+        columns, numels, lowp_dtype = zs.list_masters(self.masters, self.lowp, group_of)
         self._init_tables(numels, self.device)
-        self.offsets, total = [], 0
-        for n in numels:
-            self.offsets.append(total)
-            total += zs.state8_blocks(n) * zs.STATE8_BLOCK
+        blocks = np.cumsum([0] + [zs.state8_blocks(n) for n in numels])  # each tensor starts on a block's border
+        self.offsets, total = (blocks[:-1] * zs.STATE8_BLOCK).tolist(), int(blocks[-1]) * zs.STATE8_BLOCK
         if state_bits == 8:
             self.state8, self.exp_avg, self.exp_avg_sq = zs.new_state8(total, self.device), None, None
         else:
             self.state8 = None
             self.exp_avg = torch.zeros(total, dtype=torch.float32, device=self.device)
             self.exp_avg_sq = torch.zeros(total, dtype=torch.float32, device=self.device)
-        self._list = zs.zero_tensor_list(self.masters, [self.state_of(i) for i in range(len(numels))], self.lowp,
-                                         group_of, len(self._groups), state_bits)
+        # every tensor's moments by their address in the storages; none where there are no elements
+        at, some = blocks[:-1].astype(np.uint64), np.asarray(numels) > 0
+        fields = {"exp_avg": (self.exp_avg, 1024), "exp_avg_sq": (self.exp_avg_sq, 1024)} if state_bits == 32 else {
+            "exp_avg": (self.state8.exp_avg, 256), "exp_avg_sq": (self.state8.root, 256),
+            "exp_avg_scale": (self.state8.exp_avg_scale, 4), "root_scale": (self.state8.root_scale, 4)}
+        for nm, (t, block_bytes) in fields.items():
+            columns[nm] = np.where(some, np.uint64(t.data_ptr()) + at * np.uint64(block_bytes), np.uint64(0))
+        self._list = zs.make_tensor_list(columns, numels, group_of, len(self._groups), state_bits, lowp_dtype, self.device)
         self.ws = torch.empty(max(zs.zero_grad_sqnorm_workspace_bytes(self.total), 8), dtype=torch.uint8,
                               device=self.device)
         self.norm_buf = zs.new_norm_result(self.device)

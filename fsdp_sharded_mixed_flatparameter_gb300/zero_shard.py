@@ -662,50 +662,86 @@ class TensorList(NamedTuple):
     lowp_dtype: Optional[torch.dtype]
 
 
+_LIST_ENTRY = np.dtype([(nm, np.uint64 if ct is ctypes.c_void_p else np.int64 if ct is ctypes.c_int64 else np.int32)
+                        for nm, ct in zero_list_tensor._fields_])
+
+
+def make_tensor_list(columns: dict, numels: Sequence[int], group_of: Optional[Sequence[int]], n_groups: int,
+                     state_bits: int, lowp_dtype: Optional[torch.dtype], device) -> TensorList:
+    """Check a list given by columns of addresses (fields of zero_list_tensor; absent: NULL)
+    and copy it to the device."""
+    n = len(numels)
+    entries = np.zeros(n, dtype=_LIST_ENTRY)
+    for nm, col in columns.items():
+        entries[nm] = col
+    entries["numel"] = numels
+    if group_of is not None:
+        entries["group"] = group_of
+    first = np.zeros(n + 1, dtype=np.int32)
+    _check(lib().zero_list_chunks(entries.ctypes.data, n, n_groups, state_bits, first.ctypes.data, None))
+    return TensorList(torch.from_numpy(entries.view(np.uint8)).to(device), torch.from_numpy(first).to(device),
+                      int(first[-1]), tuple(numels), state_bits, n_groups, lowp_dtype)
+
+
+def list_masters(masters: Sequence[torch.Tensor], lowp: Optional[Sequence[Optional[torch.Tensor]]],
+                 group_of: Optional[Sequence[int]]):
+    """The checked masters and copies of a list: (columns, numels, the copies' dtype)."""
+    n = len(masters)
+    if n == 0:
+        raise ValueError("an empty tensor list")
+    if (lowp is not None and len(lowp) != n) or (group_of is not None and len(group_of) != n):
+        raise ValueError("masters, lowp and group_of differ in length")
+    dev = masters[0].device
+    ptrs, numels, copies, dts = [], [], [], set()
+    for i, p in enumerate(masters):
+        if not p.is_cuda or p.device != dev or p.dtype != torch.float32 or not p.is_contiguous():
+            _dev(p, f"masters[{i}]", torch.float32)
+            raise ValueError(f"masters[{i}] is not on one device with the list")
+        ptrs.append(p.data_ptr())
+        numels.append(p.numel())
+    for i, c in enumerate(lowp or ()):
+        if c is None:
+            copies.append(0)
+            continue
+        copies.append(_dev(c, f"lowp[{i}]"))
+        dts.add(c.dtype)
+        if c.numel() != numels[i]:
+            raise ValueError(f"lowp[{i}] differs in size from masters[{i}]")
+        if c.device != dev:
+            raise ValueError(f"lowp[{i}] is not on one device with the list")
+    if len(dts) > 1 or not dts <= {torch.bfloat16, torch.float16}:
+        raise ValueError("low-precision copies must be all bf16 or all f16")
+    columns = {"master": ptrs}
+    if lowp is not None:
+        columns["lowp"] = copies
+    return columns, numels, dts.pop() if dts else None
+
+
 def zero_tensor_list(masters: Sequence[torch.Tensor], states: Sequence[tuple],
                      lowp: Optional[Sequence[Optional[torch.Tensor]]] = None, group_of: Optional[Sequence[int]] = None,
                      n_groups: int = 1, state_bits: int = 32) -> TensorList:
     """Check a list and copy it to the device.  states[i]: (exp_avg, exp_avg_sq), fp32, or
     with state_bits=8 a State8; lowp[i]: None or a bf16/f16 copy (one dtype for the list)."""
-    n = len(masters)
-    if n == 0:
-        raise ValueError("an empty tensor list")
-    lowp = [None] * n if lowp is None else list(lowp)
-    group_of = [0] * n if group_of is None else [int(g) for g in group_of]
-    if len(states) != n or len(lowp) != n or len(group_of) != n:
-        raise ValueError("masters, states, lowp and group_of differ in length")
     if state_bits not in (8, 32):
         raise ValueError("state_bits must be 32 or 8")
-    dts = {t.dtype for t in lowp if t is not None}
-    if len(dts) > 1 or not dts <= {torch.bfloat16, torch.float16}:
-        raise ValueError("low-precision copies must be all bf16 or all f16")
-    entries = (zero_list_tensor * n)()
-    for i, (p, st, lp) in enumerate(zip(masters, states, lowp)):
-        k = p.numel()
-        e = entries[i]
-        e.master = _dev(p, f"masters[{i}]", torch.float32)
+    if len(states) != len(masters):
+        raise ValueError("masters and states differ in length")
+    columns, numels, lowp_dtype = list_masters(masters, lowp, group_of)
+    moments = []
+    for i, (st, k) in enumerate(zip(states, numels)):
+        if any(t.device != masters[0].device for t in st):
+            raise ValueError(f"states[{i}] is not on one device with the list")
         if state_bits == 8:
             q = _state8_arg(st, k, f"states[{i}]")
-            e.exp_avg, e.exp_avg_scale, e.exp_avg_sq, e.root_scale = q.exp_avg, q.exp_avg_scale, q.root, q.root_scale
+            moments.append((q.exp_avg or 0, q.root or 0, q.exp_avg_scale or 0, q.root_scale or 0))
         else:
-            for t in st:
-                if t.numel() != k:
-                    raise ValueError(f"states[{i}] differs in size from masters[{i}]")
-            e.exp_avg = _dev(st[0], f"states[{i}].exp_avg", torch.float32)
-            e.exp_avg_sq = _dev(st[1], f"states[{i}].exp_avg_sq", torch.float32)
-        if lp is not None:
-            if lp.numel() != k:
-                raise ValueError(f"lowp[{i}] differs in size from masters[{i}]")
-            e.lowp = _dev(lp, f"lowp[{i}]")
-        e.numel, e.group = k, group_of[i]
-        if p.device != masters[0].device or any(t.device != p.device for t in (*st, *([] if lp is None else [lp]))):
-            raise ValueError(f"tensor {i} is not on one device with the list")
-    first = np.zeros(n + 1, dtype=np.int32)
-    _check(lib().zero_list_chunks(entries, n, n_groups, state_bits, ctypes.c_void_p(first.ctypes.data), None))
-    dev = masters[0].device
-    raw = torch.frombuffer(bytearray(bytes(memoryview(entries))), dtype=torch.uint8)
-    return TensorList(raw.to(dev), torch.from_numpy(first).to(dev), int(first[-1]), tuple(p.numel() for p in masters), state_bits,
-                      n_groups, dts.pop() if dts else None)
+            if len(st) != 2 or st[0].numel() != k or st[1].numel() != k:
+                raise ValueError(f"states[{i}] differs in size from masters[{i}]")
+            moments.append((_dev(st[0], f"states[{i}].exp_avg", torch.float32),
+                            _dev(st[1], f"states[{i}].exp_avg_sq", torch.float32)))
+    for nm, col in zip(("exp_avg", "exp_avg_sq", "exp_avg_scale", "root_scale"), zip(*moments)):
+        columns[nm] = col
+    return make_tensor_list(columns, numels, group_of, n_groups, state_bits, lowp_dtype, masters[0].device)
 
 
 def _list_args(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float, d_scale):
