@@ -3,8 +3,17 @@
 // a parameter group.  (Moments in 8 bits: adamw_list8.cu.)
 //
 // Work split: the tensors are cut into chunks of 1024 elements, none across
-// two tensors; one block per chunk, a warp per 256 elements.  Each warp finds
-// its block's tensor by a search over the tensors' first chunks.
+// two tensors; one block of 128 threads per chunk, a warp per 256 elements, 8
+// per lane (32-byte accesses).  The block's tensor is found by a search over
+// the tensors' first chunks (list.cuh).
+//
+// Bound by HBM: 28 bytes an element with 16-bit grads and copy.  Four layers
+// of Llama-7B with embedding and head (1.07e9 elements): 4.25 ms = 7.06 TB/s;
+// 4000 log-uniform tensors (302e6): 1.20 ms = 7.04 TB/s; GPT-2 small (148
+// tensors, 124e6): 0.498 ms = 6.99 TB/s.  Ten blocks per SM (48 registers)
+// against eight (64): the ragged list 1.21 against 1.25 ms, large tensors the
+// same; chunks of 2048 in blocks of 256: 1.27.  Four layers of fp32 moments
+// with grads off the 16-byte grid: 4.27 ms.
 #include "adam.cuh"
 #include "common.cuh"
 #include "kernels.h"

@@ -11,9 +11,10 @@ namespace zs {
 // The tensor of chunk c: the last i with first[i] <= c.  The warp's 32 lanes
 // test 32 evenly spaced candidates a round (find_tensor_warp of table.cuh):
 // 2 rounds for up to 1024 tensors, 3 for 32768.  first[] is 4 bytes a tensor
-// and stays in the SM's L1, so a round is some 50 cycles; a map with one entry
-// per chunk, a single read but from L2 or HBM, left blocks waiting longer
-// before their first load (measured in adamw_list8.cu).
+// and stays in the SM's L1; a map with one entry per chunk, a single read but
+// from L2 or HBM, left blocks waiting longer before their first load (1.88e9
+// elements in 8 bits: 4.84 against 4.76 ms; 4000 ragged fp32 tensors: 1.29
+// against 1.27).
 __device__ __forceinline__ int find_chunk_tensor(const int32_t* __restrict__ first, int n, int c) {
   const int lane = threadIdx.x & 31;
   int lo = 0, span = n;

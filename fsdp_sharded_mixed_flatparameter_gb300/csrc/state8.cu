@@ -1,7 +1,9 @@
 // state8.cu -- the fp32 moments of a flat shard (or of one tensor) into the
 // 8-bit format of state8.cuh and back: a checkpoint in 32 bits, a run that
 // goes on in 8.  A warp per block of 256 elements; 8 + 2 bytes per element
-// either way, HBM-bound.
+// either way, HBM-bound: pack 400e6 elements 0.549 ms = 7.30 TB/s (0.648 at
+// four blocks per SM instead of six; seven spill: 0.741), unpack 1.63e9 2.32 ms
+// = 7.03 TB/s; 15.6e6 elements 26 us either way.
 #include "common.cuh"
 #include "kernels.h"
 #include "state8.cuh"

@@ -209,7 +209,7 @@ __device__ __forceinline__ F2 adam_update8(F2& p, F2& cm, F2& cr, F2 g, const Fa
 // elements 8l .. 8l + 7 of a full block in aligned buffers; else it has
 // elements l, l + 32, ..., l + 224, those from `left` on absent (zeros): tails
 // and unaligned buffers.  The two are separate instantiations: one code for
-// both, with the order as a variable, took 101 registers instead of 64.
+// both, with the order as a variable, took 101 registers (adamw_list8.cu).
 template <bool VEC>
 __device__ __forceinline__ int elem_of(int j) {
   const int lane = threadIdx.x & 31;
