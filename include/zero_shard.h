@@ -567,7 +567,8 @@ zero_status zero_state8_unpack(const zero_state8* q, int64_t n, float* d_exp_avg
  * (each operation rounded to nearest in binary32); the quotient is formed
  * with the hardware's root and reciprocal and is within 8 ulp.  p and lowp
  * use these m and v, which are rounded to 8 bits only when they are stored in
- * q.  An exp_avg_sq below the normal range (2^-126) counts as zero.
+ * q.  An exp_avg_sq below the normal range (2^-126) counts as zero, an eps
+ * below it as 2^-126.
  * rounding: NULL rounds to nearest, else (host memory) the seed and stream of
  * stochastic rounding.
  * 16 bytes per parameter with 16-bit grads and copy, where the fp32 state
@@ -597,7 +598,8 @@ zero_status zero_adamw_step8_tensors_device(float* d_master, const zero_state8* 
  * exp_avg_sq's root with their scales.  lowp: NULL, or the low-precision
  * copy.  Each buffer is contiguous with numel elements (scales:
  * ceil(numel / 256)), at any element alignment; the fast path needs fp32
- * buffers 32-byte, codes 8-byte, 16-bit buffers 16-byte aligned. */
+ * buffers 32-byte, codes 8-byte, 16-bit buffers 16-byte aligned.  No two
+ * tensors of a list may share a buffer that the step writes. */
 typedef struct zero_list_tensor {
   float* master;
   void* exp_avg;

@@ -189,6 +189,51 @@ def test_other_stream_and_large_list():
     assert all(torch.equal(x, y) for x, y in zip(bits_of(a.everything()), bits_of(b.everything())))
 
 
+def test_tens_of_thousands_of_tensors():
+    # four rounds of the search; empty tensors between, at the front and at the end
+    rng = np.random.default_rng(3)
+    sizes = [0, 0] + [int(x) for x in rng.integers(0, 40, 36000)] + [3000, 0, 0]
+    total = sum(sizes)
+    g = gen(0)
+    flat_x, flat_p = (torch.randn(total, generator=g).cuda() for _ in range(2))
+    opt = pkg.TensorListAdamW([t.clone() for t in torch.split(flat_p, sizes)], lr=1e-2, weight_decay=0.1, max_norm=1.0)
+    flat = pkg.FlatShardAdamW(sizes, lr=1e-2, weight_decay=0.1, max_norm=1.0, device="cuda", master=flat_p.clone(),
+                              grad_buffer=False)
+    grads = list(torch.split(flat_x, sizes))  # views at any alignment
+    assert opt.step(grads) == flat.step_tensors(grads)
+    assert torch.equal(torch.cat([p.view(-1) for p in opt.masters]), flat.master)
+    o8 = pkg.TensorListAdamW([t.clone() for t in torch.split(flat_p, sizes)], lr=1e-2, weight_decay=0.1, max_norm=1.0,
+                             state_bits=8, rounding_seed=9)
+    o8.step(grads)
+    # the first step's moments come from zero: the update is the fp32 one but for the hardware root and reciprocal
+    off = (torch.cat([p.view(-1) for p in o8.masters]) - flat.master).abs().max()
+    assert off <= 16 * R.EPS * (1e-2 + float(flat.master.abs().max()))
+    for i in rng.integers(0, len(sizes), 100):
+        if sizes[i]:
+            h = host(o8.state_of(int(i)))
+            m = 0.1 * f64(grads[int(i)]) * float(np.float32(min(1.0, 1.0 / (float(flat_x.double().norm()) + 1e-6))))
+            R.check_codes(h[0], h[1], m, 8 * R.EPS * np.abs(m), k=R.draws(9, 1, int(i), sizes[i])[0], name=str(i))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_sixty_four_groups_and_pinned_grads(bits):
+    sizes = [257] * 64
+    hps = [(1e-3 * (k + 1), 0.9 - 0.01 * k, 0.999 - 0.005 * k, 1e-8 * (k + 1), 0.01 * k) for k in range(64)]
+    a, b = (Case(sizes, bits, "bf16", "bf16", n_groups=64) for _ in range(2))
+    zs.zero_adamw_list(a.list, a.grads, a.gdt, 1.0, hps, 5)
+    pinned = [x.cpu().pin_memory() for x in b.x]
+    grads = zs.device_table(zs.zero_tensor_table(pinned, sizes)[0], 64, "cuda")
+    zs.zero_adamw_list(b.list, grads, b.gdt, 1.0, hps, 5)
+    assert all(torch.equal(x, y) for x, y in zip(bits_of(a.everything()), bits_of(b.everything())))
+    c = Case(sizes, bits, "bf16", "bf16", n_groups=64)
+    for i in range(64):  # one tensor at a time, as a group of its own
+        one = zs.zero_tensor_list(c.p[i:i + 1], c.state[i:i + 1], None if c.lowp[i] is None else c.lowp[i:i + 1],
+                                  state_bits=bits)
+        t = zs.device_table(zs.zero_tensor_table(c.x[i:i + 1])[0], 1, "cuda")
+        zs.zero_adamw_list(one, t, c.gdt, 1.0, [hps[i]], 5)
+    assert all(torch.equal(x, y) for x, y in zip(bits_of(a.everything()), bits_of(c.everything())))
+
+
 def test_one_tensor_is_the_shard_step():
     n = 9999
     a = Case([n], 8, "bf16", "bf16", n_groups=1)
