@@ -5,11 +5,12 @@
 //
 // 16 bytes an element with 16-bit grads and copy, and 45 instructions (59
 // with stochastic rounding): near the bandwidth's and the issue rate's limit
-// at once.  Eight layers of Llama-7B (1.88e9 elements), stochastic: 4.51 ms =
-// 6.70 TB/s; four layers (1.07e9): 2.47 ms to nearest (6.98 TB/s), 2.57
+// at once.  Eight layers of Llama-7B (1.88e9 elements), stochastic: 4.43 ms =
+// 6.82 TB/s; four layers (1.07e9): 2.47 ms to nearest (6.98 TB/s), 2.57
 // stochastic, 2.50 to nearest with grads off the 16-byte grid.  4000
-// log-uniform tensors (302e6): 0.80 ms = 6.09 TB/s, where short last chunks
-// leave warps idle; GPT-2 small, stochastic: 0.315 ms = 6.34 TB/s.
+// log-uniform tensors (302e6): 0.79 ms = 6.13 TB/s, where short last chunks
+// leave warps idle and the search takes a second round; GPT-2 small,
+// stochastic: 0.314 ms = 6.37 TB/s.
 //
 // The way there, 1.88e9 elements, stochastic: 9.62 ms at 100 registers (one
 // code for full and short blocks); 6.09 with the two apart at 64 registers;
@@ -18,7 +19,7 @@
 // registers) instead of four; 4.76 with the search in place of a chunk map;
 // 4.69 with blocks of 128; 4.66 with the rounding key hashed on the host; 4.57
 // with the stochastic codes collected by byte permutation; 4.51 with one
-// search per block.  Not kept: asynchronous copies into shared memory, a
+// search per block; 4.43 with its last round over 128 candidates.  Not kept: asynchronous copies into shared memory, a
 // block's chunks in a pipeline of two or three stages (6.2 to 6.9 ms at the
 // first arithmetic, against 6.1: their addressing and waits are instructions).
 #include "common.cuh"
