@@ -9,11 +9,11 @@
 // adamw_table.cuh: directly, realigned in registers, or staged in shared
 // memory where tensors meet.
 //
-// Measured: a Llama-13B ZeRO-3 shard (1.63e9 elements, flat fp16 grads) 3.70
-// ms = 7.06 TB/s; a quarter of 20,000 ragged tensors (377e6, most parts off
-// the 16-byte grid, stochastic) 1.00 ms = 6.07 TB/s, 75 instructions an
+// Measured: a Llama-13B ZeRO-3 shard (1.63e9 elements, flat fp16 grads) 3.71
+// ms = 7.04 TB/s; a quarter of 20,000 ragged tensors (377e6, most parts off
+// the 16-byte grid, stochastic) 1.02 ms = 5.94 TB/s, 79 instructions an
 // element with the search and the realignment; a GPT-2 ZeRO-1 shard with
-// accumulation (15.6e6) 52.5 us = 5.94 TB/s, ten waves of blocks.  Five
+// accumulation (15.6e6) 54 us = 5.8 TB/s, ten waves of blocks.  Five
 // blocks per SM (48 registers) against four: 3.71 and 1.09 against 3.88 and
 // 1.19 ms; six spill.  Two or four parts per block and search: 1.40 and 1.32
 // ms (ragged); blocks of 128 threads: the same; one warp's search shared

@@ -64,17 +64,30 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// Hardware root and reciprocal (relative error at most 2^-23 each, subnormal
-// arguments and results as zero).
-__device__ __forceinline__ float root_approx(float x) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
+// Hardware reciprocal and reciprocal root (relative error under 2^-22,
+// subnormal arguments and results as zero).
 __device__ __forceinline__ float reciprocal_approx(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// sqrt(v) of finite v >= 0: g = v y with y ~ 1 / sqrt(v), then one Newton step
+// g + (v - g^2) y / 2, whose residual is exact in an fma.  Its error before the
+// last rounding is of the order of y's squared, so it is the correctly rounded
+// root but for about one v in a million (1 ulp off there).  Zero gives zero;
+// below the normal range (2^-126) it is positive but too small.
+__device__ __forceinline__ F2 root2(F2 v) {
+  float v0, v1;
+  unpair(v, v0, v1);
+  const F2 y = pair(rsqrt_approx(fmaxf(v0, 0x1p-126f)), rsqrt_approx(fmaxf(v1, 0x1p-126f)));
+  const F2 g = mul2(v, y);
+  return fma2(fma2(g, g, mul2(v, both(-1.0f))), mul2(y, both(-0.5f)), g);
 }
 
 // ------------------------------------------------------------------ codes
@@ -176,27 +189,24 @@ __device__ __forceinline__ Factors8 factors8(const AdamScalars& s, float sm, flo
   return f;
 }
 
-// The 32-bit update (adam.cuh) on two elements whose moments come as codes:
-// cm, cr (the codes' values) in, m and v out.  m and v are what the 32-bit
-// update gives for the decoded moments, bit for bit.  The parameter's change
-// is step m / (sqrt(v) / sqrt(1 - beta2^t) + eps) with the hardware root and
-// reciprocal, within 8 ulp of itself: correctly rounded division and root
-// are some 25 instructions and two branches an element, together as much as
-// all the rest, for digits far below the 3 bits that the moments keep.
-// Returns r = sqrt(v).
-__device__ __forceinline__ F2 adam_update8(F2& p, F2& cm, F2& cr, F2 g, const Factors8& f) {
+// The 32-bit update (adam.cuh) on two elements, in two parts.  First the
+// moments, from codes: cm, cr (the codes' values) in, m and v out, bit for bit
+// what the 32-bit update gives for the decoded moments.
+__device__ __forceinline__ void moments8(F2& cm, F2& cr, F2 g, const Factors8& f) {
   g = mul2(g, f.coef);
-  const F2 m = fma2(f.omb1, g, mul2(cm, f.mb1));
-  const F2 v = fma2(mul2(f.omb2, g), g, mul2(mul2(cr, cr), f.vb2));
-  float v0, v1, d0, d1;
-  unpair(v, v0, v1);
-  const F2 r = pair(root_approx(v0), root_approx(v1));
+  cm = fma2(f.omb1, g, mul2(cm, f.mb1));
+  cr = fma2(mul2(f.omb2, g), g, mul2(mul2(cr, cr), f.vb2));
+}
+
+// Then the parameter: p - step m / (r / sqrt(1 - beta2^t) + eps), r = sqrt(v),
+// with the hardware's reciprocal, its change within 8 ulp of itself: correctly
+// rounded division and root by the compiler's sequences are some 25
+// instructions and two branches an element, together as much as all the rest.
+__device__ __forceinline__ F2 param8(F2 p, F2 m, F2 r, const Factors8& f) {
+  float d0, d1;
   unpair(fma2(r, f.inv_bc2, f.eps), d0, d1);
   const F2 u = mul2(m, pair(reciprocal_approx(d0), reciprocal_approx(d1)));
-  p = fma2(f.step, u, mul2(p, f.decay));
-  cm = m;
-  cr = v;
-  return r;
+  return fma2(f.step, u, mul2(p, f.decay));
 }
 
 // ------------------------------------------------------------- one block
@@ -354,30 +364,37 @@ __device__ __forceinline__ void store_block_lowp(void* lowp, int lowp_dtype, int
 }
 
 // The update of one block whose codes, scales and grads (fl(scale x), summed)
-// are in registers, and its stores.  The root's scale comes from the
-// correctly rounded root of the block's largest exp_avg_sq, so it does not
-// depend on the hardware root's last bit.
+// are in registers, and its stores.
 template <bool VEC, bool SR>
 __device__ __forceinline__ void update_block(float* p, uint8_t* qm, uint8_t* qr, float* ms, float* rs,
                                              unsigned short* lowp, int lowp_dtype, int left, const float (&x)[8],
                                              const float (&g)[8], uint2 cm, uint2 cr, float sm, float sr, float coef,
                                              const AdamScalars& s, uint32_t key, int64_t pair0) {
   const Factors8 f = factors8(s, sm, sr, coef);
-  F2 m[4], v[4], r[4];
+  F2 m[4], r[4];
   float y[8];
   decode8(cm, m);
-  decode8(cr, v);
+  decode8(cr, r);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    F2 w = pair(x[2 * i], x[2 * i + 1]);
-    r[i] = adam_update8(w, m[i], v[i], pair(g[2 * i], g[2 * i + 1]), f);
-    unpair(w, y[2 * i], y[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) moments8(m[i], r[i], pair(g[2 * i], g[2 * i + 1]), f);
+  const uint32_t amax_m = warp_amax(m), amax_v = warp_amax(r);
+  if (amax_v < 0x7f800000u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = root2(r[i]);
+  } else {  // an overflown or NaN exp_avg_sq in the block: the same, for any value
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v0, v1;
+      unpair(r[i], v0, v1);
+      r[i] = pair(__fsqrt_rn(v0), __fsqrt_rn(v1));
+    }
   }
-  const uint32_t amax_m = warp_amax(m);
-  const uint32_t amax_r = __float_as_uint(__fsqrt_rn(__uint_as_float(warp_amax(v))));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpair(param8(pair(x[2 * i], x[2 * i + 1]), m[i], r[i], f), y[2 * i], y[2 * i + 1]);
   store_block_f32<VEC>(p, left, y);
   if (lowp != nullptr) store_block_lowp<VEC>(lowp, lowp_dtype, left, y);
-  encode_block<VEC, SR>(m, r, amax_m, amax_r, key, pair0, cm, cr, sm, sr);
+  // the largest root is the root of the largest exp_avg_sq
+  encode_block<VEC, SR>(m, r, amax_m, __float_as_uint(__fsqrt_rn(__uint_as_float(amax_v))), key, pair0, cm, cr, sm, sr);
   store_codes<VEC>(qm, left, cm);
   store_codes<VEC>(qr, left, cr);
   if ((threadIdx.x & 31) == 0) {

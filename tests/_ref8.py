@@ -104,8 +104,8 @@ def grad(x, scale=1.0, acc=None, coef=1.0):
 
 def step(p, m, v, g, g_err, *, lr, b1, b2, eps, wd, t, root=1, div=1):
     """One AdamW step: {name: (value, bound)} for p, m and r = sqrt(v).  root, div: the errors of the
-    square root and of the division in EPS (1: correctly rounded; the 8-bit update's hardware root
-    and reciprocal: 2 and, with its product, 3)."""
+    square root and of the division in EPS (1: correctly rounded; the 8-bit update's Newton root
+    and hardware reciprocal: 2 and, with its product, 3)."""
     alpha, bc2 = lr / (1 - b1 ** t), math.sqrt(1 - b2 ** t)
     m1 = b1 * m + (1 - b1) * g
     m_err = EPS * (2 * np.abs(b1 * m) + np.abs((1 - b1) * g) + np.abs(m1)) + (1 - b1) * g_err
