@@ -170,7 +170,9 @@ __device__ __forceinline__ uint32_t rounding_key(const RoundingBase& rnd, const 
 // ----------------------------------------------------------------- update
 // The update's factors for one block, each twice.  The decoded moments enter
 // only as m beta1 = c (S beta1) and v beta2 = c^2 (S^2 beta2), which with S a
-// power of two are the same numbers as fl(m beta1) and fl(fl(r^2) beta2).
+// power of two are the same numbers as fl(m beta1) and fl(fl(r^2) beta2) as
+// long as S^2 beta2 is a normal number: in blocks whose largest root is above
+// 2^-54.  Below, exp_avg_sq (under 10^-32) keeps fewer bits than 24.
 struct Factors8 {
   F2 coef, decay, mb1, omb1, vb2, omb2, inv_bc2, eps, step;
 };
@@ -191,7 +193,7 @@ __device__ __forceinline__ Factors8 factors8(const AdamScalars& s, float sm, flo
 
 // The 32-bit update (adam.cuh) on two elements, in two parts.  First the
 // moments, from codes: cm, cr (the codes' values) in, m and v out, bit for bit
-// what the 32-bit update gives for the decoded moments.
+// what the 32-bit update gives for the decoded moments (but for the note above).
 __device__ __forceinline__ void moments8(F2& cm, F2& cr, F2 g, const Factors8& f) {
   g = mul2(g, f.coef);
   cm = fma2(f.omb1, g, mul2(cm, f.mb1));

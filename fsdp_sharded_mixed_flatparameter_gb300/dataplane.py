@@ -97,7 +97,7 @@ class ZeroDataPlane:
     (``grad_views()`` gives the per-tensor views); ``flat_param`` is the full
     low-precision FlatParameter (``param_views()``).  Other keyword arguments
     go to FlatShardAdamW (lr, betas, eps, weight_decay, max_norm, master,
-    capturable)."""
+    capturable, state_bits, rounding_seed)."""
 
     def __init__(self, numels: Sequence[int], *, group=None, grad_dtype: torch.dtype = torch.bfloat16,
                  lowp_dtype: torch.dtype = torch.bfloat16, device="cuda", **adam_kw):
@@ -238,6 +238,10 @@ class ZeroUnits:
                                     master=None if masters is None else masters[i],
                                     workspace=self.ws[offs[i]:offs[i + 1]] if sizes[i] else None, **kw)
                       for i, numels in enumerate(units)]
+        before = 0  # units that share a rounding_seed draw as one FlatParameter of all of them would
+        for u in self.units:
+            u.opt.rounding_stream += before
+            before += u.total
         self._local = zs.new_norm_result(dev)
 
     def reduce_scatter_grads(self, **kw) -> None:

@@ -27,7 +27,8 @@ class TensorListAdamW(GradTables):
     or per tensor None or its bf16 / f16 copy.  groups: a dict per parameter group with any
     of lr, betas, eps, weight_decay (the rest from the keyword arguments); group_of: each
     tensor's group (default: all in group 0).  rounding_seed (8 bits only): None rounds
-    the moments to nearest, an integer seeds stochastic rounding.
+    the moments to nearest, an integer seeds stochastic rounding; lists that share a seed
+    take rounding_streams that are further apart than they have tensors.
 
     The moments live in storages of this object, tensor i's at elements offsets[i] ..
     offsets[i] + numels[i]: ``exp_avg`` and ``exp_avg_sq`` (fp32), or ``state8`` (8 bits:
@@ -37,7 +38,7 @@ class TensorListAdamW(GradTables):
                  groups: Optional[Sequence[dict]] = None, group_of: Optional[Sequence[int]] = None, lr: float = 1e-4,
                  betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
                  max_norm: float = math.inf, state_bits: int = 32, rounding_seed: Optional[int] = None,
-                 capturable: bool = False):
+                 rounding_stream: int = 0, capturable: bool = False):
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 32 or 8")
         if rounding_seed is not None and state_bits == 32:
@@ -48,7 +49,7 @@ class TensorListAdamW(GradTables):
         self.lowp = None if lowp is None else list(lowp)
         self.device = self.masters[0].device
         self.state_bits, self.rounding_seed, self.capturable = state_bits, rounding_seed, capturable
-        self.max_norm = max_norm
+        self.max_norm, self.rounding_stream = max_norm, rounding_stream
         defaults = dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay)
         self._groups: List[list] = []
         for g in ([{}] if groups is None else groups):
@@ -148,10 +149,10 @@ class TensorListAdamW(GradTables):
         if self.capturable:
             zs.zero_adamw_prepare_list_device(self._dev_hp, len(self._groups), clip, self._dev_states, stream)
             zs.zero_adamw_list_device(self._list, table, dt, sc, self._dev_states, clip, stream, d_scale=dsc,
-                                      rounding_seed=self.rounding_seed)
+                                      rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream)
         else:
             zs.zero_adamw_list(self._list, table, dt, sc, self._hp, self._t + 1, clip, stream, d_scale=dsc,
-                               rounding_seed=self.rounding_seed)
+                               rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream)
 
     def finish_step(self, stream=None, norm_result: Optional[torch.Tensor] = None) -> zs.NormResult:
         """Read the step's norm (a device-to-host copy on `stream`, the stream the step was

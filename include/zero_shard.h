@@ -564,7 +564,8 @@ zero_status zero_state8_unpack(const zero_state8* q, int64_t n, float* d_exp_avg
  *   v = fma((1-beta2)*g, g, (r*r)*beta2)
  *   p = fma(-lr / (1-beta1^t), m / (sqrt(v) / sqrt(1-beta2^t) + eps), p * (1 - lr*wd))
  * m and v are those of zero_adamw_step for the decoded moments, bit for bit
- * (each operation rounded to nearest in binary32); the root is the correctly
+ * (each operation rounded to nearest in binary32; in a block whose largest
+ * root is under 2^-54, v keeps fewer bits); the root is the correctly
  * rounded one (1 ulp off for about one value in a million), the quotient is
  * formed with the hardware's reciprocal and within 8 ulp.  p and lowp use
  * these m and v, which are rounded to 8 bits only when they are stored in q.

@@ -459,6 +459,42 @@ def test_data_plane_and_units_with_8_bit_states():
     assert torch.equal(units.units[0].opt.master[:4864], ref.master[:4864])
 
 
+def test_units_that_share_a_seed_draw_differently():
+    n = 5000
+    units = pkg.ZeroUnits([[n], [n]], device="cuda:0", lr=1e-2, state_bits=8, rounding_seed=1)
+    g = (torch.randn(n, generator=gen(1)) * 1e-2).bfloat16().cuda()
+    for u in units.units:
+        u.flat_grad.copy_(g)
+    units.reduce_scatter_grads()
+    units.step()
+    a, b = (u.opt.state8 for u in units.units)
+    assert torch.equal(a.exp_avg_scale, b.exp_avg_scale) and not same(a, b)
+    one = pkg.FlatShardAdamW([n], lr=1e-2, state_bits=8, rounding_seed=1, device="cuda")
+    one.step_tensors([g])
+    assert same(one.state8, a)
+
+
+@pytest.mark.parametrize("power", [-12, -50, -60])
+def test_moments_of_any_size(power):
+    # grads scaled by a power of two move moments and scales by it: the same codes, as long as nothing underflows
+    n, s = 3000, 2.0 ** power
+    g = gen(20)
+    x = torch.randn(n, generator=g).cuda()
+    runs = []
+    for k in (1.0, s):
+        q, p = pkg.new_state8(n, "cuda"), torch.zeros(n, device="cuda")
+        for t in (1, 2):
+            shard_call(p, q, x * k, seed=3, step=t)
+        runs.append(q)
+    a, b = runs
+    if power > -54:
+        assert torch.equal(a.exp_avg.view(torch.uint8), b.exp_avg.view(torch.uint8))
+        assert torch.equal(a.root.view(torch.uint8), b.root.view(torch.uint8))
+        assert torch.equal(a.exp_avg_scale * s, b.exp_avg_scale) and torch.equal(a.root_scale * s, b.root_scale)
+    else:  # exp_avg_sq around 2^-120: still finite, still above zero wherever the grads are
+        assert ((b.root.view(torch.uint8) > 0) == (a.root.view(torch.uint8) > 0)).all() and b.root_scale.isfinite().all()
+
+
 @pytest.mark.slow
 def test_indices_past_2_to_31():
     n = (1 << 31) + 5003
