@@ -32,7 +32,7 @@
 
 namespace zs {
 
-template <int DT, bool SR, bool VEC>
+template <int DT, int SR, bool VEC>
 __device__ __forceinline__ void list8_block(const zero_list_tensor& t, const void* grad, int64_t k, int64_t rest,
                                             float gscale, float coef, const AdamScalars& s, int lowp_dtype,
                                             uint32_t key) {
@@ -51,7 +51,7 @@ __device__ __forceinline__ void list8_block(const zero_list_tensor& t, const voi
                         lowp_dtype, left, p, g, cm, cr, sm, sr, coef, s, key, k >> 1);
 }
 
-template <int DT, bool SR>
+template <int DT, int SR>
 __global__ void __launch_bounds__(kListThreads, 10)
     adamw_list8_kernel(const zero_list_tensor* __restrict__ list, int n_tensors,
                        const int32_t* __restrict__ first_chunk, const zero_tensor* __restrict__ grads, float gscale,
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kListThreads, 10)
   AdamScalars s;
   if (!group_scalars(hs, ds, t.group, s)) return;
   uint32_t key = 0u;
-  if (SR) key = rounding_key(rnd, ds, tensor, k >> 1);
+  if (SR != kNearest) key = rounding_key(rnd, ds, tensor, k >> 1);
   if (left >= kBlock8 && aligned(t.master, 32) && aligned(t.exp_avg, 8) && aligned(t.exp_avg_sq, 8))
     list8_block<DT, SR, true>(t, grad, k, left, gscale, coef, s, lowp_dtype, key);
   else
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kListThreads, 10)
                                key);
 }
 
-template <int DT, bool SR>
+template <int DT, int SR>
 static zero_status launch_list8_t(const ListArgs& a, const ListScalars& hs, cudaStream_t st) {
   adamw_list8_kernel<DT, SR><<<static_cast<unsigned>(a.n_chunks), kListThreads, 0, st>>>(
       a.list, a.n_tensors, a.first_chunk, a.grads, a.gscale, a.dscale, a.lowp_dtype, hs, a.ds, a.rounding, a.clip);
@@ -92,12 +92,16 @@ static zero_status launch_list8_t(const ListArgs& a, const ListScalars& hs, cuda
 
 ZS_DEBUG_UNIT(adamw_list8)
 
+template <int DT>
+static zero_status launch_list8_dt(const ListArgs& a, const ListScalars& hs, cudaStream_t st) {
+  if (a.rounding.root_bits == 0) return launch_list8_t<DT, kNearest>(a, hs, st);
+  return a.rounding.root_bits == 7 ? launch_list8_t<DT, kRoot7>(a, hs, st) : launch_list8_t<DT, kRoot16>(a, hs, st);
+}
+
 zero_status launch_adamw_list8(const ListArgs& a, const ListScalars& hs, cudaStream_t st) {
-  if (a.grad_dtype == ZERO_F32)
-    return a.stochastic ? launch_list8_t<ZERO_F32, true>(a, hs, st) : launch_list8_t<ZERO_F32, false>(a, hs, st);
-  if (a.grad_dtype == ZERO_BF16)
-    return a.stochastic ? launch_list8_t<ZERO_BF16, true>(a, hs, st) : launch_list8_t<ZERO_BF16, false>(a, hs, st);
-  return a.stochastic ? launch_list8_t<ZERO_F16, true>(a, hs, st) : launch_list8_t<ZERO_F16, false>(a, hs, st);
+  if (a.grad_dtype == ZERO_F32) return launch_list8_dt<ZERO_F32>(a, hs, st);
+  if (a.grad_dtype == ZERO_BF16) return launch_list8_dt<ZERO_BF16>(a, hs, st);
+  return launch_list8_dt<ZERO_F16>(a, hs, st);
 }
 
 }  // namespace zs

@@ -33,7 +33,7 @@ constexpr int kT8Block = 8 * kBlock8;
 // it: its three rounds of short reads then do not queue behind them (20,000
 // ragged tensors, 377M elements: 998 against 1040 us).  Every thread of the
 // block must call it.
-template <int DT, bool SR>
+template <int DT, int SR>
 __device__ __forceinline__ void table8_full(float* p, const zero_state8& q, const float* acc, const zero_tensor* table,
                                             int n_tensors, int64_t shard_start, int64_t k0, float gscale, void* lowp,
                                             int lowp_dtype, float coef, const AdamScalars& s, uint32_t key,
@@ -93,7 +93,7 @@ __device__ __forceinline__ void table8_full(float* p, const zero_state8& q, cons
 }
 
 // Any part: the last one, or unaligned state.
-template <int DT, bool SR>
+template <int DT, int SR>
 __device__ __forceinline__ void table8_any(float* p, const zero_state8& q, const float* acc, const zero_tensor* table,
                                            int n_tensors, int64_t shard_start, int64_t k0, int64_t n, float gscale,
                                            void* lowp, int lowp_dtype, float coef, const AdamScalars& s,
@@ -123,7 +123,7 @@ __device__ __forceinline__ void table8_any(float* p, const zero_state8& q, const
   }
 }
 
-template <int DT, bool SR>
+template <int DT, int SR>
 __global__ void __launch_bounds__(256, 5)
     adamw_table8_kernel(float* __restrict__ p, zero_state8 q, const float* __restrict__ acc,
                         const zero_tensor* __restrict__ table, int n_tensors, int64_t shard_start, int64_t n,
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256, 5)
   }
   const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kT8Block;
   uint32_t key = 0u;
-  if (SR) key = rounding_key(rnd, ds, 0u, k0 >> 1);
+  if (SR != kNearest) key = rounding_key(rnd, ds, 0u, k0 >> 1);
   const bool full = state_vec && n - k0 >= kT8Block;
   if (!ZS_CHECK(k0 < n && (!full || (aligned(p + k0, 32) && aligned(q.exp_avg + k0, 8) && aligned(q.root + k0, 8) &&
                                      (acc == nullptr || aligned(acc + k0, 32)))),
@@ -153,20 +153,20 @@ __global__ void __launch_bounds__(256, 5)
     table8_any<DT, SR>(p, q, acc, table, n_tensors, shard_start, k0, n, gscale, lowp, lowp_dtype, coef, s, key, stage);
 }
 
-template <int DT>
-static zero_status launch_table8_dt(const Table8Args& a, const AdamScalars& s, cudaStream_t st) {
+template <int DT, int SR>
+static zero_status launch_table8_t(const Table8Args& a, const AdamScalars& s, cudaStream_t st) {
   const bool sv = aligned(a.p, 32) && aligned(a.q.exp_avg, 8) && aligned(a.q.root, 8) &&
                   (a.acc == nullptr || aligned(a.acc, 32));
-  const unsigned grid = one_pass_blocks(a.n, kT8Block);
-  if (a.stochastic)
-    adamw_table8_kernel<DT, true><<<grid, 256, 0, st>>>(a.p, a.q, a.acc, a.table, a.n_tensors, a.shard_start, a.n,
-                                                        a.gscale, a.dscale, a.lowp, a.lowp_dtype, sv, s, a.ds, a.rounding,
-                                                        a.clip);
-  else
-    adamw_table8_kernel<DT, false><<<grid, 256, 0, st>>>(a.p, a.q, a.acc, a.table, a.n_tensors, a.shard_start, a.n,
-                                                         a.gscale, a.dscale, a.lowp, a.lowp_dtype, sv, s, a.ds,
-                                                         a.rounding, a.clip);
+  adamw_table8_kernel<DT, SR><<<one_pass_blocks(a.n, kT8Block), 256, 0, st>>>(
+      a.p, a.q, a.acc, a.table, a.n_tensors, a.shard_start, a.n, a.gscale, a.dscale, a.lowp, a.lowp_dtype, sv, s, a.ds,
+      a.rounding, a.clip);
   return check_launch("adamw_table8_kernel");
+}
+
+template <int DT>
+static zero_status launch_table8_dt(const Table8Args& a, const AdamScalars& s, cudaStream_t st) {
+  if (a.rounding.root_bits == 0) return launch_table8_t<DT, kNearest>(a, s, st);
+  return a.rounding.root_bits == 7 ? launch_table8_t<DT, kRoot7>(a, s, st) : launch_table8_t<DT, kRoot16>(a, s, st);
 }
 
 ZS_DEBUG_UNIT(adamw_table8)

@@ -50,10 +50,12 @@ AdamwTableInstance launch_adamw_table_p4;
 AdamwTableInstance launch_adamw_table_p4_acc;
 
 // Stochastic rounding's draws, as far as the launch knows them: the hash of the
-// seed and (unless the step is on the device) of the step, and the stream.
+// seed and (unless the step is on the device) of the step, and the stream; the
+// bits drawn for a root (0: to nearest, nothing is drawn).
 struct RoundingBase {
   uint32_t hash;
   uint32_t stream;
+  int root_bits;
 };
 
 // AdamW over a flat shard with 8-bit moments, grads through the table.
@@ -70,7 +72,6 @@ struct Table8Args {
   void* lowp;
   int lowp_dtype;
   const zero_adamw_device_state* ds;
-  bool stochastic;
   RoundingBase rounding;
   const zero_norm_result* clip;
 };
@@ -94,7 +95,6 @@ struct ListArgs {
   const float* dscale;
   int lowp_dtype;
   const zero_adamw_device_state* ds;
-  bool stochastic;
   RoundingBase rounding;
   const zero_norm_result* clip;
 };

@@ -20,13 +20,23 @@
 // root under a surviving exp_avg would make the next update m / eps.
 //
 // Rounding to the code's grid is to nearest even, or stochastic: with u the
-// grid's spacing at |x| / S and k a number in [0, 128) drawn for the element,
-//   floor((floor(128 (|x| / S) / u) + k) / 128) u,
-// whose mean is |x| / S to 1/128 of the spacing.  To nearest, a moment that
-// moves by less than half a spacing per step (3 to 6 %; exp_avg_sq moves by
-// 1 - beta2 of the difference) keeps its code until the block's S moves;
-// stochastic rounding keeps the mean of the recurrence.  The draws are a
-// hash of (seed, step, stream, element), so a step is reproducible.
+// grid's spacing at |x| / S,
+//   7 bits:  floor((floor(128 (|x| / S) / u) + k) / 128) u,  k in [0, 128) drawn,
+//   16 bits: floor((|x| / S) / u + (h + 1/2) / 65536) u,  h in [0, 65536) drawn.
+// The 16 bits keep the mean to 2^-17 u, whatever x.  The 7 bits are u / 256 low
+// on average and do not see a move of less than u / 128, which a recurrence
+// adds up over 1 / (1 - beta) steps: exp_avg is 0.7 % low at beta1 = 0.95 and
+// 3 % at 0.99, but exp_avg_sq, normal grads, 8000 steps from zero, comes to
+// 0.68 of what it should be at beta2 = 0.999 and 0.24 at 0.9999 (with the 16
+// bits to 1.04 and 1.03: the square of the root's own noise).  exp_avg takes
+// the 7 bits; the root the 16 from beta2 > 0.99 on (ZERO_ROOT7_MAX_BETA2), up
+// to which the 7 bits stay as near (0.97 at 0.99, 1.02 at 0.95; 16 bits 1.04,
+// 1.03) in 3 instructions an element less (1.88e9 elements: 4.45 against 4.51
+// ms).  To nearest, a moment that moves by
+// less than half a spacing per step (3 to 6 %) keeps its code until the
+// block's S moves: the same exp_avg_sq comes to 4.9 at beta2 = 0.95, to 0.19 at
+// 0.999.  The draws are a hash of (seed, step, stream, element), so a step is
+// reproducible.
 #pragma once
 
 #include "adam.cuh"
@@ -136,6 +146,29 @@ __device__ __forceinline__ uint32_t encode4_stochastic(F2 a, F2 b, uint32_t k0, 
   return c | (__byte_perm(h0, h1, 0x7531) & 0x80808080u);
 }
 
+// 4 roots, already scaled by 2^-24 (0 <= y <= 448 2^-24 but for an ulp), to
+// codes by stochastic rounding with 16 bits each: w0, w1 hold the numbers h in
+// their halves.  From 2^-6 (here 2^-30) on the upper 12 bits of a binary32
+// value are its e4m3 code but for the exponent, which the scale has moved to
+// 96 + e: in the word's bits 20 .. 27 stands e, then the fraction.  Four bits
+// further up the code is the upper byte and (h + 1/2) / 65536 of its unit is
+// added as the bytes 00 h h 80.  Below 2^-6 the grid is even: y / 2 + 2^-31 has
+// exponent 96, e = 0, and a fraction of the same units.  y above its limit by
+// an ulp (2^-20 u) cannot carry into the NaN code: h + 1/2 leaves 2^-17 u.
+__device__ __forceinline__ uint32_t encode4_root16(F2 a, F2 b, uint32_t w0, uint32_t w1) {
+  float y[4];
+  unpair(a, y[0], y[1]);
+  unpair(b, y[2], y[3]);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (y[i] < 0x1p-30f) y[i] = fmaf(y[i], 0.5f, 0x1p-31f);
+    const uint32_t h = __byte_perm(i < 2 ? w0 : w1, 0x80u, (i & 1) ? 0x5324 : 0x5104);
+    c[i] = (__float_as_uint(y[i]) << 4) + h;
+  }
+  return __byte_perm(__byte_perm(c[0], c[1], 0x0073), __byte_perm(c[2], c[3], 0x0073), 0x5410);
+}
+
 // ------------------------------------------------------------------ scale
 // (S, 1/S) of a block from the bits of max|x| (non-negative binary32 values
 // order like their bits, NaN above all).  max|x| with a fraction above 1.75 =
@@ -154,9 +187,17 @@ __device__ __forceinline__ void block_scale(uint32_t amax, float& s, float& inv)
 }
 
 // --------------------------------------------------------------- rounding
+// How an update rounds the moments to codes.
+enum Rounding : int {
+  kNearest = 0,
+  kRoot7 = 1,   // stochastic, 7 bits for both moments
+  kRoot16 = 2,  // stochastic, 7 bits for exp_avg, 16 for the root
+};
+
 // The key of one block's draws (pcg_hash: rounding.cuh): the word of pair i
 // (elements 2i, 2i + 1) is pcg_hash(low 32 bits of i ^ key); of each half of it
-// bits 0..6 round exp_avg and bits 7..13 the root.  The launch has hashed the
+// bits 0..6 round exp_avg and bits 7..13, or all 16, the root (the two moments'
+// roundings then share bits, which their means do not see).  The launch has hashed the
 // seed and the step; a step on the device (ds) is hashed here.  `pair`: any
 // pair of the block (a block never crosses a multiple of 2^32 pairs).
 __device__ __forceinline__ uint32_t rounding_key(const RoundingBase& rnd, const zero_adamw_device_state* ds,
@@ -238,18 +279,17 @@ __device__ __forceinline__ uint32_t warp_amax(const F2 (&x)[4]) {
 // Codes of the warp's block (byte j of the pair = this lane's element j) and
 // its scales, from m, r = sqrt(v) and the block's max|m|, max r as bits.
 // Every lane must call it.  `pair0`: the block's first pair.
-template <bool VEC, bool SR>
+template <bool VEC, int SR>
 __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4], uint32_t amax_m, uint32_t amax_r,
                                              uint32_t key, int64_t pair0, uint2& cm, uint2& cr, float& sm,
                                              float& sr) {
   float im, ir;
   block_scale(amax_m, sm, im);
   block_scale(amax_r, sr, ir);
-  if (SR) {  // 1/S >= 2^-118 in a finite block: 2^-8 of it is still normal
-    im *= 0x1p-8f;
-    ir *= 0x1p-8f;
-  }
-  const float least = SR ? 0x1p-17f : 0x1p-9f;  // the smallest code's value
+  if (SR != kNearest) im *= 0x1p-8f;  // 1/S >= 2^-118 in a finite block: 2^-8 of it is still normal
+  constexpr float to = SR == kNearest ? 1.0f : SR == kRoot7 ? 0x1p-8f : 0x1p-24f;
+  ir *= to;  // a root is at most 2^64, 1/S at least 2^-56
+  constexpr float least = 0x1p-9f * to;  // the smallest code's value
   F2 x[4], y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -262,12 +302,12 @@ __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4],
     if (r1 > 0.0f) y1 = fmaxf(y1, least);
     y[i] = pair(y0, y1);
   }
-  if (!SR) {
+  if (SR == kNearest) {
     cm = make_uint2(encode4_nearest(x[0], x[1]), encode4_nearest(x[2], x[3]));
     cr = make_uint2(encode4_nearest(y[0], y[1]), encode4_nearest(y[2], y[3]));
   } else {
     const int lane = threadIdx.x & 31;
-    uint32_t km[4], kr[4];
+    uint32_t km[4], kr[4], wr[4];
     const uint32_t p0 = static_cast<uint32_t>(pair0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -281,11 +321,15 @@ __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4],
       }
       km[i] = (w << 1) & 0x00fe00feu;
       kr[i] = (w >> 6) & 0x00fe00feu;
+      wr[i] = w;
     }
     cm = make_uint2(encode4_stochastic<true>(x[0], x[1], km[0], km[1]),
                     encode4_stochastic<true>(x[2], x[3], km[2], km[3]));
-    cr = make_uint2(encode4_stochastic<false>(y[0], y[1], kr[0], kr[1]),
-                    encode4_stochastic<false>(y[2], y[3], kr[2], kr[3]));
+    if (SR == kRoot7)
+      cr = make_uint2(encode4_stochastic<false>(y[0], y[1], kr[0], kr[1]),
+                      encode4_stochastic<false>(y[2], y[3], kr[2], kr[3]));
+    else
+      cr = make_uint2(encode4_root16(y[0], y[1], wr[0], wr[1]), encode4_root16(y[2], y[3], wr[2], wr[3]));
   }
 }
 
@@ -367,7 +411,7 @@ __device__ __forceinline__ void store_block_lowp(void* lowp, int lowp_dtype, int
 
 // The update of one block whose codes, scales and grads (fl(scale x), summed)
 // are in registers, and its stores.
-template <bool VEC, bool SR>
+template <bool VEC, int SR>
 __device__ __forceinline__ void update_block(float* p, uint8_t* qm, uint8_t* qr, float* ms, float* rs,
                                              unsigned short* lowp, int lowp_dtype, int left, const float (&x)[8],
                                              const float (&g)[8], uint2 cm, uint2 cr, float sm, float sr, float coef,

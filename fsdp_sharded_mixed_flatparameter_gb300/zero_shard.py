@@ -60,7 +60,8 @@ class zero_state8(ctypes.Structure):
 
 
 class zero_rounding(ctypes.Structure):
-    _fields_ = [("seed", ctypes.c_uint64), ("stream", ctypes.c_int64)]
+    _fields_ = [("seed", ctypes.c_uint64), ("stream", ctypes.c_int64), ("root_bits", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class zero_list_tensor(ctypes.Structure):
@@ -70,6 +71,7 @@ class zero_list_tensor(ctypes.Structure):
 
 
 STATE8_BLOCK = 256      # elements per scale of the 8-bit moments
+ROOT7_MAX_BETA2 = 0.99  # up to here 7 random bits for a root follow exp_avg_sq, above 16 do (zero_rounding)
 LIST_CHUNK = 1024       # elements per piece of a tensor list's work
 LIST_MAX_GROUPS = 64
 
@@ -558,11 +560,17 @@ def _state8_arg(state: State8, n: int, who: str = "state8") -> zero_state8:
     return q
 
 
-def _rounding(rounding_seed: Optional[int], stream: int):
-    """NULL (round to nearest) or the 64-bit seed and the stream of stochastic rounding."""
+def root_bits_for(beta2: float) -> int:
+    """The random bits by which an optimizer rounds the root of exp_avg_sq: 7 follow it up to
+    beta2 = 0.99, above 16 are needed."""
+    return 16 if beta2 > ROOT7_MAX_BETA2 else 7
+
+
+def _rounding(rounding_seed: Optional[int], stream: int, root_bits: int):
+    """NULL (round to nearest) or the 64-bit seed, the stream and the root's bits of stochastic rounding."""
     if rounding_seed is None:
         return None
-    return ctypes.byref(zero_rounding(int(rounding_seed) & 0xFFFFFFFFFFFFFFFF, int(stream)))
+    return ctypes.byref(zero_rounding(int(rounding_seed) & 0xFFFFFFFFFFFFFFFF, int(stream), int(root_bits), 0))
 
 
 def zero_state8_pack(exp_avg: torch.Tensor, exp_avg_sq: torch.Tensor, state8: State8, stream=None) -> None:
@@ -619,17 +627,18 @@ def zero_adamw_step8_tensors(master: torch.Tensor, state8: State8, d_table: torc
                              param_lowp: Optional[torch.Tensor], lr: float, beta1: float, beta2: float, eps: float,
                              weight_decay: float, step: int, clip: Optional[torch.Tensor] = None, stream=None,
                              acc: Optional[torch.Tensor] = None, d_scale: Optional[torch.Tensor] = None,
-                             rounding_seed: Optional[int] = None, rounding_stream: Optional[int] = None) -> None:
+                             rounding_seed: Optional[int] = None, rounding_stream: Optional[int] = None,
+                             root_bits: int = 0) -> None:
     """zero_adamw_step_tensors with the moments in 8 bits; rounding_seed: None rounds them to
     nearest, an integer seeds stochastic rounding, whose stream is rounding_stream (default:
-    shard_start)."""
+    shard_start).  root_bits: the bits drawn for a root, 7 or 16 (0: root_bits_for(beta2))."""
     n, q, lp, lowp_dt = _step8_common(master, state8, d_table, n_tensors, param_lowp, clip, acc)
     hp = zero_adamw_hparams(lr, beta1, beta2, eps, weight_decay)
     _check(lib().zero_adamw_step8_tensors(
         _dev(master, "master", torch.float32), ctypes.byref(q),
         _dev(d_table, "d_table", torch.uint8, allow_none=n_tensors == 0), n_tensors, total, _DT[grad_dtype],
         shard_start, grad_scale, _dscale(d_scale), _dev(acc, "acc", torch.float32, allow_none=True), lp, lowp_dt, n,
-        ctypes.byref(hp), step, _rounding(rounding_seed, shard_start if rounding_stream is None else rounding_stream),
+        ctypes.byref(hp), step, _rounding(rounding_seed, shard_start if rounding_stream is None else rounding_stream, root_bits),
         _dev(clip, "clip", allow_none=True), _stream(stream)))
 
 
@@ -638,15 +647,16 @@ def zero_adamw_step8_tensors_device(master: torch.Tensor, state8: State8, d_tabl
                                     param_lowp: Optional[torch.Tensor], state: torch.Tensor,
                                     clip: Optional[torch.Tensor] = None, stream=None,
                                     acc: Optional[torch.Tensor] = None, d_scale: Optional[torch.Tensor] = None,
-                                    rounding_seed: Optional[int] = None,
-                                    rounding_stream: Optional[int] = None) -> None:
-    """zero_adamw_step8_tensors with the scalars, step and skip decision of the device step state."""
+                                    rounding_seed: Optional[int] = None, rounding_stream: Optional[int] = None,
+                                    root_bits: int = 0) -> None:
+    """zero_adamw_step8_tensors with the scalars, step and skip decision of the device step state
+    (root_bits 0: 7, whatever beta2 the state has)."""
     n, q, lp, lowp_dt = _step8_common(master, state8, d_table, n_tensors, param_lowp, clip, acc)
     _check(lib().zero_adamw_step8_tensors_device(
         _dev(master, "master", torch.float32), ctypes.byref(q),
         _dev(d_table, "d_table", torch.uint8, allow_none=n_tensors == 0), n_tensors, total, _DT[grad_dtype],
         shard_start, grad_scale, _dscale(d_scale), _dev(acc, "acc", torch.float32, allow_none=True), lp, lowp_dt, n,
-        _state_arg(state), _rounding(rounding_seed, shard_start if rounding_stream is None else rounding_stream),
+        _state_arg(state), _rounding(rounding_seed, shard_start if rounding_stream is None else rounding_stream, root_bits),
         _dev(clip, "clip", allow_none=True), _stream(stream)))
 
 
@@ -760,30 +770,34 @@ def list_groups(groups: Sequence[Tuple[float, float, float, float, float]]):
 def zero_adamw_list(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float,
                     groups: Sequence[Tuple[float, float, float, float, float]], step: int,
                     clip: Optional[torch.Tensor] = None, stream=None, d_scale: Optional[torch.Tensor] = None,
-                    rounding_seed: Optional[int] = None, rounding_stream: int = 0) -> None:
+                    rounding_seed: Optional[int] = None, rounding_stream: int = 0, root_bits: int = 0) -> None:
     """One AdamW step over every tensor of a list.  d_grads: the device table of the grads
     (zero_tensor_table + device_table, in list order); groups: (lr, beta1, beta2, eps,
-    weight_decay) of each parameter group, or list_groups() of them made once."""
+    weight_decay) of each parameter group, or list_groups() of them made once.  rounding_seed,
+    root_bits: as for zero_adamw_step8_tensors (0: by the groups' largest beta2)."""
     if len(groups) != tl.n_groups:
         raise ValueError(f"{len(groups)} groups given, the list has {tl.n_groups}")
     if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
         raise ValueError("clip is smaller than zero_norm_result")
     hp = groups if isinstance(groups, ctypes.Array) else list_groups(groups)
     _check(lib().zero_adamw_list(*_list_args(tl, d_grads, grad_dtype, grad_scale, d_scale), hp, len(groups), step,
-                                 _rounding(rounding_seed, rounding_stream), _dev(clip, "clip", allow_none=True), _stream(stream)))
+                                 _rounding(rounding_seed, rounding_stream, root_bits),
+                                 _dev(clip, "clip", allow_none=True), _stream(stream)))
 
 
 def zero_adamw_list_device(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float,
                            states: torch.Tensor, clip: Optional[torch.Tensor] = None, stream=None,
                            d_scale: Optional[torch.Tensor] = None, rounding_seed: Optional[int] = None,
-                           rounding_stream: int = 0) -> None:
-    """zero_adamw_list with the groups' scalars, step and skip decision from device step states."""
+                           rounding_stream: int = 0, root_bits: int = 0) -> None:
+    """zero_adamw_list with the groups' scalars, step and skip decision from device step states
+    (root_bits 0: 7, whatever beta2 they have)."""
     if states.numel() * states.element_size() < tl.n_groups * DEVICE_STATE_BYTES:
         raise ValueError("states is smaller than one zero_adamw_device_state per group")
     if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
         raise ValueError("clip is smaller than zero_norm_result")
     _check(lib().zero_adamw_list_device(*_list_args(tl, d_grads, grad_dtype, grad_scale, d_scale),
-                                        _dev(states, "states"), tl.n_groups, _rounding(rounding_seed, rounding_stream),
+                                        _dev(states, "states"), tl.n_groups,
+                                        _rounding(rounding_seed, rounding_stream, root_bits),
                                         _dev(clip, "clip", allow_none=True), _stream(stream)))
 
 

@@ -510,8 +510,20 @@ zero_status zero_adamw_step_tensors_device(float* d_master, float* d_exp_avg, fl
  * power of two >= 2^-126 with max|x| <= 448 S over the block, so x / S and
  * c * S are exact and the code's rounding is the only one:
  *   nearest     c = x / S rounded to nearest even on the e4m3 grid;
- *   stochastic  |c| = floor((floor(128 |x/S| / u) + k) / 128) u, u the grid's
- *               spacing at |x/S| and k in [0, 128) drawn for the element.
+ *   stochastic  with u the grid's spacing at |x/S|, by 7 bits
+ *               |c| = floor((floor(128 |x/S| / u) + k) / 128) u, k in [0, 128)
+ *               drawn for the element, or by 16 bits
+ *               |c| = floor(|x/S| / u + (h + 1/2) / 65536) u, h in [0, 65536).
+ * The 16 bits keep the mean.  The 7 bits are u / 256 low on average and do not
+ * see moves of less than u / 128: exp_avg, always rounded by 7, comes out
+ * 0.7 % low at beta1 = 0.95 and 3 % at 0.99; a root rounded by 7 leaves
+ * exp_avg_sq within 3 % up to beta2 = 0.99, but at 0.68 of itself after 8000
+ * steps at 0.999 and at 0.24 at 0.9999; rounded by 16 it stays within 5 % at any
+ * beta2 (the square of its own noise).  Hence ZERO_ROOT7_MAX_BETA2.  To nearest,
+ * neither moment follows its recurrence: one that moves by less than half a
+ * spacing (3 to 6 %) a step stays where it is (exp_avg_sq after 8000 steps: 4.9
+ * times too large at beta2 = 0.95, 0.19 of itself at 0.999).
+ * Nearest is for conversions, single steps and comparisons, not for a run.
  * A root above zero is raised to the grid's least value 2^-9 first, so it
  * never becomes zero.  A block whose max|x| is not finite (or >= 2^126) has
  * S = NaN: all its elements read back as NaN.  Codes of zero with scales of
@@ -521,10 +533,12 @@ zero_status zero_adamw_step_tensors_device(float* d_master, float* d_exp_avg, fl
  * h), h = H(lo32 step ^ h), h = H(stream ^ h), and i the index of a pair of
  * elements 2i, 2i + 1: h = H(hi32 i ^ h), w = H(lo32 i ^ h).  The low half
  * of w is the even element's, the high half the odd one's; of each, bits 0..6
- * round exp_avg, bits 7..13 the root.  stream: the low 32 bits of
- * zero_rounding.stream, for a list of that plus the tensor's number.
+ * round exp_avg, bits 7..13 (7 bits) or the whole half (16) the root.  stream:
+ * the low 32 bits of zero_rounding.stream, for a list of that plus the tensor's
+ * number.
  * --------------------------------------------------------------------- */
 #define ZERO_STATE8_BLOCK 256
+#define ZERO_ROOT7_MAX_BETA2 0.99
 
 /* The 8-bit moments of n elements (device memory): n codes and
  * ceil(n / 256) scales each. */
@@ -539,6 +553,10 @@ typedef struct zero_state8 {
 typedef struct zero_rounding {
   uint64_t seed;
   int64_t stream; /* its low 32 bits: ranks, or lists, that share a seed take different streams */
+  int32_t root_bits; /* bits drawn for the root: 7, 16, or 0: 16 if the call's (a group's) beta2 is above
+                        ZERO_ROOT7_MAX_BETA2, else 7; the calls with a device state, which do not
+                        have it on the host, take 0 as 7 */
+  int32_t reserved;  /* 0 */
 } zero_rounding;
 
 /* zero_state8_pack -- device.
@@ -576,8 +594,8 @@ zero_status zero_state8_unpack(const zero_state8* q, int64_t n, float* d_exp_avg
  * 16 bytes per parameter with 16-bit grads and copy, where the fp32 state
  * takes 28.  Any element alignment is accepted; the fast path needs master
  * and d_acc 32-byte and the codes 8-byte aligned.
- * Errors: those of zero_adamw_step_tensors, and NULL q or NULL q buffers
- * with n > 0. */
+ * Errors: those of zero_adamw_step_tensors, NULL q or NULL q buffers with
+ * n > 0, and a root_bits of rounding other than 0, 7 and 16. */
 zero_status zero_adamw_step8_tensors(float* d_master, const zero_state8* q, const zero_tensor* d_table,
                                      int32_t n_tensors, int64_t total, zero_dtype grad_dtype, int64_t shard_start,
                                      float grad_scale, const float* d_grad_scale, const float* d_acc,

@@ -1,0 +1,53 @@
+"""Stochastic rounding of 8-bit moments without a GPU: what its two forms do to a recurrence, and the refusals of a bad one."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+from fsdp_sharded_mixed_flatparameter_gb300 import zero_shard as zs
+import _ref8 as R
+import _ref8_runs as L
+from test_state8_cpu import call_list, call_step8
+
+
+def test_halves_hold_the_seven_bit_draws():
+    h = L.halves(0x123456789ABCDEF1, 7, 5, 1001, first=3).astype(np.uint64)
+    km, kr = R.draws(0x123456789ABCDEF1, 7, 5, 1001, first=3)
+    np.testing.assert_array_equal(h & np.uint64(127), km)
+    np.testing.assert_array_equal((h >> np.uint64(7)) & np.uint64(127), kr)
+
+
+def test_sixteen_bit_rounding_has_the_right_mean():
+    # over the 65536 values of h the mean is x to 2^-17 of the spacing; the smallest code is not undercut
+    h = np.arange(65536.0)
+    for x in np.concatenate([np.random.default_rng(0).uniform(0, 448, 60), np.geomspace(2.0 ** -9, 2.0 ** -5, 30), [448.0]]):
+        u = 2.0 ** (np.floor(np.log2(max(x, 2.0 ** -6))) - 3)
+        assert abs(L.grid16(np.full(65536, x), h).mean() - x) <= u * 2.0 ** -17 * 1.001
+    assert L.grid16(np.array([0.0, 1e-6]), np.array([65535.0, 0.0])).tolist() == [0.0, 2.0 ** -9]
+
+
+@pytest.mark.parametrize("kind", ["normal", "constant"])
+@pytest.mark.parametrize("b2", [0.9, 0.95, 0.99, 0.999, 0.9999])
+def test_sixteen_bits_follow_exp_avg_sq(b2, kind):
+    v, w = L.follow(1500, b2, kind, 2048, seed=3)
+    assert 0.98 <= w.mean() / v.mean() <= 1.02 + 1 / 16  # (L.run_bounds)
+
+
+@pytest.mark.parametrize("bits", [1, 8, 17, -1])
+def test_bad_root_bits_are_refused(bits):
+    bad = zs.zero_rounding(1, 0, bits, 0)
+    assert call_step8(seed=ctypes.byref(bad)) == zs.ZERO_EINVAL
+    assert call_list(seed=ctypes.byref(bad)) == zs.ZERO_EINVAL
+
+
+def test_the_rule_for_the_bits():
+    assert [zs.root_bits_for(b) for b in (0.0, 0.95, 0.99, 0.9901, 0.999)] == [7, 7, 7, 16, 16]
+    header = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "zero_shard.h")).read()
+    assert f"#define ZERO_ROOT7_MAX_BETA2 {zs.ROOT7_MAX_BETA2}\n" in header
+
+
+def test_reserved_fields_are_refused():
+    bad = zs.zero_rounding(1, 0, 16, 1)
+    assert call_step8(seed=ctypes.byref(bad)) == zs.ZERO_EINVAL
+    assert call_list(seed=ctypes.byref(bad)) == zs.ZERO_EINVAL
