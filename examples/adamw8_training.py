@@ -5,7 +5,8 @@
 One checkpoint, four ways to go on:
 
 * TensorListAdamW, fp32 moments: one launch steps every tensor, matrices with weight decay, biases without;
-* TensorListAdamW, 8-bit moments (nearest, and stochastic rounding): the checkpoint's moments are packed on loading;
+* TensorListAdamW, 8-bit moments, rounded stochastically and, to compare, to nearest: the checkpoint's moments are
+  packed on loading;
 * FlatShardAdamW, 8-bit moments: the same parameters as one flat shard, the grads read where backward left them.
 
 Prints the loss at the end and the optimizer's bytes per parameter for each.
@@ -83,7 +84,7 @@ def run(steps=200, device="cuda:0", say=print):
     say(f"loss {start:.4f} at the start, {reached:.4f} after {steps} steps with fp32 moments")
 
     found = {"start": start, "reached": reached}
-    for name, kw in (("fp32", {}), ("8 bits, nearest", dict(state_bits=8)),
+    for name, kw in (("fp32", {}), ("8 bits, nearest", dict(state_bits=8, rounding_seed=None)),
                      ("8 bits, stochastic", dict(state_bits=8, rounding_seed=0))):
         opt, params = tensor_list([p.clone() for p in masters], **kw)
         opt.load_state_dict(checkpoint)

@@ -11,7 +11,7 @@ fp32 moments the result is FlatShardAdamW's bit for bit, tensor by tensor.
 from __future__ import annotations
 
 import math
-from typing import List, Optional, Sequence, Tuple
+from typing import List, Optional, Sequence, Tuple, Union
 
 import numpy as np
 import torch
@@ -26,11 +26,12 @@ class TensorListAdamW(GradTables):
     """masters: contiguous fp32 CUDA tensors of any shape, updated in place.  lowp: None,
     or per tensor None or its bf16 / f16 copy.  groups: a dict per parameter group with any
     of lr, betas, eps, weight_decay (the rest from the keyword arguments); group_of: each
-    tensor's group (default: all in group 0).  rounding_seed (8 bits only): None rounds
-    the moments to nearest, an integer seeds stochastic rounding; lists that share a seed
-    take rounding_streams that are further apart than they have tensors.  How many random
-    bits a root takes goes by the groups' largest beta2 (root_bits_for); a captured graph
-    keeps what they were at its capture.
+    tensor's group (default: all in group 0).  rounding_seed (8 bits only): an integer seeds
+    stochastic rounding of the moments (default 0); None rounds them to nearest, by which they
+    do not follow their recurrences over a run (optimizer.py).  Lists that share a seed take
+    rounding_streams that are further apart than they have tensors.  How many random bits a
+    root takes goes by the groups' largest beta2 (root_bits_for); a captured graph keeps what
+    they were at its capture.
 
     The moments live in storages of this object, tensor i's at elements offsets[i] ..
     offsets[i] + numels[i]: ``exp_avg`` and ``exp_avg_sq`` (fp32), or ``state8`` (8 bits:
@@ -39,12 +40,10 @@ class TensorListAdamW(GradTables):
     def __init__(self, masters: Sequence[torch.Tensor], *, lowp: Optional[Sequence[Optional[torch.Tensor]]] = None,
                  groups: Optional[Sequence[dict]] = None, group_of: Optional[Sequence[int]] = None, lr: float = 1e-4,
                  betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
-                 max_norm: float = math.inf, state_bits: int = 32, rounding_seed: Optional[int] = None,
+                 max_norm: float = math.inf, state_bits: int = 32,
+                 rounding_seed: Union[int, None, str] = zs.DEFAULT_SEED,
                  rounding_stream: int = 0, capturable: bool = False):
-        if state_bits not in (8, 32):
-            raise ValueError("state_bits must be 32 or 8")
-        if rounding_seed is not None and state_bits == 32:
-            raise ValueError("a rounding_seed needs state_bits=8")
+        rounding_seed = zs.rounding_choice(state_bits, rounding_seed)
         self.masters = list(masters)
         if not self.masters:
             raise ValueError("an empty tensor list")

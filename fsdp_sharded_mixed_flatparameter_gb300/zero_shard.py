@@ -560,6 +560,23 @@ def _state8_arg(state: State8, n: int, who: str = "state8") -> zero_state8:
     return q
 
 
+DEFAULT_SEED = "default"
+
+
+def rounding_choice(state_bits: int, rounding_seed):
+    """The rounding_seed that an optimizer keeps: stochastic rounding with seed 0 unless told
+    otherwise (8 bits), None with 32."""
+    if state_bits not in (8, 32):
+        raise ValueError("state_bits must be 32 or 8")
+    if isinstance(rounding_seed, str):
+        if rounding_seed != DEFAULT_SEED:
+            raise ValueError("rounding_seed must be an integer or None")
+        return 0 if state_bits == 8 else None
+    if rounding_seed is not None and state_bits == 32:
+        raise ValueError("a rounding_seed needs state_bits=8")
+    return rounding_seed
+
+
 def root_bits_for(beta2: float) -> int:
     """The random bits by which an optimizer rounds the root of exp_avg_sq: 7 follow it up to
     beta2 = 0.99, above 16 are needed."""

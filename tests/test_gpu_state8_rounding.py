@@ -116,6 +116,20 @@ def run_list(steps, b2, kind):
     return host(opt.state8)
 
 
+def test_the_default_is_stochastic_with_seed_0():
+    sizes = [700, 3000]
+    x = [(torch.randn(n, generator=gen(n)) * 1e-2).cuda() for n in sizes]
+    kw = dict(lr=1e-2, state_bits=8)
+    a, b, c = (pkg.TensorListAdamW([torch.zeros(n, device="cuda") for n in sizes], **kw, **more) for more in (
+        {}, dict(rounding_seed=0), dict(rounding_seed=None)))
+    d, e = (pkg.FlatShardAdamW(sizes, device="cuda", **kw, **more) for more in ({}, dict(rounding_seed=0)))
+    for o in (a, b, c):
+        o.step(x)
+    for o in (d, e):
+        o.step_tensors(x)
+    assert same(a.state8, b.state8) and not same(a.state8, c.state8) and same(d.state8, e.state8)
+
+
 @pytest.mark.parametrize("run", [run_flat, run_list])
 @pytest.mark.parametrize("kind", ["normal", "constant"])
 @pytest.mark.parametrize("b2", [0.95, 0.99, 0.999, 0.9999])

@@ -1,10 +1,12 @@
 """Stochastic rounding of 8-bit moments without a GPU: what its two forms do to a recurrence, and the refusals of a bad one."""
 import ctypes
+import inspect
 import os
 
 import numpy as np
 import pytest
 
+import fsdp_sharded_mixed_flatparameter_gb300 as pkg
 from fsdp_sharded_mixed_flatparameter_gb300 import zero_shard as zs
 import _ref8 as R
 import _ref8_runs as L
@@ -32,6 +34,21 @@ def test_sixteen_bit_rounding_has_the_right_mean():
 def test_sixteen_bits_follow_exp_avg_sq(b2, kind):
     v, w = L.follow(1500, b2, kind, 2048, seed=3)
     assert 0.98 <= w.mean() / v.mean() <= 1.02 + 1 / 16  # (L.run_bounds)
+
+
+def test_the_optimizers_round_stochastically_unless_told_otherwise():
+    for kw, want in (({}, 0), (dict(rounding_seed=7), 7), (dict(rounding_seed=None), None)):
+        assert pkg.FlatShardAdamW([300], device="cpu", state_bits=8, **kw).rounding_seed == want
+        assert pkg.ZeroDataPlane([300], device="cpu", state_bits=8, **kw).opt.rounding_seed == want
+        units = pkg.ZeroUnits([[300], [5]], device="cpu", state_bits=8, **kw)
+        assert [u.opt.rounding_seed for u in units.units] == [want, want]
+    assert pkg.FlatShardAdamW([300], device="cpu").rounding_seed is None
+    assert zs.rounding_choice(8, zs.DEFAULT_SEED) == 0 and zs.rounding_choice(32, None) is None
+    for bits, seed in ((32, 1), (16, None), (8, "nearest")):
+        with pytest.raises(ValueError):
+            zs.rounding_choice(bits, seed)
+    default = inspect.signature(pkg.TensorListAdamW).parameters["rounding_seed"].default
+    assert default == zs.DEFAULT_SEED
 
 
 @pytest.mark.parametrize("bits", [1, 8, 17, -1])
