@@ -486,20 +486,25 @@ class FlatShardAdamW(GradTables):
     def state_dict(self) -> dict:
         """The rank's optimizer state on the host: step counter, fp32 master /
         exp_avg / exp_avg_sq (or state8) and the low-precision copy (a flat shard each)."""
-        sd = {"t": self.t, "start": self.start, "end": self.end, "master": self.master.cpu()}
+        sd = {"t": self.t, "start": self.start, "end": self.end, "master": self.master.detach().cpu()}
         if self.state_bits == 8:
             sd["state8"] = tuple(x.cpu() for x in self.state8)
         else:
             sd["exp_avg"], sd["exp_avg_sq"] = self.exp_avg.cpu(), self.exp_avg_sq.cpu()
         if self.lowp is not None:
-            sd["lowp"] = self.lowp.cpu()
+            sd["lowp"] = self.lowp.detach().cpu()
         return sd
 
+    @torch.no_grad()  # the master and the low-precision copy may be parameters
     def load_state_dict(self, sd: dict) -> None:
         """Restore a checkpoint of this shard; moments of the other width (fp32 / 8 bits) are
-        converted, 32-bit ones rounded to nearest."""
-        if (sd["start"], sd["end"]) != (self.start, self.end):
+        converted, 32-bit ones rounded to nearest.  A checkpoint that does not fit is refused
+        before anything is written."""
+        if (sd["start"], sd["end"]) != (self.start, self.end) or sd["master"].numel() != self.n:
             raise ValueError("state belongs to another shard")
+        if self.lowp is not None and "lowp" in sd and sd["lowp"].numel() != self.n:
+            raise ValueError("the checkpoint's low-precision copy is not the shard's")
+        zs.check_moments(sd, self.n)
         self.t = int(sd["t"])
         self.master.copy_(sd["master"])
         zs.load_moments(sd, self.state8, self.exp_avg, self.exp_avg_sq, self.device)

@@ -610,6 +610,21 @@ def zero_state8_unpack(state8: State8, exp_avg: torch.Tensor, exp_avg_sq: torch.
                                     _dev(exp_avg_sq, "exp_avg_sq", torch.float32), _stream(stream)))
 
 
+def check_moments(sd: dict, n: int) -> None:
+    """Refuse a checkpoint whose moments are missing or not those of n elements."""
+    saved = sd.get("state8")
+    if saved is None:
+        names, got, want = ("exp_avg", "exp_avg_sq"), (sd.get("exp_avg"), sd.get("exp_avg_sq")), (n, n)
+    else:
+        b = state8_blocks(n)
+        names, got, want = State8._fields, tuple(saved), (n, b, n, b)
+    if len(got) != len(want):
+        raise ValueError("state8 of a checkpoint has four tensors")
+    for nm, t, k in zip(names, got, want):
+        if t is None or t.numel() != k:
+            raise ValueError(f"the checkpoint's {nm} does not have the {k} elements expected")
+
+
 def load_moments(sd: dict, state8: Optional[State8], exp_avg: Optional[torch.Tensor],
                  exp_avg_sq: Optional[torch.Tensor], device) -> None:
     """Copy a checkpoint's moments (fp32 exp_avg / exp_avg_sq, or state8) into an optimizer's,

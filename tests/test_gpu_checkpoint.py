@@ -1,0 +1,63 @@
+"""Checkpoints of optimizers over parameters that require grad, on the GPU."""
+import pytest
+import torch
+
+import fsdp_sharded_mixed_flatparameter_gb300 as pkg
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(40, 33), (7,), (1500,)]
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def parameters(dtype, seed=0):
+    return [torch.nn.Parameter(torch.randn(s, generator=gen(seed + i)).to(dtype).cuda()) for i, s in enumerate(SHAPES)]
+
+
+def grads(k):
+    return [(torch.randn(s, generator=gen(50 * k + i)) * 1e-2).bfloat16().cuda() for i, s in enumerate(SHAPES)]
+
+
+def optimizer(bits, seed=0, **kw):
+    return pkg.TensorListAdamW(parameters(torch.float32, seed), lowp=parameters(torch.bfloat16, seed), lr=1e-2,
+                               state_bits=bits, **kw)
+
+
+def values(o):
+    moments = [t.view(torch.uint8) for t in o.state8] if o.state_bits == 8 else [o.exp_avg, o.exp_avg_sq]
+    return [o.t, *(t.detach().clone() for t in (*o.masters, *o.lowp, *moments))]
+
+
+def equal(a, b):
+    return a[0] == b[0] and all(torch.equal(x, y) for x, y in zip(a[1:], b[1:]))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_list_of_parameters_is_restored(bits):
+    a, b = optimizer(bits), optimizer(bits, seed=9)
+    a.step(grads(1))
+    sd = a.state_dict()
+    assert not any(t.requires_grad for t in sd["masters"])
+    b.load_state_dict(sd)
+    assert equal(values(a), values(b)) and all(p.requires_grad and p.is_leaf for p in b.masters + b.lowp)
+    for o in (a, b):
+        o.step(grads(2))
+    assert equal(values(a), values(b)) and a.t == 2
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_list_checkpoint_that_does_not_fit_changes_nothing(bits):
+    a = optimizer(bits)
+    a.step(grads(1))
+    sd = a.state_dict()
+    name = "state8" if bits == 8 else "exp_avg"
+    for bad in ({**sd, "numels": sd["numels"][:-1]}, {**sd, "masters": sd["masters"][:-1]}, {**sd, name: sd[name][:-1]},
+                {k: v for k, v in sd.items() if k != name}):
+        o = optimizer(bits, seed=9)
+        before = values(o)
+        with pytest.raises(ValueError):
+            o.load_state_dict(bad)
+        assert equal(before, values(o))
