@@ -191,13 +191,14 @@ class TensorListAdamW(GradTables):
     def load_state_dict(self, sd: dict, stream=None) -> None:
         """Restore a checkpoint of the same tensors.  One with moments of the other width is
         converted: 32-bit moments are packed to nearest, 8-bit ones unpacked.  The low-precision
-        copies are rewritten from the masters.  Masters and copies may require grad.  A
+        copies are rewritten from the masters.  Masters and copies may require grad.  Everything
+        is written on `stream` (default: the current one), in order with the steps there.  A
         checkpoint that does not fit is refused before anything is written."""
         if list(sd["numels"]) != list(self.numels) or [x.numel() for x in sd["masters"]] != list(self.numels):
             raise ValueError("state belongs to another tensor list")
         zs.check_moments(sd, (self.exp_avg if self.state_bits == 32 else self.state8.exp_avg).numel())
-        self.t = int(sd["t"])
         with torch.no_grad(), torch.cuda.stream(torch_stream(stream, self.device)):
+            self.t = int(sd["t"])  # on the device with capturable=True: in the stream's order too
             for p, x in zip(self.masters, sd["masters"]):
                 p.copy_(x.view(p.shape))
             for p, c in zip(self.masters, self.lowp or ()):

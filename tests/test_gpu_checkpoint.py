@@ -61,3 +61,27 @@ def test_a_list_checkpoint_that_does_not_fit_changes_nothing(bits):
         with pytest.raises(ValueError):
             o.load_state_dict(bad)
         assert equal(before, values(o))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_load_is_ordered_on_its_stream(bits):
+    # a step waits on the side stream behind a pause; the load comes after it there, another step after the load
+    s = torch.cuda.Stream()
+    a, b = (optimizer(bits, capturable=True) for _ in range(2))
+    sd = optimizer(bits, seed=9).state_dict()
+    first, second = grads(1), grads(2)
+    for o in (a, b):  # kernels loaded, tables built
+        o.step(first, stream=s)
+        o.device_table(second)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)
+    a.launch_step(first, stream=s)
+    a.load_state_dict(sd, stream=s)
+    a.launch_step(second, stream=s)
+    torch.cuda.synchronize()
+    b.launch_step(first)
+    b.load_state_dict(sd)
+    b.launch_step(second)
+    torch.cuda.synchronize()
+    assert a.t == b.t == 1 and equal(values(a), values(b))
