@@ -183,10 +183,12 @@ class ZeroDataPlane:
 
     def load_state_dict(self, sd: dict, stream=None) -> None:
         """Restore this rank's shard, then all-gather the low-precision slices so that
-        flat_param holds every rank's parameters again (every rank must call it)."""
+        flat_param holds every rank's parameters again (every rank must call it).  Both on
+        `stream` (default: the current one), in order with the steps there."""
         if (sd["world_size"], sd["rank"], sd["total"]) != (self.world_size, self.rank, self.total):
             raise ValueError("checkpoint of another layout (world size, rank or parameter count)")
-        self.opt.load_state_dict(sd)
+        with self._on(stream):
+            self.opt.load_state_dict(sd)
         self.all_gather_params(stream)
 
     def resident_bytes(self) -> int:

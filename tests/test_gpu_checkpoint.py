@@ -85,3 +85,45 @@ def test_a_load_is_ordered_on_its_stream(bits):
     b.launch_step(second)
     torch.cuda.synchronize()
     assert a.t == b.t == 1 and equal(values(a), values(b))
+
+
+@pytest.mark.parametrize("bits,capturable", [(8, False), (8, True), (32, True)])
+def test_a_data_plane_load_is_ordered_on_its_stream(bits, capturable):
+    # as above for a shard with its exchanges (one rank); the checkpoint's moments are fp32, which 8 bits convert
+    numels = [3000, 77]
+    s = torch.cuda.Stream()
+    kw = dict(device="cuda", lr=1e-2, capturable=capturable)
+    a, b = (pkg.ZeroDataPlane(numels, state_bits=bits, **kw) for _ in range(2))
+    other = pkg.ZeroDataPlane(numels, master=torch.randn(sum(numels), generator=gen(1)).cuda(), **kw)
+    other.flat_grad.copy_(torch.randn(sum(numels), generator=gen(2)))
+    other.reduce_scatter_grads()
+    other.step()
+    sd = other.state_dict()
+
+    def steps(dp, stream):
+        dp.reduce_scatter_grads(stream=stream)
+        dp.opt.launch_step(stream=stream)
+        dp.load_state_dict(sd, stream=stream)
+        dp.reduce_scatter_grads(stream=stream)
+        dp.opt.launch_step(stream=stream)
+
+    for dp in (a, b):
+        dp.flat_grad.copy_(torch.randn(sum(numels), generator=gen(3)))
+        dp.reduce_scatter_grads(stream=s)
+        dp.step(stream=s)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)
+    steps(a, s)
+    torch.cuda.synchronize()
+    steps(b, None)
+    torch.cuda.synchronize()
+    assert a.opt.t == b.opt.t
+    for x, y in zip(values_of_shard(a.opt), values_of_shard(b.opt)):
+        assert torch.equal(x, y)
+    assert torch.equal(a.flat_param, b.flat_param)
+
+
+def values_of_shard(o):
+    moments = [t.view(torch.uint8) for t in o.state8] if o.state_bits == 8 else [o.exp_avg, o.exp_avg_sq]
+    return [o.master, o.lowp, *moments]
