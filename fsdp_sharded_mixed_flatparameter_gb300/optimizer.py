@@ -529,11 +529,13 @@ def _world(group) -> int:
 def torch_stream(stream, device) -> torch.cuda.Stream:
     """A torch stream object for a stream argument of this package: None (the
     current stream of `device`), a torch.cuda.Stream, or a raw cudaStream_t
-    handle (wrapped, not owned)."""
+    handle (wrapped, not owned; 0 is the default stream)."""
     if stream is None:
         return torch.cuda.current_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream
+    if int(stream) == 0:  # ExternalStream(0) would be a new stream
+        return torch.cuda.default_stream(device)
     return torch.cuda.ExternalStream(int(stream), device=device)
 
 
