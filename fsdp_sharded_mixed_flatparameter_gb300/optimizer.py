@@ -37,11 +37,21 @@ and the update uses the rank's slice.
 from __future__ import annotations
 
 import math
-from typing import Dict, Optional, Sequence, Tuple, Union
+from typing import Dict, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import zero_shard as zs
+
+
+#: grads lists whose device tables an optimizer keeps
+KEPT_TABLES = 64
+
+
+class GradTable(NamedTuple):
+    """A grads list's device table and the handle of the stream that its memory was allocated on."""
+    table: torch.Tensor
+    stream: int
 
 
 class GradTables:
@@ -53,9 +63,35 @@ class GradTables:
         self.total = int(sum(self.numels))
         self.device = torch.device(device)
         self._registered = None
-        self._tables: Dict[tuple, Tuple[torch.Tensor, int]] = {}
+        self._tables: Dict[tuple, GradTable] = {}
+        self._captured: Dict[int, torch.Tensor] = {}  # tables that a captured graph reads, by address
 
-    def _table(self, grads: Sequence[Optional[torch.Tensor]]) -> torch.Tensor:
+    @staticmethod
+    def _keep(cache: Dict[tuple, GradTable], key: tuple, table: torch.Tensor) -> GradTable:
+        """Cache a new table, the oldest one making room."""
+        if len(cache) >= KEPT_TABLES:
+            cache.pop(next(iter(cache)))
+        hit = cache[key] = GradTable(table, zs._stream(None))
+        return hit
+
+    def _read_on(self, hit: GradTable, stream: int) -> torch.Tensor:
+        """The table, about to be read by kernels on `stream` (a handle): its memory is not
+        given out again before they are done, whatever leaves the cache meanwhile, and never
+        where they are being captured, as the graph may be replayed at any time."""
+        if stream != hit.stream or torch.cuda.is_current_stream_capturing():
+            self._read_elsewhere(hit.table, stream)
+        return hit.table  # on its own stream its memory is reused in that stream's order
+
+    def _read_elsewhere(self, table: torch.Tensor, stream: int) -> None:
+        st = torch_stream(stream, self.device)
+        with torch.cuda.stream(st):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
+            self._captured[table.data_ptr()] = table
+        else:
+            table.record_stream(st)
+
+    def _table(self, grads: Sequence[Optional[torch.Tensor]]) -> GradTable:
         # keyed by address, size and contiguity, so a cached table is only reused for
         # grads that passed the checks below when it was built
         key = tuple(None if g is None else (g.data_ptr(), g.numel(), g.is_contiguous()) for g in grads)
@@ -68,17 +104,16 @@ class GradTables:
                     raise ValueError(f"grad {i} has {g.numel()} elements, expected {n}")
             table, total = zs.zero_tensor_table(grads, self.numels)
             assert total == self.total
-            hit = (zs.device_table(table, len(grads), self.device), total)
-            if len(self._tables) > 64:
-                self._tables.clear()
-            self._tables[key] = hit
-        return hit[0]
+            hit = self._keep(self._tables, key, zs.device_table(table, len(grads), self.device))
+        return hit
 
     def device_table(self, grads: Sequence[Optional[torch.Tensor]]) -> Tuple[torch.Tensor, int, torch.dtype]:
         """The FlatParameter table of a grads list in device memory (built once per list of
         grad addresses and cached), with its tensor count and grad dtype.  Calling it before
-        a CUDA graph capture keeps the table's host-to-device copy out of the graph."""
-        return self._resolve(grads)
+        a CUDA graph capture keeps the table's host-to-device copy out of the graph; a table that
+        is read in a capture is kept as long as the optimizer."""
+        hit, count, dt = self._resolve(grads)
+        return hit.table, count, dt
 
     def register_grads(self, grads: Sequence[Optional[torch.Tensor]]) -> None:
         """Fix the per-tensor grads once (e.g. views into one flat grad storage, as
@@ -100,6 +135,15 @@ class GradTables:
                 raise ValueError("no grads given and none registered")
             return self._registered
         return self._table(grads), len(grads), self._grad_dtype(grads)
+
+    def _launch_tables(self, grads, stream):
+        """(table, tensor count, grad dtype, stream handle) for kernels launched now on `stream`."""
+        hit, count, dt = self._resolve(grads)
+        raw = zs._stream(stream)
+        table, own = hit
+        if raw != own or torch.cuda.is_current_stream_capturing():
+            self._read_elsewhere(table, raw)
+        return table, count, dt, raw
 
     def _scale_args(self, scale, loss_scale):
         """(host scale, device scale or None, non-finite flag) of a grad pass: with a
@@ -167,8 +211,8 @@ class FlatShardAdamW(GradTables):
             self._dev_state = zs.new_adamw_device_state(dev)
         self._norm_ready = False  # the grad norm's tile partials are up to date in self.ws
         self._local_buf: Optional[torch.Tensor] = None
-        self._flat_tables: Dict[tuple, torch.Tensor] = {}
-        self._grad_table: Optional[Tuple[int, torch.Tensor]] = None
+        self._flat_tables: Dict[tuple, GradTable] = {}
+        self._grad_table: Optional[Tuple[int, GradTable]] = None
         if state_bits == 8 and grad_buffer and self.device.type == "cuda":
             self._own_grad_table()  # here, not in a graph capture
 
@@ -248,10 +292,10 @@ class FlatShardAdamW(GradTables):
         factor, read on the device when the kernel runs (so a captured graph
         follows the scale), and raises its overflow flag; `scale` is ignored.
         """
-        table, count, dt = self._resolve(grads)
+        table, count, dt, raw = self._launch_tables(grads, stream)
         sc, dsc, flag = self._scale_args(scale, loss_scale)
         zs.zero_flatten_cast(table, count, self.total, dt, self.glo, self.ghi, sc, accumulate,
-                             self.grad, flag, self.ws if fuse_norm else None, stream, d_scale=dsc)
+                             self.grad, flag, self.ws if fuse_norm else None, raw, d_scale=dsc)
         self._norm_ready = fuse_norm
 
     def accum(self, flat_src: torch.Tensor, *, accumulate: bool, scale: float = 1.0, fuse_norm: bool = False,
@@ -316,8 +360,9 @@ class FlatShardAdamW(GradTables):
         if self.capturable:
             zs.zero_adamw_prepare_device(self._dev_hp, clip, self._dev_state, stream)
         if self.state_bits == 8:
-            self._update_tables(self._own_grad_table(), 1, self.grad.numel(), torch.float32, self.start - self.glo, 1.0,
-                                None, None, clip, stream)
+            table = self._read_on(self._own_grad_table(), zs._stream(stream))
+            self._update_tables(table, 1, self.grad.numel(), torch.float32, self.start - self.glo, 1.0, None, None, clip,
+                                stream)
         elif self.capturable:
             zs.zero_adamw_step_device(self.master, self.exp_avg, self.exp_avg_sq, self.shard_grad(), self.lowp,
                                       self._dev_state, clip, stream)
@@ -326,13 +371,13 @@ class FlatShardAdamW(GradTables):
                                self.betas[0], self.betas[1], self.eps, self.weight_decay, self._t + 1,
                                clip, stream)
 
-    def _own_grad_table(self) -> torch.Tensor:
+    def _own_grad_table(self) -> GradTable:
         """The one-entry table of the fp32 grad buffer (the 8-bit step reads every grad through a table)."""
         if self.grad.numel() != self.ghi - self.glo:
             raise ValueError("this step needs the grad buffer (grad_buffer=True)")
         if self._grad_table is None or self._grad_table[0] != self.grad.data_ptr():
             table = zs.device_table(zs.zero_tensor_table([self.grad])[0], 1, self.device)
-            self._grad_table = (self.grad.data_ptr(), table)
+            self._grad_table = (self.grad.data_ptr(), GradTable(table, zs._stream(None)))
         return self._grad_table[1]
 
     def _update_tables(self, table, count: int, total: int, dt, shard_start: int, scale: float, d_scale, acc, clip,
@@ -414,8 +459,8 @@ class FlatShardAdamW(GradTables):
     def launch_step_tensors(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, scale: float = 1.0,
                             stream=None, process_group=None, accumulated: bool = False, loss_scale=None) -> None:
         """Enqueue step_tensors() without waiting (capturable with registered grads)."""
-        table, count, dt = self._resolve(grads)
-        self._launch_direct(table, count, self.total, dt, self.glo, self.ghi, self.start, scale, accumulated, stream,
+        table, count, dt, raw = self._launch_tables(grads, stream)
+        self._launch_direct(table, count, self.total, dt, self.glo, self.ghi, self.start, scale, accumulated, raw,
                             process_group, loss_scale)
 
     def step_flat(self, flat_src: torch.Tensor, *, scale: float = 1.0, stream=None, process_group=None,
@@ -433,14 +478,19 @@ class FlatShardAdamW(GradTables):
                          accumulated: bool = False, loss_scale=None) -> None:
         """Enqueue step_flat() without waiting (capturable once device_flat_table(flat_src)
         has been called outside the capture)."""
-        table = self.device_flat_table(flat_src)
+        hit = self._flat_table(flat_src)
+        raw = zs._stream(stream)
+        table = self._read_on(hit, raw)
         span = self.ghi - self.glo
-        self._launch_direct(table, 1, span, flat_src.dtype, 0, span, self.start - self.glo, scale, accumulated, stream,
+        self._launch_direct(table, 1, span, flat_src.dtype, 0, span, self.start - self.glo, scale, accumulated, raw,
                             process_group, loss_scale)
 
     def device_flat_table(self, flat_src: torch.Tensor) -> torch.Tensor:
         """The one-entry tensor table of a flat grad over the grad range, in device memory
         (built once per address and cached; call it before a CUDA graph capture)."""
+        return self._flat_table(flat_src).table
+
+    def _flat_table(self, flat_src: torch.Tensor) -> GradTable:
         span = self.ghi - self.glo
         if flat_src.numel() != span or flat_src.dim() != 1:
             raise ValueError(f"flat_src must be 1-D with the grad range's {span} elements")
@@ -449,10 +499,7 @@ class FlatShardAdamW(GradTables):
         if hit is None:
             table, total = zs.zero_tensor_table([flat_src], [span])
             assert total == span
-            hit = zs.device_table(table, 1, self.device)
-            if len(self._flat_tables) > 64:
-                self._flat_tables.clear()
-            self._flat_tables[key] = hit
+            hit = self._keep(self._flat_tables, key, zs.device_table(table, 1, self.device))
         return hit
 
     def _launch_direct(self, table, count: int, total: int, dt, lo: int, hi: int, shard_start: int, scale: float,

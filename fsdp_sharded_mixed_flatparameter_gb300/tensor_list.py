@@ -143,7 +143,7 @@ class TensorListAdamW(GradTables):
         None: the registered ones.  loss_scale: a DeviceLossScale, whose unscale factor
         replaces `scale`.  norm_result: a zero_norm_result computed elsewhere (one clip over
         several optimizers): used as is, no norm is computed."""
-        table, count, dt = self._resolve(grads)
+        table, count, dt, stream = self._launch_tables(grads, stream)
         sc, dsc, flag = self._scale_args(scale, loss_scale)
         clip = norm_result
         if clip is None:

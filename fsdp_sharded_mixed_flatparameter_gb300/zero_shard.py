@@ -196,6 +196,8 @@ def _grad_ptr(t: torch.Tensor, name: str) -> int:
 
 
 def _stream(stream) -> int:
+    if type(stream) is int:
+        return stream
     if stream is None:  # the current stream's handle, without a Stream object around it
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
@@ -702,6 +704,7 @@ class TensorList(NamedTuple):
     state_bits: int
     n_groups: int
     lowp_dtype: Optional[torch.dtype]
+    head: tuple                # the C entries' arguments that describe the list
 
 
 _LIST_ENTRY = np.dtype([(nm, np.uint64 if ct is ctypes.c_void_p else np.int64 if ct is ctypes.c_int64 else np.int32)
@@ -721,8 +724,9 @@ def make_tensor_list(columns: dict, numels: Sequence[int], group_of: Optional[Se
         entries["group"] = group_of
     first = np.zeros(n + 1, dtype=np.int32)
     _check(lib().zero_list_chunks(entries.ctypes.data, n, n_groups, state_bits, first.ctypes.data, None))
-    return TensorList(torch.from_numpy(entries.view(np.uint8)).to(device), torch.from_numpy(first).to(device),
-                      int(first[-1]), tuple(numels), state_bits, n_groups, lowp_dtype)
+    d_entries, d_first = torch.from_numpy(entries.view(np.uint8)).to(device), torch.from_numpy(first).to(device)
+    head = (d_entries.data_ptr(), n, d_first.data_ptr(), int(first[-1]), state_bits)
+    return TensorList(d_entries, d_first, int(first[-1]), tuple(numels), state_bits, n_groups, lowp_dtype, head)
 
 
 def list_masters(masters: Sequence[torch.Tensor], lowp: Optional[Sequence[Optional[torch.Tensor]]],
@@ -789,8 +793,7 @@ def zero_tensor_list(masters: Sequence[torch.Tensor], states: Sequence[tuple],
 def _list_args(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float, d_scale):
     if d_grads.numel() < len(tl.numels) * TENSOR_ENTRY_BYTES:
         raise ValueError("d_grads holds fewer entries than the list")
-    return (tl.entries.data_ptr(), len(tl.numels), tl.first_chunk.data_ptr(), tl.n_chunks, tl.state_bits,
-            _dev(d_grads, "d_grads", torch.uint8), _DT[grad_dtype], grad_scale,
+    return (*tl.head, _dev(d_grads, "d_grads", torch.uint8), _DT[grad_dtype], grad_scale,
             None if d_scale is None else _dscale(d_scale), ZERO_BF16 if tl.lowp_dtype is None else _DT[tl.lowp_dtype])
 
 
