@@ -47,8 +47,9 @@ __device__ __forceinline__ void list8_block(const zero_list_tensor& t, const voi
   const uint2 cm = load_codes<VEC>(qm, left), cr = load_codes<VEC>(qr, left);
   const float sm = *ms, sr = *rs;
   load_block_grad<DT, VEC>(grad, k, rest, gscale, g);
-  update_block<VEC, SR>(pk, qm, qr, ms, rs, t.lowp == nullptr ? nullptr : static_cast<unsigned short*>(t.lowp) + k,
-                        lowp_dtype, left, p, g, cm, cr, sm, sr, coef, s, key, k >> 1);
+  update_block<VEC, SR, kAnyRoots>(pk, qm, qr, ms, rs,
+                                   t.lowp == nullptr ? nullptr : static_cast<unsigned short*>(t.lowp) + k, lowp_dtype,
+                                   left, p, g, cm, cr, sm, sr, coef, s, key, k >> 1);
 }
 
 template <int DT, int SR>

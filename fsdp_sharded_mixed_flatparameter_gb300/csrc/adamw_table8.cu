@@ -87,9 +87,9 @@ __device__ __forceinline__ void table8_full(float* p, const zero_state8& q, cons
 #pragma unroll
     for (int j = 0; j < 8; ++j) g[j] = __fadd_rn(ar[j], g[j]);
   }
-  update_block<true, SR>(p + k, q.exp_avg + k, q.root + k, q.exp_avg_scale + b, q.root_scale + b,
-                         lowp == nullptr ? nullptr : static_cast<unsigned short*>(lowp) + k, lowp_dtype, kBlock8, pr, g,
-                         cm, cr, sm, sr, coef, s, key, k >> 1);
+  update_block_split<true, SR>(p + k, q.exp_avg + k, q.root + k, q.exp_avg_scale + b, q.root_scale + b,
+                               lowp == nullptr ? nullptr : static_cast<unsigned short*>(lowp) + k, lowp_dtype, kBlock8,
+                               pr, g, cm, cr, sm, sr, coef, s, key, k >> 1);
 }
 
 // Any part: the last one, or unaligned state.
@@ -117,9 +117,9 @@ __device__ __forceinline__ void table8_any(float* p, const zero_state8& q, const
       g[j] = e < left ? stage[stage_idx(q0 + e)] : 0.0f;
       if (acc != nullptr && e < left) g[j] = __fadd_rn(acc[k + e], g[j]);
     }
-    update_block<false, SR>(p + k, q.exp_avg + k, q.root + k, q.exp_avg_scale + b, q.root_scale + b,
-                            lowp == nullptr ? nullptr : static_cast<unsigned short*>(lowp) + k, lowp_dtype, left, pr, g,
-                            cm, cr, sm, sr, coef, s, key, k >> 1);
+    update_block_split<false, SR>(p + k, q.exp_avg + k, q.root + k, q.exp_avg_scale + b, q.root_scale + b,
+                                  lowp == nullptr ? nullptr : static_cast<unsigned short*>(lowp) + k, lowp_dtype, left,
+                                  pr, g, cm, cr, sm, sr, coef, s, key, k >> 1);
   }
 }
 

@@ -91,7 +91,7 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 // g + (v - g^2) y / 2, whose residual is exact in an fma.  Its error before the
 // last rounding is of the order of y's squared, so it is the correctly rounded
 // root but for about one v in a million (1 ulp off there).  Zero gives zero;
-// below the normal range (2^-126) it is positive but too small.
+// below the normal range (2^-126) it is positive but too small (kLift).
 __device__ __forceinline__ F2 root2(F2 v) {
   float v0, v1;
   unpair(v, v0, v1);
@@ -174,14 +174,14 @@ __device__ __forceinline__ uint32_t encode4_root16(F2 a, F2 b, uint32_t w0, uint
 // order like their bits, NaN above all).  max|x| with a fraction above 1.75 =
 // 448/256 needs the next power.  A block whose largest value is not finite,
 // or 2^126 and more (where 1/S would leave the normal range), gets S = NaN:
-// every element reads back as NaN.
-__device__ __forceinline__ void block_scale(uint32_t amax, float& s, float& inv) {
+// every element reads back as NaN.  `least`: the exponent field of the least S.
+__device__ __forceinline__ void block_scale(uint32_t amax, int least, float& s, float& inv) {
   if (amax >= 0x7e800000u) {
     s = __uint_as_float(0x7fffffffu);
     inv = 0.0f;
     return;
   }
-  const int e = max(static_cast<int>((amax + 0x1fffffu) >> 23) - 8, 1);
+  const int e = max(static_cast<int>((amax + 0x1fffffu) >> 23) - 8, least);
   s = __uint_as_float(static_cast<uint32_t>(e) << 23);
   inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 }
@@ -209,32 +209,58 @@ __device__ __forceinline__ uint32_t rounding_key(const RoundingBase& rnd, const 
 }
 
 // ----------------------------------------------------------------- update
+// Blocks of small roots are computed 2^40 times larger: v as 2^80 v, its factors
+// lifted (powers of two: no other rounding), and r's factor and its scale take
+// 2^-40.  Else S^2 beta2 would be zero from S = 2^-75 on, where v is not yet, and
+// root2 is too small for a v under 2^-126.  A block needs it where S^2 beta2 <
+// 2^-100: from there up a new v under 2^-126 has a root under 2^-10 of the new S
+// and is raised to the smallest code, whatever root2 gives; its r itself, under
+// 2^-63, is lost in eps unless eps is under 2^-34, and then every block needs it.
+// A block that could overflow by it (grads of 2^20 and more, S of 2^14 and more
+// unless beta2 is 0) is left as it is.
+constexpr float kLift = 0x1p40f;
+constexpr int kLiftLog2 = 40;
+
+__device__ __forceinline__ uint32_t warp_amax(const F2 (&x)[4]);
+
+__device__ __forceinline__ bool small_roots(const AdamScalars& s, float sr) {
+  return __fmul_rn(__fmul_rn(sr, sr), s.b2) < 0x1p-100f || s.eps < 0x1p-34f;
+}
+
+__device__ __forceinline__ bool liftable(const AdamScalars& s, float sr, const float (&g)[8], float coef) {
+  const F2 x[4] = {pair(g[0], g[1]), pair(g[2], g[3]), pair(g[4], g[5]), pair(g[6], g[7])};
+  return __fmul_rn(__uint_as_float(warp_amax(x)), fabsf(coef)) < 0x1p20f && (sr < 0x1p14f || s.b2 == 0.0f);
+}
+
 // The update's factors for one block, each twice.  The decoded moments enter
 // only as m beta1 = c (S beta1) and v beta2 = c^2 (S^2 beta2), which with S a
-// power of two are the same numbers as fl(m beta1) and fl(fl(r^2) beta2) as
-// long as S^2 beta2 is a normal number: in blocks whose largest root is above
-// 2^-54.  Below, exp_avg_sq (under 10^-32) keeps fewer bits than 24.
+// power of two are the same numbers as fl(m beta1) and fl(fl(r^2) beta2), as
+// these factors and r^2 are normal numbers (kLift; S beta1 loses a bit or two in
+// blocks of S = 2^-126).
 struct Factors8 {
   F2 coef, decay, mb1, omb1, vb2, omb2, inv_bc2, eps, step;
 };
 
-__device__ __forceinline__ Factors8 factors8(const AdamScalars& s, float sm, float sr, float coef) {
+__device__ __forceinline__ Factors8 factors8(const AdamScalars& s, float sm, float sr, float coef, bool lift) {
   Factors8 f;
+  if (lift) sr = fminf(__fmul_rn(sr, kLift), 0x1p54f);  // larger only where beta2 is 0
   f.coef = both(coef);
   f.decay = both(s.decay);
   f.mb1 = both(__fmul_rn(sm, s.b1));
   f.omb1 = both(s.omb1);
   f.vb2 = both(__fmul_rn(__fmul_rn(sr, sr), s.b2));
-  f.omb2 = both(s.omb2);
-  f.inv_bc2 = both(__frcp_rn(s.bc2_sqrt));
+  f.omb2 = both(lift ? __fmul_rn(s.omb2, kLift * kLift) : s.omb2);
+  const float inv_bc2 = __frcp_rn(s.bc2_sqrt);
+  f.inv_bc2 = both(lift ? __fmul_rn(inv_bc2, 1.0f / kLift) : inv_bc2);
   f.eps = both(fmaxf(s.eps, 0x1p-126f));  // the reciprocal's argument stays normal
   f.step = both(-s.step_size);
   return f;
 }
 
 // The 32-bit update (adam.cuh) on two elements, in two parts.  First the
-// moments, from codes: cm, cr (the codes' values) in, m and v out, bit for bit
-// what the 32-bit update gives for the decoded moments (but for the note above).
+// moments, from codes: cm, cr (the codes' values) in, m and v (lifted: 2^80 v) out,
+// bit for bit what the 32-bit update gives for the decoded moments where it has
+// 24 bits for them.
 __device__ __forceinline__ void moments8(F2& cm, F2& cr, F2 g, const Factors8& f) {
   g = mul2(g, f.coef);
   cm = fma2(f.omb1, g, mul2(cm, f.mb1));
@@ -278,14 +304,16 @@ __device__ __forceinline__ uint32_t warp_amax(const F2 (&x)[4]) {
 
 // Codes of the warp's block (byte j of the pair = this lane's element j) and
 // its scales, from m, r = sqrt(v) and the block's max|m|, max r as bits.
-// Every lane must call it.  `pair0`: the block's first pair.
+// Every lane must call it.  `pair0`: the block's first pair; lift: r is kLift times
+// the root.
 template <bool VEC, int SR>
 __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4], uint32_t amax_m, uint32_t amax_r,
                                              uint32_t key, int64_t pair0, uint2& cm, uint2& cr, float& sm,
-                                             float& sr) {
+                                             float& sr, bool lift) {
   float im, ir;
-  block_scale(amax_m, sm, im);
-  block_scale(amax_r, sr, ir);
+  block_scale(amax_m, 1, sm, im);
+  block_scale(amax_r, lift ? 1 + kLiftLog2 : 1, sr, ir);
+  if (lift) sr *= 1.0f / kLift;
   if (SR != kNearest) im *= 0x1p-8f;  // 1/S >= 2^-118 in a finite block: 2^-8 of it is still normal
   constexpr float to = SR == kNearest ? 1.0f : SR == kRoot7 ? 0x1p-8f : 0x1p-24f;
   ir *= to;  // a root is at most 2^64, 1/S at least 2^-56
@@ -410,13 +438,17 @@ __device__ __forceinline__ void store_block_lowp(void* lowp, int lowp_dtype, int
 }
 
 // The update of one block whose codes, scales and grads (fl(scale x), summed)
-// are in registers, and its stores.
-template <bool VEC, int SR>
+// are in registers, and its stores.  ROOTS: what is known of the block's
+// small_roots().
+enum Roots : int { kLarge, kSmall, kAnyRoots };
+
+template <bool VEC, int SR, int ROOTS>
 __device__ __forceinline__ void update_block(float* p, uint8_t* qm, uint8_t* qr, float* ms, float* rs,
                                              unsigned short* lowp, int lowp_dtype, int left, const float (&x)[8],
                                              const float (&g)[8], uint2 cm, uint2 cr, float sm, float sr, float coef,
                                              const AdamScalars& s, uint32_t key, int64_t pair0) {
-  const Factors8 f = factors8(s, sm, sr, coef);
+  const bool lift = ROOTS != kLarge && (ROOTS == kSmall || small_roots(s, sr)) && liftable(s, sr, g, coef);
+  const Factors8 f = factors8(s, sm, sr, coef, lift);
   F2 m[4], r[4];
   float y[8];
   decode8(cm, m);
@@ -440,13 +472,28 @@ __device__ __forceinline__ void update_block(float* p, uint8_t* qm, uint8_t* qr,
   store_block_f32<VEC>(p, left, y);
   if (lowp != nullptr) store_block_lowp<VEC>(lowp, lowp_dtype, left, y);
   // the largest root is the root of the largest exp_avg_sq
-  encode_block<VEC, SR>(m, r, amax_m, __float_as_uint(__fsqrt_rn(__uint_as_float(amax_v))), key, pair0, cm, cr, sm, sr);
+  encode_block<VEC, SR>(m, r, amax_m, __float_as_uint(__fsqrt_rn(__uint_as_float(amax_v))), key, pair0, cm, cr, sm, sr,
+                        lift);
   store_codes<VEC>(qm, left, cm);
   store_codes<VEC>(qr, left, cr);
   if ((threadIdx.x & 31) == 0) {
     *ms = sm;
     *rs = sr;
   }
+}
+
+// The same for any block with the two cases apart: in the flat-shard kernel one
+// code for both spilled (1.63e9 elements: 4.20 against 3.72 ms); in the list's,
+// two did (1.88e9, stochastic: 4.59 against 4.50).
+template <bool VEC, int SR>
+__device__ __forceinline__ void update_block_split(float* p, uint8_t* qm, uint8_t* qr, float* ms, float* rs,
+                                                   unsigned short* lowp, int lowp_dtype, int left, const float (&x)[8],
+                                                   const float (&g)[8], uint2 cm, uint2 cr, float sm, float sr, float coef,
+                                                   const AdamScalars& s, uint32_t key, int64_t pair0) {
+  if (small_roots(s, sr))
+    update_block<VEC, SR, kSmall>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key, pair0);
+  else
+    update_block<VEC, SR, kLarge>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key, pair0);
 }
 
 }  // namespace zs

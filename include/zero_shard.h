@@ -568,7 +568,8 @@ zero_status zero_state8_pack(const float* d_exp_avg, const float* d_exp_avg_sq, 
 
 /* zero_state8_unpack -- device.
  * The values q stands for: d_exp_avg = c S, d_exp_avg_sq = fl((c S)^2).
- * Packing what was unpacked gives the same values again.
+ * Packing what was unpacked gives the same values again where (c S)^2 is a
+ * normal binary32 number: roots of 2^-63 up to below 2^64.
  * Errors: as zero_state8_pack. */
 zero_status zero_state8_unpack(const zero_state8* q, int64_t n, float* d_exp_avg, float* d_exp_avg_sq, void* stream);
 
@@ -582,13 +583,13 @@ zero_status zero_state8_unpack(const zero_state8* q, int64_t n, float* d_exp_avg
  *   v = fma((1-beta2)*g, g, (r*r)*beta2)
  *   p = fma(-lr / (1-beta1^t), m / (sqrt(v) / sqrt(1-beta2^t) + eps), p * (1 - lr*wd))
  * m and v are those of zero_adamw_step for the decoded moments, bit for bit
- * (each operation rounded to nearest in binary32; in a block whose largest
- * root is under 2^-54, v keeps fewer bits); the root is the correctly
- * rounded one (1 ulp off for about one value in a million), the quotient is
- * formed with the hardware's reciprocal and within 8 ulp.  p and lowp use
- * these m and v, which are rounded to 8 bits only when they are stored in q.
- * The root of an exp_avg_sq below the normal range (2^-126) comes out too
- * small; an eps below it counts as 2^-126.
+ * (each operation rounded to nearest in binary32), and closer to the formulas
+ * where binary32 has fewer than 24 bits for them (a v under 2^-126 is computed as
+ * if it had them); the root is the correctly rounded one (1 ulp off for about
+ * one value in a million), the quotient is formed with the hardware's reciprocal
+ * and within 8 ulp.  p and lowp use these m and v, which are rounded to 8 bits
+ * only when they are stored in q.
+ * An eps below 2^-126 counts as 2^-126.
  * rounding: NULL rounds to nearest, else (host memory) the seed and stream of
  * stochastic rounding.
  * 16 bytes per parameter with 16-bit grads and copy, where the fp32 state
