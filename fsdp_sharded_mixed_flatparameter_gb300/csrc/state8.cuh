@@ -89,8 +89,10 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 
 // sqrt(v) of finite v >= 0: g = v y with y ~ 1 / sqrt(v), then one Newton step
 // g + (v - g^2) y / 2, whose residual is exact in an fma.  Its error before the
-// last rounding is of the order of y's squared, so it is the correctly rounded
-// root but for about one v in a million (1 ulp off there).  Zero gives zero;
+// last rounding is of the order of y's squared, so from any y within 2^-22 it is
+// the correctly rounded root but for a v in a million or two (1 ulp off there);
+// from this GPU's y it is the correctly rounded one for all 2^24 values of [1, 4).
+// Zero gives zero;
 // below the normal range (2^-126) it is positive but too small (kLift).
 __device__ __forceinline__ F2 root2(F2 v) {
   float v0, v1;
