@@ -195,11 +195,16 @@ def _grad_ptr(t: torch.Tensor, name: str) -> int:
     raise ValueError(f"{name} must be a CUDA tensor or a pinned host tensor")
 
 
+# the current stream's handle without a Stream object around it, where torch has that
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream) -> int:
     if type(stream) is int:
         return stream
-    if stream is None:  # the current stream's handle, without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return _current_handle(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -1,8 +1,11 @@
 """Stream arguments by handle, and what is read on streams other than their own."""
+import importlib.util
+
 import pytest
 import torch
 
 import fsdp_sharded_mixed_flatparameter_gb300 as pkg
+from fsdp_sharded_mixed_flatparameter_gb300 import zero_shard as zs
 from fsdp_sharded_mixed_flatparameter_gb300.optimizer import torch_stream
 
 pytestmark = pytest.mark.gpu
@@ -19,6 +22,23 @@ def test_handle_0_is_the_default_stream():
     assert torch_stream(s.cuda_stream, dev).cuda_stream == s.cuda_stream
     with torch.cuda.stream(s):
         assert torch_stream(None, dev) == s and torch_stream(0, dev) == torch.cuda.default_stream(dev)
+
+
+def test_the_current_streams_handle():
+    s = torch.cuda.Stream()
+    for st in (torch.cuda.default_stream(), s):
+        with torch.cuda.stream(st):
+            assert zs._stream(None) == st.cuda_stream == zs._stream(st) == zs._stream(st.cuda_stream)
+
+
+def test_without_torchs_own_accessor(monkeypatch):
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    spec = importlib.util.find_spec(zs.__name__)
+    other = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(other)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        assert other._stream(None) == s.cuda_stream
 
 
 def test_a_step_on_handle_0_waits_for_its_own_norm():
