@@ -3,14 +3,14 @@
 // per chunk of 1024 elements, a warp per 256, which here is one scale: its
 // maximum is one warp reduction, nothing is shared between warps.
 //
-// 16 bytes an element with 16-bit grads and copy, and 49 instructions (62
-// with stochastic rounding): near the bandwidth's and the issue rate's limit
-// at once.  Eight layers of Llama-7B (1.88e9 elements), stochastic: 4.45 ms =
-// 6.79 TB/s; four layers (1.07e9): 2.47 ms to nearest (6.98 TB/s), 2.56
-// stochastic, 2.50 to nearest with grads off the 16-byte grid.  4000
-// log-uniform tensors (302e6): 0.80 ms = 6.07 TB/s, where short last chunks
-// leave warps idle and the search takes a second round; GPT-2 small,
-// stochastic: 0.315 ms = 6.35 TB/s.
+// 16 bytes an element with 16-bit grads and copy, and 52 instructions (65
+// with stochastic rounding, 68 with 16 bits for the root): near the
+// bandwidth's and the issue rate's limit at once.  Eight layers of Llama-7B
+// (1.88e9 elements), stochastic: 4.50 ms = 6.72 TB/s (16 bits: 4.55); four
+// layers (1.07e9): 2.49 ms to nearest (6.93 TB/s), 2.58 stochastic, 2.51 to
+// nearest with grads off the 16-byte grid; fp32 grads 2.71 on and off theirs.  4000 log-uniform tensors (302e6):
+// 0.81 ms = 5.98 TB/s, where short last chunks leave warps idle and the search
+// takes a second round; GPT-2 small, stochastic: 0.317 ms = 6.32 TB/s.
 //
 // The way there, 1.88e9 elements, stochastic: 9.62 ms at 100 registers (one
 // code for full and short blocks); 6.09 with the two apart at 64 registers;
@@ -22,7 +22,8 @@
 // search per block; 4.41 with its last round over 128 candidates; 4.45 with the
 // root taken to the correctly rounded one by a Newton step in place of the
 // hardware's (by the compiler's sequence: 4.55), so that the stored codes are
-// those of the formula and not of the hardware's last bit.  Not kept:
+// those of the formula and not of the hardware's last bit; 4.50 with the blocks of
+// small roots computed larger (kLift).  Not kept:
 // asynchronous copies into shared memory, a block's chunks in a pipeline of two
 // or three stages (6.2 to 6.9 ms at the first arithmetic, against 6.1: their
 // addressing and waits are instructions).

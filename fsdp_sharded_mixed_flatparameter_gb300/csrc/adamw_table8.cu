@@ -9,11 +9,11 @@
 // adamw_table.cuh: directly, realigned in registers (fp32: in shared memory, a
 // warp alone), or staged in shared memory by the block where tensors meet.
 //
-// Measured: a Llama-13B ZeRO-3 shard (1.63e9 elements, flat fp16 grads) 3.71
-// ms = 7.04 TB/s; a quarter of 20,000 ragged tensors (377e6, most parts off
-// the 16-byte grid, stochastic) 1.02 ms = 5.94 TB/s, 79 instructions an
+// Measured: a Llama-13B ZeRO-3 shard (1.63e9 elements, flat fp16 grads) 3.72
+// ms = 7.03 TB/s; a quarter of 20,000 ragged tensors (377e6, most parts off
+// the 16-byte grid, stochastic) 1.03 ms = 5.88 TB/s, 81 instructions an
 // element with the search and the realignment; a GPT-2 ZeRO-1 shard with
-// accumulation (15.6e6) 54 us = 5.8 TB/s, ten waves of blocks.  Five
+// accumulation (15.6e6) 53 us = 5.85 TB/s, ten waves of blocks.  Five
 // blocks per SM (48 registers) against four: 3.71 and 1.09 against 3.88 and
 // 1.19 ms; six spill.  Two or four parts per block and search: 1.40 and 1.32
 // ms (ragged); blocks of 128 threads: the same; one warp's search shared

@@ -31,8 +31,8 @@
 // bits to 1.04 and 1.03: the square of the root's own noise).  exp_avg takes
 // the 7 bits; the root the 16 from beta2 > 0.99 on (ZERO_ROOT7_MAX_BETA2), up
 // to which the 7 bits stay as near (0.97 at 0.99, 1.02 at 0.95; 16 bits 1.04,
-// 1.03) in 3 instructions an element less (1.88e9 elements: 4.45 against 4.51
-// ms).  To nearest, a moment that moves by
+// 1.03) in 4 instructions an element less (1.88e9 elements: 4.53 against 4.58
+// ms; a flat shard of 1.63e9: 3.89 against 3.96).  To nearest, a moment that moves by
 // less than half a spacing per step (3 to 6 %) keeps its code until the
 // block's S moves: the same exp_avg_sq comes to 4.9 at beta2 = 0.95, to 0.19 at
 // 0.999.  The draws are a hash of (seed, step, stream, element), so a step is
@@ -285,7 +285,7 @@ __device__ __forceinline__ F2 param8(F2 p, F2 m, F2 r, const Factors8& f) {
 // elements 8l .. 8l + 7 of a full block in aligned buffers; else it has
 // elements l, l + 32, ..., l + 224, those from `left` on absent (zeros): tails
 // and unaligned buffers.  The two are separate instantiations: one code for
-// both, with the order as a variable, took 101 registers (adamw_list8.cu).
+// both, with the order as a variable, took 100 registers (adamw_list8.cu).
 template <bool VEC>
 __device__ __forceinline__ int elem_of(int j) {
   const int lane = threadIdx.x & 31;
