@@ -96,8 +96,10 @@ ZS_DEBUG_UNIT(adamw_list8)
 
 template <int DT>
 static zero_status launch_list8_dt(const ListArgs& a, const ListScalars& hs, cudaStream_t st) {
-  if (a.rounding.root_bits == 0) return launch_list8_t<DT, kNearest>(a, hs, st);
-  return a.rounding.root_bits == 7 ? launch_list8_t<DT, kRoot7>(a, hs, st) : launch_list8_t<DT, kRoot16>(a, hs, st);
+  if (a.rounding.how == kNearest) return launch_list8_t<DT, kNearest>(a, hs, st);
+  if (a.rounding.how == kRoot7) return launch_list8_t<DT, kRoot7>(a, hs, st);
+  if (a.rounding.how == kRoot16) return launch_list8_t<DT, kRoot16>(a, hs, st);
+  return launch_list8_t<DT, kRootBeta2>(a, hs, st);
 }
 
 zero_status launch_adamw_list8(const ListArgs& a, const ListScalars& hs, cudaStream_t st) {

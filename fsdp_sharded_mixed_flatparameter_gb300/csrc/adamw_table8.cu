@@ -165,8 +165,10 @@ static zero_status launch_table8_t(const Table8Args& a, const AdamScalars& s, cu
 
 template <int DT>
 static zero_status launch_table8_dt(const Table8Args& a, const AdamScalars& s, cudaStream_t st) {
-  if (a.rounding.root_bits == 0) return launch_table8_t<DT, kNearest>(a, s, st);
-  return a.rounding.root_bits == 7 ? launch_table8_t<DT, kRoot7>(a, s, st) : launch_table8_t<DT, kRoot16>(a, s, st);
+  if (a.rounding.how == kNearest) return launch_table8_t<DT, kNearest>(a, s, st);
+  if (a.rounding.how == kRoot7) return launch_table8_t<DT, kRoot7>(a, s, st);
+  if (a.rounding.how == kRoot16) return launch_table8_t<DT, kRoot16>(a, s, st);
+  return launch_table8_t<DT, kRootBeta2>(a, s, st);
 }
 
 ZS_DEBUG_UNIT(adamw_table8)

@@ -461,7 +461,7 @@ static zero_status step8_tensors(const char* who, float* d_master, const zero_st
                                  int32_t n_tensors, int64_t total, zero_dtype grad_dtype, int64_t shard_start,
                                  float grad_scale, const float* d_grad_scale, const float* d_acc, void* d_param_lowp,
                                  zero_dtype lowp_dtype, int64_t n, const zs::AdamScalars& s, int64_t step,
-                                 double beta2, const zero_adamw_device_state* d_state, const zero_rounding* rounding,
+                                 const zero_adamw_device_state* d_state, const zero_rounding* rounding,
                                  const zero_norm_result* d_clip, void* stream) {
   const zero_status c = check_state8(who, q, n);
   if (c != ZERO_OK) return c;
@@ -481,7 +481,9 @@ static zero_status step8_tensors(const char* who, float* d_master, const zero_st
   if (n == 0) return ZERO_OK;
   const zs::Table8Args a{d_master, *q, d_acc, d_table, n_tensors, grad_dtype, shard_start, n, grad_scale, d_grad_scale,
                          d_param_lowp, lowp_dtype, d_state,
-                         zs::rounding_base(rounding, d_state == nullptr ? &step : nullptr, beta2), d_clip};
+                         d_state == nullptr ? zs::rounding_base(rounding, &step, s.b2, s.b2)
+                                            : zs::rounding_base(rounding, nullptr, 0.0f, 1.0f),
+                         d_clip};
   return zs::launch_adamw_table8(a, s, zs::as_stream(stream));
 }
 
@@ -496,7 +498,7 @@ zero_status zero_adamw_step8_tensors(float* d_master, const zero_state8* q, cons
   const zero_status hs = adamw_scalars(who, hp, step, &s);
   if (hs != ZERO_OK) return hs;
   return step8_tensors(who, d_master, q, d_table, n_tensors, total, grad_dtype, shard_start, grad_scale, d_grad_scale,
-                       d_acc, d_param_lowp, lowp_dtype, n, s, step, hp->beta2, nullptr, rounding, d_clip, stream);
+                       d_acc, d_param_lowp, lowp_dtype, n, s, step, nullptr, rounding, d_clip, stream);
 }
 
 zero_status zero_adamw_step8_tensors_device(float* d_master, const zero_state8* q, const zero_tensor* d_table,
@@ -509,7 +511,7 @@ zero_status zero_adamw_step8_tensors_device(float* d_master, const zero_state8* 
   const zero_status c = check_state(who, d_state);
   if (c != ZERO_OK) return c;
   return step8_tensors(who, d_master, q, d_table, n_tensors, total, grad_dtype, shard_start, grad_scale, d_grad_scale,
-                       d_acc, d_param_lowp, lowp_dtype, n, zs::AdamScalars{}, 0, 0.0, d_state, rounding, d_clip,
+                       d_acc, d_param_lowp, lowp_dtype, n, zs::AdamScalars{}, 0, d_state, rounding, d_clip,
                        stream);
 }
 
@@ -563,7 +565,7 @@ static zero_status adamw_list(const char* who, const zs::ListArgs& a, const zs::
   const zero_status g = check_groups(who, n_groups);
   if (g != ZERO_OK) return g;
   if (a.state_bits != 32 && a.state_bits != 8) return fail(ZERO_EINVAL, "%s: state_bits must be 32 or 8", who);
-  if (a.rounding.root_bits != 0 && a.state_bits == 32)
+  if (a.rounding.how != zs::kNearest && a.state_bits == 32)
     return fail(ZERO_EINVAL, "%s: a rounding seed needs 8-bit states", who);
   if (!zs::valid_dtype(a.grad_dtype)) return fail(ZERO_EINVAL, "%s: bad grad_dtype %d", who, a.grad_dtype);
   if (a.lowp_dtype != ZERO_BF16 && a.lowp_dtype != ZERO_F16)
@@ -585,14 +587,15 @@ zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, c
   const zero_status r = check_rounding(who, rounding);
   if (r != ZERO_OK) return r;
   zs::ListScalars s{};
-  double beta2 = 0.0;
+  float least = 1.0f, most = 0.0f;
   for (int32_t i = 0; i < n_groups; ++i) {
     const zero_status hs = adamw_scalars(who, &groups[i], step, &s.s[i]);
     if (hs != ZERO_OK) return hs;
-    if (groups[i].beta2 > beta2) beta2 = groups[i].beta2;
+    least = s.s[i].b2 < least ? s.s[i].b2 : least;
+    most = s.s[i].b2 > most ? s.s[i].b2 : most;
   }
   const zs::ListArgs a{d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
-                       lowp_dtype, nullptr, zs::rounding_base(rounding, &step, beta2), d_clip};
+                       lowp_dtype, nullptr, zs::rounding_base(rounding, &step, least, most), d_clip};
   return adamw_list(who, a, s, n_groups, stream);
 }
 
@@ -607,7 +610,7 @@ zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_ten
   const zero_status r = check_rounding(who, rounding);
   if (r != ZERO_OK) return r;
   const zs::ListArgs a{d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
-                       lowp_dtype, d_states, zs::rounding_base(rounding, nullptr, 0.0), d_clip};
+                       lowp_dtype, d_states, zs::rounding_base(rounding, nullptr, 0.0f, 1.0f), d_clip};
   return adamw_list(who, a, zs::ListScalars{}, n_groups, stream);
 }
 

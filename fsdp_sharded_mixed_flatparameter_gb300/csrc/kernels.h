@@ -50,12 +50,17 @@ AdamwTableInstance launch_adamw_table_p4;
 AdamwTableInstance launch_adamw_table_p4_acc;
 
 // Stochastic rounding's draws, as far as the launch knows them: the hash of the
-// seed and (unless the step is on the device) of the step, and the stream; the
-// bits drawn for a root (0: to nearest, nothing is drawn).
+// seed and (unless the step is on the device) of the step, and the stream.
+enum Rounding : int {
+  kNearest = 0,   // nothing is drawn
+  kRoot7 = 1,     // 7 bits for both moments
+  kRoot16 = 2,    // 7 bits for exp_avg, 16 for the root
+  kRootBeta2 = 3  // one or the other by beta2, where the launch does not know it or has several
+};
 struct RoundingBase {
   uint32_t hash;
   uint32_t stream;
-  int root_bits;
+  int how;  // Rounding
 };
 
 // AdamW over a flat shard with 8-bit moments, grads through the table.

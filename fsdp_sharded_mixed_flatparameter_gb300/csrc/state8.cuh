@@ -30,7 +30,7 @@
 // 0.68 of what it should be at beta2 = 0.999 and 0.24 at 0.9999 (with the 16
 // bits to 1.04 and 1.03: the square of the root's own noise).  exp_avg takes
 // the 7 bits; the root the 16 from beta2 > 0.99 on (ZERO_ROOT7_MAX_BETA2), up
-// to which the 7 bits stay as near (0.97 at 0.99, 1.02 at 0.95; 16 bits 1.04,
+// to which the 7 bits stay as near (0.97 at 0.99, 1.01 at 0.95; 16 bits 1.04,
 // 1.03) in 4 instructions an element less (1.88e9 elements: 4.53 against 4.58
 // ms; a flat shard of 1.63e9: 3.89 against 3.96).  To nearest, a moment that moves by
 // less than half a spacing per step (3 to 6 %) keeps its code until the
@@ -189,13 +189,6 @@ __device__ __forceinline__ void block_scale(uint32_t amax, int least, float& s, 
 }
 
 // --------------------------------------------------------------- rounding
-// How an update rounds the moments to codes.
-enum Rounding : int {
-  kNearest = 0,
-  kRoot7 = 1,   // stochastic, 7 bits for both moments
-  kRoot16 = 2,  // stochastic, 7 bits for exp_avg, 16 for the root
-};
-
 // The key of one block's draws (pcg_hash: rounding.cuh): the word of pair i
 // (elements 2i, 2i + 1) is pcg_hash(low 32 bits of i ^ key); of each half of it
 // bits 0..6 round exp_avg and bits 7..13, or all 16, the root (the two moments'
@@ -307,19 +300,20 @@ __device__ __forceinline__ uint32_t warp_amax(const F2 (&x)[4]) {
 // Codes of the warp's block (byte j of the pair = this lane's element j) and
 // its scales, from m, r = sqrt(v) and the block's max|m|, max r as bits.
 // Every lane must call it.  `pair0`: the block's first pair; lift: r is kLift times
-// the root.
+// the root; wide: 16 bits for the root (SR == kRootBeta2).
 template <bool VEC, int SR>
 __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4], uint32_t amax_m, uint32_t amax_r,
                                              uint32_t key, int64_t pair0, uint2& cm, uint2& cr, float& sm,
-                                             float& sr, bool lift) {
+                                             float& sr, bool lift, bool wide) {
   float im, ir;
   block_scale(amax_m, 1, sm, im);
   block_scale(amax_r, lift ? 1 + kLiftLog2 : 1, sr, ir);
   if (lift) sr *= 1.0f / kLift;
   if (SR != kNearest) im *= 0x1p-8f;  // 1/S >= 2^-118 in a finite block: 2^-8 of it is still normal
-  constexpr float to = SR == kNearest ? 1.0f : SR == kRoot7 ? 0x1p-8f : 0x1p-24f;
+  if (SR != kRootBeta2) wide = SR == kRoot16;
+  const float to = SR == kNearest ? 1.0f : wide ? 0x1p-24f : 0x1p-8f;
   ir *= to;  // a root is at most 2^64, 1/S at least 2^-56
-  constexpr float least = 0x1p-9f * to;  // the smallest code's value
+  const float least = 0x1p-9f * to;  // the smallest code's value
   F2 x[4], y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -337,7 +331,7 @@ __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4],
     cr = make_uint2(encode4_nearest(y[0], y[1]), encode4_nearest(y[2], y[3]));
   } else {
     const int lane = threadIdx.x & 31;
-    uint32_t km[4], kr[4], wr[4];
+    uint32_t km[4], wr[4];
     const uint32_t p0 = static_cast<uint32_t>(pair0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -350,16 +344,18 @@ __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4],
         w = __byte_perm(a, b, (lane & 1) ? 0x7632 : 0x5410);
       }
       km[i] = (w << 1) & 0x00fe00feu;
-      kr[i] = (w >> 6) & 0x00fe00feu;
       wr[i] = w;
     }
     cm = make_uint2(encode4_stochastic<true>(x[0], x[1], km[0], km[1]),
                     encode4_stochastic<true>(x[2], x[3], km[2], km[3]));
-    if (SR == kRoot7)
-      cr = make_uint2(encode4_stochastic<false>(y[0], y[1], kr[0], kr[1]),
-                      encode4_stochastic<false>(y[2], y[3], kr[2], kr[3]));
-    else
+    if (wide) {
       cr = make_uint2(encode4_root16(y[0], y[1], wr[0], wr[1]), encode4_root16(y[2], y[3], wr[2], wr[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wr[i] = (wr[i] >> 6) & 0x00fe00feu;
+      cr = make_uint2(encode4_stochastic<false>(y[0], y[1], wr[0], wr[1]),
+                      encode4_stochastic<false>(y[2], y[3], wr[2], wr[3]));
+    }
   }
 }
 
@@ -475,7 +471,7 @@ __device__ __forceinline__ void update_block(float* p, uint8_t* qm, uint8_t* qr,
   if (lowp != nullptr) store_block_lowp<VEC>(lowp, lowp_dtype, left, y);
   // the largest root is the root of the largest exp_avg_sq
   encode_block<VEC, SR>(m, r, amax_m, __float_as_uint(__fsqrt_rn(__uint_as_float(amax_v))), key, pair0, cm, cr, sm, sr,
-                        lift);
+                        lift, root16(s.b2));
   store_codes<VEC>(qm, left, cm);
   store_codes<VEC>(qr, left, cr);
   if ((threadIdx.x & 31) == 0) {

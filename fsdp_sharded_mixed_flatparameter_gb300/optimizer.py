@@ -181,8 +181,7 @@ class FlatShardAdamW(GradTables):
             raise ValueError("master must be fp32 with the shard's size")
         self.master = master.to(dev).contiguous()
         # the moments: fp32, or 8 bits (state8; rounding_seed: an integer seeds stochastic
-        # rounding, by default 0, whose draws rounding_stream tells apart between ranks;
-        # a root's random bits go by beta2 (root_bits_for), in a captured graph by that of its capture)
+        # rounding, by default 0, whose draws rounding_stream tells apart between ranks)
         self.state_bits, self.rounding_seed, self.rounding_stream = state_bits, rounding_seed, self.start
         self.state8 = self.exp_avg = self.exp_avg_sq = None
         if state_bits == 8:
@@ -387,8 +386,7 @@ class FlatShardAdamW(GradTables):
         state = (self.state8,) if self.state_bits == 8 else (self.exp_avg, self.exp_avg_sq)
         kw = dict(acc=acc, d_scale=d_scale)
         if self.state_bits == 8:
-            kw.update(rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream,
-                      root_bits=zs.root_bits_for(self.betas[1]))
+            kw.update(rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream)
         if self.capturable:
             call = zs.zero_adamw_step8_tensors_device if self.state_bits == 8 else zs.zero_adamw_step_tensors_device
             call(self.master, *state, table, count, total, dt, shard_start, scale, self.lowp, self._dev_state, clip,

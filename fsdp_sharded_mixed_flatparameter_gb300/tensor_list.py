@@ -29,9 +29,7 @@ class TensorListAdamW(GradTables):
     tensor's group (default: all in group 0).  rounding_seed (8 bits only): an integer seeds
     stochastic rounding of the moments (default 0); None rounds them to nearest, by which they
     do not follow their recurrences over a run (optimizer.py).  Lists that share a seed take
-    rounding_streams that are further apart than they have tensors.  How many random bits a
-    root takes goes by the groups' largest beta2 (root_bits_for); a captured graph keeps what
-    they were at its capture.
+    rounding_streams that are further apart than they have tensors.
 
     The moments live in storages of this object, tensor i's at elements offsets[i] ..
     offsets[i] + numels[i]: ``exp_avg`` and ``exp_avg_sq`` (fp32), or ``state8`` (8 bits:
@@ -61,7 +59,7 @@ class TensorListAdamW(GradTables):
                                  float(h["weight_decay"])])
         if not 1 <= len(self._groups) <= zs.LIST_MAX_GROUPS:
             raise ValueError(f"1 to {zs.LIST_MAX_GROUPS} groups")
-        self._pack_groups()
+        self._hp = zs.list_groups(self._groups)
         columns, numels, lowp_dtype = zs.list_masters(self.masters, self.lowp, group_of)
         self._init_tables(numels, self.device)
         blocks = np.cumsum([0] + [zs.state8_blocks(n) for n in numels])  # each tensor starts on a block's border
@@ -88,10 +86,6 @@ class TensorListAdamW(GradTables):
         if capturable:
             self._dev_hp = torch.cat([zs.device_hparams(*g, self.device) for g in self._groups])
             self._dev_states = zs.new_adamw_device_state(self.device).repeat(len(self._groups))
-
-    def _pack_groups(self) -> None:
-        self._hp = zs.list_groups(self._groups)
-        self._root_bits = zs.root_bits_for(max(g[2] for g in self._groups))
 
     # ------------------------------------------------------------- state
     def state_of(self, i: int):
@@ -129,7 +123,7 @@ class TensorListAdamW(GradTables):
         h = {**self.group(i), **hp}
         self._groups[i] = [float(h["lr"]), float(h["betas"][0]), float(h["betas"][1]), float(h["eps"]),
                            float(h["weight_decay"])]
-        self._pack_groups()
+        self._hp = zs.list_groups(self._groups)
         if self.capturable:
             i %= len(self._groups)
             zs.device_hparams(*self._groups[i], self.device,
@@ -154,12 +148,10 @@ class TensorListAdamW(GradTables):
         if self.capturable:
             zs.zero_adamw_prepare_list_device(self._dev_hp, len(self._groups), clip, self._dev_states, stream)
             zs.zero_adamw_list_device(self._list, table, dt, sc, self._dev_states, clip, stream, d_scale=dsc,
-                                      rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream,
-                                      root_bits=self._root_bits)
+                                      rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream)
         else:
             zs.zero_adamw_list(self._list, table, dt, sc, self._hp, self._t + 1, clip, stream, d_scale=dsc,
-                               rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream,
-                               root_bits=self._root_bits)
+                               rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream)
 
     def finish_step(self, stream=None, norm_result: Optional[torch.Tensor] = None) -> zs.NormResult:
         """Read the step's norm (a device-to-host copy on `stream`, the stream the step was

@@ -71,7 +71,6 @@ class zero_list_tensor(ctypes.Structure):
 
 
 STATE8_BLOCK = 256      # elements per scale of the 8-bit moments
-ROOT7_MAX_BETA2 = 0.99  # up to here 7 random bits for a root follow exp_avg_sq, above 16 do (zero_rounding)
 LIST_CHUNK = 1024       # elements per piece of a tensor list's work
 LIST_MAX_GROUPS = 64
 
@@ -584,12 +583,6 @@ def rounding_choice(state_bits: int, rounding_seed):
     return rounding_seed
 
 
-def root_bits_for(beta2: float) -> int:
-    """The random bits by which an optimizer rounds the root of exp_avg_sq: 7 follow it up to
-    beta2 = 0.99, above 16 are needed."""
-    return 16 if beta2 > ROOT7_MAX_BETA2 else 7
-
-
 def _rounding(rounding_seed: Optional[int], stream: int, root_bits: int):
     """NULL (round to nearest) or the 64-bit seed, the stream and the root's bits of stochastic rounding."""
     if rounding_seed is None:
@@ -670,7 +663,8 @@ def zero_adamw_step8_tensors(master: torch.Tensor, state8: State8, d_table: torc
                              root_bits: int = 0) -> None:
     """zero_adamw_step_tensors with the moments in 8 bits; rounding_seed: None rounds them to
     nearest, an integer seeds stochastic rounding, whose stream is rounding_stream (default:
-    shard_start).  root_bits: the bits drawn for a root, 7 or 16 (0: root_bits_for(beta2))."""
+    shard_start).  root_bits: the bits drawn for a root, 7 or 16; 0: 7 up to beta2 = 0.99,
+    above it 16."""
     n, q, lp, lowp_dt = _step8_common(master, state8, d_table, n_tensors, param_lowp, clip, acc)
     hp = zero_adamw_hparams(lr, beta1, beta2, eps, weight_decay)
     _check(lib().zero_adamw_step8_tensors(
@@ -688,8 +682,7 @@ def zero_adamw_step8_tensors_device(master: torch.Tensor, state8: State8, d_tabl
                                     acc: Optional[torch.Tensor] = None, d_scale: Optional[torch.Tensor] = None,
                                     rounding_seed: Optional[int] = None, rounding_stream: Optional[int] = None,
                                     root_bits: int = 0) -> None:
-    """zero_adamw_step8_tensors with the scalars, step and skip decision of the device step state
-    (root_bits 0: 7, whatever beta2 the state has)."""
+    """zero_adamw_step8_tensors with the scalars, step and skip decision of the device step state."""
     n, q, lp, lowp_dt = _step8_common(master, state8, d_table, n_tensors, param_lowp, clip, acc)
     _check(lib().zero_adamw_step8_tensors_device(
         _dev(master, "master", torch.float32), ctypes.byref(q),
@@ -814,7 +807,7 @@ def zero_adamw_list(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dty
     """One AdamW step over every tensor of a list.  d_grads: the device table of the grads
     (zero_tensor_table + device_table, in list order); groups: (lr, beta1, beta2, eps,
     weight_decay) of each parameter group, or list_groups() of them made once.  rounding_seed,
-    root_bits: as for zero_adamw_step8_tensors (0: by the groups' largest beta2)."""
+    root_bits: as for zero_adamw_step8_tensors (each tensor by its group's beta2)."""
     if len(groups) != tl.n_groups:
         raise ValueError(f"{len(groups)} groups given, the list has {tl.n_groups}")
     if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
@@ -829,8 +822,7 @@ def zero_adamw_list_device(tl: TensorList, d_grads: torch.Tensor, grad_dtype: to
                            states: torch.Tensor, clip: Optional[torch.Tensor] = None, stream=None,
                            d_scale: Optional[torch.Tensor] = None, rounding_seed: Optional[int] = None,
                            rounding_stream: int = 0, root_bits: int = 0) -> None:
-    """zero_adamw_list with the groups' scalars, step and skip decision from device step states
-    (root_bits 0: 7, whatever beta2 they have)."""
+    """zero_adamw_list with the groups' scalars, step and skip decision from device step states."""
     if states.numel() * states.element_size() < tl.n_groups * DEVICE_STATE_BYTES:
         raise ValueError("states is smaller than one zero_adamw_device_state per group")
     if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:

@@ -553,9 +553,8 @@ typedef struct zero_state8 {
 typedef struct zero_rounding {
   uint64_t seed;
   int64_t stream; /* its low 32 bits: ranks, or lists, that share a seed take different streams */
-  int32_t root_bits; /* bits drawn for the root: 7, 16, or 0: 16 if the call's (a group's) beta2 is above
-                        ZERO_ROOT7_MAX_BETA2, else 7; the calls with a device state, which do not
-                        have it on the host, take 0 as 7 */
+  int32_t root_bits; /* bits drawn for a root: 7, 16, or 0: 16 where beta2 (the tensor's group's, the
+                        device state's) is above ZERO_ROOT7_MAX_BETA2, both in binary32, else 7 */
   int32_t reserved;  /* 0 */
 } zero_rounding;
 

@@ -87,7 +87,55 @@ def test_the_bits_go_by_beta2(b2, bits):
         tl = zs.zero_tensor_list([b], [a], state_bits=8)
         zs.zero_adamw_list(tl, table, x.dtype, 1.0, [(1e-2, 0.9, b2, 1e-8, 0.1)], 3, rounding_seed=1, root_bits=root_bits)
         assert same(a, got[root_bits])
+        # with the scalars on the device
+        hp = zs.device_hparams(1e-2, 0.9, b2, 1e-8, 0.1, "cuda")
+        for form in ("shard", "list"):
+            a, b, state = clone(q), p.clone(), zs.new_adamw_device_state("cuda", 2)
+            if form == "shard":
+                zs.zero_adamw_prepare_device(hp, None, state)
+                zs.zero_adamw_step8_tensors_device(b, a, table, 1, n, x.dtype, 0, 1.0, None, state, rounding_seed=1,
+                                                   root_bits=root_bits)
+            else:
+                zs.zero_adamw_prepare_list_device(hp, 1, None, state)
+                zs.zero_adamw_list_device(zs.zero_tensor_list([b], [a], state_bits=8), table, x.dtype, 1.0, state,
+                                          rounding_seed=1, root_bits=root_bits)
+            assert same(a, got[root_bits]), (form, root_bits)
     assert same(got[0], got[bits]) and not same(got[7], got[16])
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_each_group_goes_by_its_own_beta2(capturable):
+    sizes, betas = [3000, 777, 5000], [(0.9, 0.95), (0.9, 0.999), (0.8, 0.99)]
+    x = [(torch.randn(n, generator=gen(n)) * 1e-2).cuda() for n in sizes]
+    o = pkg.TensorListAdamW([torch.zeros(n, device="cuda") for n in sizes], lr=1e-2, state_bits=8, capturable=capturable,
+                            groups=[{"betas": b} for b in betas], group_of=[0, 1, 2])
+    for _ in range(2):
+        o.step(x)
+    for i, n in enumerate(sizes):
+        one = pkg.TensorListAdamW([torch.zeros(n, device="cuda")], lr=1e-2, betas=betas[i], state_bits=8, rounding_stream=i)
+        clip = norm_result_tensor("cuda", coef=1.0)
+        for _ in range(2):
+            one.launch_step([x[i]], norm_result=clip)
+            one.finish_step(norm_result=clip)
+        assert same(one.state_of(0), o.state_of(i)) and torch.equal(one.masters[0], o.masters[i]), i
+
+
+def test_a_graph_follows_a_change_of_beta2():
+    n = 3000
+    a, b = (pkg.FlatShardAdamW([n], lr=1e-2, betas=(0.9, 0.95), device="cuda", state_bits=8, grad_buffer=False, capturable=c)
+            for c in (True, False))
+    x = (torch.randn(n, generator=gen(1)) * 1e-2).cuda()
+    a.register_grads([x])
+    b.register_grads([x])
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        a.launch_step_tensors()
+    for b2 in (0.95, 0.999, 0.95):
+        a.betas = b.betas = (0.9, b2)
+        graph.replay()
+        b.step_tensors()
+        assert same(a.state8, b.state8) and torch.equal(a.master, b.master)
 
 
 N = 4096

@@ -1,7 +1,6 @@
 """Stochastic rounding of 8-bit moments without a GPU: what its two forms do to a recurrence, and the refusals of a bad one."""
 import ctypes
 import inspect
-import os
 
 import numpy as np
 import pytest
@@ -56,12 +55,6 @@ def test_bad_root_bits_are_refused(bits):
     bad = zs.zero_rounding(1, 0, bits, 0)
     assert call_step8(seed=ctypes.byref(bad)) == zs.ZERO_EINVAL
     assert call_list(seed=ctypes.byref(bad)) == zs.ZERO_EINVAL
-
-
-def test_the_rule_for_the_bits():
-    assert [zs.root_bits_for(b) for b in (0.0, 0.95, 0.99, 0.9901, 0.999)] == [7, 7, 7, 16, 16]
-    header = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "zero_shard.h")).read()
-    assert f"#define ZERO_ROOT7_MAX_BETA2 {zs.ROOT7_MAX_BETA2}\n" in header
 
 
 def test_reserved_fields_are_refused():
