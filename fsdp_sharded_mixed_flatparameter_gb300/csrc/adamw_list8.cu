@@ -8,9 +8,10 @@
 // bandwidth's and the issue rate's limit at once.  Eight layers of Llama-7B
 // (1.88e9 elements), stochastic: 4.50 ms = 6.72 TB/s (16 bits: 4.55); four
 // layers (1.07e9): 2.49 ms to nearest (6.93 TB/s), 2.58 stochastic, 2.51 to
-// nearest with grads off the 16-byte grid; fp32 grads 2.71 on and off theirs.  4000 log-uniform tensors (302e6):
-// 0.81 ms = 5.98 TB/s, where short last chunks leave warps idle and the search
-// takes a second round; GPT-2 small, stochastic: 0.317 ms = 6.32 TB/s.
+// nearest with grads off the 16-byte grid; fp32 grads 2.71 on and off theirs.
+// 4000 log-uniform tensors (302e6): 0.81 ms = 5.98 TB/s, where short last
+// chunks leave warps idle and the search takes a second round; GPT-2 small,
+// stochastic: 0.317 ms = 6.32 TB/s.
 //
 // The way there, 1.88e9 elements, stochastic: 9.62 ms at 100 registers (one
 // code for full and short blocks); 6.09 with the two apart at 64 registers;

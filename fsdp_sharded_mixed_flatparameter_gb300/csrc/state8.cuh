@@ -32,11 +32,11 @@
 // the 7 bits; the root the 16 from beta2 > 0.99 on (ZERO_ROOT7_MAX_BETA2), up
 // to which the 7 bits stay as near (0.97 at 0.99, 1.01 at 0.95; 16 bits 1.04,
 // 1.03) in 4 instructions an element less (1.88e9 elements: 4.53 against 4.58
-// ms; a flat shard of 1.63e9: 3.89 against 3.96).  To nearest, a moment that moves by
-// less than half a spacing per step (3 to 6 %) keeps its code until the
-// block's S moves: the same exp_avg_sq comes to 4.9 at beta2 = 0.95, to 0.19 at
-// 0.999.  The draws are a hash of (seed, step, stream, element), so a step is
-// reproducible.
+// ms; a flat shard of 1.63e9: 3.89 against 3.96).  To nearest, a moment that
+// moves by less than half a spacing per step (3 to 6 %) keeps its code until
+// the block's S moves: the same exp_avg_sq comes to 4.9 at beta2 = 0.95, to
+// 0.19 at 0.999.  The draws are a hash of (seed, step, stream, element), so a
+// step is reproducible.
 #pragma once
 
 #include "adam.cuh"
@@ -91,9 +91,9 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 // g + (v - g^2) y / 2, whose residual is exact in an fma.  Its error before the
 // last rounding is of the order of y's squared, so from any y within 2^-22 it is
 // the correctly rounded root but for a v in a million or two (1 ulp off there);
-// from this GPU's y it is the correctly rounded one for all 2^24 values of [1, 4).
-// Zero gives zero;
-// below the normal range (2^-126) it is positive but too small (kLift).
+// from this GPU's y it is the correctly rounded one for all 2^24 values of
+// [1, 4).  Zero gives zero; below the normal range (2^-126) it is positive but
+// too small (kLift).
 __device__ __forceinline__ F2 root2(F2 v) {
   float v0, v1;
   unpair(v, v0, v1);

@@ -584,9 +584,11 @@ zero_status zero_state8_unpack(const zero_state8* q, int64_t n, float* d_exp_avg
  * m and v are those of zero_adamw_step for the decoded moments, bit for bit
  * (each operation rounded to nearest in binary32), and closer to the formulas
  * where binary32 has fewer than 24 bits for them (a v under 2^-126 is computed as
- * if it had them); the root is the correctly rounded one (at most 1 ulp off,
- * for a value in a million if any), the quotient is formed with the hardware's reciprocal
- * and within 8 ulp.  p and lowp use these m and v, which are rounded to 8 bits
+ * if it had them where it can show: in a block's codes, and in p with an eps under
+ * 2^-34 unless the block has grads of 2^20 or an S of the root of 2^14 and more);
+ * the root is the correctly rounded one (at most 1 ulp off, for a value in a
+ * million if any), the quotient is formed with the hardware's reciprocal and
+ * within 8 ulp.  p and lowp use these m and v, which are rounded to 8 bits
  * only when they are stored in q.
  * An eps below 2^-126 counts as 2^-126.
  * rounding: NULL rounds to nearest, else (host memory) the seed and stream of
