@@ -37,7 +37,7 @@ namespace zs {
 template <int DT, int SR, bool VEC>
 __device__ __forceinline__ void list8_block(const zero_list_tensor& t, const void* grad, int64_t k, int64_t rest,
                                             float gscale, float coef, const AdamScalars& s, int lowp_dtype,
-                                            uint32_t key) {
+                                            uint32_t key, int root_bits) {
   const int left = static_cast<int>(rest < kBlock8 ? rest : kBlock8);
   float p[8], g[8];
   float* const pk = t.master + k;
@@ -51,7 +51,7 @@ __device__ __forceinline__ void list8_block(const zero_list_tensor& t, const voi
   load_block_grad<DT, VEC>(grad, k, rest, gscale, g);
   update_block<VEC, SR, kAnyRoots>(pk, qm, qr, ms, rs,
                                    t.lowp == nullptr ? nullptr : static_cast<unsigned short*>(t.lowp) + k, lowp_dtype,
-                                   left, p, g, cm, cr, sm, sr, coef, s, key, k >> 1);
+                                   left, p, g, cm, cr, sm, sr, coef, s, key, root_bits, k >> 1);
 }
 
 template <int DT, int SR>
@@ -80,10 +80,9 @@ __global__ void __launch_bounds__(kListThreads, 10)
   uint32_t key = 0u;
   if (SR != kNearest) key = rounding_key(rnd, ds, tensor, k >> 1);
   if (left >= kBlock8 && aligned(t.master, 32) && aligned(t.exp_avg, 8) && aligned(t.exp_avg_sq, 8))
-    list8_block<DT, SR, true>(t, grad, k, left, gscale, coef, s, lowp_dtype, key);
+    list8_block<DT, SR, true>(t, grad, k, left, gscale, coef, s, lowp_dtype, key, rnd.root_bits);
   else
-    list8_block<DT, SR, false>(t, grad, k, left, gscale, coef, s, lowp_dtype,
-                               key);
+    list8_block<DT, SR, false>(t, grad, k, left, gscale, coef, s, lowp_dtype, key, rnd.root_bits);
 }
 
 template <int DT, int SR>
@@ -100,7 +99,7 @@ static zero_status launch_list8_dt(const ListArgs& a, const ListScalars& hs, cud
   if (a.rounding.how == kNearest) return launch_list8_t<DT, kNearest>(a, hs, st);
   if (a.rounding.how == kRoot7) return launch_list8_t<DT, kRoot7>(a, hs, st);
   if (a.rounding.how == kRoot16) return launch_list8_t<DT, kRoot16>(a, hs, st);
-  return launch_list8_t<DT, kRootBeta2>(a, hs, st);
+  return launch_list8_t<DT, kByBeta>(a, hs, st);
 }
 
 zero_status launch_adamw_list8(const ListArgs& a, const ListScalars& hs, cudaStream_t st) {

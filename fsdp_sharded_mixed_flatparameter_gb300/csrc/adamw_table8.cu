@@ -37,7 +37,7 @@ template <int DT, int SR>
 __device__ __forceinline__ void table8_full(float* p, const zero_state8& q, const float* acc, const zero_tensor* table,
                                             int n_tensors, int64_t shard_start, int64_t k0, float gscale, void* lowp,
                                             int lowp_dtype, float coef, const AdamScalars& s, uint32_t key,
-                                            float* stage) {
+                                            int root_bits, float* stage) {
   constexpr int es = SrcTraits<DT>::esize;
   constexpr int vb = (DT == ZERO_F32) ? 32 : 16;
   const int warp = threadIdx.x >> 5;
@@ -89,7 +89,7 @@ __device__ __forceinline__ void table8_full(float* p, const zero_state8& q, cons
   }
   update_block_split<true, SR>(p + k, q.exp_avg + k, q.root + k, q.exp_avg_scale + b, q.root_scale + b,
                                lowp == nullptr ? nullptr : static_cast<unsigned short*>(lowp) + k, lowp_dtype, kBlock8,
-                               pr, g, cm, cr, sm, sr, coef, s, key, k >> 1);
+                               pr, g, cm, cr, sm, sr, coef, s, key, root_bits, k >> 1);
 }
 
 // Any part: the last one, or unaligned state.
@@ -97,7 +97,7 @@ template <int DT, int SR>
 __device__ __forceinline__ void table8_any(float* p, const zero_state8& q, const float* acc, const zero_tensor* table,
                                            int n_tensors, int64_t shard_start, int64_t k0, int64_t n, float gscale,
                                            void* lowp, int lowp_dtype, float coef, const AdamScalars& s,
-                                           uint32_t key, float* stage) {
+                                           uint32_t key, int root_bits, float* stage) {
   const int blen = static_cast<int>(n - k0 < kT8Block ? n - k0 : kT8Block);
   const int64_t f0 = shard_start + k0;
   bool unused_flag = false;
@@ -119,7 +119,7 @@ __device__ __forceinline__ void table8_any(float* p, const zero_state8& q, const
     }
     update_block_split<false, SR>(p + k, q.exp_avg + k, q.root + k, q.exp_avg_scale + b, q.root_scale + b,
                                   lowp == nullptr ? nullptr : static_cast<unsigned short*>(lowp) + k, lowp_dtype, left,
-                                  pr, g, cm, cr, sm, sr, coef, s, key, k >> 1);
+                                  pr, g, cm, cr, sm, sr, coef, s, key, root_bits, k >> 1);
   }
 }
 
@@ -148,9 +148,11 @@ __global__ void __launch_bounds__(256, 5)
                 70, k0))
     return;
   if (full)
-    table8_full<DT, SR>(p, q, acc, table, n_tensors, shard_start, k0, gscale, lowp, lowp_dtype, coef, s, key, stage);
+    table8_full<DT, SR>(p, q, acc, table, n_tensors, shard_start, k0, gscale, lowp, lowp_dtype, coef, s, key,
+                        rnd.root_bits, stage);
   else
-    table8_any<DT, SR>(p, q, acc, table, n_tensors, shard_start, k0, n, gscale, lowp, lowp_dtype, coef, s, key, stage);
+    table8_any<DT, SR>(p, q, acc, table, n_tensors, shard_start, k0, n, gscale, lowp, lowp_dtype, coef, s, key,
+                        rnd.root_bits, stage);
 }
 
 template <int DT, int SR>
@@ -168,7 +170,7 @@ static zero_status launch_table8_dt(const Table8Args& a, const AdamScalars& s, c
   if (a.rounding.how == kNearest) return launch_table8_t<DT, kNearest>(a, s, st);
   if (a.rounding.how == kRoot7) return launch_table8_t<DT, kRoot7>(a, s, st);
   if (a.rounding.how == kRoot16) return launch_table8_t<DT, kRoot16>(a, s, st);
-  return launch_table8_t<DT, kRootBeta2>(a, s, st);
+  return launch_table8_t<DT, kByBeta>(a, s, st);
 }
 
 ZS_DEBUG_UNIT(adamw_table8)

@@ -1,6 +1,7 @@
 // api.cu -- the C-ABI entry points of libzeroshard (declared in
 // include/zero_shard.h): argument checking, per-step scalars, dispatch to the
 // kernel launchers, and the per-thread error message.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -481,8 +482,8 @@ static zero_status step8_tensors(const char* who, float* d_master, const zero_st
   if (n == 0) return ZERO_OK;
   const zs::Table8Args a{d_master, *q, d_acc, d_table, n_tensors, grad_dtype, shard_start, n, grad_scale, d_grad_scale,
                          d_param_lowp, lowp_dtype, d_state,
-                         d_state == nullptr ? zs::rounding_base(rounding, &step, s.b2, s.b2)
-                                            : zs::rounding_base(rounding, nullptr, 0.0f, 1.0f),
+                         d_state == nullptr ? zs::rounding_base(rounding, &step, zs::Betas{s.b1, s.b2, s.b2})
+                                            : zs::rounding_base(rounding, nullptr, zs::Betas{}),
                          d_clip};
   return zs::launch_adamw_table8(a, s, zs::as_stream(stream));
 }
@@ -587,15 +588,16 @@ zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, c
   const zero_status r = check_rounding(who, rounding);
   if (r != ZERO_OK) return r;
   zs::ListScalars s{};
-  float least = 1.0f, most = 0.0f;
+  zs::Betas b{0.0f, 1.0f, 0.0f};
   for (int32_t i = 0; i < n_groups; ++i) {
     const zero_status hs = adamw_scalars(who, &groups[i], step, &s.s[i]);
     if (hs != ZERO_OK) return hs;
-    least = s.s[i].b2 < least ? s.s[i].b2 : least;
-    most = s.s[i].b2 > most ? s.s[i].b2 : most;
+    b.beta1 = std::max(b.beta1, s.s[i].b1);
+    b.least2 = std::min(b.least2, s.s[i].b2);
+    b.most2 = std::max(b.most2, s.s[i].b2);
   }
   const zs::ListArgs a{d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
-                       lowp_dtype, nullptr, zs::rounding_base(rounding, &step, least, most), d_clip};
+                       lowp_dtype, nullptr, zs::rounding_base(rounding, &step, b), d_clip};
   return adamw_list(who, a, s, n_groups, stream);
 }
 
@@ -610,7 +612,7 @@ zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_ten
   const zero_status r = check_rounding(who, rounding);
   if (r != ZERO_OK) return r;
   const zs::ListArgs a{d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
-                       lowp_dtype, d_states, zs::rounding_base(rounding, nullptr, 0.0f, 1.0f), d_clip};
+                       lowp_dtype, d_states, zs::rounding_base(rounding, nullptr, zs::Betas{}), d_clip};
   return adamw_list(who, a, zs::ListScalars{}, n_groups, stream);
 }
 

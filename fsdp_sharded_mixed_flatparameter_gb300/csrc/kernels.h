@@ -52,15 +52,16 @@ AdamwTableInstance launch_adamw_table_p4_acc;
 // Stochastic rounding's draws, as far as the launch knows them: the hash of the
 // seed and (unless the step is on the device) of the step, and the stream.
 enum Rounding : int {
-  kNearest = 0,   // nothing is drawn
-  kRoot7 = 1,     // 7 bits for both moments
-  kRoot16 = 2,    // 7 bits for exp_avg, 16 for the root
-  kRootBeta2 = 3  // one or the other by beta2, where the launch does not know it or has several
+  kNearest = 0,  // nothing is drawn
+  kRoot7 = 1,    // 7 bits for both moments
+  kRoot16 = 2,   // 7 bits for exp_avg, 16 for the root
+  kByBeta = 3    // each moment by its beta: where the launch does not know them, has several, or a beta1 above 0.95
 };
 struct RoundingBase {
   uint32_t hash;
   uint32_t stream;
-  int how;  // Rounding
+  int how;        // Rounding
+  int root_bits;  // kByBeta: 7 or 16 for every root, 0 by beta2
 };
 
 // AdamW over a flat shard with 8-bit moments, grads through the table.

@@ -15,22 +15,30 @@ __host__ __device__ __forceinline__ uint32_t pcg_hash(uint32_t x) {
   return (x >> 22) ^ x;
 }
 
-// Whether a root needs 16 bits (beta2 as the kernels have it, in binary32).
-__host__ __device__ __forceinline__ bool root16(float beta2) {
-  return beta2 > static_cast<float>(ZERO_ROOT7_MAX_BETA2);
+// Whether a moment needs 16 bits (its beta as the kernels have it, in binary32).
+__host__ __device__ __forceinline__ bool exp_avg16(float beta1) {
+  return beta1 > static_cast<float>(ZERO_EXP_AVG7_MAX_BETA1);
+}
+__host__ __device__ __forceinline__ bool root16(float beta2, int root_bits) {
+  return root_bits == 16 || (root_bits == 0 && beta2 > static_cast<float>(ZERO_ROOT7_MAX_BETA2));
 }
 
+// The betas of a launch: with parameter groups the largest beta1, the least and
+// the largest beta2; those that the launch does not know, as they are on the
+// device, as here.
+struct Betas {
+  float beta1 = 1.0f, least2 = 0.0f, most2 = 1.0f;
+};
+
 // r: nullptr rounds to nearest.  step: nullptr when it will be read on the device.
-// least, most: the step's beta2 (with parameter groups the least and the largest;
-// 0 and 1 when the device has them).
-inline RoundingBase rounding_base(const zero_rounding* r, const int64_t* step, float least, float most) {
-  if (r == nullptr) return RoundingBase{0u, 0u, kNearest};
+inline RoundingBase rounding_base(const zero_rounding* r, const int64_t* step, const Betas& b) {
+  if (r == nullptr) return RoundingBase{0u, 0u, kNearest, 0};
   uint32_t h = pcg_hash(static_cast<uint32_t>(r->seed));
   h = pcg_hash(static_cast<uint32_t>(r->seed >> 32) ^ h);
   if (step != nullptr) h = pcg_hash(static_cast<uint32_t>(*step) ^ h);
-  int how = r->root_bits == 16 ? kRoot16 : kRoot7;
-  if (r->root_bits == 0) how = root16(least) == root16(most) ? (root16(most) ? kRoot16 : kRoot7) : kRootBeta2;
-  return RoundingBase{h, static_cast<uint32_t>(r->stream), how};
+  const bool wide = root16(b.most2, r->root_bits);
+  const int how = exp_avg16(b.beta1) || wide != root16(b.least2, r->root_bits) ? kByBeta : wide ? kRoot16 : kRoot7;
+  return RoundingBase{h, static_cast<uint32_t>(r->stream), how, r->root_bits};
 }
 
 }  // namespace zs

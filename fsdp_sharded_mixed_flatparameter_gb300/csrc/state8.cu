@@ -29,7 +29,8 @@ __device__ __forceinline__ void pack_block(const float* __restrict__ m, const fl
   }
   uint2 cm, cr;
   float sm, sr;
-  encode_block<VEC, kNearest>(xm, xr, warp_amax(xm), warp_amax(xr), 0u, 0, cm, cr, sm, sr, false, false);
+  encode_block<VEC, kNearest>(xm, xr, warp_amax(xm), warp_amax(xr), 0u, 0, cm, cr, sm, sr, false, false,
+                              false);
   store_codes<VEC>(q.exp_avg + k, left, cm);
   store_codes<VEC>(q.root + k, left, cr);
   if ((threadIdx.x & 31) == 0) {

@@ -25,12 +25,12 @@
 //   16 bits: floor((|x| / S) / u + (h + 1/2) / 65536) u,  h in [0, 65536) drawn.
 // The 16 bits keep the mean to 2^-17 u, whatever x.  The 7 bits are u / 256 low
 // on average and do not see a move of less than u / 128, which a recurrence
-// adds up over 1 / (1 - beta) steps: exp_avg is 0.7 % low at beta1 = 0.95 and
-// 3 % at 0.99, but exp_avg_sq, normal grads, 8000 steps from zero, comes to
+// adds up over 1 / (1 - beta) steps: exp_avg comes to 0.99 of what it should be
+// at beta1 = 0.95, 0.96 at 0.99 and 0.75 at 0.999; exp_avg_sq, normal grads, 8000 steps from zero, comes to
 // 0.68 of what it should be at beta2 = 0.999 and 0.24 at 0.9999 (with the 16
 // bits to 1.04 and 1.03: the square of the root's own noise).  exp_avg takes
-// the 7 bits; the root the 16 from beta2 > 0.99 on (ZERO_ROOT7_MAX_BETA2), up
-// to which the 7 bits stay as near (0.97 at 0.99, 1.01 at 0.95; 16 bits 1.04,
+// the 16 from beta1 > 0.95 on (ZERO_EXP_AVG7_MAX_BETA1), the root from beta2 >
+// 0.99 on (ZERO_ROOT7_MAX_BETA2), up to which the 7 bits stay as near (0.97 at 0.99, 1.01 at 0.95; 16 bits 1.04,
 // 1.03) in 4 instructions an element less (1.88e9 elements: 4.53 against 4.58
 // ms; a flat shard of 1.63e9: 3.89 against 3.96).  To nearest, a moment that
 // moves by less than half a spacing per step (3 to 6 %) keeps its code until
@@ -157,18 +157,26 @@ __device__ __forceinline__ uint32_t encode4_stochastic(F2 a, F2 b, uint32_t k0, 
 // added as the bytes 00 h h 80.  Below 2^-6 the grid is even: y / 2 + 2^-31 has
 // exponent 96, e = 0, and a fraction of the same units.  y above its limit by
 // an ulp (2^-20 u) cannot carry into the NaN code: h + 1/2 leaves 2^-17 u.
-__device__ __forceinline__ uint32_t encode4_root16(F2 a, F2 b, uint32_t w0, uint32_t w1) {
+// SIGNED (exp_avg): the same of |y|, under y's sign, with h's bytes exchanged, so
+// that the two moments' roundings do not go together.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t encode4_16(F2 a, F2 b, uint32_t w0, uint32_t w1) {
   float y[4];
   unpair(a, y[0], y[1]);
   unpair(b, y[2], y[3]);
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (y[i] < 0x1p-30f) y[i] = fmaf(y[i], 0.5f, 0x1p-31f);
-    const uint32_t h = __byte_perm(i < 2 ? w0 : w1, 0x80u, (i & 1) ? 0x5324 : 0x5104);
-    c[i] = (__float_as_uint(y[i]) << 4) + h;
+    const float z = fabsf(y[i]) < 0x1p-30f ? fmaf(fabsf(y[i]), 0.5f, 0x1p-31f) : y[i];
+    const uint32_t h = __byte_perm(i < 2 ? w0 : w1, 0x80u,
+                                   SIGNED ? ((i & 1) ? 0x5234 : 0x5014) : ((i & 1) ? 0x5324 : 0x5104));
+    c[i] = (__float_as_uint(z) << 4) + h;  // the sign leaves
   }
-  return __byte_perm(__byte_perm(c[0], c[1], 0x0073), __byte_perm(c[2], c[3], 0x0073), 0x5410);
+  const uint32_t code = __byte_perm(__byte_perm(c[0], c[1], 0x0073), __byte_perm(c[2], c[3], 0x0073), 0x5410);
+  if (!SIGNED) return code;
+  const uint32_t s0 = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0073);
+  const uint32_t s1 = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0073);
+  return code | (__byte_perm(s0, s1, 0x5410) & 0x80808080u);
 }
 
 // ------------------------------------------------------------------ scale
@@ -191,8 +199,8 @@ __device__ __forceinline__ void block_scale(uint32_t amax, int least, float& s, 
 // --------------------------------------------------------------- rounding
 // The key of one block's draws (pcg_hash: rounding.cuh): the word of pair i
 // (elements 2i, 2i + 1) is pcg_hash(low 32 bits of i ^ key); of each half of it
-// bits 0..6 round exp_avg and bits 7..13, or all 16, the root (the two moments'
-// roundings then share bits, which their means do not see).  The launch has hashed the
+// bits 0..6, or all 16, round exp_avg and bits 7..13, or all 16, the root (the
+// two moments' roundings then share bits, which their means do not see).  The launch has hashed the
 // seed and the step; a step on the device (ds) is hashed here.  `pair`: any
 // pair of the block (a block never crosses a multiple of 2^32 pairs).
 __device__ __forceinline__ uint32_t rounding_key(const RoundingBase& rnd, const zero_adamw_device_state* ds,
@@ -300,18 +308,19 @@ __device__ __forceinline__ uint32_t warp_amax(const F2 (&x)[4]) {
 // Codes of the warp's block (byte j of the pair = this lane's element j) and
 // its scales, from m, r = sqrt(v) and the block's max|m|, max r as bits.
 // Every lane must call it.  `pair0`: the block's first pair; lift: r is kLift times
-// the root; wide: 16 bits for the root (SR == kRootBeta2).
+// the root; wide_m, wide_r: 16 bits (SR == kByBeta).
 template <bool VEC, int SR>
 __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4], uint32_t amax_m, uint32_t amax_r,
                                              uint32_t key, int64_t pair0, uint2& cm, uint2& cr, float& sm,
-                                             float& sr, bool lift, bool wide) {
+                                             float& sr, bool lift, bool wide_m, bool wide_r) {
   float im, ir;
   block_scale(amax_m, 1, sm, im);
   block_scale(amax_r, lift ? 1 + kLiftLog2 : 1, sr, ir);
   if (lift) sr *= 1.0f / kLift;
-  if (SR != kNearest) im *= 0x1p-8f;  // 1/S >= 2^-118 in a finite block: 2^-8 of it is still normal
-  if (SR != kRootBeta2) wide = SR == kRoot16;
-  const float to = SR == kNearest ? 1.0f : wide ? 0x1p-24f : 0x1p-8f;
+  if (SR != kByBeta) wide_m = false, wide_r = SR == kRoot16;
+  // 1/S >= 2^-118 in a finite block: 2^-24 of it is not normal any more, but exact
+  im *= SR == kNearest ? 1.0f : wide_m ? 0x1p-24f : 0x1p-8f;
+  const float to = SR == kNearest ? 1.0f : wide_r ? 0x1p-24f : 0x1p-8f;
   ir *= to;  // a root is at most 2^64, 1/S at least 2^-56
   const float least = 0x1p-9f * to;  // the smallest code's value
   F2 x[4], y[4];
@@ -346,10 +355,13 @@ __device__ __forceinline__ void encode_block(const F2 (&m)[4], const F2 (&r)[4],
       km[i] = (w << 1) & 0x00fe00feu;
       wr[i] = w;
     }
-    cm = make_uint2(encode4_stochastic<true>(x[0], x[1], km[0], km[1]),
-                    encode4_stochastic<true>(x[2], x[3], km[2], km[3]));
-    if (wide) {
-      cr = make_uint2(encode4_root16(y[0], y[1], wr[0], wr[1]), encode4_root16(y[2], y[3], wr[2], wr[3]));
+    if (wide_m)
+      cm = make_uint2(encode4_16<true>(x[0], x[1], wr[0], wr[1]), encode4_16<true>(x[2], x[3], wr[2], wr[3]));
+    else
+      cm = make_uint2(encode4_stochastic<true>(x[0], x[1], km[0], km[1]),
+                      encode4_stochastic<true>(x[2], x[3], km[2], km[3]));
+    if (wide_r) {
+      cr = make_uint2(encode4_16<false>(y[0], y[1], wr[0], wr[1]), encode4_16<false>(y[2], y[3], wr[2], wr[3]));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) wr[i] = (wr[i] >> 6) & 0x00fe00feu;
@@ -444,7 +456,7 @@ template <bool VEC, int SR, int ROOTS>
 __device__ __forceinline__ void update_block(float* p, uint8_t* qm, uint8_t* qr, float* ms, float* rs,
                                              unsigned short* lowp, int lowp_dtype, int left, const float (&x)[8],
                                              const float (&g)[8], uint2 cm, uint2 cr, float sm, float sr, float coef,
-                                             const AdamScalars& s, uint32_t key, int64_t pair0) {
+                                             const AdamScalars& s, uint32_t key, int root_bits, int64_t pair0) {
   const bool lift = ROOTS != kLarge && (ROOTS == kSmall || small_roots(s, sr)) && liftable(s, sr, g, coef);
   const Factors8 f = factors8(s, sm, sr, coef, lift);
   F2 m[4], r[4];
@@ -471,7 +483,7 @@ __device__ __forceinline__ void update_block(float* p, uint8_t* qm, uint8_t* qr,
   if (lowp != nullptr) store_block_lowp<VEC>(lowp, lowp_dtype, left, y);
   // the largest root is the root of the largest exp_avg_sq
   encode_block<VEC, SR>(m, r, amax_m, __float_as_uint(__fsqrt_rn(__uint_as_float(amax_v))), key, pair0, cm, cr, sm, sr,
-                        lift, root16(s.b2));
+                        lift, exp_avg16(s.b1), root16(s.b2, root_bits));
   store_codes<VEC>(qm, left, cm);
   store_codes<VEC>(qr, left, cr);
   if ((threadIdx.x & 31) == 0) {
@@ -487,11 +499,13 @@ template <bool VEC, int SR>
 __device__ __forceinline__ void update_block_split(float* p, uint8_t* qm, uint8_t* qr, float* ms, float* rs,
                                                    unsigned short* lowp, int lowp_dtype, int left, const float (&x)[8],
                                                    const float (&g)[8], uint2 cm, uint2 cr, float sm, float sr, float coef,
-                                                   const AdamScalars& s, uint32_t key, int64_t pair0) {
+                                                   const AdamScalars& s, uint32_t key, int root_bits, int64_t pair0) {
   if (small_roots(s, sr))
-    update_block<VEC, SR, kSmall>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key, pair0);
+    update_block<VEC, SR, kSmall>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key, root_bits,
+                                 pair0);
   else
-    update_block<VEC, SR, kLarge>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key, pair0);
+    update_block<VEC, SR, kLarge>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key, root_bits,
+                                 pair0);
 }
 
 }  // namespace zs

@@ -664,7 +664,7 @@ def zero_adamw_step8_tensors(master: torch.Tensor, state8: State8, d_table: torc
     """zero_adamw_step_tensors with the moments in 8 bits; rounding_seed: None rounds them to
     nearest, an integer seeds stochastic rounding, whose stream is rounding_stream (default:
     shard_start).  root_bits: the bits drawn for a root, 7 or 16; 0: 7 up to beta2 = 0.99,
-    above it 16."""
+    above it 16 (exp_avg: 7 up to beta1 = 0.95)."""
     n, q, lp, lowp_dt = _step8_common(master, state8, d_table, n_tensors, param_lowp, clip, acc)
     hp = zero_adamw_hparams(lr, beta1, beta2, eps, weight_decay)
     _check(lib().zero_adamw_step8_tensors(

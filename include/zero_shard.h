@@ -515,11 +515,12 @@ zero_status zero_adamw_step_tensors_device(float* d_master, float* d_exp_avg, fl
  *               drawn for the element, or by 16 bits
  *               |c| = floor(|x/S| / u + (h + 1/2) / 65536) u, h in [0, 65536).
  * The 16 bits keep the mean.  The 7 bits are u / 256 low on average and do not
- * see moves of less than u / 128: exp_avg, always rounded by 7, comes out
- * 0.7 % low at beta1 = 0.95 and 3 % at 0.99; a root rounded by 7 leaves
- * exp_avg_sq within 3 % up to beta2 = 0.99, but at 0.68 of itself after 8000
- * steps at 0.999 and at 0.24 at 0.9999; rounded by 16 it stays within 5 % at any
- * beta2 (the square of its own noise).  Hence ZERO_ROOT7_MAX_BETA2.  To nearest,
+ * see moves of less than u / 128: exp_avg comes to 0.99 of itself at beta1 = 0.95,
+ * 0.96 at 0.99 and 0.75 at 0.999; a root rounded by 7 leaves exp_avg_sq within 3 %
+ * up to beta2 = 0.99, but at 0.68 of itself after 8000 steps at 0.999 and at 0.24
+ * at 0.9999; rounded by 16 it stays within 5 % at any beta2 (the square of its own
+ * noise).  Hence ZERO_EXP_AVG7_MAX_BETA1 and ZERO_ROOT7_MAX_BETA2, up to which the
+ * 7 bits are drawn, in binary32.  To nearest,
  * neither moment follows its recurrence: one that moves by less than half a
  * spacing (3 to 6 %) a step stays where it is (exp_avg_sq after 8000 steps: 4.9
  * times too large at beta2 = 0.95, 0.19 of itself at 0.999).
@@ -532,12 +533,13 @@ zero_status zero_adamw_step_tensors_device(float* d_master, float* d_exp_avg, fl
  * H the 32-bit PCG permutation RXS-M-XS, h = H(lo32 seed), h = H(hi32 seed ^
  * h), h = H(lo32 step ^ h), h = H(stream ^ h), and i the index of a pair of
  * elements 2i, 2i + 1: h = H(hi32 i ^ h), w = H(lo32 i ^ h).  The low half
- * of w is the even element's, the high half the odd one's; of each, bits 0..6
- * round exp_avg, bits 7..13 (7 bits) or the whole half (16) the root.  stream:
- * the low 32 bits of zero_rounding.stream, for a list of that plus the tensor's
+ * of w is the even element's, the high half the odd one's.  Of each half bits
+ * 0..6 (7 bits), or the whole half with its bytes exchanged (16), round exp_avg,
+ * bits 7..13 or the whole half the root.  stream: the low 32 bits of zero_rounding.stream, for a list of that plus the tensor's
  * number.
  * --------------------------------------------------------------------- */
 #define ZERO_STATE8_BLOCK 256
+#define ZERO_EXP_AVG7_MAX_BETA1 0.95
 #define ZERO_ROOT7_MAX_BETA2 0.99
 
 /* The 8-bit moments of n elements (device memory): n codes and
@@ -554,7 +556,7 @@ typedef struct zero_rounding {
   uint64_t seed;
   int64_t stream; /* its low 32 bits: ranks, or lists, that share a seed take different streams */
   int32_t root_bits; /* bits drawn for a root: 7, 16, or 0: 16 where beta2 (the tensor's group's, the
-                        device state's) is above ZERO_ROOT7_MAX_BETA2, both in binary32, else 7 */
+                        device state's) is above ZERO_ROOT7_MAX_BETA2, else 7 */
   int32_t reserved;  /* 0 */
 } zero_rounding;
 

@@ -1,5 +1,5 @@
-"""Plain 64-bit reference of the root's 16-bit stochastic rounding, one step and whole recurrences (the format and the
-7-bit rounding: _ref8.py)."""
+"""Plain 64-bit reference of stochastic rounding by 16 bits, one step and whole recurrences (the format and the 7-bit
+rounding: _ref8.py)."""
 from __future__ import annotations
 
 import numpy as np
@@ -24,6 +24,34 @@ def grid16(y: np.ndarray, h: np.ndarray) -> np.ndarray:
     y = np.where(y > 0, np.clip(y, 2.0 ** -9, 448.0), 0.0)
     u = 2.0 ** (np.floor(np.log2(np.maximum(y, 2.0 ** -6))) - 3)
     return np.floor(y / u + (h + 0.5) / 65536) * u
+
+
+def swapped(h: np.ndarray) -> np.ndarray:
+    """The two bytes of each half exchanged: what rounds exp_avg."""
+    h = h.astype(np.uint64)
+    return ((h >> np.uint64(8)) | ((h & np.uint64(255)) << np.uint64(8))).astype(np.float64)
+
+
+def signed16(x: np.ndarray, h: np.ndarray) -> np.ndarray:
+    """exp_avg over its scale on the e4m3 grid: floor(|x| / u + (h + 1/2) / 65536) u under x's sign."""
+    a = np.minimum(np.abs(x), 448.0)
+    u = 2.0 ** (np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3)
+    return np.copysign(np.floor(a / u + (h + 0.5) / 65536) * u, x)
+
+
+def check_exp_avg16(codes, scales, value, bound, h, name="exp_avg"):
+    """The stored codes and scales are what `value`, known to +- bound, rounds to with the (exchanged) draws h."""
+    n = len(codes)
+    amax, err = np.abs(R.rows(value)), R.rows(bound)
+    lo, hi = R.scale_of(np.maximum(amax - err, 0).max(1)), R.scale_of((amax + err).max(1))
+    s = scales.astype(np.float64)
+    assert ((lo <= s) & (s <= hi)).all(), f"{name}: scales"
+    per = np.repeat(s, R.BLOCK)[:n]
+    a, b = (signed16(np.maximum(np.abs(value) + k * bound, 0) / per, h) for k in (-1, 1))
+    got = R.TABLE[codes]
+    side = (np.abs(value) <= bound) | (got == 0) | (np.sign(got) == np.sign(value))
+    bad = ~(side & (a <= np.abs(got)) & (np.abs(got) <= b))
+    assert not bad.any(), (f"{name}: {int(bad.sum())} of {n} codes", value[bad][:3], got[bad][:3], a[bad][:3], b[bad][:3])
 
 
 def check_root16(codes, scales, value, bound, h, name="root"):
@@ -60,6 +88,18 @@ def follow(steps: int, b2: float, kind: str, n: int, seed: int):
         s = np.repeat(R.scale_of(R.rows(x).max(1)), R.BLOCK)[:n]
         r = grid16(x / s, halves(seed, t, 0, n)) * s
     return v, r * r
+
+
+def follow_exp_avg(steps: int, b1: float, n: int, seed: int):
+    """exp_avg after a run from zero, grads of mean 1: (the exact one, the one stored with 16-bit rounding)."""
+    e, m = np.zeros(n), np.zeros(n)
+    for t in range(1, steps + 1):
+        g = 1.0 + grads("normal", t, n).astype(np.float64)
+        e = b1 * e + (1 - b1) * g
+        x = b1 * m + (1 - b1) * g
+        s = np.repeat(R.scale_of(np.abs(R.rows(x)).max(1)), R.BLOCK)[:n]
+        m = signed16(x / s, swapped(halves(seed, t, 0, n))) * s
+    return e, m
 
 
 def run_bounds(b2: float):

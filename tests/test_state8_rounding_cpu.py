@@ -28,6 +28,21 @@ def test_sixteen_bit_rounding_has_the_right_mean():
     assert L.grid16(np.array([0.0, 1e-6]), np.array([65535.0, 0.0])).tolist() == [0.0, 2.0 ** -9]
 
 
+def test_sixteen_bits_keep_a_signed_mean():
+    h = np.arange(65536.0)
+    assert sorted(L.swapped(h)) == h.tolist()
+    for x in np.concatenate([np.random.default_rng(1).uniform(-448, 448, 60), -np.geomspace(2.0 ** -12, 2.0 ** -5, 30), [-448.0]]):
+        u = 2.0 ** (np.floor(np.log2(max(abs(x), 2.0 ** -6))) - 3)
+        assert abs(L.signed16(np.full(65536, x), L.swapped(h)).mean() - x) <= u * 2.0 ** -17 * 1.001
+
+
+@pytest.mark.parametrize("b1", [0.95, 0.99, 0.999])
+def test_sixteen_bits_follow_exp_avg(b1):
+    # the mean is kept at each step; 2048 elements' own noise, a spacing each at most, is under 1 % of their mean
+    e, m = L.follow_exp_avg(2500, b1, 2048, seed=3)
+    assert abs(m.mean() / e.mean() - 1) <= 0.01
+
+
 @pytest.mark.parametrize("kind", ["normal", "constant"])
 @pytest.mark.parametrize("b2", [0.9, 0.95, 0.99, 0.999, 0.9999])
 def test_sixteen_bits_follow_exp_avg_sq(b2, kind):
