@@ -6,7 +6,9 @@
 // 16 bytes an element with 16-bit grads and copy, and 52 instructions (65
 // with stochastic rounding, 68 with 16 bits for the root): near the
 // bandwidth's and the issue rate's limit at once.  Eight layers of Llama-7B
-// (1.88e9 elements), stochastic: 4.50 ms = 6.72 TB/s (16 bits: 4.55); four
+// (1.88e9 elements), stochastic: 4.50 ms = 6.72 TB/s (16 bits: 4.55; with the
+// bits chosen in the kernel by the device's betas 4.60, 4.71 with 16 for the
+// root, 4.86 with 16 for both); four
 // layers (1.07e9): 2.49 ms to nearest (6.93 TB/s), 2.58 stochastic, 2.51 to
 // nearest with grads off the 16-byte grid; fp32 grads 2.71 on and off theirs.
 // 4000 log-uniform tensors (302e6): 0.81 ms = 5.98 TB/s, where short last

@@ -501,11 +501,11 @@ __device__ __forceinline__ void update_block_split(float* p, uint8_t* qm, uint8_
                                                    const float (&g)[8], uint2 cm, uint2 cr, float sm, float sr, float coef,
                                                    const AdamScalars& s, uint32_t key, int root_bits, int64_t pair0) {
   if (small_roots(s, sr))
-    update_block<VEC, SR, kSmall>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key, root_bits,
-                                 pair0);
+    update_block<VEC, SR, kSmall>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key,
+                                 root_bits, pair0);
   else
-    update_block<VEC, SR, kLarge>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key, root_bits,
-                                 pair0);
+    update_block<VEC, SR, kLarge>(p, qm, qr, ms, rs, lowp, lowp_dtype, left, x, g, cm, cr, sm, sr, coef, s, key,
+                                 root_bits, pair0);
 }
 
 }  // namespace zs

@@ -535,8 +535,8 @@ zero_status zero_adamw_step_tensors_device(float* d_master, float* d_exp_avg, fl
  * elements 2i, 2i + 1: h = H(hi32 i ^ h), w = H(lo32 i ^ h).  The low half
  * of w is the even element's, the high half the odd one's.  Of each half bits
  * 0..6 (7 bits), or the whole half with its bytes exchanged (16), round exp_avg,
- * bits 7..13 or the whole half the root.  stream: the low 32 bits of zero_rounding.stream, for a list of that plus the tensor's
- * number.
+ * bits 7..13 or the whole half the root.  stream: the low 32 bits of
+ * zero_rounding.stream, for a list of that plus the tensor's number.
  * --------------------------------------------------------------------- */
 #define ZERO_STATE8_BLOCK 256
 #define ZERO_EXP_AVG7_MAX_BETA1 0.95
