@@ -62,16 +62,24 @@ class GradTables:
         self.numels = [int(n) for n in numels]
         self.total = int(sum(self.numels))
         self.device = torch.device(device)
+        self._index = None  # of the device; its current stream is asked for at each launch
+        if self.device.type == "cuda":
+            self._index = torch.cuda.current_device() if self.device.index is None else self.device.index
         self._registered = None
         self._tables: Dict[tuple, GradTable] = {}
         self._captured: Dict[int, torch.Tensor] = {}  # tables that a captured graph reads, by address
 
-    @staticmethod
-    def _keep(cache: Dict[tuple, GradTable], key: tuple, table: torch.Tensor) -> GradTable:
+    def _handle(self, stream) -> int:
+        """The handle of a stream argument, None being the current stream of this device."""
+        if stream is None and self._index is not None:
+            return zs._current_handle(self._index)
+        return zs._stream(stream)
+
+    def _keep(self, cache: Dict[tuple, GradTable], key: tuple, table: torch.Tensor) -> GradTable:
         """Cache a new table, the oldest one making room."""
         if len(cache) >= KEPT_TABLES:
             cache.pop(next(iter(cache)))
-        hit = cache[key] = GradTable(table, zs._stream(None))
+        hit = cache[key] = GradTable(table, self._handle(None))
         return hit
 
     def _read_on(self, hit: GradTable, stream: int) -> torch.Tensor:
@@ -139,7 +147,7 @@ class GradTables:
     def _launch_tables(self, grads, stream):
         """(table, tensor count, grad dtype, stream handle) for kernels launched now on `stream`."""
         hit, count, dt = self._resolve(grads)
-        raw = zs._stream(stream)
+        raw = self._handle(stream)
         table, own = hit
         if raw != own or torch.cuda.is_current_stream_capturing():
             self._read_elsewhere(table, raw)
@@ -359,7 +367,7 @@ class FlatShardAdamW(GradTables):
         if self.capturable:
             zs.zero_adamw_prepare_device(self._dev_hp, clip, self._dev_state, stream)
         if self.state_bits == 8:
-            table = self._read_on(self._own_grad_table(), zs._stream(stream))
+            table = self._read_on(self._own_grad_table(), self._handle(stream))
             self._update_tables(table, 1, self.grad.numel(), torch.float32, self.start - self.glo, 1.0, None, None, clip,
                                 stream)
         elif self.capturable:
@@ -376,7 +384,7 @@ class FlatShardAdamW(GradTables):
             raise ValueError("this step needs the grad buffer (grad_buffer=True)")
         if self._grad_table is None or self._grad_table[0] != self.grad.data_ptr():
             table = zs.device_table(zs.zero_tensor_table([self.grad])[0], 1, self.device)
-            self._grad_table = (self.grad.data_ptr(), GradTable(table, zs._stream(None)))
+            self._grad_table = (self.grad.data_ptr(), GradTable(table, self._handle(None)))
         return self._grad_table[1]
 
     def _update_tables(self, table, count: int, total: int, dt, shard_start: int, scale: float, d_scale, acc, clip,
@@ -477,7 +485,7 @@ class FlatShardAdamW(GradTables):
         """Enqueue step_flat() without waiting (capturable once device_flat_table(flat_src)
         has been called outside the capture)."""
         hit = self._flat_table(flat_src)
-        raw = zs._stream(stream)
+        raw = self._handle(stream)
         table = self._read_on(hit, raw)
         span = self.ghi - self.glo
         self._launch_direct(table, 1, span, flat_src.dtype, 0, span, self.start - self.glo, scale, accumulated, raw,
