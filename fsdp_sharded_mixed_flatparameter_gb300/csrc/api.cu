@@ -318,6 +318,157 @@ zero_status zero_adamw_step_tensors(float* d_master, float* d_exp_avg, float* d_
                                 d_clip, zs::as_stream(stream));
 }
 
+// ------------------------------------------------ norms and clipping of a list
+zero_status zero_grad_plan(const int64_t* numels, const int32_t* groups, int32_t n_tensors, int32_t n_groups,
+                           int32_t* plan, int32_t* n_chunks, int32_t* chunk) {
+  const char* who = "zero_grad_plan";
+  if (n_tensors < 1 || n_groups < 1 || n_tensors > (1 << 30) - n_groups)
+    return fail(ZERO_EINVAL, "%s: %d tensors in %d groups", who, (int)n_tensors, (int)n_groups);
+  if (numels == nullptr || plan == nullptr || n_chunks == nullptr || chunk == nullptr)
+    return fail(ZERO_EINVAL, "%s: NULL argument", who);
+  int64_t total = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    if (numels[i] < 0) return fail(ZERO_EINVAL, "%s: numel[%d] = %lld < 0", who, (int)i, (long long)numels[i]);
+    if (numels[i] > INT64_MAX - total) return fail(ZERO_EINVAL, "%s: total overflows int64", who);
+    if (groups != nullptr && (groups[i] < 0 || groups[i] >= n_groups))
+      return fail(ZERO_EINVAL, "%s: group[%d] = %d of %d", who, (int)i, (int)groups[i], (int)n_groups);
+    total += numels[i];
+  }
+  const int32_t size = zs::grad_chunk_size(total);
+  int32_t* const first = plan;
+  int32_t* const group_first = plan + n_tensors + 1;
+  int32_t* const members = group_first + n_groups + 1;
+  int64_t count = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    first[i] = static_cast<int32_t>(count);
+    count += numels[i] / size + (numels[i] % size != 0 ? 1 : 0);
+    if (count > INT32_MAX) return fail(ZERO_EINVAL, "%s: 2^31 chunks or more up to tensor %d", who, (int)i);
+  }
+  first[n_tensors] = static_cast<int32_t>(count);
+  // counting sort: group_first[g + 1] counts group g, then becomes where it starts, then where it ends
+  for (int32_t g = 0; g <= n_groups; ++g) group_first[g] = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) ++group_first[(groups ? groups[i] : 0) + 1];
+  for (int32_t g = 0, at = 0; g < n_groups; ++g) {
+    const int32_t c = group_first[g + 1];
+    group_first[g + 1] = at;
+    at += c;
+  }
+  for (int32_t i = 0; i < n_tensors; ++i) members[group_first[(groups ? groups[i] : 0) + 1]++] = i;
+  *n_chunks = static_cast<int32_t>(count);
+  *chunk = size;
+  return ZERO_OK;
+}
+
+zero_status zero_grad_entries_check(const zero_grad_entry* entries, const int64_t* numels, int32_t n_tensors,
+                                    int32_t n_groups) {
+  const char* who = "zero_grad_entries_check";
+  if (n_tensors < 1 || n_groups < 1 || entries == nullptr || numels == nullptr)
+    return fail(ZERO_EINVAL, "%s: an empty list or a NULL argument", who);
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const zero_grad_entry& t = entries[i];
+    if (t.numel < 0 || t.numel != numels[i])
+      return fail(ZERO_EINVAL, "%s: tensor %d has %lld elements, expected %lld", who, (int)i, (long long)t.numel,
+                  (long long)numels[i]);
+    if (t.group < 0 || t.group >= n_groups)
+      return fail(ZERO_EINVAL, "%s: group[%d] = %d of %d", who, (int)i, (int)t.group, (int)n_groups);
+    if (t.reserved != 0) return fail(ZERO_EINVAL, "%s: reserved[%d] != 0", who, (int)i);
+    if (!zs::valid_dtype(t.src_dtype) || !zs::valid_dtype(t.dst_dtype))
+      return fail(ZERO_EINVAL, "%s: bad dtype of tensor %d", who, (int)i);
+    if (!zs::aligned(t.src, t.src_dtype == ZERO_F32 ? 4 : 2) || !zs::aligned(t.dst, t.dst_dtype == ZERO_F32 ? 4 : 2))
+      return fail(ZERO_EINVAL, "%s: a buffer of tensor %d is not aligned to its elements", who, (int)i);
+    if (t.dst != nullptr && t.dst == t.src && t.dst_dtype != t.src_dtype)
+      return fail(ZERO_EINVAL, "%s: tensor %d is clipped in place into another type", who, (int)i);
+  }
+  return ZERO_OK;
+}
+
+size_t zero_list_norms_workspace_bytes(int32_t n_chunks) {
+  return n_chunks <= 0 ? 0 : static_cast<size_t>(n_chunks) * sizeof(double);
+}
+
+// The list's own checks, and its arguments for the launchers.
+static zero_status grad_list_args(const char* who, const zero_grad_list* l, bool entries, float scale,
+                                  const float* d_scale, zs::GradListArgs* a) {
+  if (l == nullptr || l->n_tensors < 1 || l->n_groups < 1 || l->n_chunks < 0 || l->reserved != 0)
+    return fail(ZERO_EINVAL, "%s: bad list", who);
+  if (l->chunk < 1 || l->chunk > zs::kMaxGradChunk) return fail(ZERO_EINVAL, "%s: chunk %d", who, (int)l->chunk);
+  if (l->norm_type != ZERO_NORM_INF && l->norm_type != ZERO_NORM_1 && l->norm_type != ZERO_NORM_2)
+    return fail(ZERO_EINVAL, "%s: bad norm_type %d", who, (int)l->norm_type);
+  if (l->d_plan == nullptr || !zs::aligned(l->d_plan, 4)) return fail(ZERO_EINVAL, "%s: NULL or misaligned d_plan", who);
+  if (entries && (l->d_entries == nullptr || !zs::aligned(l->d_entries, 8)))
+    return fail(ZERO_EINVAL, "%s: NULL or misaligned d_entries", who);
+  if (!std::isfinite(scale)) return fail(ZERO_EINVAL, "%s: non-finite scale", who);
+  if (!zs::aligned(d_scale, 4)) return fail(ZERO_EINVAL, "%s: d_scale not 4-byte aligned", who);
+  *a = zs::GradListArgs{l->d_entries, l->d_plan, l->n_tensors, l->n_groups, l->n_chunks,
+                        l->chunk,     l->norm_type, scale,     d_scale};
+  return ZERO_OK;
+}
+
+static zero_status check_list_ws(const char* who, const zs::GradListArgs& a, const void* ws, size_t ws_bytes,
+                                 const double* sums) {
+  const size_t need = zero_list_norms_workspace_bytes(a.n_chunks);
+  if (need > 0 && (ws == nullptr || ws_bytes < need))
+    return fail(ZERO_EINVAL, "%s: workspace %zu bytes < %zu needed", who, ws ? ws_bytes : 0, need);
+  if (!zs::aligned(ws, 8)) return fail(ZERO_EINVAL, "%s: workspace not 8-byte aligned", who);
+  if (sums == nullptr || !zs::aligned(sums, 8)) return fail(ZERO_EINVAL, "%s: NULL or misaligned d_sums", who);
+  return ZERO_OK;
+}
+
+static zero_status check_norm_outputs(const char* who, const double* max_norms, const float* norms,
+                                      const zero_norm_result* results, const int32_t* found) {
+  if (max_norms == nullptr || norms == nullptr || results == nullptr) return fail(ZERO_EINVAL, "%s: NULL buffer", who);
+  if (!zs::aligned(max_norms, 8) || !zs::aligned(norms, 4) || !zs::aligned(results, 8) || !zs::aligned(found, 4))
+    return fail(ZERO_EINVAL, "%s: misaligned buffer", who);
+  return ZERO_OK;
+}
+
+zero_status zero_list_sums(const zero_grad_list* list, float scale, const float* d_scale, void* d_ws, size_t ws_bytes,
+                           double* d_sums, void* stream) {
+  zs::GradListArgs a;
+  zero_status s = grad_list_args("zero_list_sums", list, true, scale, d_scale, &a);
+  if (s == ZERO_OK) s = check_list_ws("zero_list_sums", a, d_ws, ws_bytes, d_sums);
+  if (s != ZERO_OK) return s;
+  return zs::launch_list_sums(a, static_cast<double*>(d_ws), d_sums, zs::as_stream(stream));
+}
+
+zero_status zero_sums_norms(const zero_grad_list* list, const double* d_sums, int32_t n_parts,
+                            const double* d_max_norms, float* d_norms, zero_norm_result* d_results,
+                            int32_t* d_found_nonfinite, void* stream) {
+  zs::GradListArgs a;
+  zero_status s = grad_list_args("zero_sums_norms", list, false, 1.0f, nullptr, &a);
+  if (s == ZERO_OK) s = check_norm_outputs("zero_sums_norms", d_max_norms, d_norms, d_results, d_found_nonfinite);
+  if (s != ZERO_OK) return s;
+  if (n_parts < 1) return fail(ZERO_EINVAL, "zero_sums_norms: n_parts %d < 1", (int)n_parts);
+  if (d_sums == nullptr || !zs::aligned(d_sums, 8)) return fail(ZERO_EINVAL, "zero_sums_norms: NULL or misaligned d_sums");
+  return zs::launch_sums_norms(a, d_sums, n_parts, d_max_norms, d_norms, d_results, d_found_nonfinite,
+                               zs::as_stream(stream));
+}
+
+zero_status zero_list_clip(const zero_grad_list* list, float scale, const float* d_scale,
+                           const zero_norm_result* d_results, void* stream) {
+  zs::GradListArgs a;
+  const zero_status s = grad_list_args("zero_list_clip", list, true, scale, d_scale, &a);
+  if (s != ZERO_OK) return s;
+  if (d_results == nullptr || !zs::aligned(d_results, 8))
+    return fail(ZERO_EINVAL, "zero_list_clip: NULL or misaligned d_results");
+  return zs::launch_list_clip(a, d_results, zs::as_stream(stream));
+}
+
+zero_status zero_list_norms(const zero_grad_list* list, float scale, const float* d_scale, int32_t clip, void* d_ws,
+                            size_t ws_bytes, double* d_sums, const double* d_max_norms, float* d_norms,
+                            zero_norm_result* d_results, int32_t* d_found_nonfinite, void* stream) {
+  zs::GradListArgs a;
+  zero_status s = grad_list_args("zero_list_norms", list, true, scale, d_scale, &a);
+  if (s == ZERO_OK) s = check_list_ws("zero_list_norms", a, d_ws, ws_bytes, d_sums);
+  if (s == ZERO_OK) s = check_norm_outputs("zero_list_norms", d_max_norms, d_norms, d_results, d_found_nonfinite);
+  if (s != ZERO_OK) return s;
+  s = zs::launch_list_sums(a, static_cast<double*>(d_ws), d_sums, zs::as_stream(stream));
+  if (s == ZERO_OK)
+    s = zs::launch_sums_norms(a, d_sums, 1, d_max_norms, d_norms, d_results, d_found_nonfinite, zs::as_stream(stream));
+  if (s == ZERO_OK && clip != 0) s = zs::launch_list_clip(a, d_results, zs::as_stream(stream));
+  return s;
+}
+
 // ------------------------------------------------------------- debug builds
 zero_status zero_debug_errors(uint64_t* out, int32_t reset) {
   if (out == nullptr) return fail(ZERO_EINVAL, "zero_debug_errors: NULL out");
@@ -327,7 +478,8 @@ zero_status zero_debug_errors(uint64_t* out, int32_t reset) {
       zs::debug_read_adamw_table_p4, zs::debug_read_adamw_table_p4_acc, zs::debug_read_adamw_device,
       zs::debug_read_adamw_list,     zs::debug_read_adamw_list8,       zs::debug_read_adamw_table8,
       zs::debug_read_state8,
-      zs::debug_read_flatten,        zs::debug_read_sqnorm};
+      zs::debug_read_flatten,        zs::debug_read_sqnorm,           zs::debug_read_list_norms,
+      zs::debug_read_list_clip};
   uint64_t total = 0, first[3] = {0, 0, 0};
   for (auto rd : readers) {
     unsigned long long r[4];

@@ -110,6 +110,27 @@ zero_status launch_adamw_list8(const ListArgs& a, const ListScalars& s, cudaStre
 zero_status launch_state8_pack(const float* m, const float* v, int64_t n, const zero_state8& q, cudaStream_t st);
 zero_status launch_state8_unpack(const zero_state8& q, int64_t n, float* m, float* v, cudaStream_t st);
 
+// Elements of a grads list's chunks, by the list's total.
+constexpr int kMaxGradChunk = 65536;
+inline int grad_chunk_size(int64_t total) {
+  return total <= (int64_t(1) << 23) ? 4096 : total <= (int64_t(1) << 28) ? 16384 : kMaxGradChunk;
+}
+
+// The norms of a grads list and its clipping (arguments checked; plan: zero_grad_plan's ints).
+struct GradListArgs {
+  const zero_grad_entry* entries;
+  const int32_t* plan;
+  int n, n_groups;
+  int32_t n_chunks;
+  int chunk, norm_type;
+  float scale;
+  const float* dscale;
+};
+zero_status launch_list_sums(const GradListArgs& a, double* partials, double* sums, cudaStream_t st);
+zero_status launch_sums_norms(const GradListArgs& a, const double* sums, int n_parts, const double* max_norms,
+                              float* norms, zero_norm_result* results, int32_t* found, cudaStream_t st);
+zero_status launch_list_clip(const GradListArgs& a, const zero_norm_result* results, cudaStream_t st);
+
 // Debug builds (ZERO_DEBUG): each translation unit's violation record
 // {count, first site, first index, first block}; reset clears it.
 zero_status debug_read_adamw(unsigned long long* out, bool reset);
@@ -123,6 +144,8 @@ zero_status debug_read_adamw_list8(unsigned long long* out, bool reset);
 zero_status debug_read_adamw_table8(unsigned long long* out, bool reset);
 zero_status debug_read_state8(unsigned long long* out, bool reset);
 zero_status debug_read_flatten(unsigned long long* out, bool reset);
+zero_status debug_read_list_norms(unsigned long long* out, bool reset);
+zero_status debug_read_list_clip(unsigned long long* out, bool reset);
 zero_status debug_read_sqnorm(unsigned long long* out, bool reset);
 zero_status launch_debug_selftest(long long index, cudaStream_t st);
 

@@ -165,10 +165,16 @@ class ZeroDataPlane:
             with self._on(stream):
                 gather_shards(self.flat_param, self.group)
 
-    def step(self, stream=None) -> zs.NormResult:
-        """Clip with the global norm, AdamW on the shard, then all-gather the
+    def grad_clip(self, **kw):
+        """A GradClip over this rank's shard grad for step(clip=...): the norm of every tensor over
+        all ranks, a limit per group of tensors (FlatShardAdamW.grad_clip)."""
+        return self.opt.grad_clip(**kw)
+
+    def step(self, stream=None, clip=None) -> zs.NormResult:
+        """Clip with the global norm, or with `clip` (a grad_clip() of this rank; the ranks exchange
+        their tensors' sums, 8 bytes per tensor and rank), AdamW on the shard, then all-gather the
         updated parameters (skipped with the step when the norm is not finite)."""
-        r = self.opt.step(stream=stream, process_group=self.group)
+        r = self.opt.step(stream=stream, process_group=self.group, clip=clip)
         if r.finite:
             self.all_gather_params(stream)
         return r

@@ -1,0 +1,242 @@
+"""GradClip: the norms of many tensors and their clipping, in place or into other buffers.
+
+``clip_grad_norm_`` of the pages' loops for grads that this library's AdamW does not
+read (it folds one clip over everything into its own pass): tensors of mixed
+types, the norm of each tensor and of groups of tensors beside the norm of all,
+p = 1, 2 or infinity, a limit for each group, unscaling in the same pass, and the
+same for one rank's flat shard, joined with the other ranks' sums.  Nothing
+waits for the host, so a whole step can be captured in a graph.
+"""
+from __future__ import annotations
+
+import contextlib
+import math
+from typing import NamedTuple, Optional, Sequence, Union
+
+import numpy as np
+import torch
+
+from . import zero_shard as zs
+from .optimizer import GradTable, GradTables, gather_sqnorms, torch_stream
+
+
+class ClipResult(NamedTuple):
+    """A clip read on the host: the norm over all tensors, whether it is finite (if not, no
+    grad was written), each group's norm (float64) and coefficient (float32)."""
+    norm: float
+    finite: bool
+    group_norms: np.ndarray
+    coefs: np.ndarray
+    whole: zs.NormResult
+
+
+class GradClip(GradTables):
+    """The clip over tensors of the sizes `numels`.  max_norm: the limit, or one per group (inf:
+    not clipped); group_of: each tensor's group (default: all in group 0), with
+    range(len(numels)) each tensor is clipped by its own norm; norm_type: 1, 2 or inf.
+
+    After a launch, on the device: ``tensor_norms``, ``group_norms`` (float32), ``norm`` (0-d),
+    ``tensor_sums`` (float64, this rank's), ``results`` (a zero_norm_result per group) and
+    ``result``, the one over all with a coefficient of 1: what launch_step(norm_result=...) of
+    the optimizers takes after the grads have been clipped here.  The buffers are rewritten by
+    each launch: launches of one object that overlap on the GPU race, and the object has to
+    outlive the graphs that captured it."""
+
+    def __init__(self, numels: Sequence[int], *, max_norm: Union[float, Sequence[float]] = math.inf,
+                 norm_type: float = 2.0, group_of: Optional[Sequence[int]] = None, device="cuda"):
+        self._init_tables(numels, device)
+        if isinstance(max_norm, (int, float)):
+            n_groups = 1 if group_of is None or len(group_of) == 0 else int(max(group_of)) + 1
+        else:
+            n_groups = len(max_norm)
+        self.norm_type, self.n_groups = float(norm_type), n_groups
+        if not self.numels:
+            raise ValueError("an empty tensor list")
+        dev = self.device
+        limits = self._limits(max_norm)
+        _not_in_capture(self._index)
+        self.plan = zs.zero_grad_plan(self.numels, group_of, n_groups, norm_type, dev)
+        n, g = len(self.numels), n_groups
+        self.max_norms = limits.to(dev)
+        self.ws = torch.empty(max(zs.zero_list_norms_workspace_bytes(self.plan.n_chunks), 8), dtype=torch.uint8,
+                              device=dev)
+        self.tensor_sums = torch.zeros(n, dtype=torch.float64, device=dev)
+        self.norms = torch.zeros(n + g + 1, dtype=torch.float32, device=dev)
+        self.tensor_norms, self.group_norms, self.norm = self.norms[:n], self.norms[n:n + g], self.norms[n + g]
+        self.results = torch.zeros((g + 1) * zs.NORM_RESULT_BYTES, dtype=torch.uint8, device=dev)
+        self.result = self.results[g * zs.NORM_RESULT_BYTES:]
+        self.found_nonfinite = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._home = self._current()  # the stream whose order the buffers' memory follows
+        self.shard: Optional[torch.Tensor] = None
+
+    @classmethod
+    def of_shard(cls, numels: Sequence[int], grad: torch.Tensor, start: int, **kw) -> "GradClip":
+        """The clip over one rank's flat grad: elements start .. start + grad.numel() of the
+        FlatParameter of the tensors `numels`.  tensor_sums are those of the pieces that lie in it
+        (0 for a tensor elsewhere); launch(process_group=...) or launch_sums() and
+        launch(gathered_sums=...) join them with the other ranks'."""
+        if grad.dim() != 1 or not grad.is_contiguous():
+            raise ValueError("the shard's grad must be 1-D and contiguous")
+        sizes = np.asarray([int(k) for k in numels], dtype=np.int64)
+        ends = np.cumsum(sizes)
+        end, total = start + grad.numel(), int(ends[-1]) if len(ends) else 0
+        if start < 0 or end > total:
+            raise ValueError(f"[{start}, {end}) is not a shard of {total} elements")
+        lo, hi = np.maximum(ends - sizes, start), np.minimum(ends, end)
+        local = np.maximum(0, hi - lo)
+        clip = cls(local.tolist(), **{"device": grad.device, **kw})
+        clip.register_grads([grad[a - start:a - start + k] if k else None for a, k in zip(lo.tolist(), local.tolist())])
+        clip.shard = grad
+        return clip
+
+    # ------------------------------------------------------------ limits
+    def _limits(self, max_norm) -> torch.Tensor:
+        values = [max_norm] * self.n_groups if isinstance(max_norm, (int, float)) else list(max_norm)
+        if len(values) != self.n_groups:
+            raise ValueError(f"{len(values)} limits for {self.n_groups} groups")
+        if any(math.isnan(v) or v < 0 for v in values):
+            raise ValueError("max_norm must be >= 0")
+        return torch.tensor([float(v) for v in values], dtype=torch.float64)
+
+    def set_max_norm(self, max_norm: Union[float, Sequence[float]]) -> None:
+        """Change the limits (also for the next replay of a captured graph)."""
+        self.max_norms.copy_(self._limits(max_norm))
+
+    # ------------------------------------------------------------- grads
+    def register_grads(self, grads: Sequence[Optional[torch.Tensor]],
+                       out: Optional[Sequence[Optional[torch.Tensor]]] = None, *, write: bool = True) -> None:
+        """Fix the grads once: per tensor an f32, bf16 or f16 tensor, or None (reads as zeros).
+        out: other buffers for the clipped grads (None for a tensor: it is not written; a
+        tensor without a grad gets zeros); without it they are clipped in place.  A launch
+        without grads then does no work per tensor on the host, and can be captured.
+        write=False: for norms only; a tensor may then be listed twice."""
+        self._registered = self._entries(grads, out, write)
+
+    def _entries(self, grads, out, write):
+        _not_in_capture(self._index)
+        gl = zs.grad_list(self.plan, grads, out, write)
+        return gl, GradTable(gl.entries, self._current()), write
+
+    def _current(self) -> int:
+        return 0 if self._index is None else self._handle(None)  # host: only to be refused at a launch
+
+    def _list(self, grads, out, write):
+        if grads is not None:
+            return self._entries(grads, out, write)
+        if out is not None:
+            raise ValueError("out needs grads")
+        if self._registered is None:
+            raise ValueError("no grads given and none registered")
+        if write and not self._registered[2]:
+            raise ValueError("the registered grads are for norms only (write=False)")
+        return self._registered
+
+    def _here(self):
+        """Make the clip's device the current one, if it is not."""
+        if self._index is None or torch.cuda.current_device() == self._index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(self._index)
+
+    def _on(self, stream, table: GradTable) -> int:
+        """The handle of the stream to launch on, its use of the object's memory noted."""
+        if self._index is None:
+            return 0
+        raw = self._handle(stream)
+        self._read_on(table, raw)
+        if raw != self._home and not torch.cuda.is_current_stream_capturing():
+            st = torch_stream(raw, self.device)
+            for t in (self.plan.ints, self.max_norms, self.ws, self.tensor_sums, self.norms, self.results):
+                t.record_stream(st)
+        return raw
+
+    # ------------------------------------------------------------ launch
+    def launch_sums(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, scale: float = 1.0,
+                    loss_scale=None, stream=None) -> None:
+        """Enqueue each tensor's sum into ``tensor_sums``: what ranks exchange."""
+        sc, dsc, _ = self._scale_args(scale, loss_scale)
+        with self._here():
+            gl, table, _ = self._list(grads, None, False)
+            zs.zero_list_sums(gl, sc, self.ws, self.tensor_sums, self._on(stream, table), d_scale=dsc)
+
+    def launch_norms(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, scale: float = 1.0,
+                     loss_scale=None, gathered_sums: Optional[torch.Tensor] = None, process_group=None,
+                     stream=None) -> None:
+        """launch() without writing any grad."""
+        self._launch(False, grads, None, scale, loss_scale, gathered_sums, process_group, stream)
+
+    def launch(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *,
+               out: Optional[Sequence[Optional[torch.Tensor]]] = None, scale: float = 1.0, loss_scale=None,
+               gathered_sums: Optional[torch.Tensor] = None, process_group=None, stream=None) -> None:
+        """Enqueue the norms and the clipping without waiting.  grads, out: as register_grads takes
+        them, for this launch (default: the registered ones).  scale: multiplies every grad before
+        the norm (unscaling, averaging); loss_scale: a DeviceLossScale, whose unscale factor
+        replaces `scale` and whose flag a norm that is not finite raises.  gathered_sums: the
+        ranks' tensor_sums in rank order, [ranks, tensors] (launch_sums() has run, its row is this
+        rank's); process_group: the sums are gathered here, ordered on `stream`.
+
+        y = scale * coefficient * x, written where the norm over all tensors is finite."""
+        self._launch(True, grads, out, scale, loss_scale, gathered_sums, process_group, stream)
+
+    def _launch(self, clip, grads, out, scale, loss_scale, gathered, process_group, stream) -> None:
+        sc, dsc, _ = self._scale_args(scale, loss_scale)
+        flag = self.found_nonfinite if loss_scale is None else loss_scale.found_inf
+        n = len(self.numels)
+        if gathered is not None and (gathered.numel() == 0 or gathered.numel() % n
+                                     or gathered.device != self.plan.ints.device):
+            raise ValueError(f"gathered_sums must be [ranks, {n}] on {self.plan.ints.device}")
+        with self._here():
+            gl, table, _ = self._list(grads, out, clip)
+            raw = self._on(stream, table)
+            if gathered is None and process_group is not None and _world(process_group) > 1:
+                zs.zero_list_sums(gl, sc, self.ws, self.tensor_sums, raw, d_scale=dsc)
+                with torch.cuda.stream(torch_stream(raw, self.device)):
+                    gathered = gather_sqnorms(self.tensor_sums, process_group)
+            if gathered is None:
+                zs.zero_list_norms(gl, sc, clip, self.ws, self.tensor_sums, self.max_norms, self.norms, self.results,
+                                   flag, raw, d_scale=dsc)
+                return
+            zs.zero_sums_norms(gl, gathered, gathered.numel() // n, self.max_norms, self.norms, self.results, flag, raw)
+            if clip:
+                zs.zero_list_clip(gl, sc, self.results, raw, d_scale=dsc)
+
+    def finish(self, stream=None) -> ClipResult:
+        """Read the last launch's result (a device-to-host copy on `stream`, where it was enqueued)."""
+        with torch.cuda.stream(torch_stream(stream, self.device)):
+            raw = self.results.cpu()
+        r = np.frombuffer(raw.numpy().tobytes(), dtype=_RESULT)
+        whole = zs.decode_norm_result(raw[self.n_groups * zs.NORM_RESULT_BYTES:])
+        return ClipResult(whole.norm, whole.finite, r["norm"][:-1].copy(), r["clip_coef"][:-1].copy(), whole)
+
+    def clip_(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, **kw) -> ClipResult:
+        """launch() and finish(): one clip, read on the host."""
+        self.launch(grads, **kw)
+        return self.finish(kw.get("stream"))
+
+
+_RESULT = np.dtype([("sqnorm", np.float64), ("norm", np.float64), ("clip_coef", np.float32), ("finite", np.int32)])
+
+
+def clip_grad_norm_(grads: Sequence[Optional[torch.Tensor]], max_norm: float, norm_type: float = 2.0, *,
+                    scale: float = 1.0, stream=None) -> torch.Tensor:
+    """Clip `grads` in place by the norm of all of them and return that norm (a 0-d float32
+    device tensor) without waiting.  Where it is not finite nothing is written.  For a
+    loop, a GradClip with registered grads spares the table's copy at each call."""
+    grads = list(grads)
+    some = [g for g in grads if g is not None]
+    if not some:
+        raise ValueError("no grads")
+    clip = GradClip([0 if g is None else g.numel() for g in grads], max_norm=max_norm, norm_type=norm_type,
+                    device=some[0].device)
+    clip.launch(grads, scale=scale, stream=stream)
+    return clip.norm
+
+
+def _not_in_capture(index) -> None:
+    """Tables are copied to the device when a clip is made or grads are registered: not in a capture."""
+    if index is not None and torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("make the GradClip and register its grads before the capture")
+
+
+def _world(group) -> int:
+    import torch.distributed as dist
+    return dist.get_world_size(group)

@@ -425,13 +425,40 @@ class FlatShardAdamW(GradTables):
         with torch.cuda.stream(stream):
             return gather_sqnorms(local, process_group)
 
-    def step(self, extra_sqnorm: float = 0.0, stream=None, process_group=None) -> zs.NormResult:
+    def grad_clip(self, **kw) -> "GradClip":
+        """A GradClip over this rank's grad buffer (max_norm, norm_type, group_of: see there): the
+        norm of every tensor and clips of groups of tensors, for step(clip=...)."""
+        from .grad_clip import GradClip
+        if self.grad.numel() != self.ghi - self.glo:
+            raise ValueError("grad_clip() needs the grad buffer (grad_buffer=True)")
+        return GradClip.of_shard(self.numels, self.grad, self.glo, **kw)
+
+    def launch_clip(self, clip: "GradClip", stream=None, process_group=None) -> None:
+        """Enqueue `clip` (a grad_clip() of this optimizer) and the step with the grads as it leaves
+        them; the process group's ranks join their norms where each holds a shard."""
+        if clip.shard is not self.grad:
+            raise ValueError("the clip is not over this optimizer's grad buffer (grad_clip())")
+        clip.launch(stream=stream, process_group=process_group if self.glo == self.start else None)
+        self._norm_ready = False
+        self.launch_step(stream=stream, norm_result=clip.result)
+
+    def step(self, extra_sqnorm: float = 0.0, stream=None, process_group=None, clip=None) -> zs.NormResult:
         """One optimizer step.  With a torch.distributed process group of more than
         one rank and a shard-only grad buffer (ZeRO-2/3), the clip norm is global:
         the ranks exchange their 8-byte local sums of squares (all-gather, rank
         order) and every rank combines the same vector, so all ranks use the same
         coefficient and agree on skipping a non-finite step.  The exchange is
-        ordered on `stream` like the kernels, whichever stream that is."""
+        ordered on `stream` like the kernels, whichever stream that is.
+
+        clip: a grad_clip() of this optimizer, in place of the one clip over all (whose max_norm is
+        not used then): its groups are clipped in the grad buffer, the step is skipped where
+        its norm over all tensors is not finite, and the result is that norm's, with a
+        coefficient of 1 (clip.finish() gives the groups')."""
+        if clip is not None:
+            if extra_sqnorm != 0.0:
+                raise ValueError("a clip takes the other ranks' sums from the process group, not extra_sqnorm")
+            self.launch_clip(clip, stream, process_group)
+            return self.finish_step(stream, result=clip.finish(stream).whole)
         if process_group is not None and self.glo == self.start and _world(process_group) > 1:
             st = torch_stream(stream, self.device)
             local = self.local_sqnorm(st)

@@ -10,6 +10,7 @@ every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import List, NamedTuple, Optional, Sequence, Tuple
 
@@ -68,6 +69,18 @@ class zero_list_tensor(ctypes.Structure):
     _fields_ = [("master", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
                 ("exp_avg_scale", ctypes.c_void_p), ("root_scale", ctypes.c_void_p), ("lowp", ctypes.c_void_p),
                 ("numel", ctypes.c_int64), ("group", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class zero_grad_entry(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class zero_grad_list(ctypes.Structure):
+    _fields_ = [("d_entries", ctypes.c_void_p), ("d_plan", ctypes.c_void_p), ("n_tensors", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("n_chunks", ctypes.c_int32), ("chunk", ctypes.c_int32),
+                ("norm_type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 STATE8_BLOCK = 256      # elements per scale of the 8-bit moments
@@ -139,6 +152,15 @@ def lib() -> ctypes.CDLL:
     L.zero_adamw_list.argtypes = [vp, i32, vp, i32, i32, vp, ci, f32, vp, ci, hpp, i32, i64, rdp, vp, vp]
     L.zero_adamw_list_device.argtypes = [vp, i32, vp, i32, i32, vp, ci, f32, vp, ci, vp, i32, rdp, vp, vp]
     L.zero_adamw_prepare_list_device.argtypes = [vp, i32, vp, vp, vp]
+    glp = ctypes.POINTER(zero_grad_list)
+    L.zero_grad_plan.argtypes = [vp, vp, i32, i32, vp, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+    L.zero_grad_entries_check.argtypes = [vp, vp, i32, i32]
+    L.zero_list_norms_workspace_bytes.argtypes = [i32]
+    L.zero_list_norms_workspace_bytes.restype = ctypes.c_size_t
+    L.zero_list_sums.argtypes = [glp, f32, vp, vp, sz, vp, vp]
+    L.zero_sums_norms.argtypes = [glp, vp, i32, vp, vp, vp, vp, vp]
+    L.zero_list_clip.argtypes = [glp, f32, vp, vp, vp]
+    L.zero_list_norms.argtypes = [glp, f32, vp, i32, vp, sz, vp, vp, vp, vp, vp, vp]
     L.zero_status_string.argtypes = [ctypes.c_int]
     L.zero_status_string.restype = ctypes.c_char_p
     L.zero_last_error.argtypes = []
@@ -151,7 +173,8 @@ def lib() -> ctypes.CDLL:
                "zero_adamw_prepare_device", "zero_adamw_step_device", "zero_adamw_step_tensors_device",
                "zero_debug_errors", "zero_debug_selftest", "zero_state8_pack", "zero_state8_unpack",
                "zero_adamw_step8_tensors", "zero_adamw_step8_tensors_device", "zero_list_chunks", "zero_adamw_list",
-               "zero_adamw_list_device", "zero_adamw_prepare_list_device"):
+               "zero_adamw_list_device", "zero_adamw_prepare_list_device", "zero_grad_plan", "zero_grad_entries_check",
+               "zero_list_sums", "zero_sums_norms", "zero_list_clip", "zero_list_norms"):
         getattr(L, nm).restype = ctypes.c_int
     _lib = L
     return L
@@ -844,6 +867,198 @@ def zero_adamw_prepare_list_device(d_hp: torch.Tensor, n_groups: int, clip: Opti
         raise ValueError("clip is smaller than zero_norm_result")
     _check(lib().zero_adamw_prepare_list_device(_dev(d_hp, "d_hp"), n_groups, _dev(clip, "clip", allow_none=True),
                                                 _dev(states, "states"), _stream(stream)))
+
+
+# ------------------------------------------------- norms and clipping of a list
+_NORM_TYPES = {math.inf: 0, 1.0: 1, 2.0: 2}
+
+
+class GradList(NamedTuple):
+    """A grads list prepared for zero_list_norms and the like: the device copies of its
+    entries and plan.  It holds addresses: keep the tensors alive."""
+    entries: Optional[torch.Tensor]  # uint8, 40 bytes per tensor; None: sums and norms of other ranks' lists only
+    plan: "GradPlan"
+    head: zero_grad_list             # the C entries' description of the list
+
+
+class GradPlan(NamedTuple):
+    """The work split of a grads list (zero_grad_plan) on the device: by sizes and groups alone."""
+    ints: torch.Tensor  # int32
+    numels: np.ndarray  # int64
+    groups: Optional[np.ndarray]  # int32, or None: all in group 0
+    n_groups: int
+    n_chunks: int
+    chunk: int
+    norm_type: int
+
+
+_GRAD_ENTRY = np.dtype([(nm, np.uint64 if ct is ctypes.c_void_p else np.int64 if ct is ctypes.c_int64 else np.int32)
+                        for nm, ct in zero_grad_entry._fields_])
+
+
+def zero_grad_plan(numels: Sequence[int], group_of: Optional[Sequence[int]], n_groups: int, norm_type: float,
+                   device) -> GradPlan:
+    """The plan of a list with these sizes and groups (group_of None: all in group 0), copied to the device."""
+    p = _NORM_TYPES.get(float(norm_type))
+    if p is None:
+        raise ValueError(f"norm_type must be 1, 2 or inf, got {norm_type}")
+    n = len(numels)
+    sizes = np.ascontiguousarray(np.asarray(numels, dtype=np.int64))
+    groups = None
+    if group_of is not None:
+        if len(group_of) != n:
+            raise ValueError("one group per tensor is required")
+        groups = np.ascontiguousarray(np.asarray(group_of, dtype=np.int32))
+    ints = np.zeros(2 * n + max(int(n_groups), 0) + 2, dtype=np.int32)
+    n_chunks, chunk = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().zero_grad_plan(sizes.ctypes.data, None if groups is None else groups.ctypes.data, n, n_groups,
+                                ints.ctypes.data, ctypes.byref(n_chunks), ctypes.byref(chunk)))
+    return GradPlan(torch.from_numpy(ints).to(device), sizes, groups, int(n_groups), n_chunks.value, chunk.value, p)
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether the elements fill one run of memory, each address once."""
+    if t.is_contiguous():
+        return True
+    size = 1
+    for stride, k in sorted((s, k) for s, k in zip(t.stride(), t.shape) if k != 1):
+        if stride != size:
+            return False
+        size *= k
+    return True
+
+
+def _overlaps(starts: np.ndarray, ends: np.ndarray, written: np.ndarray) -> bool:
+    """Whether an interval that is written overlaps any other one."""
+    order = np.argsort(starts, kind="stable")
+    s, e, w = starts[order], ends[order], written[order]
+    reach = np.maximum.accumulate(e)  # how far the earlier ones go, and the written ones among them
+    reach_w = np.maximum.accumulate(np.where(w, e, 0))
+    return bool(np.any((s[1:] < reach[:-1]) & w[1:]) or np.any(s[1:] < reach_w[:-1]))
+
+
+def grad_list(plan: GradPlan, grads: Sequence[Optional[torch.Tensor]], out: Optional[Sequence] = None,
+              write: bool = True) -> GradList:
+    """Check a list of grads (None: no grad, reads as zeros) and copy it to the device.  out:
+    where the clipped grads go, per tensor a buffer or None (that tensor is not written);
+    out=None with write: in place.  Every tensor is f32, bf16 or f16, fills one run
+    of memory (any order of its dimensions; its out in the same order), and overlaps no
+    other that is written.  The device is the plan's."""
+    n = len(plan.numels)
+    if len(grads) != n or (out is not None and len(out) != n):
+        raise ValueError("one grad (or None) per tensor is required, and one out")
+    device = plan.ints.device
+    entries = np.zeros(n, dtype=_GRAD_ENTRY)
+    src, dst, sdt, ddt = [0] * n, [0] * n, [0] * n, [0] * n
+
+    def address(t, nm, i):
+        if not isinstance(t, torch.Tensor) or t.device != device:
+            raise ValueError(f"{nm}[{i}] must be a tensor on {device}")
+        if t.dtype not in _DT:
+            raise ValueError(f"{nm}[{i}] is {t.dtype}, not f32, bf16 or f16")
+        if not _dense(t):
+            raise ValueError(f"{nm}[{i}] does not fill one run of memory (strides {t.stride()})")
+        return t.data_ptr(), _DT[t.dtype]
+
+    for i, g in enumerate(grads):
+        if g is None:
+            continue
+        src[i], sdt[i] = address(g, "grads", i)
+        if g.numel() != plan.numels[i]:
+            raise ValueError(f"grad {i} has {g.numel()} elements, expected {plan.numels[i]}")
+        if write and out is None:
+            dst[i], ddt[i] = src[i], sdt[i]
+    for i, y in enumerate(out if write and out is not None else ()):
+        if y is None:
+            continue
+        dst[i], ddt[i] = address(y, "out", i)
+        g = grads[i]
+        if y.numel() != plan.numels[i]:
+            raise ValueError(f"out {i} has {y.numel()} elements, expected {plan.numels[i]}")
+        if g is not None and not (g.is_contiguous() and y.is_contiguous()) and (
+                g.shape != y.shape or g.stride() != y.stride()):
+            raise ValueError(f"out {i} is not laid out as its grad")
+    entries["src"], entries["dst"], entries["src_dtype"], entries["dst_dtype"] = src, dst, sdt, ddt
+    entries["numel"] = plan.numels
+    if plan.groups is not None:
+        entries["group"] = plan.groups
+    _check(lib().zero_grad_entries_check(entries.ctypes.data, plan.numels.ctypes.data, n, plan.n_groups))
+    written = (entries["dst"] != 0) & (plan.numels > 0)
+    if written.any():
+        bytes_of = np.array([4, 2, 2], dtype=np.uint64)
+        size = plan.numels.astype(np.uint64)
+        read = (entries["src"] != 0) & (plan.numels > 0) & (entries["src"] != entries["dst"])
+        at = np.concatenate([entries["dst"][written], entries["src"][read]])
+        ends = at + np.concatenate([(size * bytes_of[entries["dst_dtype"]])[written],
+                                    (size * bytes_of[entries["src_dtype"]])[read]])
+        if _overlaps(at, ends, np.arange(len(at)) < int(written.sum())):
+            raise ValueError("a grad that is written overlaps another tensor of the list (is one listed twice?)")
+    d_entries = torch.from_numpy(entries.view(np.uint8)).to(device)
+    return GradList(d_entries, plan, _list_head(plan, d_entries.data_ptr()))
+
+
+def _list_head(plan: GradPlan, d_entries: Optional[int]) -> zero_grad_list:
+    return zero_grad_list(d_entries, plan.ints.data_ptr(), len(plan.numels), plan.n_groups, plan.n_chunks, plan.chunk,
+                          plan.norm_type, 0)
+
+
+def norms_only_list(plan: GradPlan) -> GradList:
+    """A list without entries, for zero_sums_norms."""
+    return GradList(None, plan, _list_head(plan, None))
+
+
+def zero_list_norms_workspace_bytes(n_chunks: int) -> int:
+    return int(lib().zero_list_norms_workspace_bytes(n_chunks))
+
+
+def _f64(t: torch.Tensor, name: str, need: int) -> int:
+    if t.numel() < need:
+        raise ValueError(f"{name} has {t.numel()} elements, {need} are needed")
+    return _dev(t, name, torch.float64)
+
+
+def _norm_outputs(gl: GradList, max_norms, norms, results, found):
+    n, g = len(gl.plan.numels), gl.plan.n_groups
+    if norms.numel() < n + g + 1:
+        raise ValueError(f"norms has {norms.numel()} elements, {n + g + 1} are needed")
+    if results.numel() * results.element_size() < (g + 1) * NORM_RESULT_BYTES:
+        raise ValueError("results is smaller than one zero_norm_result per group and one more")
+    return (_f64(max_norms, "max_norms", g), _dev(norms, "norms", torch.float32), _dev(results, "results"),
+            _dev(found, "found_nonfinite", torch.int32, allow_none=True))
+
+
+def zero_list_sums(gl: GradList, scale: float, ws: torch.Tensor, sums: torch.Tensor, stream=None,
+                   d_scale: Optional[torch.Tensor] = None) -> None:
+    """Each tensor's sum of |scale x|^p (the largest for p = inf) into sums (float64)."""
+    _check(lib().zero_list_sums(ctypes.byref(gl.head), scale, _dscale(d_scale), _dev(ws, "ws"), _ws_bytes(ws),
+                                _f64(sums, "sums", len(gl.plan.numels)), _stream(stream)))
+
+
+def zero_sums_norms(gl: GradList, sums: torch.Tensor, n_parts: int, max_norms: torch.Tensor, norms: torch.Tensor,
+                    results: torch.Tensor, found_nonfinite: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The norms of tensors, groups and all from n_parts rows of sums, joined in row order."""
+    _check(lib().zero_sums_norms(ctypes.byref(gl.head), _f64(sums, "sums", max(n_parts, 0) * len(gl.plan.numels)),
+                                 n_parts, *_norm_outputs(gl, max_norms, norms, results, found_nonfinite),
+                                 _stream(stream)))
+
+
+def zero_list_clip(gl: GradList, scale: float, results: torch.Tensor, stream=None,
+                   d_scale: Optional[torch.Tensor] = None) -> None:
+    """Every tensor with a destination scaled and clipped by its group's coefficient in results."""
+    if results.numel() * results.element_size() < (gl.plan.n_groups + 1) * NORM_RESULT_BYTES:
+        raise ValueError("results is smaller than one zero_norm_result per group and one more")
+    _check(lib().zero_list_clip(ctypes.byref(gl.head), scale, _dscale(d_scale), _dev(results, "results"),
+                                _stream(stream)))
+
+
+def zero_list_norms(gl: GradList, scale: float, clip: bool, ws: torch.Tensor, sums: torch.Tensor,
+                    max_norms: torch.Tensor, norms: torch.Tensor, results: torch.Tensor,
+                    found_nonfinite: Optional[torch.Tensor] = None, stream=None,
+                    d_scale: Optional[torch.Tensor] = None) -> None:
+    """zero_list_sums, zero_sums_norms and, with clip, zero_list_clip in one call."""
+    _check(lib().zero_list_norms(ctypes.byref(gl.head), scale, _dscale(d_scale), int(bool(clip)), _dev(ws, "ws"),
+                                 _ws_bytes(ws), _f64(sums, "sums", len(gl.plan.numels)),
+                                 *_norm_outputs(gl, max_norms, norms, results, found_nonfinite), _stream(stream)))
 
 
 # ------------------------------------------------------------ debug builds

@@ -16,8 +16,8 @@
  * variants that read the grads through the tensor table or take their
  * scalars from a device step state (graph-capturable steps), the step with
  * moments in 8 bits (zero_adamw_step8_tensors, zero_state8_pack / _unpack),
- * the step over many separate tensors (zero_adamw_list), and
- * zero_grad_sqnorm_noalloc.
+ * the step over many separate tensors (zero_adamw_list), the norms of many
+ * tensors and their clipping (zero_list_norms), and zero_grad_sqnorm_noalloc.
  *
  * Sources: the ZeRO page (ai6s.net, "cann-recipes-train" ZeRO-1/2/3 on
  * Ascend), the memory-ledger / FlatParameter page (ybb.press,
@@ -695,6 +695,130 @@ zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_ten
 zero_status zero_adamw_prepare_list_device(const zero_adamw_hparams* d_hp, int32_t n_groups,
                                            const zero_norm_result* d_clip, zero_adamw_device_state* d_states,
                                            void* stream);
+
+/* ---------------------------------------------------------------------
+ * Norms of many tensors and their clipping.  The pages' loops call
+ * clip_grad_norm_ once for all parameters and leave the grads clipped in
+ * place; zero_grad_sqnorm gives one 2-norm whose coefficient the AdamW calls
+ * apply.  Here the norm of every tensor, of groups of tensors (experts or
+ * embeddings clipped apart) and of all of them, for p = 1, 2 and infinity,
+ * over tensors of mixed types, and the clipped grads written back.  With s the
+ * scale (unscaling, averaging), x_i the elements of tensor i, M_g the limit of
+ * group g:
+ *   S_i = sum |s x_i|^p, for p = infinity max |s x_i|        (binary64)
+ *   norm of a tensor, a group, all = (sum of its S_i)^(1/p), or the largest
+ *   coef_g = min(1, M_g / (norm_g + 1e-6))                   (binary32)
+ *   y = fl_type(fl(fl(s * coef_g) * x))
+ * |s|^p multiplies the sums, not the elements.  The sums carry about 48
+ * significant bits for any finite x (chunks whose squares leave the binary32
+ * range are summed again, scaled by a power of two); an infinite x makes the
+ * norms infinite and a NaN makes them NaN.  No y is written at all where the
+ * norm over all tensors is not finite: the step is to be skipped.
+ * A step is zero_list_norms, which also clips; across ranks zero_list_sums, an
+ * all-gather of the sums in rank order, zero_sums_norms and zero_list_clip.
+ * --------------------------------------------------------------------- */
+
+/* One tensor of a grads list (40 bytes). */
+typedef struct zero_grad_entry {
+  const void* src;   /* device memory, contiguous; NULL: no grad, reads as zeros */
+  void* dst;         /* where the clipped grad goes: src itself with its type, or another buffer; NULL: nowhere */
+  int64_t numel;     /* >= 0 */
+  int32_t src_dtype; /* zero_dtype */
+  int32_t dst_dtype; /* zero_dtype */
+  int32_t group;     /* in [0, n_groups) */
+  int32_t reserved;  /* 0 */
+} zero_grad_entry;
+
+#define ZERO_NORM_INF 0
+#define ZERO_NORM_1 1
+#define ZERO_NORM_2 2
+
+/* A grads list in device memory, as the calls below take it (host struct). */
+typedef struct zero_grad_list {
+  const zero_grad_entry* d_entries; /* n_tensors entries that zero_grad_entries_check accepted */
+  const int32_t* d_plan;            /* zero_grad_plan's ints */
+  int32_t n_tensors;
+  int32_t n_groups;
+  int32_t n_chunks; /* as zero_grad_plan gave them */
+  int32_t chunk;
+  int32_t norm_type; /* ZERO_NORM_... */
+  int32_t reserved;  /* 0 */
+} zero_grad_list;
+
+/* zero_grad_plan -- host only.
+ * The work split of a grads list: chunks of *chunk elements (by the total
+ * size: 4096, 16384 or 65536), none across two tensors, numbered in list
+ * order, and the tensors of each group.  plan: 2 * n_tensors + n_groups + 2
+ * ints: the first chunk of each tensor and their count, then where each
+ * group's members start, then the members (tensor numbers, in list order in
+ * each group).  groups: NULL puts every tensor in group 0.  A group may be
+ * empty: its norm is 0.  The plan depends on sizes and groups alone.
+ * Errors: ZERO_EINVAL for n_tensors < 1, n_groups < 1, NULL numels or outputs,
+ * a numel < 0, a group outside [0, n_groups), n_tensors + n_groups of 2^30 or more, or 2^31
+ * chunks or more. */
+zero_status zero_grad_plan(const int64_t* numels, const int32_t* groups, int32_t n_tensors, int32_t n_groups,
+                           int32_t* plan, int32_t* n_chunks, int32_t* chunk);
+
+/* zero_grad_entries_check -- host only.
+ * Checks entries (host memory) entry by entry: numel as in the plan's numels,
+ * groups, types, element alignment, a src or dst that is not NULL.  src may be
+ * NULL (no grad); dst may be src only with the same type.  Whether buffers
+ * overlap is not checked: one that is written must not overlap any other of
+ * the list (a tensor listed twice would be clipped twice); that is the
+ * caller's error.
+ * Errors: ZERO_EINVAL. */
+zero_status zero_grad_entries_check(const zero_grad_entry* entries, const int64_t* numels, int32_t n_tensors,
+                                    int32_t n_groups);
+
+/* zero_list_norms_workspace_bytes -- host only.
+ * Device scratch of zero_list_sums and zero_list_norms: 8 bytes per chunk.
+ * Overwritten by each call; calls that overlap on the GPU need one each. */
+size_t zero_list_norms_workspace_bytes(int32_t n_chunks);
+
+/* zero_list_sums -- device.
+ * d_sums[i] = S_i for every tensor (binary64).  d_scale: NULL, or a device
+ * float read when the kernel runs in place of scale.
+ * Errors: ZERO_EINVAL for a bad list, NULL or misaligned buffers, a too-small
+ * workspace or a non-finite scale. */
+zero_status zero_list_sums(const zero_grad_list* list, float scale, const float* d_scale, void* d_ws, size_t ws_bytes,
+                           double* d_sums, void* stream);
+
+/* zero_sums_norms -- device.
+ * The norms from n_parts rows of sums, d_sums[r * n_tensors + i] being rank
+ * r's S_i, added (or compared) in rank order, so that every rank gets the
+ * same norms.  Only the list's plan and counts are used (d_entries may be
+ * NULL).
+ * d_norms: binary32, the n_tensors tensor norms, the n_groups group norms and
+ *   the norm over all.
+ * d_max_norms: binary64, the limit M_g >= 0 of each group (infinity: not
+ *   clipped), read when the kernel runs.
+ * d_results: n_groups + 1 zero_norm_results.  Group g's has the sum (the
+ *   largest) as `sqnorm`, its norm, its coefficient and whether its norm is
+ *   finite; the last one those over all, with a coefficient of 1, as a later
+ *   AdamW call takes it (d_clip) after the grads have been clipped.
+ * d_found_nonfinite: NULL, or a device int32 set to 1 when the norm over all
+ *   is not finite (never cleared by the call).
+ * Errors: ZERO_EINVAL for a bad list, n_parts < 1, NULL or misaligned buffers. */
+zero_status zero_sums_norms(const zero_grad_list* list, const double* d_sums, int32_t n_parts,
+                            const double* d_max_norms, float* d_norms, zero_norm_result* d_results,
+                            int32_t* d_found_nonfinite, void* stream);
+
+/* zero_list_clip -- device.
+ * y of every tensor with a dst, by its group's coefficient in d_results;
+ * nothing where d_results[n_groups].finite is 0.  A tensor without a grad and
+ * with a dst gets zeros.  Where the coefficient and the scale are 1 a tensor
+ * clipped in place is not touched.
+ * Errors: as zero_list_sums. */
+zero_status zero_list_clip(const zero_grad_list* list, float scale, const float* d_scale,
+                           const zero_norm_result* d_results, void* stream);
+
+/* zero_list_norms -- device.
+ * zero_list_sums, zero_sums_norms (one part) and, with clip != 0,
+ * zero_list_clip in one call.
+ * Errors: those of the three. */
+zero_status zero_list_norms(const zero_grad_list* list, float scale, const float* d_scale, int32_t clip, void* d_ws,
+                            size_t ws_bytes, double* d_sums, const double* d_max_norms, float* d_norms,
+                            zero_norm_result* d_results, int32_t* d_found_nonfinite, void* stream);
 
 /* ---------------------------------------------------------------------
  * Debug builds.  No counterpart on the source pages.  Built with
