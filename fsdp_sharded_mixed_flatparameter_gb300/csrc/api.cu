@@ -320,12 +320,11 @@ zero_status zero_adamw_step_tensors(float* d_master, float* d_exp_avg, float* d_
 
 // ------------------------------------------------ norms and clipping of a list
 zero_status zero_grad_plan(const int64_t* numels, const int32_t* groups, int32_t n_tensors, int32_t n_groups,
-                           int32_t* plan, int32_t* n_chunks, int32_t* chunk) {
+                           int32_t* plan, zero_grad_list* list) {
   const char* who = "zero_grad_plan";
-  if (n_tensors < 1 || n_groups < 1 || n_tensors > (1 << 30) - n_groups)
+  if (n_tensors < 1 || n_groups < 1 || n_tensors > (1 << 28) || n_groups > (1 << 28))
     return fail(ZERO_EINVAL, "%s: %d tensors in %d groups", who, (int)n_tensors, (int)n_groups);
-  if (numels == nullptr || plan == nullptr || n_chunks == nullptr || chunk == nullptr)
-    return fail(ZERO_EINVAL, "%s: NULL argument", who);
+  if (numels == nullptr || plan == nullptr || list == nullptr) return fail(ZERO_EINVAL, "%s: NULL argument", who);
   int64_t total = 0;
   for (int32_t i = 0; i < n_tensors; ++i) {
     if (numels[i] < 0) return fail(ZERO_EINVAL, "%s: numel[%d] = %lld < 0", who, (int)i, (long long)numels[i]);
@@ -336,15 +335,26 @@ zero_status zero_grad_plan(const int64_t* numels, const int32_t* groups, int32_t
   }
   const int32_t size = zs::grad_chunk_size(total);
   int32_t* const first = plan;
-  int32_t* const group_first = plan + n_tensors + 1;
+  int32_t* const group_first = first + n_tensors + 1;
   int32_t* const members = group_first + n_groups + 1;
-  int64_t count = 0;
+  int32_t* const narrow_of = members + n_tensors;
+  int32_t* const narrow = narrow_of + n_tensors;
+  int64_t wide = 0;
+  int32_t n_narrow = 0;
   for (int32_t i = 0; i < n_tensors; ++i) {
-    first[i] = static_cast<int32_t>(count);
-    count += numels[i] / size + (numels[i] % size != 0 ? 1 : 0);
-    if (count > INT32_MAX) return fail(ZERO_EINVAL, "%s: 2^31 chunks or more up to tensor %d", who, (int)i);
+    first[i] = static_cast<int32_t>(wide);
+    narrow_of[i] = -1;
+    narrow[i] = -1;
+    if (numels[i] == 0) continue;
+    if (numels[i] <= zs::kNarrow) {
+      narrow_of[i] = n_narrow;
+      narrow[n_narrow++] = i;
+      continue;
+    }
+    wide += numels[i] / size + (numels[i] % size != 0 ? 1 : 0);
+    if (wide > zs::kMaxGradPieces) return fail(ZERO_EINVAL, "%s: 2^28 chunks or more up to tensor %d", who, (int)i);
   }
-  first[n_tensors] = static_cast<int32_t>(count);
+  first[n_tensors] = static_cast<int32_t>(wide);
   // counting sort: group_first[g + 1] counts group g, then becomes where it starts, then where it ends
   for (int32_t g = 0; g <= n_groups; ++g) group_first[g] = 0;
   for (int32_t i = 0; i < n_tensors; ++i) ++group_first[(groups ? groups[i] : 0) + 1];
@@ -354,8 +364,7 @@ zero_status zero_grad_plan(const int64_t* numels, const int32_t* groups, int32_t
     at += c;
   }
   for (int32_t i = 0; i < n_tensors; ++i) members[group_first[(groups ? groups[i] : 0) + 1]++] = i;
-  *n_chunks = static_cast<int32_t>(count);
-  *chunk = size;
+  *list = zero_grad_list{nullptr, nullptr, n_tensors, n_groups, static_cast<int32_t>(wide), n_narrow, size, 0, 0};
   return ZERO_OK;
 }
 
@@ -382,16 +391,19 @@ zero_status zero_grad_entries_check(const zero_grad_entry* entries, const int64_
   return ZERO_OK;
 }
 
-size_t zero_list_norms_workspace_bytes(int32_t n_chunks) {
-  return n_chunks <= 0 ? 0 : static_cast<size_t>(n_chunks) * sizeof(double);
+size_t zero_list_norms_workspace_bytes(const zero_grad_list* list) {
+  if (list == nullptr || list->n_wide < 0 || list->n_narrow < 0) return 0;
+  return (static_cast<size_t>(list->n_wide) + static_cast<size_t>(list->n_narrow)) * sizeof(double);
 }
 
 // The list's own checks, and its arguments for the launchers.
 static zero_status grad_list_args(const char* who, const zero_grad_list* l, bool entries, float scale,
                                   const float* d_scale, zs::GradListArgs* a) {
-  if (l == nullptr || l->n_tensors < 1 || l->n_groups < 1 || l->n_chunks < 0 || l->reserved != 0)
+  if (l == nullptr || l->n_tensors < 1 || l->n_groups < 1 || l->n_wide < 0 || l->n_wide > zs::kMaxGradPieces ||
+      l->n_narrow < 0 || l->n_narrow > l->n_tensors || (l->in_place != 0 && l->in_place != 1))
     return fail(ZERO_EINVAL, "%s: bad list", who);
-  if (l->chunk < 1 || l->chunk > zs::kMaxGradChunk) return fail(ZERO_EINVAL, "%s: chunk %d", who, (int)l->chunk);
+  if (l->chunk < 1 || l->chunk > zs::kMaxGradChunk || (l->chunk & (l->chunk - 1)) != 0)
+    return fail(ZERO_EINVAL, "%s: chunk %d", who, (int)l->chunk);
   if (l->norm_type != ZERO_NORM_INF && l->norm_type != ZERO_NORM_1 && l->norm_type != ZERO_NORM_2)
     return fail(ZERO_EINVAL, "%s: bad norm_type %d", who, (int)l->norm_type);
   if (l->d_plan == nullptr || !zs::aligned(l->d_plan, 4)) return fail(ZERO_EINVAL, "%s: NULL or misaligned d_plan", who);
@@ -399,14 +411,14 @@ static zero_status grad_list_args(const char* who, const zero_grad_list* l, bool
     return fail(ZERO_EINVAL, "%s: NULL or misaligned d_entries", who);
   if (!std::isfinite(scale)) return fail(ZERO_EINVAL, "%s: non-finite scale", who);
   if (!zs::aligned(d_scale, 4)) return fail(ZERO_EINVAL, "%s: d_scale not 4-byte aligned", who);
-  *a = zs::GradListArgs{l->d_entries, l->d_plan, l->n_tensors, l->n_groups, l->n_chunks,
-                        l->chunk,     l->norm_type, scale,     d_scale};
+  *a = zs::GradListArgs{l->d_entries, l->d_plan, l->n_tensors,   l->n_groups,      l->n_wide,
+                        l->n_narrow,  l->chunk,  l->norm_type, l->in_place != 0, scale, d_scale};
   return ZERO_OK;
 }
 
-static zero_status check_list_ws(const char* who, const zs::GradListArgs& a, const void* ws, size_t ws_bytes,
+static zero_status check_list_ws(const char* who, const zero_grad_list* list, const void* ws, size_t ws_bytes,
                                  const double* sums) {
-  const size_t need = zero_list_norms_workspace_bytes(a.n_chunks);
+  const size_t need = zero_list_norms_workspace_bytes(list);
   if (need > 0 && (ws == nullptr || ws_bytes < need))
     return fail(ZERO_EINVAL, "%s: workspace %zu bytes < %zu needed", who, ws ? ws_bytes : 0, need);
   if (!zs::aligned(ws, 8)) return fail(ZERO_EINVAL, "%s: workspace not 8-byte aligned", who);
@@ -426,12 +438,13 @@ zero_status zero_list_sums(const zero_grad_list* list, float scale, const float*
                            double* d_sums, void* stream) {
   zs::GradListArgs a;
   zero_status s = grad_list_args("zero_list_sums", list, true, scale, d_scale, &a);
-  if (s == ZERO_OK) s = check_list_ws("zero_list_sums", a, d_ws, ws_bytes, d_sums);
+  if (s == ZERO_OK) s = check_list_ws("zero_list_sums", list, d_ws, ws_bytes, d_sums);
   if (s != ZERO_OK) return s;
-  return zs::launch_list_sums(a, static_cast<double*>(d_ws), d_sums, zs::as_stream(stream));
+  return zs::launch_list_norms(a, static_cast<double*>(d_ws), d_sums, nullptr, nullptr, nullptr, nullptr,
+                               zs::as_stream(stream));
 }
 
-zero_status zero_sums_norms(const zero_grad_list* list, const double* d_sums, int32_t n_parts,
+zero_status zero_sums_norms(const zero_grad_list* list, const double* d_sums, int32_t n_parts, double* d_joined,
                             const double* d_max_norms, float* d_norms, zero_norm_result* d_results,
                             int32_t* d_found_nonfinite, void* stream) {
   zs::GradListArgs a;
@@ -439,8 +452,9 @@ zero_status zero_sums_norms(const zero_grad_list* list, const double* d_sums, in
   if (s == ZERO_OK) s = check_norm_outputs("zero_sums_norms", d_max_norms, d_norms, d_results, d_found_nonfinite);
   if (s != ZERO_OK) return s;
   if (n_parts < 1) return fail(ZERO_EINVAL, "zero_sums_norms: n_parts %d < 1", (int)n_parts);
-  if (d_sums == nullptr || !zs::aligned(d_sums, 8)) return fail(ZERO_EINVAL, "zero_sums_norms: NULL or misaligned d_sums");
-  return zs::launch_sums_norms(a, d_sums, n_parts, d_max_norms, d_norms, d_results, d_found_nonfinite,
+  if (d_sums == nullptr || !zs::aligned(d_sums, 8) || d_joined == nullptr || !zs::aligned(d_joined, 8))
+    return fail(ZERO_EINVAL, "zero_sums_norms: NULL or misaligned d_sums or d_joined");
+  return zs::launch_sums_norms(a, d_sums, n_parts, d_joined, d_max_norms, d_norms, d_results, d_found_nonfinite,
                                zs::as_stream(stream));
 }
 
@@ -459,12 +473,11 @@ zero_status zero_list_norms(const zero_grad_list* list, float scale, const float
                             zero_norm_result* d_results, int32_t* d_found_nonfinite, void* stream) {
   zs::GradListArgs a;
   zero_status s = grad_list_args("zero_list_norms", list, true, scale, d_scale, &a);
-  if (s == ZERO_OK) s = check_list_ws("zero_list_norms", a, d_ws, ws_bytes, d_sums);
+  if (s == ZERO_OK) s = check_list_ws("zero_list_norms", list, d_ws, ws_bytes, d_sums);
   if (s == ZERO_OK) s = check_norm_outputs("zero_list_norms", d_max_norms, d_norms, d_results, d_found_nonfinite);
   if (s != ZERO_OK) return s;
-  s = zs::launch_list_sums(a, static_cast<double*>(d_ws), d_sums, zs::as_stream(stream));
-  if (s == ZERO_OK)
-    s = zs::launch_sums_norms(a, d_sums, 1, d_max_norms, d_norms, d_results, d_found_nonfinite, zs::as_stream(stream));
+  s = zs::launch_list_norms(a, static_cast<double*>(d_ws), d_sums, d_max_norms, d_norms, d_results, d_found_nonfinite,
+                            zs::as_stream(stream));
   if (s == ZERO_OK && clip != 0) s = zs::launch_list_clip(a, d_results, zs::as_stream(stream));
   return s;
 }

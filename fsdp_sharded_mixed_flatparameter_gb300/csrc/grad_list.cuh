@@ -2,37 +2,63 @@
 // the chunks of a list and the vectors of a chunk.  Internal.
 #pragma once
 
+#include "kernels.h"
 #include "list.cuh"
 #include "reduce.cuh"
 
 namespace zs {
 
-constexpr int kGradThreads = 256;
-
 // The parts of a plan (zero_grad_plan).
 struct GradPlan {
-  const int32_t* first;        // [n + 1] first chunks, their count
+  const int32_t* first;        // [n + 1] first wide chunks, their count
   const int32_t* group_first;  // [n_groups + 1] starts in members
   const int32_t* members;      // [n]
+  const int32_t* narrow_of;    // [n] a tensor's number in `narrow`, or -1
+  const int32_t* narrow;       // [n_narrow] tensors
+  int n_wide, n_narrow, chunk;
 };
-__host__ __device__ inline GradPlan plan_parts(const int32_t* plan, int n, int n_groups) {
-  return GradPlan{plan, plan + n + 1, plan + n + 1 + n_groups + 1};
+inline GradPlan plan_parts(const GradListArgs& a) {
+  GradPlan p;
+  p.first = a.plan;
+  p.group_first = p.first + a.n + 1;
+  p.members = p.group_first + a.n_groups + 1;
+  p.narrow_of = p.members + a.n;
+  p.narrow = p.narrow_of + a.n;
+  p.n_wide = a.n_wide;
+  p.n_narrow = a.n_narrow;
+  p.chunk = a.chunk;
+  return p;
+}
+inline unsigned grad_blocks(const GradPlan& p, int threads) {
+  return static_cast<unsigned>(p.n_wide + (p.n_narrow + threads / 32 - 1) / (threads / 32));
 }
 
-// A chunk: elements [k, k + len) of a tensor.
-struct GradChunk {
-  int tensor;
+// The work of a grid of grad_blocks() blocks of T threads: block b < n_wide has the wide chunk b,
+// `chunk` elements of a tensor; each warp of the blocks behind has a narrow
+// tensor of its own, so that a list of thousands of small tensors does not
+// cost a block's start and end for each.  len == 0: nothing left.
+struct GradPiece {
+  int tensor, len;
   int64_t k;
-  int len;
+  int at;  // its partial
 };
-__device__ __forceinline__ GradChunk grad_chunk(const zero_grad_entry* __restrict__ entries,
-                                                const int32_t* __restrict__ first, int n, int chunk, int c) {
-  GradChunk r;
-  r.tensor = block_tensor(first, n, c);
-  r.k = static_cast<int64_t>(c - __ldg(first + r.tensor)) * chunk;
+__device__ __forceinline__ GradPiece wide_piece(const zero_grad_entry* __restrict__ entries, int n, const GradPlan& p,
+                                                int block) {
+  GradPiece r;
+  r.at = block;
+  r.tensor = block_tensor(p.first, n, block);
+  r.k = static_cast<int64_t>(block - __ldg(p.first + r.tensor)) * p.chunk;
   const int64_t left = entries[r.tensor].numel - r.k;
-  r.len = static_cast<int>(left < chunk ? left : chunk);
+  r.len = static_cast<int>(left < p.chunk ? left : p.chunk);
   return r;
+}
+template <int T>
+__device__ __forceinline__ GradPiece narrow_piece(const zero_grad_entry* __restrict__ entries, const GradPlan& p,
+                                                  int block) {
+  const int j = (block - p.n_wide) * (T / 32) + static_cast<int>(threadIdx.x >> 5);
+  if (j >= p.n_narrow) return GradPiece{0, 0, 0, 0};
+  const int i = __ldg(p.narrow + j);
+  return GradPiece{i, static_cast<int>(entries[i].numel), 0, p.n_wide + j};
 }
 
 // A run of `len` elements of ES bytes at p: `head` elements up to the first
@@ -48,13 +74,41 @@ __device__ __forceinline__ Run vector_run(const void* p, int len) {
   return Run{h, (len - h) / 8};
 }
 
-// The index of this thread's element of the head (threads 0..7) or the tail
+// The index of thread t's element of the head (threads 0..7) or the tail
 // (threads 8..15) of a run, -1 for none.
-__device__ __forceinline__ int ragged_element(const Run& r, int len) {
-  const int t = threadIdx.x;
+__device__ __forceinline__ int ragged_element(const Run& r, int len, int t) {
   if (t < 8) return t < r.head ? t : -1;
   const int e = r.head + 8 * r.vecs + t - 8;
   return t < 16 && e < len ? e : -1;
+}
+
+// Programmatic dependent launch: a kernel launched by launch_after starts
+// while the one before it on the stream still runs, and sees what that one
+// wrote after wait_before().  Launched otherwise both do nothing.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// cluster: the blocks of a thread-block cluster.
+template <class... Formal, class... Actual>
+inline zero_status launch_after(const char* what, void (*kernel)(Formal...), unsigned blocks, unsigned threads,
+                                unsigned cluster, cudaStream_t st, Actual... args) {
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {cluster, 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Formal>(args)...);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(ZERO_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+  }
+  return ZERO_OK;
 }
 
 }  // namespace zs

@@ -111,24 +111,29 @@ zero_status launch_state8_pack(const float* m, const float* v, int64_t n, const 
 zero_status launch_state8_unpack(const zero_state8& q, int64_t n, float* m, float* v, cudaStream_t st);
 
 // Elements of a grads list's chunks, by the list's total.
-constexpr int kMaxGradChunk = 65536;
+constexpr int kMaxGradChunk = 65536, kMaxGradPieces = (1 << 28) - 1;
 inline int grad_chunk_size(int64_t total) {
-  return total <= (int64_t(1) << 23) ? 4096 : total <= (int64_t(1) << 28) ? 16384 : kMaxGradChunk;
+  return total <= (int64_t(1) << 23) ? 4096 : total <= (int64_t(1) << 27) ? 16384 : kMaxGradChunk;
 }
+// Elements up to which a tensor is narrow: a warp's work.
+constexpr int kNarrow = 4096;
 
 // The norms of a grads list and its clipping (arguments checked; plan: zero_grad_plan's ints).
 struct GradListArgs {
   const zero_grad_entry* entries;
   const int32_t* plan;
   int n, n_groups;
-  int32_t n_chunks;
-  int chunk, norm_type;
+  int n_wide, n_narrow, chunk, norm_type;
+  bool in_place;
   float scale;
   const float* dscale;
 };
-zero_status launch_list_sums(const GradListArgs& a, double* partials, double* sums, cudaStream_t st);
-zero_status launch_sums_norms(const GradListArgs& a, const double* sums, int n_parts, const double* max_norms,
-                              float* norms, zero_norm_result* results, int32_t* found, cudaStream_t st);
+// norms, results NULL: the sums only.
+zero_status launch_list_norms(const GradListArgs& a, double* partials, double* sums, const double* max_norms, float* norms,
+                              zero_norm_result* results, int32_t* found, cudaStream_t st);
+zero_status launch_sums_norms(const GradListArgs& a, const double* sums, int n_parts, double* joined,
+                              const double* max_norms, float* norms, zero_norm_result* results, int32_t* found,
+                              cudaStream_t st);
 zero_status launch_list_clip(const GradListArgs& a, const zero_norm_result* results, cudaStream_t st);
 
 // Debug builds (ZERO_DEBUG): each translation unit's violation record

@@ -4,7 +4,7 @@
 // y = fl_type(fl(f x)), f = fl(scale * coef): a rounding to binary32 and, for
 // 16-bit outputs, one to their type (both to nearest even).
 //
-// One block per chunk (list_norms.cu's chunks), the last chunk first: the
+// One block per wide chunk, one warp per narrow tensor, the last first: the
 // norms pass has just read the list front to back, so its end is what the
 // 129 MB L2 still holds.  Nothing is written where the norm over all tensors
 // is not finite, nor in place where scale and coefficient are 1.
@@ -13,6 +13,13 @@
 #include "kernels.h"
 
 namespace zs {
+
+constexpr int kClipThreads = 256, kClipBlocks = 4;
+// Elements of a wide chunk that a block clips: smaller than the chunk, so that
+// the blocks in flight read and write fewer places of memory at once.
+constexpr int kClipPiece = 16384;
+// Wide chunks of a block where it may find that nothing is to be clipped.
+constexpr int kClipChunks = 4;
 
 // 16 bytes that this thread may overwrite later: a coherent load.
 __device__ __forceinline__ uint4 ld16_rw(const void* p) {
@@ -68,86 +75,132 @@ __device__ __forceinline__ void store8(char* p, const float (&y)[8]) {
                        pack2_rn<DT>(y[6], y[7])));
 }
 
-template <int S, int D>
-__device__ __forceinline__ void clip_chunk(const char* src, char* dst, int len, float f) {
+// N vectors of 8, T apart, from number v on, all loaded before the first is
+// stored; those from r.vecs on are left out unless FULL.
+template <int S, int D, int T, int N, bool FULL>
+__device__ __forceinline__ void clip_vectors(const char* from, char* to, int v, const Run& r, int len, float f) {
+  constexpr int se = SrcTraits<S>::esize, de = SrcTraits<D>::esize;
+  Vec8<S> x[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int k = v + T * u;
+    if ((FULL || k < r.vecs) && ZS_CHECK(aligned(from + 8 * se * k, 8 * se) && r.head + 8 * k + 8 <= len, 75, k))
+      x[u].load(from + 8 * se * k);
+  }
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int k = v + T * u;
+    if ((FULL || k < r.vecs) && ZS_CHECK(aligned(to + 8 * de * k, 8 * de) && r.head + 8 * k + 8 <= len, 76, k)) {
+      float y[8];
+      x[u].widen(y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(f, y[j]);
+      store8<D>(to + 8 * de * k, y);
+    }
+  }
+}
+
+template <int S, int D, int T>
+__device__ __forceinline__ void clip_piece(const char* src, char* dst, int len, float f, int thread) {
   constexpr int se = SrcTraits<S>::esize, de = SrcTraits<D>::esize;
   constexpr int kAhead = (S == ZERO_F32) ? 4 : 8;
   const Run r = vector_run<se>(src, len);
-  if (aligned(dst + de * r.head, 8 * de)) {
-    const char* from = src + se * r.head;
-    char* to = dst + de * r.head;
-    for (int v0 = threadIdx.x; v0 < r.vecs; v0 += kAhead * kGradThreads) {
-      Vec8<S> x[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int v = v0 + u * kGradThreads;
-        if (v < r.vecs && ZS_CHECK(aligned(from + 8 * se * v, 8 * se) && r.head + 8 * v + 8 <= len, 75, v))
-          x[u].load(from + 8 * se * v);
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int v = v0 + u * kGradThreads;
-        if (v < r.vecs && ZS_CHECK(aligned(to + 8 * de * v, 8 * de) && r.head + 8 * v + 8 <= len, 76, v)) {
-          float y[8];
-          x[u].widen(y);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(f, y[j]);
-          store8<D>(to + 8 * de * v, y);
-        }
-      }
-    }
-    const int e = ragged_element(r, len);
+  const char* from = src + se * r.head;
+  char* to = dst + de * r.head;
+  if (aligned(to, 8 * de)) {
+    int v = thread;
+    for (; v + T * (kAhead - 1) < r.vecs; v += T * kAhead) clip_vectors<S, D, T, kAhead, true>(from, to, v, r, len, f);
+    for (; v < r.vecs; v += T * 4) clip_vectors<S, D, T, 4, false>(from, to, v, r, len, f);
+    const int e = ragged_element(r, len, thread);
     if (e >= 0 && ZS_CHECK(e < len, 77, e)) store_one<D>(dst, e, __fmul_rn(f, load_rw<S>(src, e)));
   } else {  // source and destination apart on the vector grid: element by element
 #pragma unroll 8
-    for (int e = threadIdx.x; e < len; e += kGradThreads) store_one<D>(dst, e, __fmul_rn(f, load_rw<S>(src, e)));
+    for (int e = thread; e < len; e += T) store_one<D>(dst, e, __fmul_rn(f, load_rw<S>(src, e)));
   }
 }
 
-template <int D>
-__device__ __forceinline__ void clip_to(int src_dtype, const char* src, char* dst, int len, float f) {
+template <int D, int T>
+__device__ __forceinline__ void clip_to(int src_dtype, const char* src, char* dst, int len, float f, int thread) {
   if (src == nullptr) {
-    for (int e = threadIdx.x; e < len; e += kGradThreads) store_one<D>(dst, e, 0.0f);
+    for (int e = thread; e < len; e += T) store_one<D>(dst, e, 0.0f);
   } else if (src_dtype == ZERO_F32) {
-    clip_chunk<ZERO_F32, D>(src, dst, len, f);
+    clip_piece<ZERO_F32, D, T>(src, dst, len, f, thread);
   } else if (src_dtype == ZERO_BF16) {
-    clip_chunk<ZERO_BF16, D>(src, dst, len, f);
+    clip_piece<ZERO_BF16, D, T>(src, dst, len, f, thread);
   } else {
-    clip_chunk<ZERO_F16, D>(src, dst, len, f);
+    clip_piece<ZERO_F16, D, T>(src, dst, len, f, thread);
   }
 }
 
-__global__ void __launch_bounds__(kGradThreads)
-    list_clip_kernel(const zero_grad_entry* __restrict__ entries, int n, int n_groups,
-                     const int32_t* __restrict__ first, int chunk, float scale, const float* __restrict__ dscale,
-                     const zero_norm_result* __restrict__ results) {
-  if (!results[n_groups].finite) return;
-  if (dscale != nullptr) scale = *dscale;
-  const GradChunk c = grad_chunk(entries, first, n, chunk, gridDim.x - 1 - blockIdx.x);
-  const zero_grad_entry t = entries[c.tensor];
+template <int T>
+__device__ __forceinline__ void clip_tensor(const zero_grad_entry& t, const GradPiece& c, int n_groups, float scale,
+                                            const zero_norm_result* results) {
   if (t.dst == nullptr) return;
-  if (!ZS_CHECK(c.len > 0 && c.k >= 0 && c.k + c.len <= t.numel && t.group >= 0 && t.group < n_groups, 78, blockIdx.x))
-    return;
+  if (!ZS_CHECK(c.len > 0 && c.k >= 0 && c.k + c.len <= t.numel && t.group >= 0 && t.group < n_groups, 78, c.at)) return;
   const float coef = results[t.group].clip_coef;
   if (t.dst == t.src && coef == 1.0f && scale == 1.0f) return;
   const float f = __fmul_rn(scale, coef);
+  const int thread = T == 32 ? threadIdx.x & 31 : threadIdx.x;
   const char* src = t.src == nullptr ? nullptr : static_cast<const char*>(t.src) + (t.src_dtype == ZERO_F32 ? 4 : 2) * c.k;
   char* dst = static_cast<char*>(t.dst) + (t.dst_dtype == ZERO_F32 ? 4 : 2) * c.k;
   if (t.dst_dtype == ZERO_F32)
-    clip_to<ZERO_F32>(t.src_dtype, src, dst, c.len, f);
+    clip_to<ZERO_F32, T>(t.src_dtype, src, dst, c.len, f, thread);
   else if (t.dst_dtype == ZERO_BF16)
-    clip_to<ZERO_BF16>(t.src_dtype, src, dst, c.len, f);
+    clip_to<ZERO_BF16, T>(t.src_dtype, src, dst, c.len, f, thread);
   else
-    clip_to<ZERO_F16>(t.src_dtype, src, dst, c.len, f);
+    clip_to<ZERO_F16, T>(t.src_dtype, src, dst, c.len, f, thread);
+}
+
+// The grid, from its end: the blocks of the narrow tensors, then for each wide
+// chunk `parts` blocks, or (MAY_LEAVE) one block for kClipChunks of them.
+template <bool MAY_LEAVE>
+__global__ void __launch_bounds__(kClipThreads, kClipBlocks)
+    list_clip_kernel(const zero_grad_entry* __restrict__ entries, int n, int n_groups,
+                     const __grid_constant__ GradPlan plan, int wide_blocks, int parts_log2, float scale,
+                     const float* __restrict__ dscale, const zero_norm_result* results) {
+  const int block = gridDim.x - 1 - blockIdx.x;
+  wait_before();
+  if (!results[n_groups].finite) return;
+  if (MAY_LEAVE && n_groups <= 32) {
+    // in place with a scale of 1: no group to clip, nothing to do
+    const int g = threadIdx.x & 31;
+    if (__all_sync(0xffffffffu, g >= n_groups || results[g].clip_coef == 1.0f)) return;
+  }
+  if (dscale != nullptr) scale = *dscale;
+  if (block >= wide_blocks) {
+    const GradPiece c = narrow_piece<kClipThreads>(entries, plan, block - wide_blocks + plan.n_wide);
+    if (c.len > 0) clip_tensor<32>(entries[c.tensor], c, n_groups, scale, results);
+  } else if (MAY_LEAVE) {
+    for (int chunk = min((block + 1) * kClipChunks, plan.n_wide) - 1; chunk >= block * kClipChunks; --chunk) {
+      const GradPiece c = wide_piece(entries, n, plan, chunk);
+      clip_tensor<kClipThreads>(entries[c.tensor], c, n_groups, scale, results);
+      __syncthreads();  // wide_piece's shared memory
+    }
+  } else {
+    GradPiece c = wide_piece(entries, n, plan, block >> parts_log2);
+    const int piece = plan.chunk >> parts_log2, skip = (block & ((1 << parts_log2) - 1)) * piece;
+    c.k += skip;
+    c.len = min(c.len - skip, piece);
+    if (c.len > 0) clip_tensor<kClipThreads>(entries[c.tensor], c, n_groups, scale, results);
+  }
 }
 
 ZS_DEBUG_UNIT(list_clip)
 
 zero_status launch_list_clip(const GradListArgs& a, const zero_norm_result* results, cudaStream_t st) {
-  if (a.n_chunks == 0) return ZERO_OK;
-  list_clip_kernel<<<a.n_chunks, kGradThreads, 0, st>>>(a.entries, a.n, a.n_groups, a.plan, a.chunk, a.scale, a.dscale,
-                                                        results);
-  return check_launch("list_clip_kernel");
+  const GradPlan plan = plan_parts(a);
+  const int64_t narrow = grad_blocks(plan, kClipThreads) - static_cast<unsigned>(plan.n_wide);
+  const bool may_leave = a.in_place && a.dscale == nullptr && a.scale == 1.0f;
+  int log2 = 0;
+  if (!may_leave)
+    while ((plan.chunk >> log2) > kClipPiece) ++log2;
+  const int64_t wide = may_leave ? (static_cast<int64_t>(plan.n_wide) + kClipChunks - 1) / kClipChunks
+                                 : static_cast<int64_t>(plan.n_wide) << log2;
+  if (wide + narrow > 0x7fffffffLL) return fail(ZERO_EINVAL, "zero_list_clip: %lld blocks", (long long)(wide + narrow));
+  if (wide + narrow == 0) return ZERO_OK;
+  return launch_after("list_clip_kernel", may_leave ? list_clip_kernel<true> : list_clip_kernel<false>,
+                      static_cast<unsigned>(wide + narrow), kClipThreads, 1, st, a.entries, a.n, a.n_groups, plan,
+                      static_cast<int>(wide), log2, a.scale, a.dscale, results);
 }
 
 }  // namespace zs

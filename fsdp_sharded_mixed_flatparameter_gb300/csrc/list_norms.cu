@@ -1,26 +1,33 @@
 // list_norms.cu -- the norms of every tensor of a list, of groups of tensors
 // and of all of them (p = 1, 2, infinity), tensors of mixed types.
 //
-//  1. chunk_sums_kernel: one block per chunk (4096 to 65536 elements, never
-//     across two tensors) reads it once and leaves one binary64 partial: for
-//     p = 2 the squares in double-float pairs (NormAcc of reduce.cuh; exact
-//     squares for 16-bit elements), for p = 1 the magnitudes in the same
-//     pairs, for infinity the largest magnitude by its bits (a NaN's are the
-//     largest, so it stays).  A chunk whose squares leave the binary32 range
-//     is read again scaled by a power of two, which is exact.
-//  2. tensor_sums_kernel: the partials of each tensor in a fixed order, times
-//     |scale|^p.
-//  3. norms_kernel: the sums of each group's tensors, and of all; roots,
-//     coefficients.
+//  1. chunk_sums_kernel: one block per wide chunk (4096 to 65536 elements,
+//     never across two tensors) and one warp per narrow tensor read their
+//     piece once and leave one binary64 partial: for p = 2 the squares in
+//     double-float pairs (NormAcc of reduce.cuh; exact squares for 16-bit
+//     elements), for p = 1 the magnitudes in the same pairs, for infinity the
+//     largest magnitude by its bits (a NaN's are the largest, so it stays).
+//     A piece whose squares leave the binary32 range is read again scaled by
+//     a power of two, which is exact.
+//  2. finish_kernel, one cluster: the partials of each tensor in a fixed
+//     order, times |scale|^p; the norms of tensors and of all; groups up to
+//     256, more by groups_kernel.
 //
-// No atomics: the result is bit-identical from run to run.
+// No floating-point atomics: the result is bit-identical from run to run.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "grad_list.cuh"
 #include "kernels.h"
 
 namespace zs {
 
+namespace cg = cooperative_groups;
+
 // ------------------------------------------------------------ 1: chunks
+// Vectors of 8 that a thread has in flight, and blocks on an SM (64 registers).
+constexpr int kSumThreads = 128, kAhead16 = 8, kAhead32 = 4, kSumBlocks = 8;
+
 // What a thread gathers of its elements: the sums, and in `bits` the elements'
 // bits or'ed (p = 2: whether any is not zero) or the largest magnitude's
 // (infinity).
@@ -107,105 +114,147 @@ struct Gather {
   }
 };
 
+// A piece is summed by T threads: a block's, or one warp.
+template <int T>
+__device__ __forceinline__ int thread_of() {
+  return T == 32 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+}
+
+// The T threads' sums in double-float, in a fixed order, rounded once to
+// binary64: thread 0's result.
+template <int T>
+__device__ __forceinline__ double sum_norm(const NormAcc& acc, float2* red) {
+  if (T != 32) return block_sum_norm<T>(acc, red);
+  DF x = acc.value();
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    x = df_add(x, DF{__shfl_down_sync(0xffffffffu, x.h, off), __shfl_down_sync(0xffffffffu, x.l, off)});
+  return static_cast<double>(x.h) + static_cast<double>(x.l);
+}
+
 // Every thread's result.
-__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
+template <int T>
+__device__ __forceinline__ uint32_t max_of(uint32_t m, uint32_t* red) {
   m = __reduce_max_sync(0xffffffffu, m);
+  if (T == 32) return m;
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kGradThreads / 32; ++w) m = max(m, red[w]);
+  for (int w = 0; w < T / 32; ++w) m = max(m, red[w]);
   __syncthreads();
   return m;
 }
+template <int T>
+__device__ __forceinline__ bool any_of(bool x) {
+  return T == 32 ? __any_sync(0xffffffffu, x) : __syncthreads_or(x) != 0;
+}
 
-// A chunk again, its elements scaled so that the largest lies in [1, 2): the
+// A piece again, its elements scaled so that the largest lies in [1, 2): the
 // sum of squares (magnitudes) of any finite elements.  An element whose
 // square loses bits then is below 2^-62 of the largest.  Thread 0's result.
-template <int P, int DT>
+template <int P, int DT, int T>
 __device__ __noinline__ double scaled_sum(const void* p, int len, float2* red) {
   uint32_t m = 0u;
-  for (int e = threadIdx.x; e < len; e += kGradThreads)
-    m = max(m, __float_as_uint(load_elem<DT>(p, e)) & 0x7fffffffu);
-  m = block_max(m, reinterpret_cast<uint32_t*>(red));
+  for (int e = thread_of<T>(); e < len; e += T) m = max(m, __float_as_uint(load_elem<DT>(p, e)) & 0x7fffffffu);
+  m = max_of<T>(m, reinterpret_cast<uint32_t*>(red));
   if (m >= 0x7f800000u) return static_cast<double>(__uint_as_float(m));  // infinite, or a NaN
   if (m == 0u) return 0.0;
   const int e2 = ilogbf(__uint_as_float(m));
   Gather<P> g;
-  for (int e = threadIdx.x; e < len; e += kGradThreads) g.template pair<false>(scalbnf(load_elem<DT>(p, e), -e2), 0.0f);
-  return scalbn(block_sum_norm<kGradThreads>(g.acc, red), P == ZERO_NORM_2 ? 2 * e2 : e2);
+  for (int e = thread_of<T>(); e < len; e += T) g.template pair<false>(scalbnf(load_elem<DT>(p, e), -e2), 0.0f);
+  return scalbn(sum_norm<T>(g.acc, red), P == ZERO_NORM_2 ? 2 * e2 : e2);
+}
+
+// N vectors of 8, T apart, from number v of `body` on, all loaded
+// before the first is used; those from r.vecs on are left out unless FULL.
+template <int P, int DT, int T, int N, bool FULL>
+__device__ __forceinline__ void gather_vectors(const char* body, int v, const Run& r, int len, Gather<P>& g) {
+  if (DT == ZERO_F32) {
+    float x[N][8];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int k = v + T * u;
+      if ((FULL || k < r.vecs) && ZS_CHECK(aligned(body + 32 * k, 32) && r.head + 8 * k + 8 <= len, 70, k)) {
+        ld8_ro(reinterpret_cast<const float*>(body) + 8 * k, x[u]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) g.vec32(x[u]);
+  } else {
+    uint4 w[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int k = v + T * u;
+      w[u] = make_uint4(0u, 0u, 0u, 0u);
+      if ((FULL || k < r.vecs) && ZS_CHECK(aligned(body + 16 * k, 16) && r.head + 8 * k + 8 <= len, 71, k))
+        w[u] = ld16_ro(body + 16 * k);
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) g.template vec16<DT>(w[u]);
+  }
 }
 
 // The partial of elements [0, len) at p, in thread 0.
-template <int P, int DT>
-__device__ __forceinline__ double chunk_sum(const void* p, int len, float2* red) {
+template <int P, int DT, int T>
+__device__ __forceinline__ double piece_sum(const void* p, int len, float2* red) {
   constexpr int es = SrcTraits<DT>::esize;
-  constexpr int kAhead = (DT == ZERO_F32) ? 4 : 8;  // vectors in flight per thread
+  constexpr int kAhead = (DT == ZERO_F32) ? kAhead32 : kAhead16;  // vectors in flight per thread
   const Run r = vector_run<es>(p, len);
   const char* body = static_cast<const char*>(p) + es * r.head;
   Gather<P> g;
-  for (int v0 = threadIdx.x; v0 < r.vecs; v0 += kAhead * kGradThreads) {
-    if (DT == ZERO_F32) {
-      float x[kAhead][8];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int v = v0 + u * kGradThreads;
-        if (v < r.vecs && ZS_CHECK(aligned(body + 32 * v, 32) && r.head + 8 * v + 8 <= len, 70, v)) {
-          ld8_ro(reinterpret_cast<const float*>(body) + 8 * v, x[u]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[u][i] = 0.0f;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) g.vec32(x[u]);
-    } else {
-      uint4 w[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int v = v0 + u * kGradThreads;
-        w[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (v < r.vecs && ZS_CHECK(aligned(body + 16 * v, 16) && r.head + 8 * v + 8 <= len, 71, v))
-          w[u] = ld16_ro(body + 16 * v);
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) g.template vec16<DT>(w[u]);
-    }
-  }
-  const int e = ragged_element(r, len);
+  int v = thread_of<T>();
+  for (; v + T * (kAhead - 1) < r.vecs; v += T * kAhead) gather_vectors<P, DT, T, kAhead, true>(body, v, r, len, g);
+  for (; v < r.vecs; v += T * 4) gather_vectors<P, DT, T, 4, false>(body, v, r, len, g);
+  const int e = ragged_element(r, len, thread_of<T>());
   if (e >= 0 && ZS_CHECK(e < len, 72, e)) g.template one<DT>(p, e);
+  __syncwarp();
   if (P == ZERO_NORM_INF)
-    return static_cast<double>(__uint_as_float(block_max(g.template top<DT>(), reinterpret_cast<uint32_t*>(red))));
-  const double sum = block_sum_norm<kGradThreads>(g.acc, red);
+    return static_cast<double>(__uint_as_float(max_of<T>(g.template top<DT>(), reinterpret_cast<uint32_t*>(red))));
+  const double sum = sum_norm<T>(g.acc, red);
   // Squares below 2^-126 have lost bits: at most 2^-150 each, 2^-134 of a
-  // chunk, so a sum of 2^-80 and more is right to 2^-54.  Magnitudes lose none.
+  // piece, so a sum of 2^-80 and more is right to 2^-54.  Magnitudes lose none.
   const bool fits = sum < static_cast<double>(INFINITY) && (P == ZERO_NORM_1 || sum >= 0x1p-80);
-  if (__syncthreads_and(threadIdx.x != 0 || fits)) return sum;
-  if (P == ZERO_NORM_2 && !__syncthreads_or(g.template any<DT>())) return 0.0;
-  return scaled_sum<P, DT>(p, len, red);
+  if (!any_of<T>(thread_of<T>() == 0 && !fits)) return sum;
+  if (P == ZERO_NORM_2 && !any_of<T>(g.template any<DT>())) return 0.0;
+  return scaled_sum<P, DT, T>(p, len, red);
 }
 
-template <int P>
-__global__ void __launch_bounds__(kGradThreads)
-    chunk_sums_kernel(const zero_grad_entry* __restrict__ entries, int n, const int32_t* __restrict__ first, int chunk,
-                      double* __restrict__ partials) {
-  __shared__ float2 red[kGradThreads / 32];
-  const GradChunk c = grad_chunk(entries, first, n, chunk, blockIdx.x);
-  const zero_grad_entry& t = entries[c.tensor];
-  if (!ZS_CHECK(c.len > 0 && c.k >= 0 && c.k + c.len <= t.numel, 73, blockIdx.x)) return;
+template <int P, int T>
+__device__ __forceinline__ void piece_partial(const zero_grad_entry& t, const GradPiece& c, double* partials, float2* red) {
+  if (!ZS_CHECK(c.len > 0 && c.k >= 0 && c.k + c.len <= t.numel, 73, c.at)) return;
   const char* src = static_cast<const char*>(t.src);
   double sum = 0.0;
   if (src != nullptr) {
     if (t.src_dtype == ZERO_F32)
-      sum = chunk_sum<P, ZERO_F32>(src + 4 * c.k, c.len, red);
+      sum = piece_sum<P, ZERO_F32, T>(src + 4 * c.k, c.len, red);
     else if (t.src_dtype == ZERO_BF16)
-      sum = chunk_sum<P, ZERO_BF16>(src + 2 * c.k, c.len, red);
+      sum = piece_sum<P, ZERO_BF16, T>(src + 2 * c.k, c.len, red);
     else
-      sum = chunk_sum<P, ZERO_F16>(src + 2 * c.k, c.len, red);
+      sum = piece_sum<P, ZERO_F16, T>(src + 2 * c.k, c.len, red);
   }
-  if (threadIdx.x == 0) partials[blockIdx.x] = sum;
+  if (thread_of<T>() == 0) partials[c.at] = sum;
 }
 
-// ----------------------------------------------------------- 2: tensors
+template <int P>
+__global__ void __launch_bounds__(kSumThreads, kSumBlocks)
+    chunk_sums_kernel(const zero_grad_entry* __restrict__ entries, int n, const __grid_constant__ GradPlan plan,
+                      double* __restrict__ partials) {
+  __shared__ float2 red[kSumThreads / 32];
+  const int block = blockIdx.x;
+  let_next_start();
+  if (block < plan.n_wide) {
+    const GradPiece c = wide_piece(entries, n, plan, block);
+    piece_partial<P, kSumThreads>(entries[c.tensor], c, partials, red);
+  } else {
+    const GradPiece c = narrow_piece<kSumThreads>(entries, plan, block);
+    if (c.len > 0) piece_partial<P, 32>(entries[c.tensor], c, partials, red);
+  }
+}
+
+// ------------------------------------------ 2: tensors, groups and all
 // The two ways of joining: sums, and the largest with NaN above all.
 template <int P>
 __device__ __forceinline__ double join(double a, double b) {
@@ -213,24 +262,29 @@ __device__ __forceinline__ double join(double a, double b) {
   return (a > b || a != a) ? a : b;
 }
 
+// Lane 0's result, of the first `lanes` lanes.  (binary64 additions are a
+// 64th of the binary32 rate: a warp's takes 16 cycles, so none is wasted.)
 template <int P>
-__device__ __forceinline__ double warp_join(double x) {
+__device__ __forceinline__ double warp_join(double x, int lanes = 32) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x = join<P>(x, __shfl_down_sync(0xffffffffu, x, off));
+  for (int off = 16; off > 0; off >>= 1)
+    if (off < lanes) x = join<P>(x, __shfl_down_sync(0xffffffffu, x, off));
   return x;
 }
 
-// Thread 0's result; every thread of the block must call it.
-template <int P, int THREADS>
-__device__ __forceinline__ double block_join(double x, double* red) {
-  x = warp_join<P>(x);
+constexpr int kFinishThreads = 1024;
+constexpr int kFinishBlocks = 8;  // at most: one cluster
+
+// Thread 0's result, of the first `lanes` lanes of each warp; every thread of
+// the block must call it.
+template <int P>
+__device__ __forceinline__ double block_join(double x, int lanes, double* red) {
+  x = warp_join<P>(x, lanes);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
   __syncthreads();
-  double r = red[0];
-  if (threadIdx.x == 0)
-    for (int w = 1; w < THREADS / 32; ++w) r = join<P>(r, red[w]);
+  if (threadIdx.x < 32) x = warp_join<P>(red[threadIdx.x]);
   __syncthreads();
-  return r;
+  return x;
 }
 
 // load(at), load(at + step), ... below count, eight in flight.
@@ -242,70 +296,75 @@ __device__ __forceinline__ double strided(int at, int count, int step, const Loa
 #pragma unroll
     for (int u = 0; u < 8; ++u) v[u] = i + u * step < count ? load(static_cast<int>(i + u * step)) : 0.0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) acc = join<P>(acc, v[u]);
+    for (int u = 0; u < 8; ++u)
+      if (i + u * step < count) acc = join<P>(acc, v[u]);
   }
   return acc;
 }
 
-// Partials up to which one warp adds a tensor's; above, the block does.
-constexpr int kWarpPartials = 2048;
-
-template <int P>
-__global__ void __launch_bounds__(kGradThreads)
-    tensor_sums_kernel(const double* __restrict__ partials, const int32_t* __restrict__ first, int n, float scale,
-                       const float* __restrict__ dscale, double* __restrict__ sums) {
-  __shared__ double red[kGradThreads / 32];
-  const double s = fabs(static_cast<double>(dscale != nullptr ? *dscale : scale));
-  const double factor = P == ZERO_NORM_2 ? s * s : s;
-  const int base = blockIdx.x * (kGradThreads / 32);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mine = base + warp;
-  if (mine < n) {
-    const int lo = __ldg(first + mine), count = __ldg(first + mine + 1) - lo;
-    if (count <= kWarpPartials) {
-      const double x = warp_join<P>(strided<P>(lane, count, 32, [&](int i) { return __ldg(partials + lo + i); }));
-      if (lane == 0) sums[mine] = x * factor;
-    }
-  }
-  for (int i = base; i < min(base + kGradThreads / 32, n); ++i) {
-    const int lo = __ldg(first + i), count = __ldg(first + i + 1) - lo;
-    if (count <= kWarpPartials) continue;
-    const double x = block_join<P, kGradThreads>(
-        strided<P>(threadIdx.x, count, kGradThreads, [&](int j) { return __ldg(partials + lo + j); }), red);
-    if (threadIdx.x == 0) sums[i] = x * factor;
-  }
-}
-
-// ------------------------------------------------------ 3: groups and all
-constexpr int kNormThreads = 1024;
-
-struct NormsArgs {
+struct FinishArgs {
   GradPlan plan;
   int n, n_groups;
-  const double* sums;
+  const double* partials;  // of the chunks; or the ranks' sums, n_parts rows of n
   int n_parts;
+  float scale;
+  const float* dscale;
+  double* sums;            // of the tensors, over all parts
   const double* max_norms;
   float* norms;
-  zero_norm_result* results;
+  zero_norm_result* results;  // NULL: the sums only
   int32_t* found;
 };
 
-template <int P>
-__device__ __forceinline__ double root(double s) {
-  return P == ZERO_NORM_2 ? __dsqrt_rn(s) : s;
+// Groups up to which finish_kernel finishes them too.
+constexpr int kFinishGroups = 256;
+// Partials of a tensor up to which a thread adds them, and a warp; above, a block.
+constexpr int kThreadPartials = 16, kWarpPartials = 1024;
+// Up to these one block finishes.
+constexpr int kBlockTensors = 128, kBlockPartials = 2048;
+// Tensors above which tensors_kernel makes their sums, and the partials up to
+// which 8 of its lanes add a tensor's; above, a block.
+constexpr int kFinishTensors = 1024, kOctetPartials = 512;
+static_assert(kFinishTensors <= kFinishThreads, "a thread of finish_kernel has at most one tensor");
+
+// What finish_kernel finds: the chunks' partials, the ranks' sums, or the
+// tensors' sums that tensors_kernel has left.
+enum Have { kPartials, kParts, kSums };
+
+__device__ __forceinline__ void partials_of(const GradPlan& p, int i, int& lo, int& count) {
+  const int j = __ldg(p.narrow_of + i);
+  lo = j >= 0 ? p.n_wide + j : __ldg(p.first + i);
+  count = j >= 0 ? 1 : __ldg(p.first + i + 1) - lo;
 }
 
-// Tensor i's sum over the parts, in their order.
 template <int P>
-__device__ __forceinline__ double tensor_sum(const NormsArgs& a, int i) {
-  double s = __ldg(a.sums + i);
-  for (int r = 1; r < a.n_parts; ++r) s = join<P>(s, __ldg(a.sums + static_cast<int64_t>(r) * a.n + i));
-  return s;
+__device__ __forceinline__ double scale_power(const FinishArgs& a) {
+  const double s = fabs(static_cast<double>(a.dscale != nullptr ? *a.dscale : a.scale));
+  return P == ZERO_NORM_2 ? s * s : s;
 }
 
 template <int P>
-__device__ __forceinline__ void write_result(const NormsArgs& a, int g, double sum) {
-  const double norm = root<P>(sum);
+__device__ __forceinline__ double join_parts(const FinishArgs& a, int i) {
+  const double* const row = a.partials + i;
+  return strided<P>(0, a.n_parts, 1, [&](int r) { return __ldcg(row + static_cast<int64_t>(r) * a.n); });
+}
+
+// A tensor's norm in binary32, at most 2^-24 (1 + 2^-22) off: the binary32 root and
+// one Newton step whose residual is a binary64 fma (__dsqrt_rn takes some 25
+// binary64 instructions; 20,000 tensors' would be most of this kernel).
+template <int P>
+__device__ __forceinline__ float tensor_norm(double s) {
+  if (P != ZERO_NORM_2) return __double2float_rn(s);
+  const float f = __double2float_rn(s);
+  if (!(f > 0x1p-100f && f < 0x1p100f)) return __double2float_rn(__dsqrt_rn(s));
+  const float y = __fsqrt_rn(f);
+  const float rest = __double2float_rn(fma(-static_cast<double>(y), static_cast<double>(y), s));
+  return __fadd_rn(y, __fdiv_rn(rest, 2.0f * y));
+}
+
+template <int P>
+__device__ __forceinline__ void write_result(const FinishArgs& a, int g, double sum) {
+  const double norm = P == ZERO_NORM_2 ? __dsqrt_rn(sum) : sum;
   zero_norm_result r;
   r.sqnorm = sum;
   r.norm = norm;
@@ -321,74 +380,216 @@ __device__ __forceinline__ void write_result(const NormsArgs& a, int g, double s
   a.norms[a.n + g] = __double2float_rn(norm);
 }
 
-// Block 0: all tensors.  The others: a group each (WARPS == false), or 32
-// groups, a warp each, where groups are small.
-template <int P, bool WARPS>
-__global__ void __launch_bounds__(kNormThreads) norms_kernel(const __grid_constant__ NormsArgs a) {
-  __shared__ double red[kNormThreads / 32];
-  if (blockIdx.x == 0) {
-    const double s = block_join<P, kNormThreads>(
-        strided<P>(threadIdx.x, a.n, kNormThreads, [&](int i) { return tensor_sum<P>(a, i); }), red);
-    if (threadIdx.x == 0) write_result<P>(a, a.n_groups, s);
+// The sums and norms of many tensors over all SMs (the binary64 pipes of
+// finish_kernel's 8 SMs alone took 38 us for 20,000 tensors): 8 lanes for
+// each, or a thread to join the ranks' sums.
+template <int P, bool PARTS>
+__global__ void __launch_bounds__(256) tensors_kernel(const __grid_constant__ FinishArgs a) {
+  __shared__ double red[32];
+  let_next_start();
+  wait_before();
+  if (PARTS) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.n) return;
+    const double s = join_parts<P>(a, i);
+    a.sums[i] = s;
+    a.norms[i] = tensor_norm<P>(s);
     return;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = WARPS ? (blockIdx.x - 1) * (kNormThreads / 32) + warp : blockIdx.x - 1;
-  if (g >= a.n_groups) return;  // WARPS: a whole warp, and no barrier follows
-  const int lo = __ldg(a.plan.group_first + g), count = __ldg(a.plan.group_first + g + 1) - lo;
-  const auto member = [&](int j) {
-    const int i = __ldg(a.plan.members + lo + j);
-    const double s = tensor_sum<P>(a, i);
-    a.norms[i] = __double2float_rn(root<P>(s));
-    return s;
+  const int base = blockIdx.x * 32, i = base + (threadIdx.x >> 3), lane = threadIdx.x & 7;
+  int lo = 0, count = 0;
+  if (i < a.n) partials_of(a.plan, i, lo, count);
+  const double factor = scale_power<P>(a);
+  const auto finish = [&](int k, double s) {
+    s *= factor;
+    a.sums[k] = s;
+    if (a.norms != nullptr) a.norms[k] = tensor_norm<P>(s);
   };
-  if (WARPS) {
-    const double s = warp_join<P>(strided<P>(lane, count, 32, member));
-    if (lane == 0) write_result<P>(a, g, s);
+  double s = 0.0;
+  if (count <= kOctetPartials) s = strided<P>(lane, count, 8, [&](int j) { return __ldcg(a.partials + lo + j); });
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) s = join<P>(s, __shfl_down_sync(0xffffffffu, s, off, 8));
+  if (lane == 0 && i < a.n && count <= kOctetPartials) finish(i, s);
+  if (!__syncthreads_or(count > kOctetPartials)) return;
+  if (threadIdx.x < 32) red[threadIdx.x] = 0.0;  // block_join reads 32
+  for (int k = base; k < base + 32 && k < a.n; ++k) {
+    partials_of(a.plan, k, lo, count);
+    if (count <= kOctetPartials) continue;
+    __syncthreads();
+    s = block_join<P>(strided<P>(threadIdx.x, count, 256, [&](int j) { return __ldcg(a.partials + lo + j); }), 32, red);
+    if (threadIdx.x == 0) finish(k, s);
+  }
+}
+
+// One cluster of 8 blocks, or one block.  Of its W warps tensor i belongs to
+// warp i % W, lane i / W: long tensors, whose partials a warp or a block adds,
+// spread over the warps.  Every thread adds its tensors to the sum over all;
+// the blocks' sums meet in distributed shared memory.  Then the groups.
+template <int P, Have HAVE>
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ FinishArgs a) {
+  __shared__ double red[kFinishThreads / 32], long_sums[kFinishThreads], block_total;
+  __shared__ int long_tensors[kFinishThreads], n_long;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int blocks = gridDim.x, warps = blocks * (kFinishThreads / 32);
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) * blocks + rank;
+  let_next_start();
+  // what the plan says of this thread's tensor and group, while the kernel before still runs
+  const int i = lane * warps + warp;
+  int lo = 0, count = 0, group_lo = 0, group_count = 0, first_member = 0;
+  if (HAVE == kPartials && i < a.n) partials_of(a.plan, i, lo, count);
+  if (warp < a.n_groups) {
+    group_lo = __ldg(a.plan.group_first + warp);
+    group_count = __ldg(a.plan.group_first + warp + 1) - group_lo;
+    if (lane < group_count) first_member = __ldg(a.plan.members + group_lo + lane);
+  }
+  if (threadIdx.x == 0) n_long = 0;
+  wait_before();
+  double all = 0.0;
+  if (HAVE == kSums) {
+    all = strided<P>(i, a.n, warps * 32, [&](int j) { return __ldcg(a.sums + j); });
   } else {
-    const double s = block_join<P, kNormThreads>(strided<P>(threadIdx.x, count, kNormThreads, member), red);
-    if (threadIdx.x == 0) write_result<P>(a, g, s);
+    if (HAVE == kParts) {
+      if (i < a.n) all = join_parts<P>(a, i);
+    } else {
+      if (count <= kThreadPartials) all = strided<P>(0, count, 1, [&](int j) { return __ldcg(a.partials + lo + j); });
+      unsigned mid = __ballot_sync(0xffffffffu, count > kThreadPartials && count <= kWarpPartials);
+      for (; mid != 0u; mid &= mid - 1u) {
+        const int l = __ffs(mid) - 1, from = __shfl_sync(0xffffffffu, lo, l), len = __shfl_sync(0xffffffffu, count, l);
+        double x = warp_join<P>(strided<P>(lane, len, 32, [&](int j) { return __ldcg(a.partials + from + j); }));
+        x = __shfl_sync(0xffffffffu, x, 0);
+        if (lane == l) all = x;
+      }
+      if (__syncthreads_or(count > kWarpPartials)) {
+        int slot = 0;
+        if (count > kWarpPartials) long_tensors[slot = atomicAdd(&n_long, 1)] = i;  // their order does not matter
+        __syncthreads();
+        const int k = n_long;
+        for (int q = 0; q < k; ++q) {
+          int from, len;
+          partials_of(a.plan, long_tensors[q], from, len);
+          const double x = block_join<P>(
+              strided<P>(threadIdx.x, len, kFinishThreads, [&](int j) { return __ldcg(a.partials + from + j); }), 32, red);
+          if (threadIdx.x == 0) long_sums[q] = x;
+        }
+        __syncthreads();
+        if (count > kWarpPartials) all = long_sums[slot];
+      }
+      all *= scale_power<P>(a);
+    }
+    if (i < a.n) {
+      a.sums[i] = all;
+      if (a.norms != nullptr) a.norms[i] = tensor_norm<P>(all);
+    } else {
+      all = 0.0;
+    }
+  }
+  if (a.results == nullptr) return;
+  const int lanes = min((a.n + warps - 1) / warps, 32);
+  all = block_join<P>(all, lanes, red);
+  if (threadIdx.x == 0) block_total = all;
+  cluster.sync();  // the blocks' totals, and the tensors' sums
+  if (rank == 0 && threadIdx.x < 32) {
+    double x = 0.0;
+    if (lane < blocks) x = *cluster.map_shared_rank(&block_total, lane);
+    x = warp_join<P>(x, blocks);
+    if (lane == 0) {
+      write_result<P>(a, a.n_groups, x);
+      if (a.n_groups == 1) write_result<P>(a, 0, x);
+    }
+  }
+  if (a.n_groups > 1 && a.n_groups <= kFinishGroups) {
+    const auto sum_of = [&](int lo, int count, int from, int step) {
+      return strided<P>(from, count, step, [&](int j) { return __ldcg(a.sums + __ldg(a.plan.members + lo + j)); });
+    };
+    if (a.n / a.n_groups <= 512) {
+      for (int g = warp; g < a.n_groups; g += warps) {
+        const bool again = g != warp;
+        const int from = again ? __ldg(a.plan.group_first + g) : group_lo;
+        const int len = again ? __ldg(a.plan.group_first + g + 1) - from : group_count;
+        if (again) first_member = lane < len ? __ldg(a.plan.members + from + lane) : 0;
+        double x = lane < len ? __ldcg(a.sums + first_member) : 0.0;
+        x = warp_join<P>(join<P>(x, sum_of(from, len, lane + 32, 32)));
+        if (lane == 0) write_result<P>(a, g, x);
+      }
+    } else {
+      for (int g = rank; g < a.n_groups; g += blocks) {
+        const int lo = __ldg(a.plan.group_first + g), count = __ldg(a.plan.group_first + g + 1) - lo;
+        const double x = block_join<P>(sum_of(lo, count, threadIdx.x, kFinishThreads), 32, red);
+        if (threadIdx.x == 0) write_result<P>(a, g, x);
+      }
+    }
+  }
+  cluster.sync();  // block_total is read until here
+}
+
+// Many groups, over all SMs: a thread each where they have few tensors, else
+// a warp each.
+template <int P, bool WARPS>
+__global__ void __launch_bounds__(128) groups_kernel(const __grid_constant__ FinishArgs a) {
+  let_next_start();
+  const int t = blockIdx.x * 128 + threadIdx.x, lane = threadIdx.x & 31;
+  const int g = WARPS ? t >> 5 : t;
+  wait_before();
+  if (g >= a.n_groups) return;
+  const int lo = __ldg(a.plan.group_first + g), count = __ldg(a.plan.group_first + g + 1) - lo;
+  const auto member = [&](int j) { return __ldcg(a.sums + __ldg(a.plan.members + lo + j)); };
+  if (WARPS) {
+    const double x = warp_join<P>(strided<P>(lane, count, 32, member));
+    if (lane == 0) write_result<P>(a, g, x);
+  } else {
+    write_result<P>(a, g, strided<P>(0, count, 1, member));
   }
 }
 
 // -------------------------------------------------------------- launches
-template <int P>
-static zero_status launch_sums_t(const GradListArgs& a, double* partials, double* sums, cudaStream_t st) {
-  const GradPlan plan = plan_parts(a.plan, a.n, a.n_groups);
-  if (a.n_chunks > 0) {
-    chunk_sums_kernel<P><<<a.n_chunks, kGradThreads, 0, st>>>(a.entries, a.n, plan.first, a.chunk, partials);
-    const zero_status s = check_launch("chunk_sums_kernel");
-    if (s != ZERO_OK) return s;
+template <int P, bool PARTS>
+static zero_status launch_finish(const FinishArgs& k, cudaStream_t st) {
+  zero_status s = ZERO_OK;
+  if (k.n <= kFinishTensors) {
+    const bool few = k.n <= kBlockTensors && (PARTS || k.plan.n_wide + k.plan.n_narrow <= kBlockPartials);
+    const int blocks = few ? 1 : kFinishBlocks;
+    s = launch_after("finish_kernel", finish_kernel<P, PARTS ? kParts : kPartials>, blocks, kFinishThreads, blocks, st, k);
+  } else {
+    s = launch_after("tensors_kernel", tensors_kernel<P, PARTS>, one_pass_blocks(k.n, PARTS ? 256 : 32), 256, 1, st, k);
+    if (s == ZERO_OK && k.results != nullptr)
+      s = launch_after("finish_kernel", finish_kernel<P, kSums>, kFinishBlocks, kFinishThreads, kFinishBlocks, st, k);
   }
-  tensor_sums_kernel<P><<<one_pass_blocks(a.n, kGradThreads / 32), kGradThreads, 0, st>>>(partials, plan.first, a.n,
-                                                                                       a.scale, a.dscale, sums);
-  return check_launch("tensor_sums_kernel");
+  if (s != ZERO_OK || k.results == nullptr || k.n_groups <= kFinishGroups) return s;
+  if (k.n / k.n_groups < 16)
+    return launch_after("groups_kernel", groups_kernel<P, false>, one_pass_blocks(k.n_groups, 128), 128, 1, st, k);
+  return launch_after("groups_kernel", groups_kernel<P, true>, one_pass_blocks(k.n_groups, 4), 128, 1, st, k);
 }
 
 template <int P>
-static zero_status launch_norms_t(const NormsArgs& a, cudaStream_t st) {
-  if (a.n / a.n_groups >= 256 || a.n_groups <= 64) {
-    norms_kernel<P, false><<<1 + a.n_groups, kNormThreads, 0, st>>>(a);
-  } else {
-    norms_kernel<P, true><<<1 + one_pass_blocks(a.n_groups, kNormThreads / 32), kNormThreads, 0, st>>>(a);
+static zero_status launch_norms_t(const GradListArgs& a, double* partials, const FinishArgs& k, cudaStream_t st) {
+  if (grad_blocks(k.plan, kSumThreads) > 0) {
+    chunk_sums_kernel<P><<<grad_blocks(k.plan, kSumThreads), kSumThreads, 0, st>>>(a.entries, a.n, k.plan, partials);
+    const zero_status s = check_launch("chunk_sums_kernel");
+    if (s != ZERO_OK) return s;
   }
-  return check_launch("norms_kernel");
+  return launch_finish<P, false>(k, st);
 }
 
 ZS_DEBUG_UNIT(list_norms)
 
-zero_status launch_list_sums(const GradListArgs& a, double* partials, double* sums, cudaStream_t st) {
-  if (a.norm_type == ZERO_NORM_2) return launch_sums_t<ZERO_NORM_2>(a, partials, sums, st);
-  if (a.norm_type == ZERO_NORM_1) return launch_sums_t<ZERO_NORM_1>(a, partials, sums, st);
-  return launch_sums_t<ZERO_NORM_INF>(a, partials, sums, st);
+zero_status launch_list_norms(const GradListArgs& a, double* partials, double* sums, const double* max_norms, float* norms,
+                              zero_norm_result* results, int32_t* found, cudaStream_t st) {
+  const FinishArgs k{plan_parts(a), a.n, a.n_groups, partials, 1, a.scale, a.dscale, sums,
+                     max_norms, norms, results, found};
+  if (a.norm_type == ZERO_NORM_2) return launch_norms_t<ZERO_NORM_2>(a, partials, k, st);
+  if (a.norm_type == ZERO_NORM_1) return launch_norms_t<ZERO_NORM_1>(a, partials, k, st);
+  return launch_norms_t<ZERO_NORM_INF>(a, partials, k, st);
 }
 
-zero_status launch_sums_norms(const GradListArgs& a, const double* sums, int n_parts, const double* max_norms,
-                              float* norms, zero_norm_result* results, int32_t* found, cudaStream_t st) {
-  const NormsArgs k{plan_parts(a.plan, a.n, a.n_groups), a.n, a.n_groups, sums, n_parts, max_norms, norms, results, found};
-  if (a.norm_type == ZERO_NORM_2) return launch_norms_t<ZERO_NORM_2>(k, st);
-  if (a.norm_type == ZERO_NORM_1) return launch_norms_t<ZERO_NORM_1>(k, st);
-  return launch_norms_t<ZERO_NORM_INF>(k, st);
+zero_status launch_sums_norms(const GradListArgs& a, const double* sums, int n_parts, double* joined,
+                              const double* max_norms, float* norms, zero_norm_result* results, int32_t* found,
+                              cudaStream_t st) {
+  const FinishArgs k{plan_parts(a), a.n, a.n_groups, sums, n_parts, 1.0f, nullptr, joined,
+                     max_norms, norms, results, found};
+  if (a.norm_type == ZERO_NORM_2) return launch_finish<ZERO_NORM_2, true>(k, st);
+  if (a.norm_type == ZERO_NORM_1) return launch_finish<ZERO_NORM_1, true>(k, st);
+  return launch_finish<ZERO_NORM_INF, true>(k, st);
 }
 
 }  // namespace zs

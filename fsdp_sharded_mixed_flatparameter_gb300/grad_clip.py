@@ -36,7 +36,7 @@ class GradClip(GradTables):
     range(len(numels)) each tensor is clipped by its own norm; norm_type: 1, 2 or inf.
 
     After a launch, on the device: ``tensor_norms``, ``group_norms`` (float32), ``norm`` (0-d),
-    ``tensor_sums`` (float64, this rank's), ``results`` (a zero_norm_result per group) and
+    ``tensor_sums`` (float64, this rank's; ``joined_sums``: of gathered ones, all ranks'), ``results`` (a zero_norm_result per group) and
     ``result``, the one over all with a coefficient of 1: what launch_step(norm_result=...) of
     the optimizers takes after the grads have been clipped here.  The buffers are rewritten by
     each launch: launches of one object that overlap on the GPU race, and the object has to
@@ -58,12 +58,10 @@ class GradClip(GradTables):
         self.plan = zs.zero_grad_plan(self.numels, group_of, n_groups, norm_type, dev)
         n, g = len(self.numels), n_groups
         self.max_norms = limits.to(dev)
-        self.ws = torch.empty(max(zs.zero_list_norms_workspace_bytes(self.plan.n_chunks), 8), dtype=torch.uint8,
-                              device=dev)
-        self.tensor_sums = torch.zeros(n, dtype=torch.float64, device=dev)
-        self.norms = torch.zeros(n + g + 1, dtype=torch.float32, device=dev)
-        self.tensor_norms, self.group_norms, self.norm = self.norms[:n], self.norms[n:n + g], self.norms[n + g]
-        self.results = torch.zeros((g + 1) * zs.NORM_RESULT_BYTES, dtype=torch.uint8, device=dev)
+        self.buffers = zs.norm_buffers(self.plan, self.max_norms)
+        self.tensor_sums, self.joined_sums = self.buffers.sums, self.buffers.joined
+        norms, self.results = self.buffers.norms, self.buffers.results
+        self.tensor_norms, self.group_norms, self.norm = norms[:n], norms[n:n + g], norms[n + g]
         self.result = self.results[g * zs.NORM_RESULT_BYTES:]
         self.found_nonfinite = torch.zeros(1, dtype=torch.int32, device=dev)
         self._home = self._current()  # the stream whose order the buffers' memory follows
@@ -145,7 +143,7 @@ class GradClip(GradTables):
         self._read_on(table, raw)
         if raw != self._home and not torch.cuda.is_current_stream_capturing():
             st = torch_stream(raw, self.device)
-            for t in (self.plan.ints, self.max_norms, self.ws, self.tensor_sums, self.norms, self.results):
+            for t in (self.plan.ints, *self.buffers[:6], self.found_nonfinite):
                 t.record_stream(st)
         return raw
 
@@ -156,7 +154,7 @@ class GradClip(GradTables):
         sc, dsc, _ = self._scale_args(scale, loss_scale)
         with self._here():
             gl, table, _ = self._list(grads, None, False)
-            zs.zero_list_sums(gl, sc, self.ws, self.tensor_sums, self._on(stream, table), d_scale=dsc)
+            zs.zero_list_sums(gl, sc, self.buffers, self._on(stream, table), d_scale=dsc)
 
     def launch_norms(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, scale: float = 1.0,
                      loss_scale=None, gathered_sums: Optional[torch.Tensor] = None, process_group=None,
@@ -188,16 +186,15 @@ class GradClip(GradTables):
             gl, table, _ = self._list(grads, out, clip)
             raw = self._on(stream, table)
             if gathered is None and process_group is not None and _world(process_group) > 1:
-                zs.zero_list_sums(gl, sc, self.ws, self.tensor_sums, raw, d_scale=dsc)
+                zs.zero_list_sums(gl, sc, self.buffers, raw, d_scale=dsc)
                 with torch.cuda.stream(torch_stream(raw, self.device)):
                     gathered = gather_sqnorms(self.tensor_sums, process_group)
             if gathered is None:
-                zs.zero_list_norms(gl, sc, clip, self.ws, self.tensor_sums, self.max_norms, self.norms, self.results,
-                                   flag, raw, d_scale=dsc)
+                zs.zero_list_norms(gl, sc, clip, self.buffers, flag, raw, d_scale=dsc)
                 return
-            zs.zero_sums_norms(gl, gathered, gathered.numel() // n, self.max_norms, self.norms, self.results, flag, raw)
+            zs.zero_sums_norms(gl, gathered, gathered.numel() // n, self.buffers, flag, raw)
             if clip:
-                zs.zero_list_clip(gl, sc, self.results, raw, d_scale=dsc)
+                zs.zero_list_clip(gl, sc, self.buffers, raw, d_scale=dsc)
 
     def finish(self, stream=None) -> ClipResult:
         """Read the last launch's result (a device-to-host copy on `stream`, where it was enqueued)."""

@@ -79,8 +79,8 @@ class zero_grad_entry(ctypes.Structure):
 
 class zero_grad_list(ctypes.Structure):
     _fields_ = [("d_entries", ctypes.c_void_p), ("d_plan", ctypes.c_void_p), ("n_tensors", ctypes.c_int32),
-                ("n_groups", ctypes.c_int32), ("n_chunks", ctypes.c_int32), ("chunk", ctypes.c_int32),
-                ("norm_type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("n_groups", ctypes.c_int32), ("n_wide", ctypes.c_int32), ("n_narrow", ctypes.c_int32),
+                ("chunk", ctypes.c_int32), ("norm_type", ctypes.c_int32), ("in_place", ctypes.c_int32)]
 
 
 STATE8_BLOCK = 256      # elements per scale of the 8-bit moments
@@ -153,12 +153,12 @@ def lib() -> ctypes.CDLL:
     L.zero_adamw_list_device.argtypes = [vp, i32, vp, i32, i32, vp, ci, f32, vp, ci, vp, i32, rdp, vp, vp]
     L.zero_adamw_prepare_list_device.argtypes = [vp, i32, vp, vp, vp]
     glp = ctypes.POINTER(zero_grad_list)
-    L.zero_grad_plan.argtypes = [vp, vp, i32, i32, vp, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+    L.zero_grad_plan.argtypes = [vp, vp, i32, i32, vp, glp]
     L.zero_grad_entries_check.argtypes = [vp, vp, i32, i32]
-    L.zero_list_norms_workspace_bytes.argtypes = [i32]
+    L.zero_list_norms_workspace_bytes.argtypes = [glp]
     L.zero_list_norms_workspace_bytes.restype = ctypes.c_size_t
     L.zero_list_sums.argtypes = [glp, f32, vp, vp, sz, vp, vp]
-    L.zero_sums_norms.argtypes = [glp, vp, i32, vp, vp, vp, vp, vp]
+    L.zero_sums_norms.argtypes = [glp, vp, i32, vp, vp, vp, vp, vp, vp]
     L.zero_list_clip.argtypes = [glp, f32, vp, vp, vp]
     L.zero_list_norms.argtypes = [glp, f32, vp, i32, vp, sz, vp, vp, vp, vp, vp, vp]
     L.zero_status_string.argtypes = [ctypes.c_int]
@@ -878,7 +878,7 @@ class GradList(NamedTuple):
     entries and plan.  It holds addresses: keep the tensors alive."""
     entries: Optional[torch.Tensor]  # uint8, 40 bytes per tensor; None: sums and norms of other ranks' lists only
     plan: "GradPlan"
-    head: zero_grad_list             # the C entries' description of the list
+    ref: object                      # a pointer to the C entries' description of the list
 
 
 class GradPlan(NamedTuple):
@@ -887,9 +887,7 @@ class GradPlan(NamedTuple):
     numels: np.ndarray  # int64
     groups: Optional[np.ndarray]  # int32, or None: all in group 0
     n_groups: int
-    n_chunks: int
-    chunk: int
-    norm_type: int
+    head: zero_grad_list  # the C entries' description of the plan
 
 
 _GRAD_ENTRY = np.dtype([(nm, np.uint64 if ct is ctypes.c_void_p else np.int64 if ct is ctypes.c_int64 else np.int32)
@@ -909,11 +907,13 @@ def zero_grad_plan(numels: Sequence[int], group_of: Optional[Sequence[int]], n_g
         if len(group_of) != n:
             raise ValueError("one group per tensor is required")
         groups = np.ascontiguousarray(np.asarray(group_of, dtype=np.int32))
-    ints = np.zeros(2 * n + max(int(n_groups), 0) + 2, dtype=np.int32)
-    n_chunks, chunk = ctypes.c_int32(), ctypes.c_int32()
+    ints = np.zeros(4 * n + max(int(n_groups), 0) + 2, dtype=np.int32)
+    head = zero_grad_list()
     _check(lib().zero_grad_plan(sizes.ctypes.data, None if groups is None else groups.ctypes.data, n, n_groups,
-                                ints.ctypes.data, ctypes.byref(n_chunks), ctypes.byref(chunk)))
-    return GradPlan(torch.from_numpy(ints).to(device), sizes, groups, int(n_groups), n_chunks.value, chunk.value, p)
+                                ints.ctypes.data, ctypes.byref(head)))
+    d_ints = torch.from_numpy(ints).to(device)
+    head.d_plan, head.norm_type = d_ints.data_ptr(), p
+    return GradPlan(d_ints, sizes, groups, int(n_groups), head)
 
 
 def _dense(t: torch.Tensor) -> bool:
@@ -994,71 +994,91 @@ def grad_list(plan: GradPlan, grads: Sequence[Optional[torch.Tensor]], out: Opti
         if _overlaps(at, ends, np.arange(len(at)) < int(written.sum())):
             raise ValueError("a grad that is written overlaps another tensor of the list (is one listed twice?)")
     d_entries = torch.from_numpy(entries.view(np.uint8)).to(device)
-    return GradList(d_entries, plan, _list_head(plan, d_entries.data_ptr()))
+    elsewhere = (entries["dst"] != 0) & (entries["dst"] != entries["src"])
+    return GradList(d_entries, plan, _list_ref(plan, d_entries.data_ptr(), int(not elsewhere.any())))
 
 
-def _list_head(plan: GradPlan, d_entries: Optional[int]) -> zero_grad_list:
-    return zero_grad_list(d_entries, plan.ints.data_ptr(), len(plan.numels), plan.n_groups, plan.n_chunks, plan.chunk,
-                          plan.norm_type, 0)
+def _list_ref(plan: GradPlan, d_entries: Optional[int], in_place: int):
+    head = zero_grad_list.from_buffer_copy(plan.head)
+    head.d_entries, head.in_place = d_entries, in_place
+    return ctypes.pointer(head)
 
 
 def norms_only_list(plan: GradPlan) -> GradList:
     """A list without entries, for zero_sums_norms."""
-    return GradList(None, plan, _list_head(plan, None))
+    return GradList(None, plan, _list_ref(plan, None, 0))
 
 
-def zero_list_norms_workspace_bytes(n_chunks: int) -> int:
-    return int(lib().zero_list_norms_workspace_bytes(n_chunks))
+def zero_list_norms_workspace_bytes(plan: GradPlan) -> int:
+    return int(lib().zero_list_norms_workspace_bytes(ctypes.byref(plan.head)))
 
 
-def _f64(t: torch.Tensor, name: str, need: int) -> int:
-    if t.numel() < need:
-        raise ValueError(f"{name} has {t.numel()} elements, {need} are needed")
-    return _dev(t, name, torch.float64)
+class NormBuffers(NamedTuple):
+    """What the calls on a grads list write, checked once (norm_buffers)."""
+    ws: torch.Tensor           # uint8, zero_list_norms_workspace_bytes
+    sums: torch.Tensor         # float64, a tensor's sum each
+    joined: torch.Tensor       # float64, the same over all ranks (zero_sums_norms)
+    max_norms: torch.Tensor    # float64, the groups' limits (read)
+    norms: torch.Tensor        # float32: tensors, groups, all
+    results: torch.Tensor      # a zero_norm_result per group and one for all
+    addresses: tuple           # ws, its bytes, sums, joined, max_norms, norms, results
 
 
-def _norm_outputs(gl: GradList, max_norms, norms, results, found):
-    n, g = len(gl.plan.numels), gl.plan.n_groups
-    if norms.numel() < n + g + 1:
-        raise ValueError(f"norms has {norms.numel()} elements, {n + g + 1} are needed")
-    if results.numel() * results.element_size() < (g + 1) * NORM_RESULT_BYTES:
-        raise ValueError("results is smaller than one zero_norm_result per group and one more")
-    return (_f64(max_norms, "max_norms", g), _dev(norms, "norms", torch.float32), _dev(results, "results"),
-            _dev(found, "found_nonfinite", torch.int32, allow_none=True))
+def norm_buffers(plan: GradPlan, max_norms: torch.Tensor) -> NormBuffers:
+    """Buffers for lists of this plan; max_norms: the groups' limits (float64, on the device)."""
+    dev, n, g = plan.ints.device, len(plan.numels), plan.n_groups
+    if max_norms.dtype != torch.float64 or max_norms.numel() != g or max_norms.device != dev:
+        raise ValueError(f"max_norms must be {g} float64 on {dev}")
+    ws = torch.empty(max(zero_list_norms_workspace_bytes(plan), 8), dtype=torch.uint8, device=dev)
+    sums, joined = (torch.zeros(n, dtype=torch.float64, device=dev) for _ in range(2))
+    norms = torch.zeros(n + g + 1, dtype=torch.float32, device=dev)
+    results = torch.zeros((g + 1) * NORM_RESULT_BYTES, dtype=torch.uint8, device=dev)
+    addresses = (ws.data_ptr(), ws.numel(), sums.data_ptr(), joined.data_ptr(), max_norms.data_ptr(), norms.data_ptr(),
+                 results.data_ptr())
+    return NormBuffers(ws, sums, joined, max_norms, norms, results, addresses)
 
 
-def zero_list_sums(gl: GradList, scale: float, ws: torch.Tensor, sums: torch.Tensor, stream=None,
+def _on_device(buffers: NormBuffers, gl: GradList) -> tuple:
+    """The buffers' addresses, which must be device memory and of this list's plan."""
+    if not buffers.ws.is_cuda:
+        raise ValueError("the buffers must be CUDA tensors")
+    if buffers.sums.numel() != len(gl.plan.numels) or buffers.max_norms.numel() != gl.plan.n_groups:
+        raise ValueError("the buffers belong to another plan")
+    return buffers.addresses
+
+
+def zero_list_sums(gl: GradList, scale: float, buffers: NormBuffers, stream=None,
                    d_scale: Optional[torch.Tensor] = None) -> None:
-    """Each tensor's sum of |scale x|^p (the largest for p = inf) into sums (float64)."""
-    _check(lib().zero_list_sums(ctypes.byref(gl.head), scale, _dscale(d_scale), _dev(ws, "ws"), _ws_bytes(ws),
-                                _f64(sums, "sums", len(gl.plan.numels)), _stream(stream)))
+    """Each tensor's sum of |scale x|^p (the largest for p = inf) into buffers.sums."""
+    ws, nb, sums, *_ = _on_device(buffers, gl)
+    _check(lib().zero_list_sums(gl.ref, scale, _dscale(d_scale), ws, nb, sums, _stream(stream)))
 
 
-def zero_sums_norms(gl: GradList, sums: torch.Tensor, n_parts: int, max_norms: torch.Tensor, norms: torch.Tensor,
-                    results: torch.Tensor, found_nonfinite: Optional[torch.Tensor] = None, stream=None) -> None:
+def zero_sums_norms(gl: GradList, sums: torch.Tensor, n_parts: int, buffers: NormBuffers,
+                    found_nonfinite: Optional[torch.Tensor] = None, stream=None) -> None:
     """The norms of tensors, groups and all from n_parts rows of sums, joined in row order."""
-    _check(lib().zero_sums_norms(ctypes.byref(gl.head), _f64(sums, "sums", max(n_parts, 0) * len(gl.plan.numels)),
-                                 n_parts, *_norm_outputs(gl, max_norms, norms, results, found_nonfinite),
+    _, _, _, joined, limits, norms, results = _on_device(buffers, gl)
+    if sums.numel() < n_parts * len(gl.plan.numels):
+        raise ValueError(f"sums has fewer than {n_parts} rows")
+    _check(lib().zero_sums_norms(gl.ref, _dev(sums, "sums", torch.float64), n_parts, joined, limits, norms, results,
+                                 _dev(found_nonfinite, "found_nonfinite", torch.int32, allow_none=True),
                                  _stream(stream)))
 
 
-def zero_list_clip(gl: GradList, scale: float, results: torch.Tensor, stream=None,
+def zero_list_clip(gl: GradList, scale: float, buffers: NormBuffers, stream=None,
                    d_scale: Optional[torch.Tensor] = None) -> None:
-    """Every tensor with a destination scaled and clipped by its group's coefficient in results."""
-    if results.numel() * results.element_size() < (gl.plan.n_groups + 1) * NORM_RESULT_BYTES:
-        raise ValueError("results is smaller than one zero_norm_result per group and one more")
-    _check(lib().zero_list_clip(ctypes.byref(gl.head), scale, _dscale(d_scale), _dev(results, "results"),
-                                _stream(stream)))
+    """Every tensor with a destination scaled and clipped by its group's coefficient in buffers.results."""
+    _check(lib().zero_list_clip(gl.ref, scale, _dscale(d_scale), _on_device(buffers, gl)[6], _stream(stream)))
 
 
-def zero_list_norms(gl: GradList, scale: float, clip: bool, ws: torch.Tensor, sums: torch.Tensor,
-                    max_norms: torch.Tensor, norms: torch.Tensor, results: torch.Tensor,
+def zero_list_norms(gl: GradList, scale: float, clip: bool, buffers: NormBuffers,
                     found_nonfinite: Optional[torch.Tensor] = None, stream=None,
                     d_scale: Optional[torch.Tensor] = None) -> None:
-    """zero_list_sums, zero_sums_norms and, with clip, zero_list_clip in one call."""
-    _check(lib().zero_list_norms(ctypes.byref(gl.head), scale, _dscale(d_scale), int(bool(clip)), _dev(ws, "ws"),
-                                 _ws_bytes(ws), _f64(sums, "sums", len(gl.plan.numels)),
-                                 *_norm_outputs(gl, max_norms, norms, results, found_nonfinite), _stream(stream)))
+    """zero_list_sums, zero_sums_norms of one part and, with clip, zero_list_clip in one call."""
+    ws, nb, sums, _, limits, norms, results = _on_device(buffers, gl)
+    _check(lib().zero_list_norms(gl.ref, scale, _dscale(d_scale), clip, ws, nb, sums, limits, norms, results,
+                                 _dev(found_nonfinite, "found_nonfinite", torch.int32, allow_none=True),
+                                 _stream(stream)))
 
 
 # ------------------------------------------------------------ debug builds

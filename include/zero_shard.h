@@ -739,25 +739,29 @@ typedef struct zero_grad_list {
   const int32_t* d_plan;            /* zero_grad_plan's ints */
   int32_t n_tensors;
   int32_t n_groups;
-  int32_t n_chunks; /* as zero_grad_plan gave them */
+  int32_t n_wide;   /* this and the next two as zero_grad_plan gave them */
+  int32_t n_narrow;
   int32_t chunk;
   int32_t norm_type; /* ZERO_NORM_... */
-  int32_t reserved;  /* 0 */
+  int32_t in_place;  /* 1: no entry has a dst other than its src (and zero_list_clip may leave early), else 0 */
 } zero_grad_list;
 
 /* zero_grad_plan -- host only.
- * The work split of a grads list: chunks of *chunk elements (by the total
- * size: 4096, 16384 or 65536), none across two tensors, numbered in list
- * order, and the tensors of each group.  plan: 2 * n_tensors + n_groups + 2
- * ints: the first chunk of each tensor and their count, then where each
- * group's members start, then the members (tensor numbers, in list order in
- * each group).  groups: NULL puts every tensor in group 0.  A group may be
- * empty: its norm is 0.  The plan depends on sizes and groups alone.
- * Errors: ZERO_EINVAL for n_tensors < 1, n_groups < 1, NULL numels or outputs,
- * a numel < 0, a group outside [0, n_groups), n_tensors + n_groups of 2^30 or more, or 2^31
- * chunks or more. */
+ * The work split of a grads list.  Tensors of up to 4096 elements are narrow,
+ * a warp's work each; longer ones are cut into wide chunks (4096, 16384 or
+ * 65536 elements by the list's total), none across two tensors.  plan:
+ * 4 * n_tensors + n_groups + 2 ints: the first wide chunk of each tensor and
+ * their count; where each group's members start and their count; the members
+ * (tensor numbers, in list order in each group); each tensor's number among
+ * the narrow ones or -1; the narrow tensors.  groups: NULL puts every tensor
+ * in group 0.  A group may be empty: its norm is 0.  Fills n_tensors,
+ * n_groups, n_wide, n_narrow and chunk of *list and clears the rest.  The
+ * plan depends on sizes and groups alone.
+ * Errors: ZERO_EINVAL for n_tensors or n_groups outside [1, 2^28], NULL
+ * arguments, a numel < 0, a group outside [0, n_groups), or 2^28 chunks or
+ * more (2^44 elements). */
 zero_status zero_grad_plan(const int64_t* numels, const int32_t* groups, int32_t n_tensors, int32_t n_groups,
-                           int32_t* plan, int32_t* n_chunks, int32_t* chunk);
+                           int32_t* plan, zero_grad_list* list);
 
 /* zero_grad_entries_check -- host only.
  * Checks entries (host memory) entry by entry: numel as in the plan's numels,
@@ -771,9 +775,10 @@ zero_status zero_grad_entries_check(const zero_grad_entry* entries, const int64_
                                     int32_t n_groups);
 
 /* zero_list_norms_workspace_bytes -- host only.
- * Device scratch of zero_list_sums and zero_list_norms: 8 bytes per chunk.
- * Overwritten by each call; calls that overlap on the GPU need one each. */
-size_t zero_list_norms_workspace_bytes(int32_t n_chunks);
+ * Device scratch of zero_list_sums and zero_list_norms: 8 bytes per wide chunk
+ * and narrow tensor.  Overwritten by each call; calls that overlap on the GPU
+ * need one each. */
+size_t zero_list_norms_workspace_bytes(const zero_grad_list* list);
 
 /* zero_list_sums -- device.
  * d_sums[i] = S_i for every tensor (binary64).  d_scale: NULL, or a device
@@ -788,6 +793,7 @@ zero_status zero_list_sums(const zero_grad_list* list, float scale, const float*
  * r's S_i, added (or compared) in rank order, so that every rank gets the
  * same norms.  Only the list's plan and counts are used (d_entries may be
  * NULL).
+ * d_joined: binary64, the n_tensors joined sums (not d_sums).
  * d_norms: binary32, the n_tensors tensor norms, the n_groups group norms and
  *   the norm over all.
  * d_max_norms: binary64, the limit M_g >= 0 of each group (infinity: not
@@ -799,7 +805,7 @@ zero_status zero_list_sums(const zero_grad_list* list, float scale, const float*
  * d_found_nonfinite: NULL, or a device int32 set to 1 when the norm over all
  *   is not finite (never cleared by the call).
  * Errors: ZERO_EINVAL for a bad list, n_parts < 1, NULL or misaligned buffers. */
-zero_status zero_sums_norms(const zero_grad_list* list, const double* d_sums, int32_t n_parts,
+zero_status zero_sums_norms(const zero_grad_list* list, const double* d_sums, int32_t n_parts, double* d_joined,
                             const double* d_max_norms, float* d_norms, zero_norm_result* d_results,
                             int32_t* d_found_nonfinite, void* stream);
 

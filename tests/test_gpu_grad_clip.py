@@ -1,8 +1,8 @@
 """The norms of many tensors and their clipping against the formulas in 64 bits.
 
-Tolerances.  Sums: a thread adds at most 128 pairs to a lane whose tail l stays below 128 x 2^-24 of the sum, each
-addition to it rounded by 2^-24: 128^2 / 2 x 2^-48 = 2.9e-11 at worst, the rest of the tree a few 2^-48 more: SUM = 4e-11
-(half of that for a root).  Binary32 outputs add 2^-24.  A clipped grad: the coefficient, scale x coefficient and the
+Tolerances.  Sums: a thread adds at most 65536 / 256 / 2 = 128 pairs, the j-th with a tail l of at most j x 2^-24 of the
+sum, whose addition is rounded by 2^-24 of it: 128^2 / 2 x 2^-48 = 2.9e-11 at worst, the rest of the tree a few 2^-48
+more: SUM = 4e-11 (half of that for a root).  Binary32 outputs add 2^-24.  A clipped grad: the coefficient, scale x coefficient and the
 product are each rounded to binary32, 3 x 2^-24 (and their cross terms), then eps / 2 of a 16-bit type; where the value is
 subnormal there, half its type's least step."""
 import math
@@ -117,7 +117,7 @@ def test_norms_of_tensors_groups_and_all(dtype, offset, p):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("total", [(1 << 23) + 77, (1 << 28) + 4099])  # the two larger chunk sizes
+@pytest.mark.parametrize("total", [(1 << 23) + 77, (1 << 27) + 4099])  # the two larger chunk sizes
 def test_norms_of_long_tensors(dtype, total):
     sizes = [total - 1003, 0, 1000, 3]
     base = torch.empty(total + 1, dtype=dtype, device="cuda")
@@ -145,7 +145,7 @@ def test_norms_do_not_depend_on_the_run():
     c.launch_norms(xs)
     for _ in range(3):
         d.launch_norms(xs)
-        assert torch.equal(c.results, d.results) and torch.equal(c.norms.view(torch.int32), d.norms.view(torch.int32))
+        assert torch.equal(c.results, d.results) and torch.equal(c.buffers.norms, d.buffers.norms)
         assert torch.equal(c.tensor_sums, d.tensor_sums)
 
 
@@ -315,6 +315,27 @@ def test_the_function_against_torchs():
             assert torch.allclose(a, p.grad, rtol=2e-5, atol=0)
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.5])
+@pytest.mark.parametrize("dtype,to", [(F32, None), (BF16, None), (F16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("total", [(1 << 23) - 9, (1 << 25) + 77, (1 << 27) + 4099])  # the three chunk sizes
+def test_clip_of_long_tensors(total, dtype, to, scale):
+    sizes = [total - 71003, 0, 70000, 1000, 3]
+    g = torch.Generator("cuda").manual_seed(total)
+    base = torch.empty(total + 9, dtype=dtype, device="cuda").normal_(0, 1, generator=g)
+    flat = base[5:5 + total]
+    before = flat.clone()
+    out = flat if to is None else torch.full((total + 9,), 7.0, dtype=to, device="cuda")[5:5 + total]
+    c = pkg.GradClip(sizes, max_norm=0.5 * scale * math.sqrt(total), group_of=[0, 0, 1, 0, 0])
+    c.launch(list(flat.split(sizes)), out=None if to is None else list(out.split(sizes)), scale=scale)
+    coefs = c.finish().coefs
+    assert coefs[0] == pytest.approx(0.5, rel=1e-2) and coefs[1] == 1.0  # total normal values: within 1e-2 by far
+    f = torch.full((total,), float(np.float32(scale) * coefs[0]), device="cuda")
+    f[sizes[0]:sizes[0] + 70000] = float(np.float32(scale) * coefs[1])
+    assert torch.equal(out, (before.float() * f).to(out.dtype))
+    if to is not None:
+        assert torch.equal(flat, before) and bool((out._base[:5] == 7).all()) and bool((out._base[5 + total:] == 7).all())
+
+
 def test_an_element_beyond_32_bits():
     n = (1 << 31) + 70001
     x = torch.zeros(n + 3, dtype=BF16, device="cuda")[3:]
@@ -329,15 +350,59 @@ def test_an_element_beyond_32_bits():
 
 
 def test_more_chunks_than_a_warp_adds():
-    # one tensor of 3001 chunks beside small ones: its partials are added by a whole block
-    sizes = [5, 3001 * 16384 + 9 - 16384, 70000, 0, 1]
+    # tensors of 4101 chunks beside small ones: their partials are added by whole blocks
+    sizes = [5, 4100 * 65536 + 9, 70000, 0, 1, 4101 * 65536]
     xs = [torch.full((n,), 0.5, dtype=BF16, device="cuda") for n in sizes]
-    c = pkg.GradClip(sizes, max_norm=[1.0, 2.0], group_of=[0, 1, 0, 0, 1])
-    assert c.plan.n_chunks > 2048 + 3
+    c = pkg.GradClip(sizes, max_norm=[1.0, 2.0], group_of=[0, 1, 0, 0, 1, 0])
+    assert (c.plan.head.n_wide, c.plan.head.n_narrow) == (4101 + 2 + 4101, 2)
     r = c.clip_(xs)
     assert c.tensor_sums.tolist() == [n / 4 for n in sizes]
-    for x, g in zip(xs, (0, 1, 0, 0, 1)):
+    for x, g in zip(xs, (0, 1, 0, 0, 1, 0)):
         assert bool((x == (torch.tensor(0.5) * r.coefs[g]).to(BF16).item()).all())
+
+
+@pytest.mark.parametrize("n,groups", [(1023, 256), (1025, 257), (5200, 300), (9000, 1), (9000, 2), (20000, 20000)])
+def test_thousands_of_tensors(n, groups):
+    """The counts at which the work is split another way; two long tensors among them where the list is long."""
+    rng = np.random.default_rng(n)
+    sizes = [int(k) for k in rng.integers(0, 60, n)]
+    if 1024 < n < 9000:
+        sizes[700], sizes[33] = 600 * 65536 + 5, 1100 * 65536 + 1  # more partials than 8 lanes add, than a warp adds
+    total = sum(sizes)
+    flat = torch.randint(-8, 9, (total,), generator=torch.Generator("cuda").manual_seed(n), device="cuda", dtype=torch.int32).to(BF16)
+    xs = list(flat.split(sizes))
+    of = rng.integers(0, groups, n)
+    of[0] = groups - 1
+    limits = list(rng.uniform(1.0, 100.0, groups))
+    # sums of squares of small whole numbers are exact
+    ends = np.cumsum(sizes)
+    run = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), flat.int().square().cumsum(0)]).cpu().numpy()
+    s = (run[ends] - run[ends - sizes]).astype(np.float64)
+    c = pkg.GradClip(sizes, max_norm=limits, group_of=of)
+    before = flat.clone()
+    r = c.clip_(xs)
+    sums = np.zeros(groups)
+    np.add.at(sums, of, s)
+    assert np.array_equal(c.tensor_sums.cpu().numpy(), s)
+    near(c.tensor_norms.cpu(), np.sqrt(s), 1.01 * ULP)
+    near(r.group_norms, np.sqrt(sums), 2.0 ** -52)
+    assert r.norm == pytest.approx(math.sqrt(s.sum()), rel=2.0 ** -52)
+    coefs = np.minimum(1.0, np.array(limits) / (np.sqrt(sums) + 1e-6))
+    near(r.coefs, coefs, 1.01 * ULP)
+    f = torch.repeat_interleave(torch.tensor(coefs[of].astype(np.float32)).cuda(), torch.tensor(sizes).cuda())
+    assert torch.equal(flat, (before.float() * f).to(BF16))
+    # and as shards, joined by threads over all SMs
+    shards = [zs.zero_shard_range(total, 3, k) for k in range(3)]
+    flat.copy_(before)
+    clips = [pkg.GradClip.of_shard(sizes, flat[a:b], a, max_norm=limits, group_of=of) for a, b in shards]
+    for k in clips:
+        k.launch_sums()
+    gathered = torch.stack([k.tensor_sums for k in clips])
+    for k in clips:
+        k.launch(gathered_sums=gathered)
+        assert np.array_equal(k.joined_sums.cpu().numpy(), s)
+        assert torch.equal(k.results, c.results) and torch.equal(k.buffers.norms, c.buffers.norms)
+    assert torch.equal(flat, (before.float() * f).to(BF16))
 
 
 # ------------------------------------------------- scales, graphs, streams
@@ -427,10 +492,11 @@ def test_refuses_at_launch():
         c.launch([x[:4], x[4:]], gathered_sums=torch.zeros(3, dtype=torch.float64, device="cuda"))
     with pytest.raises(ValueError, match="float64"):
         c.launch([x[:4], x[4:]], gathered_sums=torch.zeros(2, device="cuda"))
-    with pytest.raises(ValueError, match="needed"):
-        zs.zero_list_sums(zs.grad_list(c.plan, [x[:4], x[4:]]), 1.0, c.ws, c.tensor_sums[:1])
-    with pytest.raises(ValueError, match="results"):
-        zs.zero_list_clip(zs.grad_list(c.plan, [x[:4], x[4:]]), 1.0, c.results[:24])
+    other = pkg.GradClip([9])
+    for call in (lambda: zs.zero_list_norms(zs.grad_list(c.plan, [x[:4], x[4:]]), 1.0, False, other.buffers),
+                 lambda: zs.zero_list_clip(other._entries([x], None, True)[0], 1.0, c.buffers)):
+        with pytest.raises(ValueError, match="another plan"):
+            call()
 
 
 # ---------------------------------------------------------------- shards
@@ -457,7 +523,7 @@ def test_shards_join_to_the_whole(p, world):
         near(res.group_norms, norms, SUM)
         near(c.tensor_norms.cpu(), rooted(s, p), SUM + ULP)
         assert res.norm == pytest.approx(rooted(joined(s, p), p), rel=SUM)
-        assert torch.equal(c.results, clips[0].results) and torch.equal(c.norms, clips[0].norms)
+        assert torch.equal(c.results, clips[0].results) and torch.equal(c.buffers.norms, clips[0].buffers.norms)
     got = torch.cat(shards).cpu().split(SIZES)
     for i, (y, x) in enumerate(zip(got, xs)):
         check_clipped(y, x, 0.5 * coefs[of[i]], F32)

@@ -13,37 +13,47 @@ from fsdp_sharded_mixed_flatparameter_gb300 import zero_shard as zs
 def parts(plan):
     n, g = len(plan.numels), plan.n_groups
     a = plan.ints.numpy()
-    return a[:n + 1], a[n + 1:n + g + 2], a[n + g + 2:]
+    assert len(a) == 4 * n + g + 2
+    return a[:n + 1], a[n + 1:n + g + 2], a[n + g + 2:2 * n + g + 2], a[2 * n + g + 2:3 * n + g + 2], a[3 * n + g + 2:]
 
 
 @pytest.mark.parametrize("sizes,chunk", [([1], 4096), ([0], 4096), ([4096, 4097, 0, 4095, 0, 0, 1], 4096), ([1 << 23], 4096),
-                                         ([(1 << 23) + 1], 16384), ([1 << 28], 16384), ([1, 1 << 28, 5], 65536),
-                                         ([1 << 40, 3], 65536)])
-def test_plan_cuts_each_tensor_into_chunks(sizes, chunk):
+                                         ([(1 << 23) + 1], 16384), ([1 << 27], 16384), ([1, 1 << 27, 5], 65536),
+                                         ([4095, 1 << 40, 3], 65536)])
+def test_plan_cuts_long_tensors_into_chunks(sizes, chunk):
     p = zs.zero_grad_plan(sizes, None, 1, 2, "cpu")
-    first, group_first, members = parts(p)
-    assert p.chunk == chunk
-    assert first.tolist() == np.concatenate([[0], np.cumsum([-(-n // chunk) for n in sizes])]).tolist()
-    assert p.n_chunks == first[-1] and members.tolist() == list(range(len(sizes))) and group_first.tolist() == [0, len(sizes)]
+    first, group_first, members, narrow_of, narrow = parts(p)
+    assert p.head.chunk == chunk
+    assert first.tolist() == np.concatenate([[0], np.cumsum([-(-n // chunk) if n > 4096 else 0 for n in sizes])]).tolist()
+    small = [i for i, n in enumerate(sizes) if 0 < n <= 4096]
+    assert narrow[:len(small)].tolist() == small and p.head.n_narrow == len(small) and p.head.n_wide == first[-1]
+    assert narrow_of.tolist() == [small.index(i) if i in small else -1 for i in range(len(sizes))]
+    assert members.tolist() == list(range(len(sizes))) and group_first.tolist() == [0, len(sizes)]
+    assert zs.zero_list_norms_workspace_bytes(p) == 8 * (p.head.n_wide + len(small))
+    assert (p.head.n_tensors, p.head.n_groups, p.head.in_place, p.head.d_entries) == (len(sizes), 1, 0, None)
 
 
 def test_plan_sorts_groups_and_keeps_list_order():
     of = [2, 0, 2, 4, 0, 0, 2]
-    first, group_first, members = parts(zs.zero_grad_plan([3] * 7, of, 6, math.inf, "cpu"))
+    _, group_first, members, _, _ = parts(zs.zero_grad_plan([3] * 7, of, 6, math.inf, "cpu"))
     got = [members[group_first[g]:group_first[g + 1]].tolist() for g in range(6)]
     assert got == [[i for i, k in enumerate(of) if k == g] for g in range(6)]
 
 
 @pytest.mark.parametrize("args", [([], None, 1), ([1], None, 0), ([-1], None, 1), ([1, 1], [0, 2], 2), ([1, 1], [0, -1], 2),
-                                  ([1 << 62, 1 << 62], None, 1), ([1 << 50], None, 1), ([1], None, 1 << 30)])
+                                  ([1 << 62, 1 << 62], None, 1), ([1 << 50], None, 1)])
 def test_plan_refuses(args):
-    if args[2] == 1 << 30:  # only the count is looked at
-        c, k = ctypes.c_int32(), ctypes.c_int32()
-        a = np.zeros(8, np.int64)
-        assert zs.lib().zero_grad_plan(a.ctypes.data, None, 1, args[2], a.ctypes.data, ctypes.byref(c), ctypes.byref(k)) == zs.ZERO_EINVAL
-        return
     with pytest.raises(zs.ZeroError):
         zs.zero_grad_plan(*args, 2, "cpu")
+
+
+def test_plan_refuses_counts_and_nothing():
+    a, h = np.zeros(16, np.int64), zs.zero_grad_list()
+    call = zs.lib().zero_grad_plan
+    ok = (a.ctypes.data, None, 1, 1, a.ctypes.data, ctypes.byref(h))
+    for i, bad in ((0, None), (2, (1 << 28) + 1), (3, (1 << 28) + 1), (4, None), (5, None)):
+        assert call(*ok[:i], bad, *ok[i + 1:]) == zs.ZERO_EINVAL
+    assert zs.lib().zero_list_norms_workspace_bytes(None) == 0
 
 
 def test_plan_refuses_by_name():
@@ -143,18 +153,19 @@ def test_c_entries_refuse_before_any_launch():
     a = (buf + 63) & ~63
 
     def head(**kw):
-        f = dict(d_entries=a, d_plan=a, n_tensors=2, n_groups=1, n_chunks=3, chunk=4096, norm_type=2, reserved=0)
+        f = dict(d_entries=a, d_plan=a, n_tensors=2, n_groups=1, n_wide=1, n_narrow=2, chunk=4096, norm_type=2, in_place=0)
         f.update(kw)
         return ctypes.byref(zs.zero_grad_list(**f))
 
-    heads = [dict(d_plan=None), dict(d_plan=a + 2), dict(n_tensors=0), dict(n_groups=0), dict(n_chunks=-1), dict(chunk=0),
-             dict(chunk=65537), dict(norm_type=3), dict(norm_type=-1), dict(reserved=1)]
+    heads = [dict(d_plan=None), dict(d_plan=a + 2), dict(n_tensors=0), dict(n_groups=0), dict(n_wide=-1), dict(n_narrow=-1), dict(n_narrow=3),
+             dict(n_wide=1 << 28), dict(chunk=0), dict(chunk=5000),
+             dict(chunk=65537), dict(norm_type=3), dict(norm_type=-1), dict(in_place=2)]
     for kw in heads + [dict(d_entries=None), dict(d_entries=a + 4)]:
         assert L.zero_list_sums(head(**kw), 1.0, None, a, 24, a, None) == zs.ZERO_EINVAL, kw
         assert L.zero_list_clip(head(**kw), 1.0, None, a, None) == zs.ZERO_EINVAL, kw
         assert L.zero_list_norms(head(**kw), 1.0, None, 1, a, 24, a, a, a, a, a, None) == zs.ZERO_EINVAL, kw
     for kw in heads:
-        assert L.zero_sums_norms(head(**kw), a, 1, a, a, a, None, None) == zs.ZERO_EINVAL, kw
+        assert L.zero_sums_norms(head(**kw), a, 1, a, a, a, a, None, None) == zs.ZERO_EINVAL, kw
     h = head()
     assert L.zero_list_sums(None, 1.0, None, a, 24, a, None) == zs.ZERO_EINVAL
     for bad in ((math.nan, None, a, 24, a), (math.inf, None, a, 24, a), (1.0, a + 1, a, 24, a), (1.0, None, None, 24, a), (1.0, None, a, 23, a),
@@ -162,15 +173,12 @@ def test_c_entries_refuse_before_any_launch():
         assert L.zero_list_sums(h, *bad, None) == zs.ZERO_EINVAL, bad
         sc, ds, ws, nb, sums = bad
         assert L.zero_list_norms(h, sc, ds, 0, ws, nb, sums, a, a, a, None, None) == zs.ZERO_EINVAL, bad
-    for bad in ((None, 1, a, a, a, None), (a + 4, 1, a, a, a, None), (a, 0, a, a, a, None), (a, 1, None, a, a, None), (a, 1, a + 4, a, a, None),
-                (a, 1, a, None, a, None), (a, 1, a, a + 2, a, None), (a, 1, a, a, None, None), (a, 1, a, a, a + 4, None), (a, 1, a, a, a, a + 2)):
+    ok = (a, 1, a, a, a, a, None)
+    for i, v in ((0, None), (0, a + 4), (1, 0), (2, None), (2, a + 4), (3, None), (3, a + 4), (4, None), (4, a + 2), (5, None), (5, a + 4), (6, a + 2)):
+        bad = ok[:i] + (v,) + ok[i + 1:]
         assert L.zero_sums_norms(h, *bad, None) == zs.ZERO_EINVAL, bad
     assert L.zero_list_clip(h, 1.0, None, None, None) == zs.ZERO_EINVAL
     assert L.zero_list_clip(h, math.nan, None, a, None) == zs.ZERO_EINVAL
-
-
-def test_workspace_bytes():
-    assert [zs.zero_list_norms_workspace_bytes(k) for k in (-1, 0, 1, 1 << 30)] == [0, 0, 8, 8 << 30]
 
 
 def test_clip_refuses_on_the_host():
@@ -196,6 +204,8 @@ def test_clip_refuses_on_the_host():
     c.register_grads([x[:4], x[:5]], write=False)
     with pytest.raises(ValueError, match="norms only"):
         c.launch()
+    with pytest.raises(ValueError, match="max_norms"):
+        zs.norm_buffers(c.plan, torch.zeros(3, dtype=torch.float64))
     with pytest.raises(ValueError, match="CUDA"):  # host memory never reaches a kernel
         c.launch_norms()
     with pytest.raises(ValueError, match="gathered_sums"):
