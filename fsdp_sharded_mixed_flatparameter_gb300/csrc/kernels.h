@@ -110,10 +110,19 @@ zero_status launch_adamw_list8(const ListArgs& a, const ListScalars& s, cudaStre
 zero_status launch_state8_pack(const float* m, const float* v, int64_t n, const zero_state8& q, cudaStream_t st);
 zero_status launch_state8_unpack(const zero_state8& q, int64_t n, float* m, float* v, cudaStream_t st);
 
-// Elements of a grads list's chunks, by the list's total.
+// Elements of a grads list's wide chunks, by the list's total.  Long chunks
+// for long lists (a chunk's search and sum take as long as 20 KB of loads),
+// short ones where few chunks would leave SMs without work at the end.  Sums of 48 equal bf16
+// tensors, us, with chunks of 8192 / 16384 / 32768 / 65536: 2^24 elements
+// 16.3 / 20.3 / 19.3 / 20.3; 2^26: 36.3 / 32.2 / 31.4 / 34.4; 2^28: 116 / 96 /
+// 88 / 89; 2^30: 456 / 376 / 317 / 309; 2^30 in fp32: 676 / 661 / 629 / 616.
 constexpr int kMaxGradChunk = 65536, kMaxGradPieces = (1 << 28) - 1;
 inline int grad_chunk_size(int64_t total) {
-  return total <= (int64_t(1) << 23) ? 4096 : total <= (int64_t(1) << 27) ? 16384 : kMaxGradChunk;
+  return total <= (int64_t(1) << 21)   ? 4096
+         : total <= (int64_t(1) << 24) ? 8192
+         : total <= (int64_t(1) << 26) ? 16384
+         : total <= (int64_t(1) << 28) ? 32768
+                                       : kMaxGradChunk;
 }
 // Elements up to which a tensor is narrow: a warp's work.
 constexpr int kNarrow = 4096;

@@ -159,6 +159,14 @@ __global__ void __launch_bounds__(kClipThreads, kClipBlocks)
                      const __grid_constant__ GradPlan plan, int wide_blocks, int parts_log2, float scale,
                      const float* __restrict__ dscale, const zero_norm_result* results) {
   const int block = gridDim.x - 1 - blockIdx.x;
+  GradPiece c;
+  if (!MAY_LEAVE && block < wide_blocks) {
+    // of the plan: while the kernel before still runs
+    c = wide_piece(entries, n, plan, block >> parts_log2);
+    const int piece = plan.chunk >> parts_log2, skip = (block & ((1 << parts_log2) - 1)) * piece;
+    c.k += skip;
+    c.len = min(c.len - skip, piece);
+  }
   wait_before();
   if (!results[n_groups].finite) return;
   if (MAY_LEAVE && n_groups <= 32) {
@@ -168,20 +176,16 @@ __global__ void __launch_bounds__(kClipThreads, kClipBlocks)
   }
   if (dscale != nullptr) scale = *dscale;
   if (block >= wide_blocks) {
-    const GradPiece c = narrow_piece<kClipThreads>(entries, plan, block - wide_blocks + plan.n_wide);
+    c = narrow_piece<kClipThreads>(entries, plan, block - wide_blocks + plan.n_wide);
     if (c.len > 0) clip_tensor<32>(entries[c.tensor], c, n_groups, scale, results);
   } else if (MAY_LEAVE) {
     for (int chunk = min((block + 1) * kClipChunks, plan.n_wide) - 1; chunk >= block * kClipChunks; --chunk) {
-      const GradPiece c = wide_piece(entries, n, plan, chunk);
+      c = wide_piece(entries, n, plan, chunk);
       clip_tensor<kClipThreads>(entries[c.tensor], c, n_groups, scale, results);
       __syncthreads();  // wide_piece's shared memory
     }
-  } else {
-    GradPiece c = wide_piece(entries, n, plan, block >> parts_log2);
-    const int piece = plan.chunk >> parts_log2, skip = (block & ((1 << parts_log2) - 1)) * piece;
-    c.k += skip;
-    c.len = min(c.len - skip, piece);
-    if (c.len > 0) clip_tensor<kClipThreads>(entries[c.tensor], c, n_groups, scale, results);
+  } else if (c.len > 0) {
+    clip_tensor<kClipThreads>(entries[c.tensor], c, n_groups, scale, results);
   }
 }
 

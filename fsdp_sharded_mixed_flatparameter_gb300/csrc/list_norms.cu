@@ -246,10 +246,12 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocks)
   const int block = blockIdx.x;
   let_next_start();
   if (block < plan.n_wide) {
-    const GradPiece c = wide_piece(entries, n, plan, block);
+    const GradPiece c = wide_piece(entries, n, plan, block);  // of the plan, not of what runs before
+    wait_before();
     piece_partial<P, kSumThreads>(entries[c.tensor], c, partials, red);
   } else {
     const GradPiece c = narrow_piece<kSumThreads>(entries, plan, block);
+    wait_before();
     if (c.len > 0) piece_partial<P, 32>(entries[c.tensor], c, partials, red);
   }
 }
@@ -321,7 +323,7 @@ constexpr int kFinishGroups = 256;
 // Partials of a tensor up to which a thread adds them, and a warp; above, a block.
 constexpr int kThreadPartials = 16, kWarpPartials = 1024;
 // Up to these one block finishes.
-constexpr int kBlockTensors = 128, kBlockPartials = 2048;
+constexpr int kBlockTensors = 128, kBlockPartials = 2048, kBlockParts = 256;
 // Tensors above which tensors_kernel makes their sums, and the partials up to
 // which 8 of its lanes add a tensor's; above, a block.
 constexpr int kFinishTensors = 1024, kOctetPartials = 512;
@@ -349,35 +351,57 @@ __device__ __forceinline__ double join_parts(const FinishArgs& a, int i) {
   return strided<P>(0, a.n_parts, 1, [&](int r) { return __ldcg(row + static_cast<int64_t>(r) * a.n); });
 }
 
-// A tensor's norm in binary32, at most 2^-24 (1 + 2^-22) off: the binary32 root and
-// one Newton step whose residual is a binary64 fma (__dsqrt_rn takes some 25
-// binary64 instructions; 20,000 tensors' would be most of this kernel).
+// Roots and quotients from binary32 ones and binary64 residuals: __dsqrt_rn and
+// __ddiv_rn take some 25 dependent binary64 instructions each, half a
+// microsecond where one thread works, and most of the time for thousands.
+//
+// The root of s: y + rest / 2y twice; after the first step the error is
+// (2^-24)^2 / 2 of it, after the second what the last addition rounds.
+__device__ __forceinline__ bool in_float_range(float f) { return f > 0x1p-100f && f < 0x1p100f; }
+__device__ __forceinline__ double root(double s) {
+  const float f = __double2float_rn(s);
+  if (!in_float_range(f)) return __dsqrt_rn(s);
+  const float y0 = __fsqrt_rn(f);
+  const double half = static_cast<double>(__fdiv_rn(0.5f, y0));
+  double y = static_cast<double>(y0);
+  y = fma(fma(-y, y, s), half, y);
+  return fma(fma(-y, y, s), half, y);
+}
+// A tensor's norm in binary32, at most 2^-24 (1 + 2^-22) off.
 template <int P>
 __device__ __forceinline__ float tensor_norm(double s) {
-  if (P != ZERO_NORM_2) return __double2float_rn(s);
   const float f = __double2float_rn(s);
-  if (!(f > 0x1p-100f && f < 0x1p100f)) return __double2float_rn(__dsqrt_rn(s));
+  if (P != ZERO_NORM_2) return f;
+  if (!in_float_range(f)) return __double2float_rn(__dsqrt_rn(s));
   const float y = __fsqrt_rn(f);
   const float rest = __double2float_rn(fma(-static_cast<double>(y), static_cast<double>(y), s));
   return __fadd_rn(y, __fdiv_rn(rest, 2.0f * y));
 }
+// min(1, limit / d) in binary32, at most 2^-24 (1 + 2^-22) off.
+__device__ __forceinline__ float clip_coefficient(double limit, double d) {
+  if (!(limit < d)) return 1.0f;  // a NaN too
+  const float fd = __double2float_rn(d), fl = __double2float_rn(limit);
+  if (!in_float_range(fd) || !in_float_range(fl)) return __double2float_rn(__ddiv_rn(limit, d));
+  const float q = __fdiv_rn(fl, fd);
+  const float rest = __double2float_rn(fma(-static_cast<double>(q), d, limit));
+  return fminf(1.0f, __fadd_rn(q, __fdiv_rn(rest, fd)));
+}
 
 template <int P>
-__device__ __forceinline__ void write_result(const FinishArgs& a, int g, double sum) {
-  const double norm = P == ZERO_NORM_2 ? __dsqrt_rn(sum) : sum;
+__device__ __forceinline__ void write_result(const FinishArgs& a, int g, double sum, double limit) {
+  const double norm = P == ZERO_NORM_2 ? root(sum) : sum;
   zero_norm_result r;
   r.sqnorm = sum;
   r.norm = norm;
-  r.clip_coef = 1.0f;
+  r.clip_coef = g < a.n_groups ? clip_coefficient(limit, __dadd_rn(norm, 1e-6)) : 1.0f;
   r.finite = isfinite(norm) ? 1 : 0;
-  if (g < a.n_groups) {
-    const double q = __ddiv_rn(__ldg(a.max_norms + g), __dadd_rn(norm, 1e-6));
-    if (q < 1.0) r.clip_coef = __double2float_rn(q);
-  } else if (a.found != nullptr && !r.finite) {
-    *a.found = 1;
-  }
+  if (g == a.n_groups && a.found != nullptr && !r.finite) *a.found = 1;
   a.results[g] = r;
   a.norms[a.n + g] = __double2float_rn(norm);
+}
+template <int P>
+__device__ __forceinline__ void write_group(const FinishArgs& a, int g, double sum) {
+  write_result<P>(a, g, sum, __ldg(a.max_norms + g));
 }
 
 // The sums and norms of many tensors over all SMs (the binary64 pipes of
@@ -423,7 +447,8 @@ __global__ void __launch_bounds__(256) tensors_kernel(const __grid_constant__ Fi
 
 // One cluster of 8 blocks, or one block.  Of its W warps tensor i belongs to
 // warp i % W, lane i / W: long tensors, whose partials a warp or a block adds,
-// spread over the warps.  Every thread adds its tensors to the sum over all;
+// spread over the warps.  (kParts: as few warps as hold the tensors, since a
+// warp's binary64 addition takes 16 cycles for one lane too.)  Every thread adds its tensors to the sum over all;
 // the blocks' sums meet in distributed shared memory.  Then the groups.
 template <int P, Have HAVE>
 __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ FinishArgs a) {
@@ -435,7 +460,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) * blocks + rank;
   let_next_start();
   // what the plan says of this thread's tensor and group, while the kernel before still runs
-  const int i = lane * warps + warp;
+  const int i = HAVE == kParts ? threadIdx.x * blocks + rank : lane * warps + warp;
   int lo = 0, count = 0, group_lo = 0, group_count = 0, first_member = 0;
   if (HAVE == kPartials && i < a.n) partials_of(a.plan, i, lo, count);
   if (warp < a.n_groups) {
@@ -485,18 +510,19 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
     }
   }
   if (a.results == nullptr) return;
-  const int lanes = min((a.n + warps - 1) / warps, 32);
-  all = block_join<P>(all, lanes, red);
-  if (threadIdx.x == 0) block_total = all;
-  cluster.sync();  // the blocks' totals, and the tensors' sums
-  if (rank == 0 && threadIdx.x < 32) {
-    double x = 0.0;
-    if (lane < blocks) x = *cluster.map_shared_rank(&block_total, lane);
-    x = warp_join<P>(x, blocks);
-    if (lane == 0) {
-      write_result<P>(a, a.n_groups, x);
-      if (a.n_groups == 1) write_result<P>(a, 0, x);
+  const int lanes = HAVE == kParts ? 32 : min((a.n + warps - 1) / warps, 32);
+  all = block_join<P>(all, lanes, red);  // its barriers order the tensors' sums within the block
+  if (blocks > 1) {
+    if (threadIdx.x == 0) block_total = all;
+    cluster.sync();  // the blocks' totals, and the tensors' sums
+    if (rank == 0 && threadIdx.x < 32) {
+      all = lane < blocks ? *cluster.map_shared_rank(&block_total, lane) : 0.0;
+      all = warp_join<P>(all, blocks);
     }
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    write_result<P>(a, a.n_groups, all, 0.0);
+    if (a.n_groups == 1) write_group<P>(a, 0, all);
   }
   if (a.n_groups > 1 && a.n_groups <= kFinishGroups) {
     const auto sum_of = [&](int lo, int count, int from, int step) {
@@ -510,17 +536,17 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
         if (again) first_member = lane < len ? __ldg(a.plan.members + from + lane) : 0;
         double x = lane < len ? __ldcg(a.sums + first_member) : 0.0;
         x = warp_join<P>(join<P>(x, sum_of(from, len, lane + 32, 32)));
-        if (lane == 0) write_result<P>(a, g, x);
+        if (lane == 0) write_group<P>(a, g, x);
       }
     } else {
       for (int g = rank; g < a.n_groups; g += blocks) {
         const int lo = __ldg(a.plan.group_first + g), count = __ldg(a.plan.group_first + g + 1) - lo;
         const double x = block_join<P>(sum_of(lo, count, threadIdx.x, kFinishThreads), 32, red);
-        if (threadIdx.x == 0) write_result<P>(a, g, x);
+        if (threadIdx.x == 0) write_group<P>(a, g, x);
       }
     }
   }
-  cluster.sync();  // block_total is read until here
+  if (blocks > 1) cluster.sync();  // block_total is read until here
 }
 
 // Many groups, over all SMs: a thread each where they have few tensors, else
@@ -536,9 +562,9 @@ __global__ void __launch_bounds__(128) groups_kernel(const __grid_constant__ Fin
   const auto member = [&](int j) { return __ldcg(a.sums + __ldg(a.plan.members + lo + j)); };
   if (WARPS) {
     const double x = warp_join<P>(strided<P>(lane, count, 32, member));
-    if (lane == 0) write_result<P>(a, g, x);
+    if (lane == 0) write_group<P>(a, g, x);
   } else {
-    write_result<P>(a, g, strided<P>(0, count, 1, member));
+    write_group<P>(a, g, strided<P>(0, count, 1, member));
   }
 }
 
@@ -547,7 +573,7 @@ template <int P, bool PARTS>
 static zero_status launch_finish(const FinishArgs& k, cudaStream_t st) {
   zero_status s = ZERO_OK;
   if (k.n <= kFinishTensors) {
-    const bool few = k.n <= kBlockTensors && (PARTS || k.plan.n_wide + k.plan.n_narrow <= kBlockPartials);
+    const bool few = PARTS ? k.n <= kBlockParts : k.n <= kBlockTensors && k.plan.n_wide + k.plan.n_narrow <= kBlockPartials;
     const int blocks = few ? 1 : kFinishBlocks;
     s = launch_after("finish_kernel", finish_kernel<P, PARTS ? kParts : kPartials>, blocks, kFinishThreads, blocks, st, k);
   } else {
@@ -564,8 +590,8 @@ static zero_status launch_finish(const FinishArgs& k, cudaStream_t st) {
 template <int P>
 static zero_status launch_norms_t(const GradListArgs& a, double* partials, const FinishArgs& k, cudaStream_t st) {
   if (grad_blocks(k.plan, kSumThreads) > 0) {
-    chunk_sums_kernel<P><<<grad_blocks(k.plan, kSumThreads), kSumThreads, 0, st>>>(a.entries, a.n, k.plan, partials);
-    const zero_status s = check_launch("chunk_sums_kernel");
+    const zero_status s = launch_after("chunk_sums_kernel", chunk_sums_kernel<P>, grad_blocks(k.plan, kSumThreads),
+                                       kSumThreads, 1, st, a.entries, a.n, k.plan, partials);
     if (s != ZERO_OK) return s;
   }
   return launch_finish<P, false>(k, st);

@@ -9,7 +9,6 @@ waits for the host, so a whole step can be captured in a graph.
 """
 from __future__ import annotations
 
-import contextlib
 import math
 from typing import NamedTuple, Optional, Sequence, Union
 
@@ -63,7 +62,7 @@ class GradClip(GradTables):
         norms, self.results = self.buffers.norms, self.buffers.results
         self.tensor_norms, self.group_norms, self.norm = norms[:n], norms[n:n + g], norms[n + g]
         self.result = self.results[g * zs.NORM_RESULT_BYTES:]
-        self.found_nonfinite = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.found_nonfinite = self.buffers.found
         self._home = self._current()  # the stream whose order the buffers' memory follows
         self.shard: Optional[torch.Tensor] = None
 
@@ -129,21 +128,17 @@ class GradClip(GradTables):
             raise ValueError("the registered grads are for norms only (write=False)")
         return self._registered
 
-    def _here(self):
-        """Make the clip's device the current one, if it is not."""
-        if self._index is None or torch.cuda.current_device() == self._index:
-            return contextlib.nullcontext()
-        return torch.cuda.device(self._index)
-
     def _on(self, stream, table: GradTable) -> int:
         """The handle of the stream to launch on, its use of the object's memory noted."""
         if self._index is None:
             return 0
         raw = self._handle(stream)
+        if raw == self._home == table.stream and not torch.cuda.is_current_stream_capturing():
+            return raw
         self._read_on(table, raw)
         if raw != self._home and not torch.cuda.is_current_stream_capturing():
             st = torch_stream(raw, self.device)
-            for t in (self.plan.ints, *self.buffers[:6], self.found_nonfinite):
+            for t in (self.plan.ints, *self.buffers[1:8]):
                 t.record_stream(st)
         return raw
 
@@ -151,10 +146,16 @@ class GradClip(GradTables):
     def launch_sums(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, scale: float = 1.0,
                     loss_scale=None, stream=None) -> None:
         """Enqueue each tensor's sum into ``tensor_sums``: what ranks exchange."""
+        if self._elsewhere():
+            with torch.cuda.device(self._index):
+                return self.launch_sums(grads, scale=scale, loss_scale=loss_scale, stream=stream)
         sc, dsc, _ = self._scale_args(scale, loss_scale)
-        with self._here():
-            gl, table, _ = self._list(grads, None, False)
-            zs.zero_list_sums(gl, sc, self.buffers, self._on(stream, table), d_scale=dsc)
+        gl, table, _ = self._list(grads, None, False)
+        zs.zero_list_sums(gl, sc, self.buffers, self._on(stream, table), d_scale=dsc)
+
+    def _elsewhere(self) -> bool:
+        """Whether another device than the clip's is the current one."""
+        return self._index is not None and torch.cuda.current_device() != self._index
 
     def launch_norms(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, scale: float = 1.0,
                      loss_scale=None, gathered_sums: Optional[torch.Tensor] = None, process_group=None,
@@ -176,25 +177,27 @@ class GradClip(GradTables):
         self._launch(True, grads, out, scale, loss_scale, gathered_sums, process_group, stream)
 
     def _launch(self, clip, grads, out, scale, loss_scale, gathered, process_group, stream) -> None:
-        sc, dsc, _ = self._scale_args(scale, loss_scale)
-        flag = self.found_nonfinite if loss_scale is None else loss_scale.found_inf
-        n = len(self.numels)
-        if gathered is not None and (gathered.numel() == 0 or gathered.numel() % n
-                                     or gathered.device != self.plan.ints.device):
-            raise ValueError(f"gathered_sums must be [ranks, {n}] on {self.plan.ints.device}")
-        with self._here():
-            gl, table, _ = self._list(grads, out, clip)
-            raw = self._on(stream, table)
-            if gathered is None and process_group is not None and _world(process_group) > 1:
-                zs.zero_list_sums(gl, sc, self.buffers, raw, d_scale=dsc)
-                with torch.cuda.stream(torch_stream(raw, self.device)):
-                    gathered = gather_sqnorms(self.tensor_sums, process_group)
-            if gathered is None:
-                zs.zero_list_norms(gl, sc, clip, self.buffers, flag, raw, d_scale=dsc)
-                return
-            zs.zero_sums_norms(gl, gathered, gathered.numel() // n, self.buffers, flag, raw)
-            if clip:
-                zs.zero_list_clip(gl, sc, self.buffers, raw, d_scale=dsc)
+        if self._elsewhere():
+            with torch.cuda.device(self._index):
+                return self._launch(clip, grads, out, scale, loss_scale, gathered, process_group, stream)
+        n, dev = len(self.numels), self.plan.ints.device
+        if gathered is not None and (gathered.numel() == 0 or gathered.numel() % n or gathered.device != dev):
+            raise ValueError(f"gathered_sums must be [ranks, {n}] on {dev}")
+        gl, table, _ = self._list(grads, out, clip)
+        raw = self._on(stream, table)
+        sc, dsc, flag = self._scale_args(scale, loss_scale)
+        if loss_scale is None:
+            flag = None  # the buffers' own
+        if gathered is None and process_group is not None and _world(process_group) > 1:
+            zs.zero_list_sums(gl, sc, self.buffers, raw, d_scale=dsc)
+            with torch.cuda.stream(torch_stream(raw, self.device)):
+                gathered = gather_sqnorms(self.tensor_sums, process_group)
+        if gathered is None:
+            zs.zero_list_norms(gl, sc, clip, self.buffers, flag, raw, d_scale=dsc)
+            return
+        zs.zero_sums_norms(gl, gathered, gathered.numel() // n, self.buffers, flag, raw)
+        if clip:
+            zs.zero_list_clip(gl, sc, self.buffers, raw, d_scale=dsc)
 
     def finish(self, stream=None) -> ClipResult:
         """Read the last launch's result (a device-to-host copy on `stream`, where it was enqueued)."""

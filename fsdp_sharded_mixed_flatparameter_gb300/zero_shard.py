@@ -1014,71 +1014,77 @@ def zero_list_norms_workspace_bytes(plan: GradPlan) -> int:
 
 
 class NormBuffers(NamedTuple):
-    """What the calls on a grads list write, checked once (norm_buffers)."""
+    """What the calls on lists of one plan read and write, made by norm_buffers."""
+    plan: GradPlan
     ws: torch.Tensor           # uint8, zero_list_norms_workspace_bytes
     sums: torch.Tensor         # float64, a tensor's sum each
     joined: torch.Tensor       # float64, the same over all ranks (zero_sums_norms)
     max_norms: torch.Tensor    # float64, the groups' limits (read)
     norms: torch.Tensor        # float32: tensors, groups, all
     results: torch.Tensor      # a zero_norm_result per group and one for all
-    addresses: tuple           # ws, its bytes, sums, joined, max_norms, norms, results
+    found: torch.Tensor        # int32, set where the norm over all is not finite
+    addresses: Optional[tuple]  # ws, its bytes, sums, joined, max_norms, norms, results, found; None: host memory
 
 
 def norm_buffers(plan: GradPlan, max_norms: torch.Tensor) -> NormBuffers:
     """Buffers for lists of this plan; max_norms: the groups' limits (float64, on the device)."""
     dev, n, g = plan.ints.device, len(plan.numels), plan.n_groups
-    if max_norms.dtype != torch.float64 or max_norms.numel() != g or max_norms.device != dev:
+    if max_norms.dtype != torch.float64 or max_norms.numel() != g or max_norms.device != dev or not max_norms.is_contiguous():
         raise ValueError(f"max_norms must be {g} float64 on {dev}")
     ws = torch.empty(max(zero_list_norms_workspace_bytes(plan), 8), dtype=torch.uint8, device=dev)
     sums, joined = (torch.zeros(n, dtype=torch.float64, device=dev) for _ in range(2))
     norms = torch.zeros(n + g + 1, dtype=torch.float32, device=dev)
     results = torch.zeros((g + 1) * NORM_RESULT_BYTES, dtype=torch.uint8, device=dev)
+    found = torch.zeros(1, dtype=torch.int32, device=dev)
     addresses = (ws.data_ptr(), ws.numel(), sums.data_ptr(), joined.data_ptr(), max_norms.data_ptr(), norms.data_ptr(),
-                 results.data_ptr())
-    return NormBuffers(ws, sums, joined, max_norms, norms, results, addresses)
+                 results.data_ptr(), found.data_ptr()) if ws.is_cuda else None
+    return NormBuffers(plan, ws, sums, joined, max_norms, norms, results, found, addresses)
 
 
-def _on_device(buffers: NormBuffers, gl: GradList) -> tuple:
+def _addresses(buffers: NormBuffers, gl: GradList, found: Optional[torch.Tensor] = None) -> tuple:
     """The buffers' addresses, which must be device memory and of this list's plan."""
-    if not buffers.ws.is_cuda:
-        raise ValueError("the buffers must be CUDA tensors")
-    if buffers.sums.numel() != len(gl.plan.numels) or buffers.max_norms.numel() != gl.plan.n_groups:
+    if buffers.plan is not gl.plan:
         raise ValueError("the buffers belong to another plan")
-    return buffers.addresses
+    if buffers.addresses is None:
+        raise ValueError("the buffers must be CUDA tensors")
+    if found is None:
+        return buffers.addresses
+    return buffers.addresses[:7] + (_dev(found, "found_nonfinite", torch.int32),)
 
 
 def zero_list_sums(gl: GradList, scale: float, buffers: NormBuffers, stream=None,
                    d_scale: Optional[torch.Tensor] = None) -> None:
     """Each tensor's sum of |scale x|^p (the largest for p = inf) into buffers.sums."""
-    ws, nb, sums, *_ = _on_device(buffers, gl)
-    _check(lib().zero_list_sums(gl.ref, scale, _dscale(d_scale), ws, nb, sums, _stream(stream)))
+    a = _addresses(buffers, gl)
+    _check(lib().zero_list_sums(gl.ref, scale, None if d_scale is None else _dscale(d_scale), a[0], a[1], a[2],
+                                _stream(stream)))
 
 
 def zero_sums_norms(gl: GradList, sums: torch.Tensor, n_parts: int, buffers: NormBuffers,
                     found_nonfinite: Optional[torch.Tensor] = None, stream=None) -> None:
-    """The norms of tensors, groups and all from n_parts rows of sums, joined in row order."""
-    _, _, _, joined, limits, norms, results = _on_device(buffers, gl)
+    """The norms of tensors, groups and all from n_parts rows of sums, joined in row order.
+    found_nonfinite: in place of the buffers' own."""
+    _, _, _, joined, limits, norms, results, found = _addresses(buffers, gl, found_nonfinite)
     if sums.numel() < n_parts * len(gl.plan.numels):
         raise ValueError(f"sums has fewer than {n_parts} rows")
     _check(lib().zero_sums_norms(gl.ref, _dev(sums, "sums", torch.float64), n_parts, joined, limits, norms, results,
-                                 _dev(found_nonfinite, "found_nonfinite", torch.int32, allow_none=True),
-                                 _stream(stream)))
+                                 found, _stream(stream)))
 
 
 def zero_list_clip(gl: GradList, scale: float, buffers: NormBuffers, stream=None,
                    d_scale: Optional[torch.Tensor] = None) -> None:
     """Every tensor with a destination scaled and clipped by its group's coefficient in buffers.results."""
-    _check(lib().zero_list_clip(gl.ref, scale, _dscale(d_scale), _on_device(buffers, gl)[6], _stream(stream)))
+    _check(lib().zero_list_clip(gl.ref, scale, None if d_scale is None else _dscale(d_scale),
+                                _addresses(buffers, gl)[6], _stream(stream)))
 
 
 def zero_list_norms(gl: GradList, scale: float, clip: bool, buffers: NormBuffers,
                     found_nonfinite: Optional[torch.Tensor] = None, stream=None,
                     d_scale: Optional[torch.Tensor] = None) -> None:
     """zero_list_sums, zero_sums_norms of one part and, with clip, zero_list_clip in one call."""
-    ws, nb, sums, _, limits, norms, results = _on_device(buffers, gl)
-    _check(lib().zero_list_norms(gl.ref, scale, _dscale(d_scale), clip, ws, nb, sums, limits, norms, results,
-                                 _dev(found_nonfinite, "found_nonfinite", torch.int32, allow_none=True),
-                                 _stream(stream)))
+    ws, nb, sums, _, limits, norms, results, found = _addresses(buffers, gl, found_nonfinite)
+    _check(lib().zero_list_norms(gl.ref, scale, None if d_scale is None else _dscale(d_scale), clip, ws, nb, sums,
+                                 limits, norms, results, found, _stream(stream)))
 
 
 # ------------------------------------------------------------ debug builds

@@ -748,8 +748,8 @@ typedef struct zero_grad_list {
 
 /* zero_grad_plan -- host only.
  * The work split of a grads list.  Tensors of up to 4096 elements are narrow,
- * a warp's work each; longer ones are cut into wide chunks (4096, 16384 or
- * 65536 elements by the list's total), none across two tensors.  plan:
+ * a warp's work each; longer ones are cut into wide chunks (4096 to 65536
+ * elements by the list's total), none across two tensors.  plan:
  * 4 * n_tensors + n_groups + 2 ints: the first wide chunk of each tensor and
  * their count; where each group's members start and their count; the members
  * (tensor numbers, in list order in each group); each tensor's number among

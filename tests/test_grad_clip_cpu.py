@@ -17,8 +17,9 @@ def parts(plan):
     return a[:n + 1], a[n + 1:n + g + 2], a[n + g + 2:2 * n + g + 2], a[2 * n + g + 2:3 * n + g + 2], a[3 * n + g + 2:]
 
 
-@pytest.mark.parametrize("sizes,chunk", [([1], 4096), ([0], 4096), ([4096, 4097, 0, 4095, 0, 0, 1], 4096), ([1 << 23], 4096),
-                                         ([(1 << 23) + 1], 16384), ([1 << 27], 16384), ([1, 1 << 27, 5], 65536),
+@pytest.mark.parametrize("sizes,chunk", [([1], 4096), ([0], 4096), ([4096, 4097, 0, 4095, 0, 0, 1], 4096), ([1 << 21], 4096),
+                                         ([(1 << 21) + 1], 8192), ([1 << 24], 8192), ([1, 1 << 24, 5], 16384),
+                                         ([1 << 26], 16384), ([1 << 27], 32768), ([(1 << 28) + 1], 65536),
                                          ([4095, 1 << 40, 3], 65536)])
 def test_plan_cuts_long_tensors_into_chunks(sizes, chunk):
     p = zs.zero_grad_plan(sizes, None, 1, 2, "cpu")
