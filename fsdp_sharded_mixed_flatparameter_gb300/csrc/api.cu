@@ -333,7 +333,7 @@ zero_status zero_grad_plan(const int64_t* numels, const int32_t* groups, int32_t
       return fail(ZERO_EINVAL, "%s: group[%d] = %d of %d", who, (int)i, (int)groups[i], (int)n_groups);
     total += numels[i];
   }
-  const int32_t size = zs::grad_chunk_size(total);
+  const int32_t size = zs::grad_chunk_size(total), narrow_size = zs::grad_narrow_size(size);
   int32_t* const first = plan;
   int32_t* const group_first = first + n_tensors + 1;
   int32_t* const members = group_first + n_groups + 1;
@@ -346,13 +346,13 @@ zero_status zero_grad_plan(const int64_t* numels, const int32_t* groups, int32_t
     narrow_of[i] = -1;
     narrow[i] = -1;
     if (numels[i] == 0) continue;
-    if (numels[i] <= zs::kNarrow) {
+    if (numels[i] <= narrow_size) {
       narrow_of[i] = n_narrow;
       narrow[n_narrow++] = i;
       continue;
     }
     wide += numels[i] / size + (numels[i] % size != 0 ? 1 : 0);
-    if (wide > zs::kMaxGradPieces) return fail(ZERO_EINVAL, "%s: 2^28 chunks or more up to tensor %d", who, (int)i);
+    if (wide > zs::kMaxGradPieces) return fail(ZERO_EINVAL, "%s: 2^27 chunks or more up to tensor %d", who, (int)i);
   }
   first[n_tensors] = static_cast<int32_t>(wide);
   // counting sort: group_first[g + 1] counts group g, then becomes where it starts, then where it ends

@@ -112,20 +112,23 @@ zero_status launch_state8_unpack(const zero_state8& q, int64_t n, float* m, floa
 
 // Elements of a grads list's wide chunks, by the list's total.  Long chunks
 // for long lists (a chunk's search and sum take as long as 20 KB of loads),
-// short ones where few chunks would leave SMs without work at the end.  Sums of 48 equal bf16
-// tensors, us, with chunks of 8192 / 16384 / 32768 / 65536: 2^24 elements
-// 16.3 / 20.3 / 19.3 / 20.3; 2^26: 36.3 / 32.2 / 31.4 / 34.4; 2^28: 116 / 96 /
-// 88 / 89; 2^30: 456 / 376 / 317 / 309; 2^30 in fp32: 676 / 661 / 629 / 616.
-constexpr int kMaxGradChunk = 65536, kMaxGradPieces = (1 << 28) - 1;
+// short ones where few chunks would leave SMs without work at the end.  Sums
+// of 48 equal bf16 tensors, us, with chunks of 8192 / 16384 / 32768 / 65536:
+// 2^24 elements 16.3 / 20.3 / 19.3 / 20.3; 2^26: 36.3 / 32.2 / 31.4 / 34.4; 2^28:
+// 116 / 96 / 88 / 89; 2^29: 244 / 179 / 164 / 160.  With 32768 / 65536 /
+// 131072: 4000 ragged fp16 tensors, 302e6 elements, 99 / 112 / 109; 20,000,
+// 1.51e9: 460 / 459 / 447; four layers of Llama-7B, 1.07e9: 321 / 310 / 302.
+constexpr int kMaxGradChunk = 131072, kMaxGradPieces = (1 << 27) - 1;
 inline int grad_chunk_size(int64_t total) {
   return total <= (int64_t(1) << 21)   ? 4096
          : total <= (int64_t(1) << 24) ? 8192
          : total <= (int64_t(1) << 26) ? 16384
-         : total <= (int64_t(1) << 28) ? 32768
+         : total <= (int64_t(1) << 29) ? 32768
                                        : kMaxGradChunk;
 }
-// Elements up to which a tensor is narrow: a warp's work.
-constexpr int kNarrow = 4096;
+// Elements up to which a tensor is narrow, a warp's work: a chunk, but no more
+// than 16384 (the 20,000 ragged tensors: 460 us with 4096, 450 with 16384).
+inline int grad_narrow_size(int chunk) { return chunk < 16384 ? chunk : 16384; }
 
 // The norms of a grads list and its clipping (arguments checked; plan: zero_grad_plan's ints).
 struct GradListArgs {

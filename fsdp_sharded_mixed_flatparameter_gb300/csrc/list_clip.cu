@@ -15,11 +15,11 @@
 namespace zs {
 
 constexpr int kClipThreads = 256, kClipBlocks = 4;
-// Elements of a wide chunk that a block clips: smaller than the chunk, so that
-// the blocks in flight read and write fewer places of memory at once.
+// Elements of a wide chunk that a block clips: fewer than the chunk has, so that
+// the blocks in flight read and write fewer places of memory at once (eight
+// layers of Llama-7B in bf16, 7.5 GB: 1056 us with 16384, 1067 with 32768, 1084
+// with 65536, 1139 with 8192).
 constexpr int kClipPiece = 16384;
-// Wide chunks of a block where it may find that nothing is to be clipped.
-constexpr int kClipChunks = 4;
 
 // 16 bytes that this thread may overwrite later: a coherent load.
 __device__ __forceinline__ uint4 ld16_rw(const void* p) {
@@ -151,41 +151,34 @@ __device__ __forceinline__ void clip_tensor(const zero_grad_entry& t, const Grad
     clip_to<ZERO_F16, T>(t.src_dtype, src, dst, c.len, f, thread);
 }
 
-// The grid, from its end: the blocks of the narrow tensors, then for each wide
-// chunk `parts` blocks, or (MAY_LEAVE) one block for kClipChunks of them.
+// The grid, from its end: the blocks of the narrow tensors, then 2^share blocks
+// for each wide chunk.  MAY_LEAVE (in place with a scale of 1): the blocks look
+// first whether any group is to be clipped; a chunk has one block then, as
+// leaving takes 0.7 ns a block.
 template <bool MAY_LEAVE>
 __global__ void __launch_bounds__(kClipThreads, kClipBlocks)
     list_clip_kernel(const zero_grad_entry* __restrict__ entries, int n, int n_groups,
-                     const __grid_constant__ GradPlan plan, int wide_blocks, int parts_log2, float scale,
-                     const float* __restrict__ dscale, const zero_norm_result* results) {
-  const int block = gridDim.x - 1 - blockIdx.x;
+                     const __grid_constant__ GradPlan plan, int share, float scale, const float* __restrict__ dscale,
+                     const zero_norm_result* results) {
+  const int block = gridDim.x - 1 - blockIdx.x, wide_blocks = plan.n_wide << share;
   GradPiece c;
-  if (!MAY_LEAVE && block < wide_blocks) {
-    // of the plan: while the kernel before still runs
-    c = wide_piece(entries, n, plan, block >> parts_log2);
-    const int piece = plan.chunk >> parts_log2, skip = (block & ((1 << parts_log2) - 1)) * piece;
-    c.k += skip;
-    c.len = min(c.len - skip, piece);
-  }
+  if (!MAY_LEAVE && block < wide_blocks) c = wide_piece(entries, n, plan, block >> share);  // while the kernel before still runs
   wait_before();
   if (!results[n_groups].finite) return;
   if (MAY_LEAVE && n_groups <= 32) {
-    // in place with a scale of 1: no group to clip, nothing to do
     const int g = threadIdx.x & 31;
     if (__all_sync(0xffffffffu, g >= n_groups || results[g].clip_coef == 1.0f)) return;
   }
   if (dscale != nullptr) scale = *dscale;
-  if (block >= wide_blocks) {
+  if (block < wide_blocks) {
+    if (MAY_LEAVE) c = wide_piece(entries, n, plan, block >> share);
+    const int piece = plan.chunk >> share, skip = (block & ((1 << share) - 1)) * piece;
+    c.k += skip;
+    c.len = min(c.len - skip, piece);
+    if (c.len > 0) clip_tensor<kClipThreads>(entries[c.tensor], c, n_groups, scale, results);
+  } else {
     c = narrow_piece<kClipThreads>(entries, plan, block - wide_blocks + plan.n_wide);
     if (c.len > 0) clip_tensor<32>(entries[c.tensor], c, n_groups, scale, results);
-  } else if (MAY_LEAVE) {
-    for (int chunk = min((block + 1) * kClipChunks, plan.n_wide) - 1; chunk >= block * kClipChunks; --chunk) {
-      c = wide_piece(entries, n, plan, chunk);
-      clip_tensor<kClipThreads>(entries[c.tensor], c, n_groups, scale, results);
-      __syncthreads();  // wide_piece's shared memory
-    }
-  } else if (c.len > 0) {
-    clip_tensor<kClipThreads>(entries[c.tensor], c, n_groups, scale, results);
   }
 }
 
@@ -195,16 +188,15 @@ zero_status launch_list_clip(const GradListArgs& a, const zero_norm_result* resu
   const GradPlan plan = plan_parts(a);
   const int64_t narrow = grad_blocks(plan, kClipThreads) - static_cast<unsigned>(plan.n_wide);
   const bool may_leave = a.in_place && a.dscale == nullptr && a.scale == 1.0f;
-  int log2 = 0;
+  int share = 0;
   if (!may_leave)
-    while ((plan.chunk >> log2) > kClipPiece) ++log2;
-  const int64_t wide = may_leave ? (static_cast<int64_t>(plan.n_wide) + kClipChunks - 1) / kClipChunks
-                                 : static_cast<int64_t>(plan.n_wide) << log2;
-  if (wide + narrow > 0x7fffffffLL) return fail(ZERO_EINVAL, "zero_list_clip: %lld blocks", (long long)(wide + narrow));
-  if (wide + narrow == 0) return ZERO_OK;
+    while ((plan.chunk >> share) > kClipPiece) ++share;
+  const int64_t blocks = (static_cast<int64_t>(plan.n_wide) << share) + narrow;
+  if (blocks > 0x7fffffffLL) return fail(ZERO_EINVAL, "zero_list_clip: %lld blocks", (long long)blocks);
+  if (blocks == 0) return ZERO_OK;
   return launch_after("list_clip_kernel", may_leave ? list_clip_kernel<true> : list_clip_kernel<false>,
-                      static_cast<unsigned>(wide + narrow), kClipThreads, 1, st, a.entries, a.n, a.n_groups, plan,
-                      static_cast<int>(wide), log2, a.scale, a.dscale, results);
+                      static_cast<unsigned>(blocks), kClipThreads, 1, st, a.entries, a.n, a.n_groups, plan, share,
+                      a.scale, a.dscale, results);
 }
 
 }  // namespace zs

@@ -25,8 +25,11 @@ namespace zs {
 namespace cg = cooperative_groups;
 
 // ------------------------------------------------------------ 1: chunks
-// Vectors of 8 that a thread has in flight, and blocks on an SM (64 registers).
-constexpr int kSumThreads = 128, kAhead16 = 8, kAhead32 = 4, kSumBlocks = 8;
+// Threads of a block, vectors of 8 that a thread has in flight, and blocks on
+// an SM (72 registers).  Llama-7B's four layers in bf16, us: 304; with 8 blocks
+// (64 registers, some spilled) 313, with 6 and 3 vectors 310, with blocks of
+// 64 or 192 323 and 309.
+constexpr int kSumThreads = 128, kAhead16 = 8, kAhead32 = 4, kSumBlocks = 7;
 
 // What a thread gathers of its elements: the sums, and in `bits` the elements'
 // bits or'ed (p = 2: whether any is not zero) or the largest magnitude's

@@ -709,10 +709,10 @@ zero_status zero_adamw_prepare_list_device(const zero_adamw_hparams* d_hp, int32
  *   norm of a tensor, a group, all = (sum of its S_i)^(1/p), or the largest
  *   coef_g = min(1, M_g / (norm_g + 1e-6))                   (binary32)
  *   y = fl_type(fl(fl(s * coef_g) * x))
- * |s|^p multiplies the sums, not the elements.  The sums carry about 48
- * significant bits for any finite x (chunks whose squares leave the binary32
- * range are summed again, scaled by a power of two); an infinite x makes the
- * norms infinite and a NaN makes them NaN.  No y is written at all where the
+ * |s|^p multiplies the sums, not the elements.  The sums are right to 5e-10
+ * relative at worst and 1e-14 in practice, for any finite x (chunks whose
+ * squares leave the binary32 range are summed again, scaled by a power of
+ * two); an infinite x makes the norms infinite and a NaN makes them NaN.  No y is written at all where the
  * norm over all tensors is not finite: the step is to be skipped.
  * A step is zero_list_norms, which also clips; across ranks zero_list_sums, an
  * all-gather of the sums in rank order, zero_sums_norms and zero_list_clip.
@@ -747,9 +747,9 @@ typedef struct zero_grad_list {
 } zero_grad_list;
 
 /* zero_grad_plan -- host only.
- * The work split of a grads list.  Tensors of up to 4096 elements are narrow,
- * a warp's work each; longer ones are cut into wide chunks (4096 to 65536
- * elements by the list's total), none across two tensors.  plan:
+ * The work split of a grads list.  Long tensors are cut into wide chunks (4096
+ * to 131072 elements by the list's total), none across two tensors; tensors of
+ * up to a chunk and up to 16384 elements are narrow, a warp's work each.  plan:
  * 4 * n_tensors + n_groups + 2 ints: the first wide chunk of each tensor and
  * their count; where each group's members start and their count; the members
  * (tensor numbers, in list order in each group); each tensor's number among
@@ -758,7 +758,7 @@ typedef struct zero_grad_list {
  * n_groups, n_wide, n_narrow and chunk of *list and clears the rest.  The
  * plan depends on sizes and groups alone.
  * Errors: ZERO_EINVAL for n_tensors or n_groups outside [1, 2^28], NULL
- * arguments, a numel < 0, a group outside [0, n_groups), or 2^28 chunks or
+ * arguments, a numel < 0, a group outside [0, n_groups), or 2^27 chunks or
  * more (2^44 elements). */
 zero_status zero_grad_plan(const int64_t* numels, const int32_t* groups, int32_t n_tensors, int32_t n_groups,
                            int32_t* plan, zero_grad_list* list);

@@ -1,8 +1,8 @@
 """The norms of many tensors and their clipping against the formulas in 64 bits.
 
-Tolerances.  Sums: a thread adds at most 65536 / 256 / 2 = 128 pairs, the j-th with a tail l of at most j x 2^-24 of the
-sum, whose addition is rounded by 2^-24 of it: 128^2 / 2 x 2^-48 = 2.9e-11 at worst, the rest of the tree a few 2^-48
-more: SUM = 4e-11 (half of that for a root).  Binary32 outputs add 2^-24.  A clipped grad: the coefficient, scale x coefficient and the
+Tolerances.  Sums: a thread adds at most 131072 / 128 / 2 = 512 pairs, the j-th with a tail l of at most j x 2^-24 of the
+sum, whose addition is rounded by 2^-24 of it: 512^2 / 2 x 2^-48 = 4.66e-10 at worst, the rest of the tree a few 2^-48
+more: SUM = 5e-10 (half of that for a root).  Binary32 outputs add 2^-24.  A clipped grad: the coefficient, scale x coefficient and the
 product are each rounded to binary32, 3 x 2^-24 (and their cross terms), then eps / 2 of a 16-bit type; where the value is
 subnormal there, half its type's least step."""
 import math
@@ -18,7 +18,7 @@ pytestmark = pytest.mark.gpu
 
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 TYPES = [F32, BF16, F16]
-SUM, ULP = 4e-11, 2.0 ** -24
+SUM, ULP = 5e-10, 2.0 ** -24
 LEAST = {F32: 2.0 ** -150, BF16: 2.0 ** -134, F16: 2.0 ** -25}
 SIZES = [1, 0, 7, 8, 9, 255, 4095, 4096, 4097, 3, 70001, 0, 33, 65536, 8200]
 
@@ -117,7 +117,7 @@ def test_norms_of_tensors_groups_and_all(dtype, offset, p):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("total", [(1 << 23) + 77, (1 << 25) + 1, (1 << 27) + 4099, (1 << 28) + 4099])  # the larger chunk sizes
+@pytest.mark.parametrize("total", [(1 << 23) + 77, (1 << 25) + 1, (1 << 27) + 4099, (1 << 29) + 4099])  # the larger chunk sizes
 def test_norms_of_long_tensors(dtype, total):
     sizes = [total - 1003, 0, 1000, 3]
     base = torch.empty(total + 1, dtype=dtype, device="cuda")
@@ -317,7 +317,7 @@ def test_the_function_against_torchs():
 
 @pytest.mark.parametrize("scale", [1.0, 0.5])
 @pytest.mark.parametrize("dtype,to", [(F32, None), (BF16, None), (F16, F32), (BF16, BF16)])
-@pytest.mark.parametrize("total", [(1 << 21) - 9, (1 << 24) - 1, (1 << 25) + 77, (1 << 27) + 4099, (1 << 28) + 4099])
+@pytest.mark.parametrize("total", [(1 << 21) - 9, (1 << 24) - 1, (1 << 25) + 77, (1 << 27) + 4099, (1 << 29) + 4099])
 def test_clip_of_long_tensors(total, dtype, to, scale):
     sizes = [total - 71003, 0, 70000, 1000, 3]
     g = torch.Generator("cuda").manual_seed(total)
@@ -352,10 +352,10 @@ def test_an_element_beyond_32_bits():
 
 def test_more_chunks_than_a_warp_adds():
     # tensors of 4101 chunks beside small ones: their partials are added by whole blocks
-    sizes = [5, 4100 * 65536 + 9, 70000, 0, 1, 4101 * 65536]
+    sizes = [5, 4100 * 131072 + 9, 270000, 0, 1, 4101 * 131072]
     xs = [torch.full((n,), 0.5, dtype=BF16, device="cuda") for n in sizes]
     c = pkg.GradClip(sizes, max_norm=[1.0, 2.0], group_of=[0, 1, 0, 0, 1, 0])
-    assert (c.plan.head.n_wide, c.plan.head.n_narrow) == (4101 + 2 + 4101, 2)
+    assert (c.plan.head.n_wide, c.plan.head.n_narrow) == (4101 + 3 + 4101, 2)
     r = c.clip_(xs)
     assert c.tensor_sums.tolist() == [n / 4 for n in sizes]
     for x, g in zip(xs, (0, 1, 0, 0, 1, 0)):
@@ -368,7 +368,7 @@ def test_thousands_of_tensors(n, groups):
     rng = np.random.default_rng(n)
     sizes = [int(k) for k in rng.integers(0, 60, n)]
     if 1024 < n < 9000:
-        sizes[700], sizes[33] = 600 * 65536 + 5, 1100 * 65536 + 1  # more partials than 8 lanes add, than a warp adds
+        sizes[700], sizes[33] = 600 * 32768 + 5, 1100 * 32768 + 1  # more partials than 8 lanes add, than a warp adds
     total = sum(sizes)
     flat = torch.randint(-8, 9, (total,), generator=torch.Generator("cuda").manual_seed(n), device="cuda", dtype=torch.int32).to(BF16)
     xs = list(flat.split(sizes))

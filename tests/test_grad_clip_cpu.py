@@ -19,14 +19,14 @@ def parts(plan):
 
 @pytest.mark.parametrize("sizes,chunk", [([1], 4096), ([0], 4096), ([4096, 4097, 0, 4095, 0, 0, 1], 4096), ([1 << 21], 4096),
                                          ([(1 << 21) + 1], 8192), ([1 << 24], 8192), ([1, 1 << 24, 5], 16384),
-                                         ([1 << 26], 16384), ([1 << 27], 32768), ([(1 << 28) + 1], 65536),
-                                         ([4095, 1 << 40, 3], 65536)])
+                                         ([1 << 26], 16384), ([16384, 1 << 27, 16385], 32768), ([(1 << 29) + 1], 131072),
+                                         ([4095, 1 << 40, 16384, 16385, 3], 131072)])
 def test_plan_cuts_long_tensors_into_chunks(sizes, chunk):
     p = zs.zero_grad_plan(sizes, None, 1, 2, "cpu")
     first, group_first, members, narrow_of, narrow = parts(p)
     assert p.head.chunk == chunk
-    assert first.tolist() == np.concatenate([[0], np.cumsum([-(-n // chunk) if n > 4096 else 0 for n in sizes])]).tolist()
-    small = [i for i, n in enumerate(sizes) if 0 < n <= 4096]
+    assert first.tolist() == np.concatenate([[0], np.cumsum([-(-n // chunk) if n > min(chunk, 16384) else 0 for n in sizes])]).tolist()
+    small = [i for i, n in enumerate(sizes) if 0 < n <= min(chunk, 16384)]
     assert narrow[:len(small)].tolist() == small and p.head.n_narrow == len(small) and p.head.n_wide == first[-1]
     assert narrow_of.tolist() == [small.index(i) if i in small else -1 for i in range(len(sizes))]
     assert members.tolist() == list(range(len(sizes))) and group_first.tolist() == [0, len(sizes)]
@@ -160,7 +160,7 @@ def test_c_entries_refuse_before_any_launch():
 
     heads = [dict(d_plan=None), dict(d_plan=a + 2), dict(n_tensors=0), dict(n_groups=0), dict(n_wide=-1), dict(n_narrow=-1), dict(n_narrow=3),
              dict(n_wide=1 << 28), dict(chunk=0), dict(chunk=5000),
-             dict(chunk=65537), dict(norm_type=3), dict(norm_type=-1), dict(in_place=2)]
+             dict(chunk=262144), dict(norm_type=3), dict(norm_type=-1), dict(in_place=2)]
     for kw in heads + [dict(d_entries=None), dict(d_entries=a + 4)]:
         assert L.zero_list_sums(head(**kw), 1.0, None, a, 24, a, None) == zs.ZERO_EINVAL, kw
         assert L.zero_list_clip(head(**kw), 1.0, None, a, None) == zs.ZERO_EINVAL, kw
