@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kListThreads, 10)
     adamw_list_kernel(const zero_list_tensor* __restrict__ list, int n_tensors,
                       const int32_t* __restrict__ first_chunk, const zero_tensor* __restrict__ grads, float gscale,
                       const float* __restrict__ dscale, int lowp_dtype, const __grid_constant__ ListScalars hs,
-                      const zero_adamw_device_state* __restrict__ ds, const zero_norm_result* __restrict__ clip) {
+                      const zero_adamw_device_state* __restrict__ ds, const zero_norm_result* __restrict__ clip, int clips) {
   const int tensor = block_tensor(first_chunk, n_tensors, blockIdx.x);
   const int chunk = blockIdx.x - __ldg(first_chunk + tensor);
   const zero_list_tensor t = list[tensor];
@@ -54,8 +54,8 @@ __global__ void __launch_bounds__(kListThreads, 10)
   if (!ZS_CHECK(chunk >= 0 && chunk < (t.numel + kListChunk - 1) / kListChunk, 60, blockIdx.x)) return;
   float coef = 1.0f;
   if (clip != nullptr) {
-    if (!clip->finite) return;  // non-finite grad norm: the step is skipped
-    coef = clip->clip_coef;
+    if (!clip[clips].finite) return;  // non-finite grad norm: the step is skipped
+    coef = clip[clips != 0 ? t.group : 0].clip_coef;
   }
   if (dscale != nullptr) gscale = *dscale;
   const int64_t k = static_cast<int64_t>(chunk) * kListChunk + kBlock8 * (threadIdx.x >> 5);
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kListThreads, 10)
 template <int DT>
 static zero_status launch_list_t(const ListArgs& a, const ListScalars& hs, cudaStream_t st) {
   adamw_list_kernel<DT><<<static_cast<unsigned>(a.n_chunks), kListThreads, 0, st>>>(
-      a.list, a.n_tensors, a.first_chunk, a.grads, a.gscale, a.dscale, a.lowp_dtype, hs, a.ds, a.clip);
+      a.list, a.n_tensors, a.first_chunk, a.grads, a.gscale, a.dscale, a.lowp_dtype, hs, a.ds, a.clip, a.clips);
   return check_launch("adamw_list_kernel");
 }
 

@@ -741,12 +741,12 @@ static zero_status adamw_list(const char* who, const zs::ListArgs& a, const zs::
   return zs::launch_adamw_list(a, s, zs::as_stream(stream));
 }
 
-zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, const int32_t* d_first_chunk,
-                            int32_t n_chunks, int32_t state_bits, const zero_tensor* d_grads, zero_dtype grad_dtype,
-                            float grad_scale, const float* d_grad_scale, zero_dtype lowp_dtype,
-                            const zero_adamw_hparams* groups, int32_t n_groups, int64_t step,
-                            const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream) {
-  const char* who = "zero_adamw_list";
+static zero_status adamw_list_host(const char* who, const zero_list_tensor* d_list, int32_t n_tensors,
+                                   const int32_t* d_first_chunk, int32_t n_chunks, int32_t state_bits,
+                                   const zero_tensor* d_grads, zero_dtype grad_dtype, float grad_scale,
+                                   const float* d_grad_scale, zero_dtype lowp_dtype, const zero_adamw_hparams* groups,
+                                   int32_t n_groups, int64_t step, const zero_rounding* rounding,
+                                   const zero_norm_result* d_clip, int clips, void* stream) {
   const zero_status g = check_groups(who, n_groups);
   if (g != ZERO_OK) return g;
   if (groups == nullptr) return fail(ZERO_EINVAL, "%s: NULL groups", who);
@@ -762,8 +762,33 @@ zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, c
     b.most2 = std::max(b.most2, s.s[i].b2);
   }
   const zs::ListArgs a{d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
-                       lowp_dtype, nullptr, zs::rounding_base(rounding, &step, b), d_clip};
+                       lowp_dtype, nullptr, zs::rounding_base(rounding, &step, b), d_clip, clips};
   return adamw_list(who, a, s, n_groups, stream);
+}
+
+static zero_status adamw_list_dev(const char* who, const zero_list_tensor* d_list, int32_t n_tensors,
+                                  const int32_t* d_first_chunk, int32_t n_chunks, int32_t state_bits,
+                                  const zero_tensor* d_grads, zero_dtype grad_dtype, float grad_scale,
+                                  const float* d_grad_scale, zero_dtype lowp_dtype,
+                                  const zero_adamw_device_state* d_states, int32_t n_groups,
+                                  const zero_rounding* rounding, const zero_norm_result* d_clip, int clips,
+                                  void* stream) {
+  const zero_status c = check_state(who, d_states);
+  if (c != ZERO_OK) return c;
+  const zero_status r = check_rounding(who, rounding);
+  if (r != ZERO_OK) return r;
+  const zs::ListArgs a{d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
+                       lowp_dtype, d_states, zs::rounding_base(rounding, nullptr, zs::Betas{}), d_clip, clips};
+  return adamw_list(who, a, zs::ListScalars{}, n_groups, stream);
+}
+
+zero_status zero_adamw_list(const zero_list_tensor* d_list, int32_t n_tensors, const int32_t* d_first_chunk,
+                            int32_t n_chunks, int32_t state_bits, const zero_tensor* d_grads, zero_dtype grad_dtype,
+                            float grad_scale, const float* d_grad_scale, zero_dtype lowp_dtype,
+                            const zero_adamw_hparams* groups, int32_t n_groups, int64_t step,
+                            const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream) {
+  return adamw_list_host("zero_adamw_list", d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype,
+                         grad_scale, d_grad_scale, lowp_dtype, groups, n_groups, step, rounding, d_clip, 0, stream);
 }
 
 zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_tensors, const int32_t* d_first_chunk,
@@ -771,14 +796,41 @@ zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_ten
                                    zero_dtype grad_dtype, float grad_scale, const float* d_grad_scale,
                                    zero_dtype lowp_dtype, const zero_adamw_device_state* d_states, int32_t n_groups,
                                    const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream) {
-  const char* who = "zero_adamw_list_device";
-  const zero_status c = check_state(who, d_states);
-  if (c != ZERO_OK) return c;
-  const zero_status r = check_rounding(who, rounding);
-  if (r != ZERO_OK) return r;
-  const zs::ListArgs a{d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale, d_grad_scale,
-                       lowp_dtype, d_states, zs::rounding_base(rounding, nullptr, zs::Betas{}), d_clip};
-  return adamw_list(who, a, zs::ListScalars{}, n_groups, stream);
+  return adamw_list_dev("zero_adamw_list_device", d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads,
+                        grad_dtype, grad_scale, d_grad_scale, lowp_dtype, d_states, n_groups, rounding, d_clip, 0, stream);
+}
+
+static zero_status check_clips(const char* who, const zero_norm_result* d_results) {
+  if (d_results == nullptr || !zs::aligned(d_results, 8))
+    return fail(ZERO_EINVAL, "%s: NULL or misaligned d_results", who);
+  return ZERO_OK;
+}
+
+zero_status zero_adamw_list_clips(const zero_list_tensor* d_list, int32_t n_tensors, const int32_t* d_first_chunk,
+                                  int32_t n_chunks, int32_t state_bits, const zero_tensor* d_grads,
+                                  zero_dtype grad_dtype, float grad_scale, const float* d_grad_scale,
+                                  zero_dtype lowp_dtype, const zero_adamw_hparams* groups, int32_t n_groups,
+                                  int64_t step, const zero_rounding* rounding, const zero_norm_result* d_results,
+                                  void* stream) {
+  const char* who = "zero_adamw_list_clips";
+  const zero_status s = check_clips(who, d_results);
+  if (s != ZERO_OK) return s;
+  return adamw_list_host(who, d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale,
+                         d_grad_scale, lowp_dtype, groups, n_groups, step, rounding, d_results, n_groups, stream);
+}
+
+zero_status zero_adamw_list_clips_device(const zero_list_tensor* d_list, int32_t n_tensors,
+                                         const int32_t* d_first_chunk, int32_t n_chunks, int32_t state_bits,
+                                         const zero_tensor* d_grads, zero_dtype grad_dtype, float grad_scale,
+                                         const float* d_grad_scale, zero_dtype lowp_dtype,
+                                         const zero_adamw_device_state* d_states, int32_t n_groups,
+                                         const zero_rounding* rounding, const zero_norm_result* d_results,
+                                         void* stream) {
+  const char* who = "zero_adamw_list_clips_device";
+  const zero_status s = check_clips(who, d_results);
+  if (s != ZERO_OK) return s;
+  return adamw_list_dev(who, d_list, n_tensors, d_first_chunk, n_chunks, state_bits, d_grads, grad_dtype, grad_scale,
+                        d_grad_scale, lowp_dtype, d_states, n_groups, rounding, d_results, n_groups, stream);
 }
 
 zero_status zero_adamw_prepare_list_device(const zero_adamw_hparams* d_hp, int32_t n_groups,

@@ -103,6 +103,7 @@ struct ListArgs {
   const zero_adamw_device_state* ds;
   RoundingBase rounding;
   const zero_norm_result* clip;
+  int clips;  // 0: one result; else clip has that many groups' results, then the one over all
 };
 zero_status launch_adamw_list(const ListArgs& a, const ListScalars& s, cudaStream_t st);
 zero_status launch_adamw_list8(const ListArgs& a, const ListScalars& s, cudaStream_t st);

@@ -53,7 +53,7 @@ class GradClip(GradTables):
             raise ValueError("an empty tensor list")
         dev = self.device
         limits = self._limits(max_norm)
-        _not_in_capture(self._index)
+        not_in_capture(self._index)
         self.plan = zs.zero_grad_plan(self.numels, group_of, n_groups, norm_type, dev)
         n, g = len(self.numels), n_groups
         self.max_norms = limits.to(dev)
@@ -110,7 +110,7 @@ class GradClip(GradTables):
         self._registered = self._entries(grads, out, write)
 
     def _entries(self, grads, out, write):
-        _not_in_capture(self._index)
+        not_in_capture(self._index)
         gl = zs.grad_list(self.plan, grads, out, write)
         return gl, GradTable(gl.entries, self._current()), write
 
@@ -231,7 +231,7 @@ def clip_grad_norm_(grads: Sequence[Optional[torch.Tensor]], max_norm: float, no
     return clip.norm
 
 
-def _not_in_capture(index) -> None:
+def not_in_capture(index) -> None:
     """Tables are copied to the device when a clip is made or grads are registered: not in a capture."""
     if index is not None and torch.cuda.is_current_stream_capturing():
         raise RuntimeError("make the GradClip and register its grads before the capture")

@@ -17,6 +17,7 @@ import numpy as np
 import torch
 
 from . import zero_shard as zs
+from .grad_clip import GradClip, not_in_capture
 from .optimizer import GradTables, torch_stream
 
 _DEFAULTS = ("lr", "betas", "eps", "weight_decay")
@@ -31,6 +32,11 @@ class TensorListAdamW(GradTables):
     do not follow their recurrences over a run (optimizer.py).  Lists that share a seed take
     rounding_streams that are further apart than they have tensors.
 
+    max_norm: the limit of the norm over all grads, or a limit for each group (inf: not clipped):
+    then every group's grads are clipped by the group's own norm (``clip``, a GradClip, has the
+    norms and limits; the grads themselves stay as they are), the step is skipped where the norm
+    over all is not finite, and step() gives that norm with a coefficient of 1.
+
     The moments live in storages of this object, tensor i's at elements offsets[i] ..
     offsets[i] + numels[i]: ``exp_avg`` and ``exp_avg_sq`` (fp32), or ``state8`` (8 bits:
     codes at offsets[i], scales at offsets[i] / 256).  Offsets are multiples of 256."""
@@ -38,7 +44,7 @@ class TensorListAdamW(GradTables):
     def __init__(self, masters: Sequence[torch.Tensor], *, lowp: Optional[Sequence[Optional[torch.Tensor]]] = None,
                  groups: Optional[Sequence[dict]] = None, group_of: Optional[Sequence[int]] = None, lr: float = 1e-4,
                  betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
-                 max_norm: float = math.inf, state_bits: int = 32,
+                 max_norm: Union[float, Sequence[float]] = math.inf, state_bits: int = 32,
                  rounding_seed: Union[int, None, str] = zs.DEFAULT_SEED,
                  rounding_stream: int = 0, capturable: bool = False):
         rounding_seed = zs.rounding_choice(state_bits, rounding_seed)
@@ -60,6 +66,9 @@ class TensorListAdamW(GradTables):
         if not 1 <= len(self._groups) <= zs.LIST_MAX_GROUPS:
             raise ValueError(f"1 to {zs.LIST_MAX_GROUPS} groups")
         self._hp = zs.list_groups(self._groups)
+        per_group = not isinstance(max_norm, (int, float))
+        if per_group and len(max_norm) != len(self._groups):
+            raise ValueError(f"{len(max_norm)} limits for {len(self._groups)} groups")
         columns, numels, lowp_dtype = zs.list_masters(self.masters, self.lowp, group_of)
         self._init_tables(numels, self.device)
         blocks = np.cumsum([0] + [zs.state8_blocks(n) for n in numels])  # each tensor starts on a block's border
@@ -80,8 +89,14 @@ class TensorListAdamW(GradTables):
         self._list = zs.make_tensor_list(columns, numels, group_of, len(self._groups), state_bits, lowp_dtype, self.device)
         self.ws = torch.empty(max(zs.zero_grad_sqnorm_workspace_bytes(self.total), 8), dtype=torch.uint8,
                               device=self.device)
-        self.norm_buf = zs.new_norm_result(self.device)
-        self.found_nonfinite = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.clip: Optional[GradClip] = None
+        if per_group:
+            of = [0] * len(numels) if group_of is None else group_of
+            self.clip = GradClip(numels, max_norm=max_norm, group_of=of, device=self.device)
+            self.norm_buf, self.found_nonfinite = self.clip.result, self.clip.found_nonfinite
+        else:
+            self.norm_buf = zs.new_norm_result(self.device)
+            self.found_nonfinite = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._t = 0
         if capturable:
             self._dev_hp = torch.cat([zs.device_hparams(*g, self.device) for g in self._groups])
@@ -130,6 +145,12 @@ class TensorListAdamW(GradTables):
                               out=self._dev_hp[i * zs.HPARAMS_BYTES:(i + 1) * zs.HPARAMS_BYTES])
 
     # -------------------------------------------------------------- step
+    def register_grads(self, grads: Sequence[Optional[torch.Tensor]]) -> None:
+        """Fix the grads once (see GradTables); with a limit for each group needed before a capture."""
+        super().register_grads(grads)
+        if self.clip is not None:
+            self.clip.register_grads(grads, write=False)
+
     def launch_step(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, scale: float = 1.0, stream=None,
                     loss_scale=None, norm_result: Optional[torch.Tensor] = None) -> None:
         """Enqueue the grad norm over the whole list and the update for step t + 1 without
@@ -137,21 +158,28 @@ class TensorListAdamW(GradTables):
         None: the registered ones.  loss_scale: a DeviceLossScale, whose unscale factor
         replaces `scale`.  norm_result: a zero_norm_result computed elsewhere (one clip over
         several optimizers): used as is, no norm is computed."""
+        if grads is not None and norm_result is None and self.clip is not None:
+            not_in_capture(self._index)
         table, count, dt, stream = self._launch_tables(grads, stream)
         sc, dsc, flag = self._scale_args(scale, loss_scale)
-        clip = norm_result
-        if clip is None:
+        clip, clips = norm_result, norm_result is None and self.clip is not None
+        if clips:
+            self.clip.launch_norms(grads, scale=scale, loss_scale=loss_scale, stream=stream)
+            clip = self.clip.results
+        elif clip is None:
             clip = self.norm_buf
             zs.zero_flatten_cast(table, count, self.total, dt, 0, self.total, sc, False, None, flag, self.ws, stream,
                                  d_scale=dsc)
             zs.zero_grad_sqnorm_finalize(self.ws, self.total, 0.0, self.max_norm, clip, stream)
         if self.capturable:
-            zs.zero_adamw_prepare_list_device(self._dev_hp, len(self._groups), clip, self._dev_states, stream)
+            zs.zero_adamw_prepare_list_device(self._dev_hp, len(self._groups), self.clip.result if clips else clip,
+                                              self._dev_states, stream)
             zs.zero_adamw_list_device(self._list, table, dt, sc, self._dev_states, clip, stream, d_scale=dsc,
-                                      rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream)
+                                      rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream,
+                                      clips=clips)
         else:
             zs.zero_adamw_list(self._list, table, dt, sc, self._hp, self._t + 1, clip, stream, d_scale=dsc,
-                               rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream)
+                               rounding_seed=self.rounding_seed, rounding_stream=self.rounding_stream, clips=clips)
 
     def finish_step(self, stream=None, norm_result: Optional[torch.Tensor] = None) -> zs.NormResult:
         """Read the step's norm (a device-to-host copy on `stream`, the stream the step was

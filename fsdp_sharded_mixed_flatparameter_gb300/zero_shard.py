@@ -151,6 +151,8 @@ def lib() -> ctypes.CDLL:
     L.zero_list_chunks.argtypes = [vp, i32, i32, i32, vp, ctypes.POINTER(i32)]
     L.zero_adamw_list.argtypes = [vp, i32, vp, i32, i32, vp, ci, f32, vp, ci, hpp, i32, i64, rdp, vp, vp]
     L.zero_adamw_list_device.argtypes = [vp, i32, vp, i32, i32, vp, ci, f32, vp, ci, vp, i32, rdp, vp, vp]
+    L.zero_adamw_list_clips.argtypes = L.zero_adamw_list.argtypes
+    L.zero_adamw_list_clips_device.argtypes = L.zero_adamw_list_device.argtypes
     L.zero_adamw_prepare_list_device.argtypes = [vp, i32, vp, vp, vp]
     glp = ctypes.POINTER(zero_grad_list)
     L.zero_grad_plan.argtypes = [vp, vp, i32, i32, vp, glp]
@@ -174,7 +176,8 @@ def lib() -> ctypes.CDLL:
                "zero_debug_errors", "zero_debug_selftest", "zero_state8_pack", "zero_state8_unpack",
                "zero_adamw_step8_tensors", "zero_adamw_step8_tensors_device", "zero_list_chunks", "zero_adamw_list",
                "zero_adamw_list_device", "zero_adamw_prepare_list_device", "zero_grad_plan", "zero_grad_entries_check",
-               "zero_list_sums", "zero_sums_norms", "zero_list_clip", "zero_list_norms"):
+               "zero_list_sums", "zero_sums_norms", "zero_list_clip", "zero_list_norms", "zero_adamw_list_clips",
+               "zero_adamw_list_clips_device"):
         getattr(L, nm).restype = ctypes.c_int
     _lib = L
     return L
@@ -823,37 +826,47 @@ def list_groups(groups: Sequence[Tuple[float, float, float, float, float]]):
     return (zero_adamw_hparams * len(groups))(*[zero_adamw_hparams(*g) for g in groups])
 
 
+def _check_clip(tl: TensorList, clip: Optional[torch.Tensor], clips: bool) -> None:
+    need = (tl.n_groups + 1 if clips else 1) * NORM_RESULT_BYTES
+    if clips and clip is None:
+        raise ValueError("clips needs the groups' results")
+    if clip is not None and clip.numel() * clip.element_size() < need:
+        raise ValueError("clip is smaller than one zero_norm_result per group and one more" if clips
+                         else "clip is smaller than zero_norm_result")
+
+
 def zero_adamw_list(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float,
                     groups: Sequence[Tuple[float, float, float, float, float]], step: int,
                     clip: Optional[torch.Tensor] = None, stream=None, d_scale: Optional[torch.Tensor] = None,
-                    rounding_seed: Optional[int] = None, rounding_stream: int = 0, root_bits: int = 0) -> None:
+                    rounding_seed: Optional[int] = None, rounding_stream: int = 0, root_bits: int = 0,
+                    clips: bool = False) -> None:
     """One AdamW step over every tensor of a list.  d_grads: the device table of the grads
     (zero_tensor_table + device_table, in list order); groups: (lr, beta1, beta2, eps,
     weight_decay) of each parameter group, or list_groups() of them made once.  rounding_seed,
-    root_bits: as for zero_adamw_step8_tensors (each tensor by its group's beta2)."""
+    root_bits: as for zero_adamw_step8_tensors (each tensor by its group's beta2).  clips: clip
+    holds a result for each group and one over all (GradClip.results), not one."""
     if len(groups) != tl.n_groups:
         raise ValueError(f"{len(groups)} groups given, the list has {tl.n_groups}")
-    if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
-        raise ValueError("clip is smaller than zero_norm_result")
+    _check_clip(tl, clip, clips)
     hp = groups if isinstance(groups, ctypes.Array) else list_groups(groups)
-    _check(lib().zero_adamw_list(*_list_args(tl, d_grads, grad_dtype, grad_scale, d_scale), hp, len(groups), step,
-                                 _rounding(rounding_seed, rounding_stream, root_bits),
-                                 _dev(clip, "clip", allow_none=True), _stream(stream)))
+    call = lib().zero_adamw_list_clips if clips else lib().zero_adamw_list
+    _check(call(*_list_args(tl, d_grads, grad_dtype, grad_scale, d_scale), hp, len(groups), step,
+                _rounding(rounding_seed, rounding_stream, root_bits), _dev(clip, "clip", allow_none=True),
+                _stream(stream)))
 
 
 def zero_adamw_list_device(tl: TensorList, d_grads: torch.Tensor, grad_dtype: torch.dtype, grad_scale: float,
                            states: torch.Tensor, clip: Optional[torch.Tensor] = None, stream=None,
                            d_scale: Optional[torch.Tensor] = None, rounding_seed: Optional[int] = None,
-                           rounding_stream: int = 0, root_bits: int = 0) -> None:
+                           rounding_stream: int = 0, root_bits: int = 0, clips: bool = False) -> None:
     """zero_adamw_list with the groups' scalars, step and skip decision from device step states."""
     if states.numel() * states.element_size() < tl.n_groups * DEVICE_STATE_BYTES:
         raise ValueError("states is smaller than one zero_adamw_device_state per group")
-    if clip is not None and clip.numel() * clip.element_size() < NORM_RESULT_BYTES:
-        raise ValueError("clip is smaller than zero_norm_result")
-    _check(lib().zero_adamw_list_device(*_list_args(tl, d_grads, grad_dtype, grad_scale, d_scale),
-                                        _dev(states, "states"), tl.n_groups,
-                                        _rounding(rounding_seed, rounding_stream, root_bits),
-                                        _dev(clip, "clip", allow_none=True), _stream(stream)))
+    _check_clip(tl, clip, clips)
+    call = lib().zero_adamw_list_clips_device if clips else lib().zero_adamw_list_device
+    _check(call(*_list_args(tl, d_grads, grad_dtype, grad_scale, d_scale), _dev(states, "states"), tl.n_groups,
+                _rounding(rounding_seed, rounding_stream, root_bits), _dev(clip, "clip", allow_none=True),
+                _stream(stream)))
 
 
 def zero_adamw_prepare_list_device(d_hp: torch.Tensor, n_groups: int, clip: Optional[torch.Tensor],

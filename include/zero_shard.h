@@ -685,6 +685,27 @@ zero_status zero_adamw_list_device(const zero_list_tensor* d_list, int32_t n_ten
                                    zero_dtype lowp_dtype, const zero_adamw_device_state* d_states, int32_t n_groups,
                                    const zero_rounding* rounding, const zero_norm_result* d_clip, void* stream);
 
+/* zero_adamw_list_clips, zero_adamw_list_clips_device -- device.
+ * zero_adamw_list and zero_adamw_list_device with a clip for each parameter
+ * group: d_results[g] gives group g's coefficient, and d_results[n_groups], the
+ * result over all, whether the step runs, as zero_list_norms writes them for
+ * the same groups.  Pass d_results + n_groups to
+ * zero_adamw_prepare_list_device.
+ * Errors: theirs, and NULL or misaligned d_results. */
+zero_status zero_adamw_list_clips(const zero_list_tensor* d_list, int32_t n_tensors, const int32_t* d_first_chunk,
+                                  int32_t n_chunks, int32_t state_bits, const zero_tensor* d_grads,
+                                  zero_dtype grad_dtype, float grad_scale, const float* d_grad_scale,
+                                  zero_dtype lowp_dtype, const zero_adamw_hparams* groups, int32_t n_groups,
+                                  int64_t step, const zero_rounding* rounding, const zero_norm_result* d_results,
+                                  void* stream);
+zero_status zero_adamw_list_clips_device(const zero_list_tensor* d_list, int32_t n_tensors,
+                                         const int32_t* d_first_chunk, int32_t n_chunks, int32_t state_bits,
+                                         const zero_tensor* d_grads, zero_dtype grad_dtype, float grad_scale,
+                                         const float* d_grad_scale, zero_dtype lowp_dtype,
+                                         const zero_adamw_device_state* d_states, int32_t n_groups,
+                                         const zero_rounding* rounding, const zero_norm_result* d_results,
+                                         void* stream);
+
 /* zero_adamw_prepare_list_device -- device (one block).
  * zero_adamw_prepare_device for n_groups groups at once: d_hp[g] and
  * d_states[g].  All groups step or none does: when d_clip's norm is not

@@ -249,3 +249,15 @@ def test_optimizer_refuses_a_clip_over_another_buffer():
         o.step(1.0, clip=o.grad_clip())
     with pytest.raises(ValueError, match="grad buffer"):
         pkg.FlatShardAdamW([8], device="cpu", grad_buffer=False).grad_clip()
+
+
+def test_list_steps_with_clips_refuse():
+    L = zs.lib()
+    buf = ctypes.cast(ctypes.create_string_buffer(4096 + 64), ctypes.c_void_p).value
+    a = (buf + 63) & ~63
+    hp = zs.list_groups([(1e-3, 0.9, 0.99, 1e-8, 0.0)])
+    for bad in (None, a + 4):
+        assert L.zero_adamw_list_clips(a, 1, a, 1, 32, a, 0, 1.0, None, 1, hp, 1, 1, None, bad, None) == zs.ZERO_EINVAL
+        assert L.zero_adamw_list_clips_device(a, 1, a, 1, 32, a, 0, 1.0, None, 1, a, 1, None, bad, None) == zs.ZERO_EINVAL
+    assert L.zero_adamw_list_clips(a, 1, a, 1, 16, a, 0, 1.0, None, 1, hp, 1, 1, None, a, None) == zs.ZERO_EINVAL
+    assert L.zero_adamw_list_clips(a, 1, a, 0, 32, a, 0, 1.0, None, 1, hp, 1, 1, None, a, None) == zs.ZERO_OK
