@@ -88,6 +88,40 @@ __device__ __forceinline__ int ragged_element(const Run& r, int len, int t) {
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// What an earlier kernel of the stream wrote is read by these alone: as
+// volatile assembly they stay behind wait_before() and barriers, which loads
+// through the read-only path (__ldg, const __restrict__) and __ldcg need not.
+// Of the plan and the entries, which no kernel writes, those are used.
+__device__ __forceinline__ uint4 ld16_behind(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ void ld8_behind(const float* p, float (&r)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ double ld_behind(const double* p) {
+  double r;
+  asm volatile("ld.global.cg.f64 %0, [%1];" : "=d"(r) : "l"(p) : "memory");
+  return r;
+}
+// The bits of one element of a grad.
+template <int DT>
+__device__ __forceinline__ uint32_t bits_behind(const void* p, int e) {
+  if (DT == ZERO_F32) return static_cast<const volatile uint32_t*>(p)[e];
+  return static_cast<const volatile unsigned short*>(p)[e];
+}
+template <int DT>
+__device__ __forceinline__ float elem_behind(const void* p, int e) {
+  return DT == ZERO_F32 ? __uint_as_float(bits_behind<DT>(p, e)) : half_bits_to_f32<DT>(bits_behind<DT>(p, e));
+}
+
 // cluster: the blocks of a thread-block cluster.
 template <class... Formal, class... Actual>
 inline zero_status launch_after(const char* what, void (*kernel)(Formal...), unsigned blocks, unsigned threads,

@@ -21,17 +21,14 @@ constexpr int kClipThreads = 256, kClipBlocks = 4;
 // with 65536, 1139 with 8192).
 constexpr int kClipPiece = 16384;
 
-// 16 bytes that this thread may overwrite later: a coherent load.
+// 16 bytes that this thread overwrites later.
 __device__ __forceinline__ uint4 ld16_rw(const void* p) {
   uint4 r;
-  asm volatile("ld.global.cs.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  asm volatile("ld.global.cs.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
   return r;
-}
-
-template <int DT>
-__device__ __forceinline__ float load_rw(const void* p, int e) {
-  if (DT == ZERO_F32) return static_cast<const volatile float*>(p)[e];
-  return half_bits_to_f32<DT>(static_cast<const volatile unsigned short*>(p)[e]);
 }
 
 template <int DT>
@@ -112,10 +109,10 @@ __device__ __forceinline__ void clip_piece(const char* src, char* dst, int len, 
     for (; v + T * (kAhead - 1) < r.vecs; v += T * kAhead) clip_vectors<S, D, T, kAhead, true>(from, to, v, r, len, f);
     for (; v < r.vecs; v += T * 4) clip_vectors<S, D, T, 4, false>(from, to, v, r, len, f);
     const int e = ragged_element(r, len, thread);
-    if (e >= 0 && ZS_CHECK(e < len, 77, e)) store_one<D>(dst, e, __fmul_rn(f, load_rw<S>(src, e)));
+    if (e >= 0 && ZS_CHECK(e < len, 77, e)) store_one<D>(dst, e, __fmul_rn(f, elem_behind<S>(src, e)));
   } else {  // source and destination apart on the vector grid: element by element
 #pragma unroll 8
-    for (int e = thread; e < len; e += T) store_one<D>(dst, e, __fmul_rn(f, load_rw<S>(src, e)));
+    for (int e = thread; e < len; e += T) store_one<D>(dst, e, __fmul_rn(f, elem_behind<S>(src, e)));
   }
 }
 
@@ -158,7 +155,7 @@ __device__ __forceinline__ void clip_tensor(const zero_grad_entry& t, const Grad
 template <bool MAY_LEAVE>
 __global__ void __launch_bounds__(kClipThreads, kClipBlocks)
     list_clip_kernel(const zero_grad_entry* __restrict__ entries, int n, int n_groups,
-                     const __grid_constant__ GradPlan plan, int share, float scale, const float* __restrict__ dscale,
+                     const __grid_constant__ GradPlan plan, int share, float scale, const float* dscale,
                      const zero_norm_result* results) {
   const int block = gridDim.x - 1 - blockIdx.x, wide_blocks = plan.n_wide << share;
   GradPiece c;

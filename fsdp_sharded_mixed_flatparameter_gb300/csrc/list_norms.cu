@@ -86,7 +86,7 @@ struct Gather {
   template <int DT>
   __device__ __forceinline__ void one(const void* p, int e) {
     if (DT == ZERO_F32) {
-      const uint32_t b = __float_as_uint(load_elem<DT>(p, e));
+      const uint32_t b = __float_as_uint(elem_behind<DT>(p, e));
       if (P == ZERO_NORM_INF) {
         bits = max(bits, b & 0x7fffffffu);
       } else {
@@ -94,7 +94,7 @@ struct Gather {
         pair<false>(__uint_as_float(b), 0.0f);
       }
     } else {
-      const uint32_t h = __ldg(static_cast<const unsigned short*>(p) + e);
+      const uint32_t h = bits_behind<DT>(p, e);
       if (P == ZERO_NORM_INF) {
         bits = __vmaxu2(bits, h & 0x7fffu);
       } else {
@@ -158,13 +158,13 @@ __device__ __forceinline__ bool any_of(bool x) {
 template <int P, int DT, int T>
 __device__ __noinline__ double scaled_sum(const void* p, int len, float2* red) {
   uint32_t m = 0u;
-  for (int e = thread_of<T>(); e < len; e += T) m = max(m, __float_as_uint(load_elem<DT>(p, e)) & 0x7fffffffu);
+  for (int e = thread_of<T>(); e < len; e += T) m = max(m, __float_as_uint(elem_behind<DT>(p, e)) & 0x7fffffffu);
   m = max_of<T>(m, reinterpret_cast<uint32_t*>(red));
   if (m >= 0x7f800000u) return static_cast<double>(__uint_as_float(m));  // infinite, or a NaN
   if (m == 0u) return 0.0;
   const int e2 = ilogbf(__uint_as_float(m));
   Gather<P> g;
-  for (int e = thread_of<T>(); e < len; e += T) g.template pair<false>(scalbnf(load_elem<DT>(p, e), -e2), 0.0f);
+  for (int e = thread_of<T>(); e < len; e += T) g.template pair<false>(scalbnf(elem_behind<DT>(p, e), -e2), 0.0f);
   return scalbn(sum_norm<T>(g.acc, red), P == ZERO_NORM_2 ? 2 * e2 : e2);
 }
 
@@ -178,7 +178,7 @@ __device__ __forceinline__ void gather_vectors(const char* body, int v, const Ru
     for (int u = 0; u < N; ++u) {
       const int k = v + T * u;
       if ((FULL || k < r.vecs) && ZS_CHECK(aligned(body + 32 * k, 32) && r.head + 8 * k + 8 <= len, 70, k)) {
-        ld8_ro(reinterpret_cast<const float*>(body) + 8 * k, x[u]);
+        ld8_behind(reinterpret_cast<const float*>(body) + 8 * k, x[u]);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[u][i] = 0.0f;
@@ -193,7 +193,7 @@ __device__ __forceinline__ void gather_vectors(const char* body, int v, const Ru
       const int k = v + T * u;
       w[u] = make_uint4(0u, 0u, 0u, 0u);
       if ((FULL || k < r.vecs) && ZS_CHECK(aligned(body + 16 * k, 16) && r.head + 8 * k + 8 <= len, 71, k))
-        w[u] = ld16_ro(body + 16 * k);
+        w[u] = ld16_behind(body + 16 * k);
     }
 #pragma unroll
     for (int u = 0; u < N; ++u) g.template vec16<DT>(w[u]);
@@ -351,7 +351,7 @@ __device__ __forceinline__ double scale_power(const FinishArgs& a) {
 template <int P>
 __device__ __forceinline__ double join_parts(const FinishArgs& a, int i) {
   const double* const row = a.partials + i;
-  return strided<P>(0, a.n_parts, 1, [&](int r) { return __ldcg(row + static_cast<int64_t>(r) * a.n); });
+  return strided<P>(0, a.n_parts, 1, [&](int r) { return ld_behind(row + static_cast<int64_t>(r) * a.n); });
 }
 
 // Roots and quotients from binary32 ones and binary64 residuals: __dsqrt_rn and
@@ -404,7 +404,7 @@ __device__ __forceinline__ void write_result(const FinishArgs& a, int g, double 
 }
 template <int P>
 __device__ __forceinline__ void write_group(const FinishArgs& a, int g, double sum) {
-  write_result<P>(a, g, sum, __ldg(a.max_norms + g));
+  write_result<P>(a, g, sum, ld_behind(a.max_norms + g));
 }
 
 // The sums and norms of many tensors over all SMs (the binary64 pipes of
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(256) tensors_kernel(const __grid_constant__ Fi
     if (a.norms != nullptr) a.norms[k] = tensor_norm<P>(s);
   };
   double s = 0.0;
-  if (count <= kOctetPartials) s = strided<P>(lane, count, 8, [&](int j) { return __ldcg(a.partials + lo + j); });
+  if (count <= kOctetPartials) s = strided<P>(lane, count, 8, [&](int j) { return ld_behind(a.partials + lo + j); });
 #pragma unroll
   for (int off = 4; off > 0; off >>= 1) s = join<P>(s, __shfl_down_sync(0xffffffffu, s, off, 8));
   if (lane == 0 && i < a.n && count <= kOctetPartials) finish(i, s);
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(256) tensors_kernel(const __grid_constant__ Fi
     partials_of(a.plan, k, lo, count);
     if (count <= kOctetPartials) continue;
     __syncthreads();
-    s = block_join<P>(strided<P>(threadIdx.x, count, 256, [&](int j) { return __ldcg(a.partials + lo + j); }), 32, red);
+    s = block_join<P>(strided<P>(threadIdx.x, count, 256, [&](int j) { return ld_behind(a.partials + lo + j); }), 32, red);
     if (threadIdx.x == 0) finish(k, s);
   }
 }
@@ -475,16 +475,16 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   wait_before();
   double all = 0.0;
   if (HAVE == kSums) {
-    all = strided<P>(i, a.n, warps * 32, [&](int j) { return __ldcg(a.sums + j); });
+    all = strided<P>(i, a.n, warps * 32, [&](int j) { return ld_behind(a.sums + j); });
   } else {
     if (HAVE == kParts) {
       if (i < a.n) all = join_parts<P>(a, i);
     } else {
-      if (count <= kThreadPartials) all = strided<P>(0, count, 1, [&](int j) { return __ldcg(a.partials + lo + j); });
+      if (count <= kThreadPartials) all = strided<P>(0, count, 1, [&](int j) { return ld_behind(a.partials + lo + j); });
       unsigned mid = __ballot_sync(0xffffffffu, count > kThreadPartials && count <= kWarpPartials);
       for (; mid != 0u; mid &= mid - 1u) {
         const int l = __ffs(mid) - 1, from = __shfl_sync(0xffffffffu, lo, l), len = __shfl_sync(0xffffffffu, count, l);
-        double x = warp_join<P>(strided<P>(lane, len, 32, [&](int j) { return __ldcg(a.partials + from + j); }));
+        double x = warp_join<P>(strided<P>(lane, len, 32, [&](int j) { return ld_behind(a.partials + from + j); }));
         x = __shfl_sync(0xffffffffu, x, 0);
         if (lane == l) all = x;
       }
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
           int from, len;
           partials_of(a.plan, long_tensors[q], from, len);
           const double x = block_join<P>(
-              strided<P>(threadIdx.x, len, kFinishThreads, [&](int j) { return __ldcg(a.partials + from + j); }), 32, red);
+              strided<P>(threadIdx.x, len, kFinishThreads, [&](int j) { return ld_behind(a.partials + from + j); }), 32, red);
           if (threadIdx.x == 0) long_sums[q] = x;
         }
         __syncthreads();
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   }
   if (a.n_groups > 1 && a.n_groups <= kFinishGroups) {
     const auto sum_of = [&](int lo, int count, int from, int step) {
-      return strided<P>(from, count, step, [&](int j) { return __ldcg(a.sums + __ldg(a.plan.members + lo + j)); });
+      return strided<P>(from, count, step, [&](int j) { return ld_behind(a.sums + __ldg(a.plan.members + lo + j)); });
     };
     if (a.n / a.n_groups <= 512) {
       for (int g = warp; g < a.n_groups; g += warps) {
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
         const int from = again ? __ldg(a.plan.group_first + g) : group_lo;
         const int len = again ? __ldg(a.plan.group_first + g + 1) - from : group_count;
         if (again) first_member = lane < len ? __ldg(a.plan.members + from + lane) : 0;
-        double x = lane < len ? __ldcg(a.sums + first_member) : 0.0;
+        double x = lane < len ? ld_behind(a.sums + first_member) : 0.0;
         x = warp_join<P>(join<P>(x, sum_of(from, len, lane + 32, 32)));
         if (lane == 0) write_group<P>(a, g, x);
       }
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(128) groups_kernel(const __grid_constant__ Fin
   wait_before();
   if (g >= a.n_groups) return;
   const int lo = __ldg(a.plan.group_first + g), count = __ldg(a.plan.group_first + g + 1) - lo;
-  const auto member = [&](int j) { return __ldcg(a.sums + __ldg(a.plan.members + lo + j)); };
+  const auto member = [&](int j) { return ld_behind(a.sums + __ldg(a.plan.members + lo + j)); };
   if (WARPS) {
     const double x = warp_join<P>(strided<P>(lane, count, 32, member));
     if (lane == 0) write_group<P>(a, g, x);

@@ -10,6 +10,7 @@ waits for the host, so a whole step can be captured in a graph.
 from __future__ import annotations
 
 import math
+import numbers
 from typing import NamedTuple, Optional, Sequence, Union
 
 import numpy as np
@@ -44,7 +45,7 @@ class GradClip(GradTables):
     def __init__(self, numels: Sequence[int], *, max_norm: Union[float, Sequence[float]] = math.inf,
                  norm_type: float = 2.0, group_of: Optional[Sequence[int]] = None, device="cuda"):
         self._init_tables(numels, device)
-        if isinstance(max_norm, (int, float)):
+        if isinstance(max_norm, numbers.Real):
             n_groups = 1 if group_of is None or len(group_of) == 0 else int(max(group_of)) + 1
         else:
             n_groups = len(max_norm)
@@ -88,7 +89,7 @@ class GradClip(GradTables):
 
     # ------------------------------------------------------------ limits
     def _limits(self, max_norm) -> torch.Tensor:
-        values = [max_norm] * self.n_groups if isinstance(max_norm, (int, float)) else list(max_norm)
+        values = [max_norm] * self.n_groups if isinstance(max_norm, numbers.Real) else list(max_norm)
         if len(values) != self.n_groups:
             raise ValueError(f"{len(values)} limits for {self.n_groups} groups")
         if any(math.isnan(v) or v < 0 for v in values):

@@ -11,6 +11,7 @@ fp32 moments the result is FlatShardAdamW's bit for bit, tensor by tensor.
 from __future__ import annotations
 
 import math
+import numbers
 from typing import List, Optional, Sequence, Tuple, Union
 
 import numpy as np
@@ -66,7 +67,7 @@ class TensorListAdamW(GradTables):
         if not 1 <= len(self._groups) <= zs.LIST_MAX_GROUPS:
             raise ValueError(f"1 to {zs.LIST_MAX_GROUPS} groups")
         self._hp = zs.list_groups(self._groups)
-        per_group = not isinstance(max_norm, (int, float))
+        per_group = not isinstance(max_norm, numbers.Real)
         if per_group and len(max_norm) != len(self._groups):
             raise ValueError(f"{len(max_norm)} limits for {len(self._groups)} groups")
         columns, numels, lowp_dtype = zs.list_masters(self.masters, self.lowp, group_of)

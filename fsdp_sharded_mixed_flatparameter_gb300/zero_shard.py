@@ -950,6 +950,26 @@ def _overlaps(starts: np.ndarray, ends: np.ndarray, written: np.ndarray) -> bool
     return bool(np.any((s[1:] < reach[:-1]) & w[1:]) or np.any(s[1:] < reach_w[:-1]))
 
 
+def _addresses_of(tensors: Sequence[Optional[torch.Tensor]], sizes: List[int], device: torch.device, name: str):
+    """The checked tensors' addresses and types (0 for None)."""
+    cuda, index = device.type == "cuda", device.index if device.type == "cuda" else -1
+    ptrs, dts = [0] * len(sizes), [0] * len(sizes)
+    for i, t in enumerate(tensors):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not (t.is_cuda if cuda else t.is_cpu) or t.get_device() != index:
+            raise ValueError(f"{name}[{i}] must be a tensor on {device}")
+        dt = _DT.get(t.dtype)
+        if dt is None:
+            raise ValueError(f"{name}[{i}] is {t.dtype}, not f32, bf16 or f16")
+        if t.numel() != sizes[i]:
+            raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {sizes[i]}")
+        if not t.is_contiguous() and not _dense(t):
+            raise ValueError(f"{name}[{i}] does not fill one run of memory (strides {t.stride()})")
+        ptrs[i], dts[i] = t.data_ptr(), dt
+    return ptrs, dts
+
+
 def grad_list(plan: GradPlan, grads: Sequence[Optional[torch.Tensor]], out: Optional[Sequence] = None,
               write: bool = True) -> GradList:
     """Check a list of grads (None: no grad, reads as zeros) and copy it to the device.  out:
@@ -962,35 +982,19 @@ def grad_list(plan: GradPlan, grads: Sequence[Optional[torch.Tensor]], out: Opti
         raise ValueError("one grad (or None) per tensor is required, and one out")
     device = plan.ints.device
     entries = np.zeros(n, dtype=_GRAD_ENTRY)
-    src, dst, sdt, ddt = [0] * n, [0] * n, [0] * n, [0] * n
-
-    def address(t, nm, i):
-        if not isinstance(t, torch.Tensor) or t.device != device:
-            raise ValueError(f"{nm}[{i}] must be a tensor on {device}")
-        if t.dtype not in _DT:
-            raise ValueError(f"{nm}[{i}] is {t.dtype}, not f32, bf16 or f16")
-        if not _dense(t):
-            raise ValueError(f"{nm}[{i}] does not fill one run of memory (strides {t.stride()})")
-        return t.data_ptr(), _DT[t.dtype]
-
-    for i, g in enumerate(grads):
-        if g is None:
-            continue
-        src[i], sdt[i] = address(g, "grads", i)
-        if g.numel() != plan.numels[i]:
-            raise ValueError(f"grad {i} has {g.numel()} elements, expected {plan.numels[i]}")
-        if write and out is None:
-            dst[i], ddt[i] = src[i], sdt[i]
-    for i, y in enumerate(out if write and out is not None else ()):
-        if y is None:
-            continue
-        dst[i], ddt[i] = address(y, "out", i)
-        g = grads[i]
-        if y.numel() != plan.numels[i]:
-            raise ValueError(f"out {i} has {y.numel()} elements, expected {plan.numels[i]}")
-        if g is not None and not (g.is_contiguous() and y.is_contiguous()) and (
-                g.shape != y.shape or g.stride() != y.stride()):
-            raise ValueError(f"out {i} is not laid out as its grad")
+    sizes = plan.numels.tolist()
+    src, sdt = _addresses_of(grads, sizes, device, "grads")
+    if not write:
+        dst, ddt = [0] * n, [0] * n
+    elif out is None:
+        dst, ddt = src, sdt
+    else:
+        dst, ddt = _addresses_of(out, sizes, device, "out")
+        for i, (g, y) in enumerate(zip(grads, out)):
+            if g is None or y is None or (g.is_contiguous() and y.is_contiguous()):
+                continue
+            if g.shape != y.shape or g.stride() != y.stride():
+                raise ValueError(f"out[{i}] is not laid out as its grad")
     entries["src"], entries["dst"], entries["src_dtype"], entries["dst_dtype"] = src, dst, sdt, ddt
     entries["numel"] = plan.numels
     if plan.groups is not None:

@@ -460,6 +460,31 @@ def test_captured_and_replayed():
         assert max(float(x.float().abs().max()) for x in xs) <= 0.25 * (1 + 2.0 ** -8)
 
 
+def test_back_to_back_launches_see_each_other():
+    """Each kernel may start before the one ahead of it has ended: clips in place one after the other, with kernels of
+    torch between them or not, as if each had ended first."""
+    n = 1 << 22
+    sizes = [n // 7] * 6 + [n - 6 * (n // 7)]
+    x = torch.randn(n, generator=gen(3)).bfloat16().cuda()
+    want, y = x.clone(), x.clone()
+    clips = [pkg.GradClip(sizes, max_norm=2.0 ** -k * 1000.0) for k in range(6)]
+    for c in clips:
+        c.register_grads(list(x.split(sizes)))
+    for c in clips:  # with a wait after each
+        c.launch(scale=1.5)
+        torch.cuda.synchronize()
+    first = x.clone()
+    for gap in (False, True):
+        for _ in range(5):
+            x.copy_(y)
+            for c in clips:
+                c.launch(scale=1.5)
+                if gap:
+                    x.mul_(1.0)
+            assert torch.equal(x, first)
+    assert not torch.equal(first, want)
+
+
 def test_launches_on_another_stream():
     xs = tensors("mixed", 1)
     before = [x.clone() for x in xs]
@@ -529,6 +554,26 @@ def test_shards_join_to_the_whole(p, world):
     for i, (y, x) in enumerate(zip(got, xs)):
         check_clipped(y, x, 0.5 * coefs[of[i]], F32)
     assert all(guards_intact(v) for v in shards)
+
+
+def test_ranks_without_elements():
+    x = torch.full((3,), 2.0, device="cuda")
+    parts = [zs.zero_shard_range(3, 8, r) for r in range(8)]
+    shards = [x[a:b].clone() for a, b in parts]
+    clips = [pkg.GradClip.of_shard([2, 1], s, a, max_norm=np.float32(1.0)) for s, (a, _) in zip(shards, parts)]
+    for c in clips:
+        c.launch_sums()
+    sums = torch.stack([c.tensor_sums for c in clips])
+    assert sums.sum(0).tolist() == [8.0, 4.0] and sums[3:].abs().sum() == 0
+    for c in clips:
+        c.launch(gathered_sums=sums)
+        assert c.finish().norm == math.sqrt(12.0)
+    want = torch.full((3,), 2.0) * clips[0].finish().coefs[0]
+    assert torch.equal(torch.cat(shards).cpu(), want)
+    o = pkg.FlatShardAdamW([2, 1], world_size=8, rank=7, device="cuda")
+    assert o.step(clip=o.grad_clip(max_norm=1.0)).finite and o.t == 1
+    e = pkg.GradClip([0, 0], max_norm=1.0)
+    assert e.clip_([None, torch.zeros(0, device="cuda")]).norm == 0.0
 
 
 def test_one_ranks_overflow_stops_every_rank():

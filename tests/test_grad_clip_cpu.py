@@ -123,7 +123,7 @@ def test_list_refuses_other_layouts_of_out():
     with pytest.raises(ValueError, match="laid out"):
         zs.grad_list(plan, [torch.zeros(4, 6).t()], [torch.zeros(6, 4)])
     zs.grad_list(plan, [torch.zeros(4, 6).t()], [torch.zeros(4, 6, dtype=torch.bfloat16).t()])
-    with pytest.raises(ValueError, match="out 0 has"):
+    with pytest.raises(ValueError, match="has 23 elements"):
         zs.grad_list(plan, [torch.zeros(24)], [torch.zeros(23)])
 
 
