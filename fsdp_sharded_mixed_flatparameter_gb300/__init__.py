@@ -13,7 +13,7 @@ from .zero_shard import (  # noqa: F401
     zero_adamw_scalars, zero_adamw_step_device, zero_adamw_step_tensors_device, zero_loss_scale_update_device,
     State8, TensorList, new_state8, zero_adamw_list, zero_adamw_list_device, zero_adamw_prepare_list_device,
     zero_adamw_step8_tensors, zero_adamw_step8_tensors_device, zero_state8_pack, zero_state8_unpack, zero_tensor_list,
-    GradList, GradPlan, NormBuffers, grad_list, norm_buffers, norms_only_list, zero_grad_plan, zero_list_clip, zero_list_norms,
+    GradList, GradPlan, NormBuffers, flat_grad_list, grad_list, norm_buffers, norms_only_list, zero_grad_plan, zero_list_clip, zero_list_norms,
     zero_list_norms_workspace_bytes, zero_list_sums, zero_sums_norms)
 from .optimizer import FlatShardAdamW, gather_sqnorms, torch_stream  # noqa: F401
 from .grad_clip import ClipResult, GradClip, clip_grad_norm_  # noqa: F401

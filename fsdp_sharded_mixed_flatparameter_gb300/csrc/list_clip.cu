@@ -4,10 +4,15 @@
 // y = fl_type(fl(f x)), f = fl(scale * coef): a rounding to binary32 and, for
 // 16-bit outputs, one to their type (both to nearest even).
 //
-// One block per wide chunk, one warp per narrow tensor, the last first: the
-// norms pass has just read the list front to back, so its end is what the
-// 129 MB L2 still holds.  Nothing is written where the norm over all tensors
-// is not finite, nor in place where scale and coefficient are 1.
+// Up to 8 blocks per wide chunk, one warp per narrow tensor (list_norms.cu's
+// work split), the last first: the norms pass has just read the list front to
+// back, and its end may be in L2 (128 MB in place 37.9 us, front to back 39.9).
+// Nothing is written where the norm over all tensors is not finite, nor in
+// place where scale and coefficient are 1.
+//
+// Bound by HBM: 1.88e9 bf16 elements in place 1056 us = 7.1 TB/s, 302e6 fp16
+// into fp32 264 us = 6.9 TB/s.  What lies in L2 is no faster: 32 to 64 MB read and
+// written there at 7.5 to 8 TB/s.
 #include "common.cuh"
 #include "grad_list.cuh"
 #include "kernels.h"

@@ -75,7 +75,7 @@ class GradClip(GradTables):
         launch(gathered_sums=...) join them with the other ranks'."""
         if grad.dim() != 1 or not grad.is_contiguous():
             raise ValueError("the shard's grad must be 1-D and contiguous")
-        sizes = np.asarray([int(k) for k in numels], dtype=np.int64)
+        sizes = np.asarray(numels, dtype=np.int64)
         ends = np.cumsum(sizes)
         end, total = start + grad.numel(), int(ends[-1]) if len(ends) else 0
         if start < 0 or end > total:
@@ -83,8 +83,8 @@ class GradClip(GradTables):
         lo, hi = np.maximum(ends - sizes, start), np.minimum(ends, end)
         local = np.maximum(0, hi - lo)
         clip = cls(local.tolist(), **{"device": grad.device, **kw})
-        clip.register_grads([grad[a - start:a - start + k] if k else None for a, k in zip(lo.tolist(), local.tolist())])
-        clip.shard = grad
+        gl = zs.flat_grad_list(clip.plan, grad, lo - start)
+        clip._registered, clip.shard = (gl, GradTable(gl.entries, clip._current()), True), grad
         return clip
 
     # ------------------------------------------------------------ limits

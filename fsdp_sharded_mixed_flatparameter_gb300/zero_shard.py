@@ -996,10 +996,28 @@ def grad_list(plan: GradPlan, grads: Sequence[Optional[torch.Tensor]], out: Opti
             if g.shape != y.shape or g.stride() != y.stride():
                 raise ValueError(f"out[{i}] is not laid out as its grad")
     entries["src"], entries["dst"], entries["src_dtype"], entries["dst_dtype"] = src, dst, sdt, ddt
+    return _checked_list(plan, entries)
+
+
+def flat_grad_list(plan: GradPlan, flat: torch.Tensor, starts: np.ndarray) -> GradList:
+    """The list of a flat grad's pieces, clipped in place: tensor i's plan.numels[i] elements from starts[i]."""
+    if flat.device != plan.ints.device or flat.dtype not in _DT or flat.dim() != 1 or not flat.is_contiguous():
+        raise ValueError(f"the flat grad must be 1-D, contiguous, f32, bf16 or f16, on {plan.ints.device}")
+    some = plan.numels > 0
+    if np.any(some & ((starts < 0) | (starts + plan.numels > flat.numel()))):
+        raise ValueError("a piece lies outside the flat grad")
+    entries = np.zeros(len(plan.numels), dtype=_GRAD_ENTRY)
+    entries["src"] = np.where(some, np.uint64(flat.data_ptr()) + np.where(some, starts, 0).astype(np.uint64) *
+                              np.uint64(flat.element_size()), np.uint64(0))
+    entries["dst"], entries["src_dtype"], entries["dst_dtype"] = entries["src"], _DT[flat.dtype], _DT[flat.dtype]
+    return _checked_list(plan, entries)
+
+
+def _checked_list(plan: GradPlan, entries: np.ndarray) -> GradList:
     entries["numel"] = plan.numels
     if plan.groups is not None:
         entries["group"] = plan.groups
-    _check(lib().zero_grad_entries_check(entries.ctypes.data, plan.numels.ctypes.data, n, plan.n_groups))
+    _check(lib().zero_grad_entries_check(entries.ctypes.data, plan.numels.ctypes.data, len(entries), plan.n_groups))
     written = (entries["dst"] != 0) & (plan.numels > 0)
     if written.any():
         bytes_of = np.array([4, 2, 2], dtype=np.uint64)
@@ -1010,7 +1028,7 @@ def grad_list(plan: GradPlan, grads: Sequence[Optional[torch.Tensor]], out: Opti
                                     (size * bytes_of[entries["src_dtype"]])[read]])
         if _overlaps(at, ends, np.arange(len(at)) < int(written.sum())):
             raise ValueError("a grad that is written overlaps another tensor of the list (is one listed twice?)")
-    d_entries = torch.from_numpy(entries.view(np.uint8)).to(device)
+    d_entries = torch.from_numpy(entries.view(np.uint8)).to(plan.ints.device)
     elsewhere = (entries["dst"] != 0) & (entries["dst"] != entries["src"])
     return GradList(d_entries, plan, _list_ref(plan, d_entries.data_ptr(), int(not elsewhere.any())))
 

@@ -238,6 +238,10 @@ def test_shard_pieces_cover_every_tensor_once(world):
         pkg.GradClip.of_shard(sizes, flat, 1)
     with pytest.raises(ValueError, match="1-D"):
         pkg.GradClip.of_shard([4], torch.zeros(2, 2), 0)
+    with pytest.raises(ValueError, match="1-D"):
+        pkg.GradClip.of_shard([4], torch.zeros(4, dtype=torch.float64), 0)
+    with pytest.raises(ValueError, match="outside"):
+        zs.flat_grad_list(a_plan([4, 3]), torch.zeros(7), np.array([0, 5]))
 
 
 def test_optimizer_refuses_a_clip_over_another_buffer():
