@@ -10,14 +10,14 @@
 //     A piece whose squares leave the binary32 range is read again scaled by
 //     a power of two, which is exact.
 //  2. finish_kernel, one cluster or block: the partials of each tensor in a
-//     fixed order, times |scale|^p; the norms of tensors and of all; groups up
-//     to 256.  Thousands of tensors: tensors_kernel before it; more groups:
-//     groups_kernel behind it.
+//     fixed order, times |scale|^p; the norms of tensors, groups and all.  For
+//     more than 1024 tensors or groups tensors_kernel and groups_kernel, over
+//     all SMs.
 //
 // Bound by HBM from about 100 MB on: 1.63e9 fp16 elements, p = infinity, 454 us
 // = 7.2 TB/s; 1.07e9 bf16, p = 2, 302 us = 7.1 TB/s (issue slots half busy, a
 // third of the FMA pipe); 124e6 fp32, p = 1, 84 us = 5.9 TB/s, of which 72 are
-// step 1; 20,000 ragged tensors of mixed types (3.1 GB) 462 us = 6.6 TB/s.
+// step 1; 20,000 ragged tensors of mixed types (3.1 GB) 457 us = 6.7 TB/s.
 // Below, by latency: 1.3e6 fp32 elements 7.1 us, 5.4 without the results of
 // groups and all.  A warp for every chunk of 16384 was slower (1.63e9: 549
 // against 491 us: more places of memory read at once), one block of 256
@@ -277,8 +277,7 @@ __device__ __forceinline__ double join(double a, double b) {
   return (a > b || a != a) ? a : b;
 }
 
-// Lane 0's result, of the first `lanes` lanes.  (binary64 additions are a
-// 64th of the binary32 rate: a warp's takes 16 cycles, so none is wasted.)
+// Lane 0's result, of the first `lanes` lanes.
 template <int P>
 __device__ __forceinline__ double warp_join(double x, int lanes = 32) {
 #pragma unroll
@@ -290,14 +289,46 @@ __device__ __forceinline__ double warp_join(double x, int lanes = 32) {
 constexpr int kFinishThreads = 1024;
 constexpr int kFinishBlocks = 8;  // at most: one cluster
 
-// Thread 0's result, of the first `lanes` lanes of each warp; every thread of
-// the block must call it.
-template <int P>
-__device__ __forceinline__ double block_join(double x, int lanes, double* red) {
-  x = warp_join<P>(x, lanes);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+// Shared memory of a block that joins.
+template <int T>
+struct Joining {
+  double buf[T];
+  int queue[T];
+  int queued;
+};
+
+// Thread 0's result; every thread of the block must call it.  A warp's
+// binary64 addition takes 16 cycles whether for one lane or 32, so an eighth of
+// the threads first adds eight values each.
+template <int P, int T>
+__device__ __forceinline__ double block_join(double x, double* buf) {
+  constexpr int kAdding = T / 8;
+  buf[threadIdx.x] = x;
   __syncthreads();
-  if (threadIdx.x < 32) x = warp_join<P>(red[threadIdx.x]);
+  if (threadIdx.x < kAdding) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) x = join<P>(x, buf[threadIdx.x + k * kAdding]);
+    x = warp_join<P>(x);
+  }
+  __syncthreads();
+  if (threadIdx.x < kAdding && (threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+  __syncthreads();
+  if (threadIdx.x == 0)
+#pragma unroll
+    for (int w = 1; w < kAdding / 32; ++w) x = join<P>(x, buf[w]);
+  __syncthreads();
+  return x;
+}
+
+// The same where only the first few lanes of each warp have something (zeros
+// in the others): fewer barriers.
+template <int P, int T>
+__device__ __forceinline__ double block_join_few(double x, int lanes, double* buf) {
+  static_assert(T == 1024, "one value of a lane for each warp");
+  x = warp_join<P>(x, lanes);
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+  __syncthreads();
+  if (threadIdx.x < 32) x = warp_join<P>(buf[threadIdx.x]);
   __syncthreads();
   return x;
 }
@@ -317,6 +348,46 @@ __device__ __forceinline__ double strided(int at, int count, int step, const Loa
   return acc;
 }
 
+// A run of values up to which a thread joins it, and a warp; above, a block.
+constexpr int kThreadRun = 16, kWarpRun = 1024;
+
+// load(lo), ..., load(lo + count - 1) joined, each thread's own run; every
+// thread of the block must call it.
+template <int P, int T, class Load>
+__device__ __forceinline__ double run_join(int lo, int count, const Load& load, Joining<T>& sh) {
+  double s = 0.0;
+  if (threadIdx.x == 0) sh.queued = 0;
+  if (count <= kThreadRun) s = strided<P>(0, count, 1, [&](int j) { return load(lo + j); });
+  unsigned mid = __ballot_sync(0xffffffffu, count > kThreadRun && count <= kWarpRun);
+  for (; mid != 0u; mid &= mid - 1u) {
+    const int l = __ffs(mid) - 1, from = __shfl_sync(0xffffffffu, lo, l), len = __shfl_sync(0xffffffffu, count, l);
+    double x = warp_join<P>(strided<P>(threadIdx.x & 31, len, 32, [&](int j) { return load(from + j); }));
+    x = __shfl_sync(0xffffffffu, x, 0);
+    if ((threadIdx.x & 31) == l) s = x;
+  }
+  if (!__syncthreads_or(count > kWarpRun)) return s;
+  int slot = 0;
+  if (count > kWarpRun) sh.queue[slot = atomicAdd(&sh.queued, 1)] = threadIdx.x;  // their order does not matter
+  __syncthreads();
+  const int n = sh.queued;
+  for (int q = 0; q < n; ++q) {
+    // the run of the queued thread, by way of the buffer that block_join uses
+    if (static_cast<int>(threadIdx.x) == sh.queue[q]) {
+      reinterpret_cast<int*>(sh.buf)[0] = lo;
+      reinterpret_cast<int*>(sh.buf)[1] = count;
+    }
+    __syncthreads();
+    const int from = reinterpret_cast<int*>(sh.buf)[0], len = reinterpret_cast<int*>(sh.buf)[1];
+    __syncthreads();
+    const double x = block_join<P, T>(strided<P>(threadIdx.x, len, T, [&](int j) { return load(from + j); }), sh.buf);
+    if (threadIdx.x == 0) sh.buf[0] = x;
+    __syncthreads();
+    if (count > kWarpRun && slot == q) s = sh.buf[0];
+    __syncthreads();
+  }
+  return s;
+}
+
 struct FinishArgs {
   GradPlan plan;
   int n, n_groups;
@@ -331,20 +402,13 @@ struct FinishArgs {
   int32_t* found;
 };
 
-// Groups up to which finish_kernel finishes them too.
-constexpr int kFinishGroups = 256;
-// Partials of a tensor up to which a thread adds them, and a warp; above, a block.
-constexpr int kThreadPartials = 16, kWarpPartials = 1024;
+// Tensors, and groups, that finish_kernel takes.
+constexpr int kFinishMost = 1024;
+static_assert(kFinishMost <= kFinishThreads, "a thread of finish_kernel has at most one tensor and one group");
 // Up to these one block finishes.
 constexpr int kBlockTensors = 128, kBlockPartials = 2048, kBlockParts = 256;
-// Tensors above which tensors_kernel makes their sums, and the partials up to
-// which 8 of its lanes add a tensor's; above, a block.
-constexpr int kFinishTensors = 1024, kOctetPartials = 512;
-static_assert(kFinishTensors <= kFinishThreads, "a thread of finish_kernel has at most one tensor");
-
-// What finish_kernel finds: the chunks' partials, the ranks' sums, or the
-// tensors' sums that tensors_kernel has left.
-enum Have { kPartials, kParts, kSums };
+// Partials up to which 8 lanes of tensors_kernel add a tensor's; above, a block.
+constexpr int kOctetPartials = 512;
 
 __device__ __forceinline__ void partials_of(const GradPlan& p, int i, int& lo, int& count) {
   const int j = __ldg(p.narrow_of + i);
@@ -422,10 +486,10 @@ __device__ __forceinline__ void write_group(const FinishArgs& a, int g, double s
 // each, or a thread to join the ranks' sums.
 template <int P, bool PARTS>
 __global__ void __launch_bounds__(256) tensors_kernel(const __grid_constant__ FinishArgs a) {
-  __shared__ double red[32];
+  __shared__ double buf[256];
   let_next_start();
-  wait_before();
   if (PARTS) {
+    wait_before();
     const int i = blockIdx.x * 256 + threadIdx.x;
     if (i >= a.n) return;
     const double s = join_parts<P>(a, i);
@@ -435,7 +499,8 @@ __global__ void __launch_bounds__(256) tensors_kernel(const __grid_constant__ Fi
   }
   const int base = blockIdx.x * 32, i = base + (threadIdx.x >> 3), lane = threadIdx.x & 7;
   int lo = 0, count = 0;
-  if (i < a.n) partials_of(a.plan, i, lo, count);
+  if (i < a.n) partials_of(a.plan, i, lo, count);  // of the plan: while the kernel before still runs
+  wait_before();
   const double factor = scale_power<P>(a);
   const auto finish = [&](int k, double s) {
     s *= factor;
@@ -448,88 +513,29 @@ __global__ void __launch_bounds__(256) tensors_kernel(const __grid_constant__ Fi
   for (int off = 4; off > 0; off >>= 1) s = join<P>(s, __shfl_down_sync(0xffffffffu, s, off, 8));
   if (lane == 0 && i < a.n && count <= kOctetPartials) finish(i, s);
   if (!__syncthreads_or(count > kOctetPartials)) return;
-  if (threadIdx.x < 32) red[threadIdx.x] = 0.0;  // block_join reads 32
   for (int k = base; k < base + 32 && k < a.n; ++k) {
     partials_of(a.plan, k, lo, count);
     if (count <= kOctetPartials) continue;
-    __syncthreads();
-    s = block_join<P>(strided<P>(threadIdx.x, count, 256, [&](int j) { return ld_behind(a.partials + lo + j); }), 32, red);
+    s = block_join<P, 256>(strided<P>(threadIdx.x, count, 256, [&](int j) { return ld_behind(a.partials + lo + j); }), buf);
     if (threadIdx.x == 0) finish(k, s);
   }
 }
 
-// One cluster of 8 blocks, or one block.  Of its W warps tensor i belongs to
-// warp i % W, lane i / W: long tensors, whose partials a warp or a block adds,
-// spread over the warps.  (kParts: as few warps as hold the tensors, since a
-// warp's binary64 addition takes 16 cycles for one lane too.)  Every thread adds its tensors to the sum over all;
-// the blocks' sums meet in distributed shared memory.  Then the groups.
-template <int P, Have HAVE>
-__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ FinishArgs a) {
-  __shared__ double red[kFinishThreads / 32], long_sums[kFinishThreads], block_total;
-  __shared__ int long_tensors[kFinishThreads], n_long;
+// The sum over all, from the blocks of a cluster, and its result (and that of
+// a single group, which is the same); `all`: this thread's part of it, where
+// lanes > 0 in that many lanes of a warp.  The barriers also order what the
+// blocks have written.
+template <int P>
+__device__ __forceinline__ void finish_all(const FinishArgs& a, double all, int lanes, Joining<kFinishThreads>& sh,
+                                           double* total, int blocks) {
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank());
-  const int blocks = gridDim.x, warps = blocks * (kFinishThreads / 32);
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) * blocks + rank;
-  let_next_start();
-  // what the plan says of this thread's tensor and group, while the kernel before still runs
-  const int i = HAVE == kParts ? threadIdx.x * blocks + rank : lane * warps + warp;
-  int lo = 0, count = 0, group_lo = 0, group_count = 0, first_member = 0;
-  if (HAVE == kPartials && i < a.n) partials_of(a.plan, i, lo, count);
-  if (warp < a.n_groups) {
-    group_lo = __ldg(a.plan.group_first + warp);
-    group_count = __ldg(a.plan.group_first + warp + 1) - group_lo;
-    if (lane < group_count) first_member = __ldg(a.plan.members + group_lo + lane);
-  }
-  if (threadIdx.x == 0) n_long = 0;
-  wait_before();
-  double all = 0.0;
-  if (HAVE == kSums) {
-    all = strided<P>(i, a.n, warps * 32, [&](int j) { return ld_behind(a.sums + j); });
-  } else {
-    if (HAVE == kParts) {
-      if (i < a.n) all = join_parts<P>(a, i);
-    } else {
-      if (count <= kThreadPartials) all = strided<P>(0, count, 1, [&](int j) { return ld_behind(a.partials + lo + j); });
-      unsigned mid = __ballot_sync(0xffffffffu, count > kThreadPartials && count <= kWarpPartials);
-      for (; mid != 0u; mid &= mid - 1u) {
-        const int l = __ffs(mid) - 1, from = __shfl_sync(0xffffffffu, lo, l), len = __shfl_sync(0xffffffffu, count, l);
-        double x = warp_join<P>(strided<P>(lane, len, 32, [&](int j) { return ld_behind(a.partials + from + j); }));
-        x = __shfl_sync(0xffffffffu, x, 0);
-        if (lane == l) all = x;
-      }
-      if (__syncthreads_or(count > kWarpPartials)) {
-        int slot = 0;
-        if (count > kWarpPartials) long_tensors[slot = atomicAdd(&n_long, 1)] = i;  // their order does not matter
-        __syncthreads();
-        const int k = n_long;
-        for (int q = 0; q < k; ++q) {
-          int from, len;
-          partials_of(a.plan, long_tensors[q], from, len);
-          const double x = block_join<P>(
-              strided<P>(threadIdx.x, len, kFinishThreads, [&](int j) { return ld_behind(a.partials + from + j); }), 32, red);
-          if (threadIdx.x == 0) long_sums[q] = x;
-        }
-        __syncthreads();
-        if (count > kWarpPartials) all = long_sums[slot];
-      }
-      all *= scale_power<P>(a);
-    }
-    if (i < a.n) {
-      a.sums[i] = all;
-      if (a.norms != nullptr) a.norms[i] = tensor_norm<P>(all);
-    } else {
-      all = 0.0;
-    }
-  }
-  if (a.results == nullptr) return;
-  const int lanes = HAVE == kParts ? 32 : min((a.n + warps - 1) / warps, 32);
-  all = block_join<P>(all, lanes, red);  // its barriers order the tensors' sums within the block
+  const int rank = static_cast<int>(cluster.block_rank()), lane = threadIdx.x & 31;
+  all = lanes > 0 ? block_join_few<P, kFinishThreads>(all, lanes, sh.buf) : block_join<P, kFinishThreads>(all, sh.buf);
   if (blocks > 1) {
-    if (threadIdx.x == 0) block_total = all;
-    cluster.sync();  // the blocks' totals, and the tensors' sums
+    if (threadIdx.x == 0) *total = all;
+    cluster.sync();
     if (rank == 0 && threadIdx.x < 32) {
-      all = lane < blocks ? *cluster.map_shared_rank(&block_total, lane) : 0.0;
+      all = lane < blocks ? *cluster.map_shared_rank(total, lane) : 0.0;
       all = warp_join<P>(all, blocks);
     }
   }
@@ -537,67 +543,108 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
     write_result<P>(a, a.n_groups, all, 0.0);
     if (a.n_groups == 1) write_group<P>(a, 0, all);
   }
-  if (a.n_groups > 1 && a.n_groups <= kFinishGroups) {
-    const auto sum_of = [&](int lo, int count, int from, int step) {
-      return strided<P>(from, count, step, [&](int j) { return ld_behind(a.sums + __ldg(a.plan.members + lo + j)); });
-    };
-    if (a.n / a.n_groups <= 512) {
-      for (int g = warp; g < a.n_groups; g += warps) {
-        const bool again = g != warp;
-        const int from = again ? __ldg(a.plan.group_first + g) : group_lo;
-        const int len = again ? __ldg(a.plan.group_first + g + 1) - from : group_count;
-        if (again) first_member = lane < len ? __ldg(a.plan.members + from + lane) : 0;
-        double x = lane < len ? ld_behind(a.sums + first_member) : 0.0;
-        x = warp_join<P>(join<P>(x, sum_of(from, len, lane + 32, 32)));
-        if (lane == 0) write_group<P>(a, g, x);
-      }
-    } else {
-      for (int g = rank; g < a.n_groups; g += blocks) {
-        const int lo = __ldg(a.plan.group_first + g), count = __ldg(a.plan.group_first + g + 1) - lo;
-        const double x = block_join<P>(sum_of(lo, count, threadIdx.x, kFinishThreads), 32, red);
-        if (threadIdx.x == 0) write_group<P>(a, g, x);
-      }
-    }
-  }
-  if (blocks > 1) cluster.sync();  // block_total is read until here
 }
 
-// Many groups, over all SMs: a thread each where they have few tensors, else
-// a warp each.
-template <int P, bool WARPS>
-__global__ void __launch_bounds__(128) groups_kernel(const __grid_constant__ FinishArgs a) {
+// Group g of a thread (-1: none): its tensors' sums joined, its result.
+template <int P>
+__device__ __forceinline__ void finish_group(const FinishArgs& a, int g, int lo, int count, Joining<kFinishThreads>& sh) {
+  const double s = run_join<P, kFinishThreads>(
+      lo, count, [&](int j) { return ld_behind(a.sums + __ldg(a.plan.members + j)); }, sh);
+  if (g >= 0) write_group<P>(a, g, s);
+}
+__device__ __forceinline__ void members_of(const GradPlan& p, int g, int& lo, int& count) {
+  lo = count = 0;
+  if (g < 0) return;
+  lo = __ldg(p.group_first + g);
+  count = __ldg(p.group_first + g + 1) - lo;
+}
+
+// Whether most groups' sums are a thread's work: then as few warps as hold the
+// groups make them, since 15 binary64 operations for a result take 240 cycles
+// of a warp for one group as for 32; else the groups spread over the warps.
+__device__ __forceinline__ bool few_members(const FinishArgs& a) { return a.n / a.n_groups < kThreadRun; }
+
+// Up to 1024 tensors and groups: one cluster of 8 blocks, or one block.  Of its
+// W warps tensor i belongs to warp i % W, lane i / W: long tensors, whose
+// partials a warp or a block adds, spread over the warps.  (PARTS: as few
+// warps as hold the tensors.)
+template <int P, bool PARTS>
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ FinishArgs a) {
+  __shared__ Joining<kFinishThreads> sh;
+  __shared__ double total;
+  const int blocks = gridDim.x, warps = blocks * (kFinishThreads / 32), rank = blockIdx.x;
+  const int spread = (threadIdx.x & 31) * warps + (threadIdx.x >> 5) * blocks + rank, dense = threadIdx.x * blocks + rank;
+  const int i = PARTS ? dense : spread, k = few_members(a) ? dense : spread;
+  const int g = a.n_groups > 1 && k < a.n_groups ? k : -1;
   let_next_start();
-  const int t = blockIdx.x * 128 + threadIdx.x, lane = threadIdx.x & 31;
-  const int g = WARPS ? t >> 5 : t;
+  // of the plan: while the kernel before still runs
+  int lo = 0, count = 0, group_lo, group_count;
+  if (!PARTS && i < a.n) partials_of(a.plan, i, lo, count);
+  members_of(a.plan, g, group_lo, group_count);
   wait_before();
-  if (g >= a.n_groups) return;
-  const int lo = __ldg(a.plan.group_first + g), count = __ldg(a.plan.group_first + g + 1) - lo;
-  const auto member = [&](int j) { return ld_behind(a.sums + __ldg(a.plan.members + lo + j)); };
-  if (WARPS) {
-    const double x = warp_join<P>(strided<P>(lane, count, 32, member));
-    if (lane == 0) write_group<P>(a, g, x);
+  double s = 0.0;
+  if (PARTS) {
+    if (i < a.n) s = join_parts<P>(a, i);
   } else {
-    write_group<P>(a, g, strided<P>(0, count, 1, member));
+    s = run_join<P, kFinishThreads>(lo, count, [&](int j) { return ld_behind(a.partials + j); }, sh) * scale_power<P>(a);
+  }
+  if (i < a.n) {
+    a.sums[i] = s;
+    if (a.norms != nullptr) a.norms[i] = tensor_norm<P>(s);
+  }
+  if (a.results == nullptr) return;
+  finish_all<P>(a, i < a.n ? s : 0.0, PARTS ? 0 : (a.n + warps - 1) / warps, sh, &total, blocks);
+  if (a.n_groups > 1) finish_group<P>(a, g, group_lo, group_count, sh);
+  if (blocks > 1) cg::this_cluster().sync();  // total is read until here
+}
+
+// More of either: the first cluster makes the result over all, the other
+// blocks those of `per` groups each.
+template <int P>
+__global__ void __launch_bounds__(kFinishThreads) groups_kernel(const __grid_constant__ FinishArgs a, int per) {
+  __shared__ Joining<kFinishThreads> sh;
+  __shared__ double total;
+  let_next_start();
+  if (blockIdx.x < kFinishBlocks) {
+    wait_before();
+    const int at = blockIdx.x * kFinishThreads + threadIdx.x;
+    const double s = strided<P>(at, a.n, kFinishBlocks * kFinishThreads, [&](int j) { return ld_behind(a.sums + j); });
+    finish_all<P>(a, s, 0, sh, &total, kFinishBlocks);
+    cg::this_cluster().sync();  // total is read until here
+  } else {
+    const int k = few_members(a) ? threadIdx.x : (threadIdx.x & 31) * (kFinishThreads / 32) + (threadIdx.x >> 5);
+    const int64_t at = static_cast<int64_t>(blockIdx.x - kFinishBlocks) * per + k;
+    const int g = k < per && at < a.n_groups ? static_cast<int>(at) : -1;
+    int lo, count;
+    members_of(a.plan, g, lo, count);
+    wait_before();
+    finish_group<P>(a, g, lo, count, sh);
   }
 }
 
 // -------------------------------------------------------------- launches
 template <int P, bool PARTS>
 static zero_status launch_finish(const FinishArgs& k, cudaStream_t st) {
+  const bool small = k.n <= kFinishMost, whole = small && (k.n_groups <= kFinishMost || k.results == nullptr);
   zero_status s = ZERO_OK;
-  if (k.n <= kFinishTensors) {
+  if (small) {
     const bool few = PARTS ? k.n <= kBlockParts : k.n <= kBlockTensors && k.plan.n_wide + k.plan.n_narrow <= kBlockPartials;
-    const int blocks = few ? 1 : kFinishBlocks;
-    s = launch_after("finish_kernel", finish_kernel<P, PARTS ? kParts : kPartials>, blocks, kFinishThreads, blocks, st, k);
+    const unsigned blocks = few ? 1 : kFinishBlocks;
+    FinishArgs f = k;
+    if (!whole) f.results = nullptr;
+    s = launch_after("finish_kernel", finish_kernel<P, PARTS>, blocks, kFinishThreads, blocks, st, f);
   } else {
     s = launch_after("tensors_kernel", tensors_kernel<P, PARTS>, one_pass_blocks(k.n, PARTS ? 256 : 32), 256, 1, st, k);
-    if (s == ZERO_OK && k.results != nullptr)
-      s = launch_after("finish_kernel", finish_kernel<P, kSums>, kFinishBlocks, kFinishThreads, kFinishBlocks, st, k);
   }
-  if (s != ZERO_OK || k.results == nullptr || k.n_groups <= kFinishGroups) return s;
-  if (k.n / k.n_groups < 16)
-    return launch_after("groups_kernel", groups_kernel<P, false>, one_pass_blocks(k.n_groups, 128), 128, 1, st, k);
-  return launch_after("groups_kernel", groups_kernel<P, true>, one_pass_blocks(k.n_groups, 4), 128, 1, st, k);
+  if (s != ZERO_OK || whole || k.results == nullptr) return s;
+  int per = 0;
+  unsigned blocks = kFinishBlocks;
+  if (k.n_groups > 1) {  // over the SMs, in whole clusters
+    per = k.n_groups <= 144 ? 1 : k.n_groups >= 144 * kFinishThreads ? kFinishThreads : (k.n_groups + 143) / 144;
+    const unsigned need = one_pass_blocks(k.n_groups, per);
+    blocks += (need + kFinishBlocks - 1) / kFinishBlocks * kFinishBlocks;
+  }
+  return launch_after("groups_kernel", groups_kernel<P>, blocks, kFinishThreads, kFinishBlocks, st, k, per);
 }
 
 template <int P>
