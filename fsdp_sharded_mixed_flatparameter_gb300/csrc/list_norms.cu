@@ -227,9 +227,9 @@ __device__ __forceinline__ double piece_sum(const void* p, int len, float2* red)
   if (P == ZERO_NORM_INF)
     return static_cast<double>(__uint_as_float(max_of<T>(g.template top<DT>(), reinterpret_cast<uint32_t*>(red))));
   const double sum = sum_norm<T>(g.acc, red);
-  // Squares below 2^-126 have lost bits: at most 2^-150 each, 2^-134 of a
-  // piece, so a sum of 2^-80 and more is right to 2^-54.  Magnitudes lose none.
-  const bool fits = sum < static_cast<double>(INFINITY) && (P == ZERO_NORM_1 || sum >= 0x1p-80);
+  // Squares below 2^-126 have lost bits: at most 2^-150 each, 2^-133 of a
+  // piece, so a sum of 2^-96 and more has lost at most 2^-37.  Magnitudes lose none.
+  const bool fits = sum < static_cast<double>(INFINITY) && (P == ZERO_NORM_1 || sum >= 0x1p-96);
   if (!any_of<T>(thread_of<T>() == 0 && !fits)) return sum;
   if (P == ZERO_NORM_2 && !any_of<T>(g.template any<DT>())) return 0.0;
   return scaled_sum<P, DT, T>(p, len, red);

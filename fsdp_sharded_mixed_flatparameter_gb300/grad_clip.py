@@ -10,7 +10,6 @@ waits for the host, so a whole step can be captured in a graph.
 from __future__ import annotations
 
 import math
-import numbers
 from typing import NamedTuple, Optional, Sequence, Union
 
 import numpy as np
@@ -36,16 +35,21 @@ class GradClip(GradTables):
     range(len(numels)) each tensor is clipped by its own norm; norm_type: 1, 2 or inf.
 
     After a launch, on the device: ``tensor_norms``, ``group_norms`` (float32), ``norm`` (0-d),
-    ``tensor_sums`` (float64, this rank's; ``joined_sums``: of gathered ones, all ranks'), ``results`` (a zero_norm_result per group) and
-    ``result``, the one over all with a coefficient of 1: what launch_step(norm_result=...) of
-    the optimizers takes after the grads have been clipped here.  The buffers are rewritten by
+    ``tensor_sums`` (float64, this rank's; ``joined_sums``: of gathered ones, all ranks'),
+    ``results`` (a zero_norm_result per group) and ``result``, the one over all with a
+    coefficient of 1: what launch_step(norm_result=...) of the optimizers takes after the grads have been clipped here.  The buffers are rewritten by
     each launch: launches of one object that overlap on the GPU race, and the object has to
-    outlive the graphs that captured it."""
+    outlive the graphs that captured it.
+
+    Making a GradClip and registering grads copies tables to the device and waits for the current
+    stream.  A launch waits for nothing, but for one with grads of its own on a stream that is
+    not the current one (its table is copied first).  wait=False: nothing is waited for, and the
+    clip is for the current stream alone."""
 
     def __init__(self, numels: Sequence[int], *, max_norm: Union[float, Sequence[float]] = math.inf,
-                 norm_type: float = 2.0, group_of: Optional[Sequence[int]] = None, device="cuda"):
+                 norm_type: float = 2.0, group_of: Optional[Sequence[int]] = None, device="cuda", wait: bool = True):
         self._init_tables(numels, device)
-        if isinstance(max_norm, numbers.Real):
+        if one_limit(max_norm):
             n_groups = 1 if group_of is None or len(group_of) == 0 else int(max(group_of)) + 1
         else:
             n_groups = len(max_norm)
@@ -55,10 +59,10 @@ class GradClip(GradTables):
         dev = self.device
         limits = self._limits(max_norm)
         not_in_capture(self._index)
-        self.plan = zs.zero_grad_plan(self.numels, group_of, n_groups, norm_type, dev)
+        self.plan = zs.zero_grad_plan(self.numels, group_of, n_groups, norm_type, dev, wait)
         n, g = len(self.numels), n_groups
-        self.max_norms = limits.to(dev)
-        self.buffers = zs.norm_buffers(self.plan, self.max_norms)
+        self.max_norms = zs._to_device(limits.numpy(), dev, wait)
+        self.buffers = zs.norm_buffers(self.plan, self.max_norms, wait)
         self.tensor_sums, self.joined_sums = self.buffers.sums, self.buffers.joined
         norms, self.results = self.buffers.norms, self.buffers.results
         self.tensor_norms, self.group_norms, self.norm = norms[:n], norms[n:n + g], norms[n + g]
@@ -89,7 +93,7 @@ class GradClip(GradTables):
 
     # ------------------------------------------------------------ limits
     def _limits(self, max_norm) -> torch.Tensor:
-        values = [max_norm] * self.n_groups if isinstance(max_norm, numbers.Real) else list(max_norm)
+        values = [max_norm] * self.n_groups if one_limit(max_norm) else list(max_norm)
         if len(values) != self.n_groups:
             raise ValueError(f"{len(values)} limits for {self.n_groups} groups")
         if any(math.isnan(v) or v < 0 for v in values):
@@ -110,17 +114,18 @@ class GradClip(GradTables):
         write=False: for norms only; a tensor may then be listed twice."""
         self._registered = self._entries(grads, out, write)
 
-    def _entries(self, grads, out, write):
+    def _entries(self, grads, out, write, wait=True):
         not_in_capture(self._index)
-        gl = zs.grad_list(self.plan, grads, out, write)
+        gl = zs.grad_list(self.plan, grads, out, write, wait)
         return gl, GradTable(gl.entries, self._current()), write
 
     def _current(self) -> int:
         return 0 if self._index is None else self._handle(None)  # host: only to be refused at a launch
 
-    def _list(self, grads, out, write):
+    def _list(self, grads, out, write, stream):
         if grads is not None:
-            return self._entries(grads, out, write)
+            here = self._index is not None and self._handle(stream) == self._current()
+            return self._entries(grads, out, write, wait=not here)
         if out is not None:
             raise ValueError("out needs grads")
         if self._registered is None:
@@ -151,7 +156,7 @@ class GradClip(GradTables):
             with torch.cuda.device(self._index):
                 return self.launch_sums(grads, scale=scale, loss_scale=loss_scale, stream=stream)
         sc, dsc, _ = self._scale_args(scale, loss_scale)
-        gl, table, _ = self._list(grads, None, False)
+        gl, table, _ = self._list(grads, None, False, stream)
         zs.zero_list_sums(gl, sc, self.buffers, self._on(stream, table), d_scale=dsc)
 
     def _elsewhere(self) -> bool:
@@ -182,9 +187,10 @@ class GradClip(GradTables):
             with torch.cuda.device(self._index):
                 return self._launch(clip, grads, out, scale, loss_scale, gathered, process_group, stream)
         n, dev = len(self.numels), self.plan.ints.device
-        if gathered is not None and (gathered.numel() == 0 or gathered.numel() % n or gathered.device != dev):
+        if gathered is not None and (gathered.numel() == 0 or gathered.numel() % n or gathered.device != dev
+                                     or (gathered.dim() > 1 and gathered.shape[-1] != n)):
             raise ValueError(f"gathered_sums must be [ranks, {n}] on {dev}")
-        gl, table, _ = self._list(grads, out, clip)
+        gl, table, _ = self._list(grads, out, clip, stream)
         raw = self._on(stream, table)
         sc, dsc, flag = self._scale_args(scale, loss_scale)
         if loss_scale is None:
@@ -220,16 +226,21 @@ _RESULT = np.dtype([("sqnorm", np.float64), ("norm", np.float64), ("clip_coef", 
 def clip_grad_norm_(grads: Sequence[Optional[torch.Tensor]], max_norm: float, norm_type: float = 2.0, *,
                     scale: float = 1.0, stream=None) -> torch.Tensor:
     """Clip `grads` in place by the norm of all of them and return that norm (a 0-d float32
-    device tensor) without waiting.  Where it is not finite nothing is written.  For a
-    loop, a GradClip with registered grads spares the table's copy at each call."""
+    device tensor) without waiting, on the current stream or on `stream`.  Where it is not finite
+    nothing is written.  For a loop, a GradClip with registered grads spares the tables."""
     grads = list(grads)
     some = [g for g in grads if g is not None]
     if not some:
         raise ValueError("no grads")
     clip = GradClip([0 if g is None else g.numel() for g in grads], max_norm=max_norm, norm_type=norm_type,
-                    device=some[0].device)
+                    device=some[0].device, wait=stream is not None)
     clip.launch(grads, scale=scale, stream=stream)
     return clip.norm
+
+
+def one_limit(max_norm) -> bool:
+    """Whether max_norm is a number and not one for each group."""
+    return not hasattr(max_norm, "__len__") or getattr(max_norm, "ndim", 1) == 0
 
 
 def not_in_capture(index) -> None:

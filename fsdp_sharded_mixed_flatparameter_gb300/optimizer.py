@@ -451,7 +451,8 @@ class FlatShardAdamW(GradTables):
         ordered on `stream` like the kernels, whichever stream that is.
 
         clip: a grad_clip() of this optimizer, in place of the one clip over all (whose max_norm is
-        not used then): its groups are clipped in the grad buffer, the step is skipped where
+        not used then): its groups are clipped in the grad buffer, by their norms over the process
+        group's ranks (without one: over this rank's buffer alone), the step is skipped where
         its norm over all tensors is not finite, and the result is that norm's, with a
         coefficient of 1 (clip.finish() gives the groups')."""
         if clip is not None:

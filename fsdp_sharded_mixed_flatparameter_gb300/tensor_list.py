@@ -11,14 +11,13 @@ fp32 moments the result is FlatShardAdamW's bit for bit, tensor by tensor.
 from __future__ import annotations
 
 import math
-import numbers
 from typing import List, Optional, Sequence, Tuple, Union
 
 import numpy as np
 import torch
 
 from . import zero_shard as zs
-from .grad_clip import GradClip, not_in_capture
+from .grad_clip import GradClip, not_in_capture, one_limit
 from .optimizer import GradTables, torch_stream
 
 _DEFAULTS = ("lr", "betas", "eps", "weight_decay")
@@ -35,7 +34,7 @@ class TensorListAdamW(GradTables):
 
     max_norm: the limit of the norm over all grads, or a limit for each group (inf: not clipped):
     then every group's grads are clipped by the group's own norm (``clip``, a GradClip, has the
-    norms and limits; the grads themselves stay as they are), the step is skipped where the norm
+    norms, and its set_max_norm() changes the limits; the grads themselves stay as they are), the step is skipped where the norm
     over all is not finite, and step() gives that norm with a coefficient of 1.
 
     The moments live in storages of this object, tensor i's at elements offsets[i] ..
@@ -67,7 +66,7 @@ class TensorListAdamW(GradTables):
         if not 1 <= len(self._groups) <= zs.LIST_MAX_GROUPS:
             raise ValueError(f"1 to {zs.LIST_MAX_GROUPS} groups")
         self._hp = zs.list_groups(self._groups)
-        per_group = not isinstance(max_norm, numbers.Real)
+        per_group = not one_limit(max_norm)
         if per_group and len(max_norm) != len(self._groups):
             raise ValueError(f"{len(max_norm)} limits for {len(self._groups)} groups")
         columns, numels, lowp_dtype = zs.list_masters(self.masters, self.lowp, group_of)

@@ -907,9 +907,19 @@ _GRAD_ENTRY = np.dtype([(nm, np.uint64 if ct is ctypes.c_void_p else np.int64 if
                         for nm, ct in zero_grad_entry._fields_])
 
 
+def _to_device(a: np.ndarray, device, wait: bool) -> torch.Tensor:
+    """A copy on the device.  wait: done when this returns, so that any stream may read it; else
+    in the order of the current stream, without waiting for what runs there."""
+    t = torch.from_numpy(a)
+    if wait or torch.device(device).type != "cuda":
+        return t.to(device)
+    return t.pin_memory().to(device, non_blocking=True)
+
+
 def zero_grad_plan(numels: Sequence[int], group_of: Optional[Sequence[int]], n_groups: int, norm_type: float,
-                   device) -> GradPlan:
-    """The plan of a list with these sizes and groups (group_of None: all in group 0), copied to the device."""
+                   device, wait: bool = True) -> GradPlan:
+    """The plan of a list with these sizes and groups (group_of None: all in group 0), copied to the
+    device.  wait=False: for the current stream alone, here and in what follows."""
     p = _NORM_TYPES.get(float(norm_type))
     if p is None:
         raise ValueError(f"norm_type must be 1, 2 or inf, got {norm_type}")
@@ -924,7 +934,7 @@ def zero_grad_plan(numels: Sequence[int], group_of: Optional[Sequence[int]], n_g
     head = zero_grad_list()
     _check(lib().zero_grad_plan(sizes.ctypes.data, None if groups is None else groups.ctypes.data, n, n_groups,
                                 ints.ctypes.data, ctypes.byref(head)))
-    d_ints = torch.from_numpy(ints).to(device)
+    d_ints = _to_device(ints, device, wait)
     head.d_plan, head.norm_type = d_ints.data_ptr(), p
     return GradPlan(d_ints, sizes, groups, int(n_groups), head)
 
@@ -971,7 +981,7 @@ def _addresses_of(tensors: Sequence[Optional[torch.Tensor]], sizes: List[int], d
 
 
 def grad_list(plan: GradPlan, grads: Sequence[Optional[torch.Tensor]], out: Optional[Sequence] = None,
-              write: bool = True) -> GradList:
+              write: bool = True, wait: bool = True) -> GradList:
     """Check a list of grads (None: no grad, reads as zeros) and copy it to the device.  out:
     where the clipped grads go, per tensor a buffer or None (that tensor is not written);
     out=None with write: in place.  Every tensor is f32, bf16 or f16, fills one run
@@ -996,7 +1006,7 @@ def grad_list(plan: GradPlan, grads: Sequence[Optional[torch.Tensor]], out: Opti
             if g.shape != y.shape or g.stride() != y.stride():
                 raise ValueError(f"out[{i}] is not laid out as its grad")
     entries["src"], entries["dst"], entries["src_dtype"], entries["dst_dtype"] = src, dst, sdt, ddt
-    return _checked_list(plan, entries)
+    return _checked_list(plan, entries, wait)
 
 
 def flat_grad_list(plan: GradPlan, flat: torch.Tensor, starts: np.ndarray) -> GradList:
@@ -1013,7 +1023,7 @@ def flat_grad_list(plan: GradPlan, flat: torch.Tensor, starts: np.ndarray) -> Gr
     return _checked_list(plan, entries)
 
 
-def _checked_list(plan: GradPlan, entries: np.ndarray) -> GradList:
+def _checked_list(plan: GradPlan, entries: np.ndarray, wait: bool = True) -> GradList:
     entries["numel"] = plan.numels
     if plan.groups is not None:
         entries["group"] = plan.groups
@@ -1028,7 +1038,7 @@ def _checked_list(plan: GradPlan, entries: np.ndarray) -> GradList:
                                     (size * bytes_of[entries["src_dtype"]])[read]])
         if _overlaps(at, ends, np.arange(len(at)) < int(written.sum())):
             raise ValueError("a grad that is written overlaps another tensor of the list (is one listed twice?)")
-    d_entries = torch.from_numpy(entries.view(np.uint8)).to(plan.ints.device)
+    d_entries = _to_device(entries.view(np.uint8), plan.ints.device, wait)
     elsewhere = (entries["dst"] != 0) & (entries["dst"] != entries["src"])
     return GradList(d_entries, plan, _list_ref(plan, d_entries.data_ptr(), int(not elsewhere.any())))
 
@@ -1061,8 +1071,8 @@ class NormBuffers(NamedTuple):
     addresses: Optional[tuple]  # ws, its bytes, sums, joined, max_norms, norms, results, found; None: host memory
 
 
-def norm_buffers(plan: GradPlan, max_norms: torch.Tensor) -> NormBuffers:
-    """Buffers for lists of this plan; max_norms: the groups' limits (float64, on the device)."""
+def norm_buffers(plan: GradPlan, max_norms: torch.Tensor, wait: bool = True) -> NormBuffers:
+    """Buffers for lists of this plan, zeros; max_norms: the groups' limits (float64, on the device)."""
     dev, n, g = plan.ints.device, len(plan.numels), plan.n_groups
     if max_norms.dtype != torch.float64 or max_norms.numel() != g or max_norms.device != dev or not max_norms.is_contiguous():
         raise ValueError(f"max_norms must be {g} float64 on {dev}")
@@ -1071,6 +1081,8 @@ def norm_buffers(plan: GradPlan, max_norms: torch.Tensor) -> NormBuffers:
     norms = torch.zeros(n + g + 1, dtype=torch.float32, device=dev)
     results = torch.zeros((g + 1) * NORM_RESULT_BYTES, dtype=torch.uint8, device=dev)
     found = torch.zeros(1, dtype=torch.int32, device=dev)
+    if wait and ws.is_cuda:  # the zeros are there before a launch on any stream
+        torch.cuda.current_stream(dev).synchronize()
     addresses = (ws.data_ptr(), ws.numel(), sums.data_ptr(), joined.data_ptr(), max_norms.data_ptr(), norms.data_ptr(),
                  results.data_ptr(), found.data_ptr()) if ws.is_cuda else None
     return NormBuffers(plan, ws, sums, joined, max_norms, norms, results, found, addresses)

@@ -2,7 +2,7 @@
 
 Tolerances.  Sums: a thread adds at most 131072 / 128 / 2 = 512 pairs, the j-th with a tail l of at most j x 2^-24 of the
 sum, whose addition is rounded by 2^-24 of it: 512^2 / 2 x 2^-48 = 4.66e-10 at worst, the rest of the tree a few 2^-48
-more: SUM = 5e-10 (half of that for a root).  Binary32 outputs add 2^-24.  A clipped grad: the coefficient, scale x coefficient and the
+more, and squares of tiny values up to 2^-37: SUM = 5e-10 (half of that for a root).  Binary32 outputs add 2^-24.  A clipped grad: the coefficient, scale x coefficient and the
 product are each rounded to binary32, 3 x 2^-24 (and their cross terms), then eps / 2 of a 16-bit type; where the value is
 subnormal there, half its type's least step."""
 import math
@@ -159,6 +159,8 @@ def test_norms_of_extreme_values(dtype, p):
         "subnormal": [2.0 ** -24 if dtype == F16 else 2.0 ** -133] * 700,
         "tiny": [2.0 ** -14 if dtype == F16 else 1e-30] * 9000,
         "tiny and one": [2.0 ** -14 if dtype == F16 else 1e-30] * 9000 + [1.0],
+        "at the border": [2.0 ** -24 if dtype == F16 else 2.0 ** -54] * 4000 + [2.0 ** -24 if dtype == F16 else 2.0 ** -70] * 4000,
+        "below it": [2.0 ** -24 if dtype == F16 else 2.0 ** -55] * 4000,
         "zero": [0.0, -0.0] * 3000,
         "inf": [1.0] * 20 + [-math.inf] + [1.0] * 5000,
         "nan": [1.0] * 5000 + [math.nan],
@@ -505,6 +507,33 @@ def test_launches_on_another_stream():
     assert float(n) == pytest.approx(0.5, rel=1e-3)
 
 
+def test_what_waits_and_what_does_not():
+    xs = [x for x in tensors("mixed", 1) if x.numel()]
+    sizes = [x.numel() for x in xs]
+    before = [x.clone() for x in xs]
+    s = math.sqrt(sums_of(before, 2).sum())
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):  # made there, used here: its tables and zeros are in place
+        torch.cuda._sleep(20_000_000)
+        c = pkg.GradClip(sizes, max_norm=0.5)
+        assert side.query()
+    assert c.clip_(xs).norm == pytest.approx(s, rel=SUM) and int(c.found_nonfinite) == 0
+    for x, b in zip(xs, before):
+        x.copy_(b)
+    pkg.clip_grad_norm_([x.clone() for x in xs], 0.5)  # pinned memory is there from now on
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # a backward pass that still runs
+    n = pkg.clip_grad_norm_(xs, 0.5)
+    busy = not torch.cuda.current_stream().query()
+    assert busy and float(n) == pytest.approx(s, rel=SUM + ULP)
+    for x, b in zip(xs, before):
+        check_clipped(x, b, 0.5 / (s + 1e-6), x.dtype)
+    torch.cuda._sleep(200_000_000)
+    c.launch(xs)
+    assert not torch.cuda.current_stream().query()
+    assert c.finish().norm == pytest.approx(0.5, rel=1e-2)
+
+
 def test_refuses_at_launch():
     x = torch.zeros(9, device="cuda")
     c = pkg.GradClip([4, 5])
@@ -516,6 +545,8 @@ def test_refuses_at_launch():
             c.launch(bad)
     with pytest.raises(ValueError, match="gathered_sums"):
         c.launch([x[:4], x[4:]], gathered_sums=torch.zeros(3, dtype=torch.float64, device="cuda"))
+    with pytest.raises(ValueError, match="gathered_sums"):  # [tensors, ranks]
+        c.launch_norms([x[:4], x[4:]], gathered_sums=torch.zeros(2, 3, dtype=torch.float64, device="cuda"))
     with pytest.raises(ValueError, match="float64"):
         c.launch([x[:4], x[4:]], gathered_sums=torch.zeros(2, device="cuda"))
     other = pkg.GradClip([9])

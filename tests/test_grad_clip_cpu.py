@@ -255,6 +255,13 @@ def test_optimizer_refuses_a_clip_over_another_buffer():
         pkg.FlatShardAdamW([8], device="cpu", grad_buffer=False).grad_clip()
 
 
+def test_one_limit_or_one_for_each_group():
+    for one in (1, 1.0, np.float32(1), np.array(1.0), torch.tensor(1.0), math.inf):
+        assert pkg.GradClip([4, 5], device="cpu", group_of=[0, 1], max_norm=one).max_norms.tolist() == [float(one)] * 2
+    for each in ([1, 2.0], (1.0, 2.0), np.array([1.0, 2.0]), torch.tensor([1.0, 2.0])):
+        assert pkg.GradClip([4, 5], device="cpu", group_of=[0, 1], max_norm=each).max_norms.tolist() == [1.0, 2.0]
+
+
 def test_list_steps_with_clips_refuse():
     L = zs.lib()
     buf = ctypes.cast(ctypes.create_string_buffer(4096 + 64), ctypes.c_void_p).value
