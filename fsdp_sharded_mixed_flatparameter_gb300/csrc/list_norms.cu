@@ -428,12 +428,11 @@ __device__ __forceinline__ double join_parts(const FinishArgs& a, int i) {
   return strided<P>(0, a.n_parts, 1, [&](int r) { return ld_behind(row + static_cast<int64_t>(r) * a.n); });
 }
 
-// Roots and quotients from binary32 ones and binary64 residuals: __dsqrt_rn and
-// __ddiv_rn take some 25 dependent binary64 instructions each, half a
-// microsecond where one thread works, and most of the time for thousands.
-//
-// The root of s: y + rest / 2y twice; after the first step the error is
-// (2^-24)^2 / 2 of it, after the second what the last addition rounds.
+// Roots and quotients: binary32 ones corrected by Newton's method with binary64
+// residuals, where the chain of binary64 operations of __dsqrt_rn and __ddiv_rn
+// is much of the time that one thread takes for a result (a small list's norms 8.4
+// against 7.8 us).  The root of s: y + (s - y y) / 2y twice; after the first step the
+// error is (2^-24)^2 / 2 of it, after the second what the last addition rounds.
 __device__ __forceinline__ bool in_float_range(float f) { return f > 0x1p-100f && f < 0x1p100f; }
 __device__ __forceinline__ double root(double s) {
   const float f = __double2float_rn(s);
@@ -560,8 +559,8 @@ __device__ __forceinline__ void members_of(const GradPlan& p, int g, int& lo, in
 }
 
 // Whether most groups' sums are a thread's work: then as few warps as hold the
-// groups make them, since 15 binary64 operations for a result take 240 cycles
-// of a warp for one group as for 32; else the groups spread over the warps.
+// groups make them, since a result's binary64 operations take a warp as long
+// for one group as for 32; else the groups spread over the warps.
 __device__ __forceinline__ bool few_members(const FinishArgs& a) { return a.n / a.n_groups < kThreadRun; }
 
 // Up to 1024 tensors and groups: one cluster of 8 blocks, or one block.  Of its

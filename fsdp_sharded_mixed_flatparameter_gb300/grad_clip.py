@@ -70,6 +70,7 @@ class GradClip(GradTables):
         self.found_nonfinite = self.buffers.found
         self._home = self._current()  # the stream whose order the buffers' memory follows
         self.shard: Optional[torch.Tensor] = None
+        self._kept: tuple = ()
 
     @classmethod
     def of_shard(cls, numels: Sequence[int], grad: torch.Tensor, start: int, **kw) -> "GradClip":
@@ -110,9 +111,11 @@ class GradClip(GradTables):
         """Fix the grads once: per tensor an f32, bf16 or f16 tensor, or None (reads as zeros).
         out: other buffers for the clipped grads (None for a tensor: it is not written; a
         tensor without a grad gets zeros); without it they are clipped in place.  A launch
-        without grads then does no work per tensor on the host, and can be captured.
+        without grads then does no work per tensor on the host, and can be captured.  The
+        tensors are kept alive until others are registered.
         write=False: for norms only; a tensor may then be listed twice."""
         self._registered = self._entries(grads, out, write)
+        self._kept = (list(grads), None if out is None else list(out))
 
     def _entries(self, grads, out, write, wait=True):
         not_in_capture(self._index)
@@ -148,6 +151,16 @@ class GradClip(GradTables):
                 t.record_stream(st)
         return raw
 
+    def _used_on(self, raw: int, *lists) -> None:
+        """Tensors of this launch that are read or written on a stream other than the current one:
+        their memory is not given out again before that is done."""
+        if self._index is None or raw == self._current():
+            return
+        st = torch_stream(raw, self.device)
+        for t in (t for ts in lists if ts is not None for t in ts):
+            if t is not None:
+                t.record_stream(st)
+
     # ------------------------------------------------------------ launch
     def launch_sums(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, scale: float = 1.0,
                     loss_scale=None, stream=None) -> None:
@@ -157,7 +170,9 @@ class GradClip(GradTables):
                 return self.launch_sums(grads, scale=scale, loss_scale=loss_scale, stream=stream)
         sc, dsc, _ = self._scale_args(scale, loss_scale)
         gl, table, _ = self._list(grads, None, False, stream)
-        zs.zero_list_sums(gl, sc, self.buffers, self._on(stream, table), d_scale=dsc)
+        raw = self._on(stream, table)
+        self._used_on(raw, grads)
+        zs.zero_list_sums(gl, sc, self.buffers, raw, d_scale=dsc)
 
     def _elsewhere(self) -> bool:
         """Whether another device than the clip's is the current one."""
@@ -192,6 +207,8 @@ class GradClip(GradTables):
             raise ValueError(f"gathered_sums must be [ranks, {n}] on {dev}")
         gl, table, _ = self._list(grads, out, clip, stream)
         raw = self._on(stream, table)
+        if grads is not None or gathered is not None:
+            self._used_on(raw, grads, out, None if gathered is None else [gathered])
         sc, dsc, flag = self._scale_args(scale, loss_scale)
         if loss_scale is None:
             flag = None  # the buffers' own

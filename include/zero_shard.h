@@ -733,8 +733,11 @@ zero_status zero_adamw_prepare_list_device(const zero_adamw_hparams* d_hp, int32
  * |s|^p multiplies the sums, not the elements.  The sums are right to 5e-10
  * relative at worst and 1e-14 in practice, for any finite x (chunks whose
  * squares leave the binary32 range are summed again, scaled by a power of
- * two); an infinite x makes the norms infinite and a NaN makes them NaN.  No y is written at all where the
- * norm over all tensors is not finite: the step is to be skipped.
+ * two); an infinite x makes the norms infinite and a NaN makes them NaN.  No y
+ * is written at all where the norm over all tensors is not finite: the step is
+ * to be skipped.  The kernels of a call, and of calls that follow one another,
+ * start while the one before ends (programmatic dependent launches), and read
+ * what it wrote when it has ended: the stream's order is kept.
  * A step is zero_list_norms, which also clips; across ranks zero_list_sums, an
  * all-gather of the sums in rank order, zero_sums_norms and zero_list_clip.
  * --------------------------------------------------------------------- */

@@ -364,8 +364,9 @@ def test_more_chunks_than_a_warp_adds():
         assert bool((x == (torch.tensor(0.5) * r.coefs[g]).to(BF16).item()).all())
 
 
-@pytest.mark.parametrize("n,groups", [(1023, 256), (1025, 257), (5200, 300), (9000, 1), (9000, 2), (20000, 20000)])
-def test_thousands_of_tensors(n, groups):
+@pytest.mark.parametrize("n,groups,skewed", [(1023, 256, False), (1025, 257, False), (5200, 300, False), (9000, 1, False), (9000, 2, False), (20000, 20000, False),
+                                             (1000, 900, True), (1024, 40, True), (1030, 1030, True), (6000, 500, True), (9000, 300, True), (700, 1500, False)])
+def test_thousands_of_tensors(n, groups, skewed):
     """The counts at which the work is split another way; two long tensors among them where the list is long."""
     rng = np.random.default_rng(n)
     sizes = [int(k) for k in rng.integers(0, 60, n)]
@@ -375,6 +376,8 @@ def test_thousands_of_tensors(n, groups):
     flat = torch.randint(-8, 9, (total,), generator=torch.Generator("cuda").manual_seed(n), device="cuda", dtype=torch.int32).to(BF16)
     xs = list(flat.split(sizes))
     of = rng.integers(0, groups, n)
+    if skewed:  # one group has most tensors
+        of = np.where(rng.random(n) < 0.9, groups // 3, of)
     of[0] = groups - 1
     limits = list(rng.uniform(1.0, 100.0, groups))
     # sums of squares of small whole numbers are exact
@@ -505,6 +508,31 @@ def test_launches_on_another_stream():
         n = pkg.clip_grad_norm_(xs, 0.25)
     side.synchronize()
     assert float(n) == pytest.approx(0.5, rel=1e-3)
+
+
+def test_memory_of_a_launch_on_another_stream_is_not_given_out():
+    n = 1 << 20
+    c = pkg.GradClip([n], max_norm=0.5)
+    side = torch.cuda.Stream()
+    x, y = torch.full((n,), 2.0, device="cuda"), torch.empty(n, dtype=BF16, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    c.launch([x], out=[y], stream=side)
+    gathered = torch.full((2, 1), 9.0, dtype=torch.float64, device="cuda")
+    at = {x.data_ptr(), y.data_ptr(), gathered.data_ptr()}
+    d = pkg.GradClip([n])
+    d.launch_norms([x], gathered_sums=gathered, stream=side)
+    del x, y, gathered
+    new = [torch.full((n,), 7.0, device="cuda"), torch.zeros(n, dtype=BF16, device="cuda"), torch.zeros((2, 1), dtype=torch.float64, device="cuda")]
+    assert not at & {t.data_ptr() for t in new}
+    assert c.finish(side).norm == 2.0 * 1024 and d.finish(side).norm == math.sqrt(18.0)
+    # registered ones stay
+    z = torch.full((n,), 3.0, device="cuda")
+    c.register_grads([z])
+    del z
+    torch.full((n,), 7.0, device="cuda")
+    assert c.clip_().norm == 3.0 * 1024
 
 
 def test_what_waits_and_what_does_not():

@@ -119,6 +119,7 @@ def test_limits_per_group_refused():
         zs.zero_adamw_list(a._list, a.device_table(grads(0, torch.float32))[0], torch.float32, 1.0, a._hp, 1, None, clips=True)
     xs = grads(0, torch.float32)
     with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        xs[0].mul_(1.0)
         with pytest.raises(RuntimeError, match="before the capture"):
             a.launch_step(xs)
     assert a.step(xs).finite and a.t == 1
