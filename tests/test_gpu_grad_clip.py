@@ -677,6 +677,59 @@ def test_a_shards_step_with_a_clip_per_group(bits, capturable):
     assert not a.step(clip=clip).finite and a.t == 3 and torch.equal(a.master, before)
 
 
+@pytest.mark.parametrize("grad_range", ["shard", "full"])
+def test_a_captured_shard_step_with_a_clip(grad_range):
+    """Flatten, clip by groups and AdamW of a rank's shard (ZeRO-2 and ZeRO-1), captured and replayed against eager steps."""
+    total = sum(SIZES)
+    s, e = zs.zero_shard_range(total, 2, 1)
+    master = torch.randn(total, generator=gen(8))[s:e].cuda()
+    kw = dict(world_size=2, rank=1, lr=1e-2, device="cuda", grad_range=grad_range, capturable=True)
+    a, b = (pkg.FlatShardAdamW(SIZES, master=master.clone(), **kw) for _ in range(2))
+    of = [i % 2 for i in range(len(SIZES))]
+    ca, cb = (o.grad_clip(group_of=of, max_norm=[0.05, 0.5]) for o in (a, b))
+    xs = tensors(BF16)
+    a.register_grads(xs)
+    b.register_grads(xs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.flatten(accumulate=False, scale=0.5, fuse_norm=True)
+        a.launch_clip(ca)
+    for k in range(3):
+        for i, x in enumerate(xs):
+            x.copy_((torch.randn(x.numel(), generator=gen(90 * k + i)) * 0.02).cuda())
+        if k == 1:
+            a.grad.fill_(math.nan)  # flatten writes it anew
+            xs[13][5] = math.inf
+        graph.replay()
+        b.flatten(accumulate=False, scale=0.5)
+        r = b.step(clip=cb)
+        assert torch.equal(ca.results.view(torch.int32), cb.results.view(torch.int32)) and r.finite == (k != 1)
+        assert torch.equal(a.master, b.master) and torch.equal(a.exp_avg, b.exp_avg) and torch.equal(a.lowp, b.lowp)
+    assert a.t == b.t == 2
+
+
+def test_two_clips_at_once():
+    sizes = [1 << 20, 5, 300000, 16384]
+    data = [[torch.randn(n, generator=gen(n + k)).to(TYPES[k]).cuda() for n in sizes] for k in range(3)]
+    want = []
+    for xs in data:
+        one = [x.clone() for x in xs]
+        c = pkg.GradClip(sizes, max_norm=[3.0, 1.0], group_of=[0, 1, 1, 0])
+        for _ in range(6):
+            c.launch(one, scale=1.5)
+        want.append((one, c.results.clone()))
+    torch.cuda.synchronize()
+    clips, streams = [pkg.GradClip(sizes, max_norm=[3.0, 1.0], group_of=[0, 1, 1, 0]) for _ in data], [torch.cuda.Stream() for _ in data]
+    for c, xs in zip(clips, data):
+        c.register_grads(xs)
+    for _ in range(6):
+        for c, st in zip(clips, streams):
+            c.launch(scale=1.5, stream=st)
+    torch.cuda.synchronize()
+    for c, xs, (one, results) in zip(clips, data, want):
+        assert torch.equal(c.results, results) and all(torch.equal(x, y) for x, y in zip(xs, one))
+
+
 def test_a_list_step_after_a_clip_in_one_graph():
     """Unscale and clip fp16 grads into fp32 by groups, then AdamW over the list, captured once."""
     sizes = [300, 7, 4100]
