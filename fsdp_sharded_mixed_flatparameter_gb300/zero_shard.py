@@ -1072,14 +1072,16 @@ class NormBuffers(NamedTuple):
 
 
 def norm_buffers(plan: GradPlan, max_norms: torch.Tensor, wait: bool = True) -> NormBuffers:
-    """Buffers for lists of this plan, zeros; max_norms: the groups' limits (float64, on the device)."""
+    """Buffers for lists of this plan, zeros (wait=False: as a launch fills them); max_norms: the
+    groups' limits (float64, on the device)."""
     dev, n, g = plan.ints.device, len(plan.numels), plan.n_groups
     if max_norms.dtype != torch.float64 or max_norms.numel() != g or max_norms.device != dev or not max_norms.is_contiguous():
         raise ValueError(f"max_norms must be {g} float64 on {dev}")
     ws = torch.empty(max(zero_list_norms_workspace_bytes(plan), 8), dtype=torch.uint8, device=dev)
-    sums, joined = (torch.zeros(n, dtype=torch.float64, device=dev) for _ in range(2))
-    norms = torch.zeros(n + g + 1, dtype=torch.float32, device=dev)
-    results = torch.zeros((g + 1) * NORM_RESULT_BYTES, dtype=torch.uint8, device=dev)
+    new = torch.zeros if wait else torch.empty
+    sums, joined = (new(n, dtype=torch.float64, device=dev) for _ in range(2))
+    norms = new(n + g + 1, dtype=torch.float32, device=dev)
+    results = new((g + 1) * NORM_RESULT_BYTES, dtype=torch.uint8, device=dev)
     found = torch.zeros(1, dtype=torch.int32, device=dev)
     if wait and ws.is_cuda:  # the zeros are there before a launch on any stream
         torch.cuda.current_stream(dev).synchronize()

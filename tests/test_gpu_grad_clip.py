@@ -490,6 +490,44 @@ def test_back_to_back_launches_see_each_other():
     assert not torch.equal(first, want)
 
 
+def test_captured_behind_copies_fills_and_other_streams():
+    """What a launch follows in a graph: a copy, a fill, a join of another stream, another launch."""
+    sizes = [70000, 300]
+    y = torch.randn(70300, generator=gen(2)).cuda()
+    x, host = torch.zeros_like(y), torch.zeros(70300).pin_memory()
+    c, d = pkg.GradClip(sizes, max_norm=1.0), pkg.GradClip(sizes, max_norm=0.5)
+    for k in (c, d):
+        k.register_grads(list(x.split(sizes)))
+    norms = torch.zeros(4, device="cuda")
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        x.copy_(y)
+        c.launch_norms()
+        norms[0].copy_(c.norm)
+        x.zero_()
+        d.launch_norms()
+        norms[1].copy_(d.norm)
+        x.copy_(host, non_blocking=True)
+        c.launch()
+        norms[2].copy_(c.norm)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            x.mul_(3.0)
+        torch.cuda.current_stream().wait_stream(side)
+        d.launch()
+        norms[3].copy_(d.norm)
+    for k in range(3):
+        host.copy_(torch.randn(70300, generator=gen(k)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = norms.tolist()
+        assert got[0] == pytest.approx(float(y.double().norm()), rel=2 * ULP) and got[1] == 0.0
+        assert got[2] == pytest.approx(float(host.double().norm()), rel=2 * ULP)
+        # c left a norm of 1 - 1e-6 / |host| (and the elements' roundings, 2 x 2^-24 each), tripled
+        assert got[3] == pytest.approx(3.0, rel=1e-6) and float(x.double().norm()) == pytest.approx(0.5, rel=3e-6)
+
+
 def test_launches_on_another_stream():
     xs = tensors("mixed", 1)
     before = [x.clone() for x in xs]
