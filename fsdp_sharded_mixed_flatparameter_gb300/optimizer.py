@@ -177,6 +177,9 @@ class FlatShardAdamW(GradTables):
         self.start, self.end = zs.zero_shard_range(self.total, world_size, rank)
         self.n = self.end - self.start
         self.glo, self.ghi = (0, self.total) if grad_range == "full" else (self.start, self.end)
+        # whether the ranks hold grads of their own shards, whose norms they join: the same on every
+        # rank (rank 0's whole grad starts where its shard does, and may be all of it)
+        self._shard_grads = grad_range == "shard" or world_size == 1
         self.capturable = capturable
         self._hp = [float(lr), float(betas[0]), float(betas[1]), float(eps), float(weight_decay)]
         self.max_norm = max_norm
@@ -318,7 +321,7 @@ class FlatShardAdamW(GradTables):
         """Reduce the ranks' received chunks of this shard into the fp32 shard grad (ZeRO-2/3,
         zero_reduce_chunks): chunks is [world_size, chunk] in rank order, the first n of each
         row are this shard's values; fuse_norm and loss_scale as for flatten()."""
-        if self.glo != self.start:
+        if not self._shard_grads:
             raise ValueError("reduce() needs a shard-only grad buffer (grad_range='shard')")
         sc, dsc, flag = self._scale_args(scale, loss_scale)
         zs.zero_reduce_chunks(self.grad, chunks, self.n, sc, accumulate, flag, self.ws if fuse_norm else None, stream,
@@ -438,7 +441,7 @@ class FlatShardAdamW(GradTables):
         them; the process group's ranks join their norms where each holds a shard."""
         if clip.shard is not self.grad:
             raise ValueError("the clip is not over this optimizer's grad buffer (grad_clip())")
-        clip.launch(stream=stream, process_group=process_group if self.glo == self.start else None)
+        clip.launch(stream=stream, process_group=process_group if self._shard_grads else None)
         self._norm_ready = False
         self.launch_step(stream=stream, norm_result=clip.result)
 
@@ -460,7 +463,7 @@ class FlatShardAdamW(GradTables):
                 raise ValueError("a clip takes the other ranks' sums from the process group, not extra_sqnorm")
             self.launch_clip(clip, stream, process_group)
             return self.finish_step(stream, result=clip.finish(stream).whole)
-        if process_group is not None and self.glo == self.start and _world(process_group) > 1:
+        if process_group is not None and self._shard_grads and _world(process_group) > 1:
             st = torch_stream(stream, self.device)
             local = self.local_sqnorm(st)
             self.launch_step(stream=st, gathered_sqnorms=self._global_norm(local, process_group, st))
@@ -548,7 +551,7 @@ class FlatShardAdamW(GradTables):
                                  d_scale=dsc)
         else:
             zs.zero_flatten_cast(table, count, total, dt, lo, hi, sc, False, None, flag, self.ws, stream, d_scale=dsc)
-        if process_group is not None and self.glo == self.start and _world(process_group) > 1:
+        if process_group is not None and self._shard_grads and _world(process_group) > 1:
             if self._local_buf is None:
                 self._local_buf = zs.new_norm_result(self.device)
             st = torch_stream(stream, self.device)
