@@ -438,12 +438,15 @@ class FlatShardAdamW(GradTables):
 
     def launch_clip(self, clip: "GradClip", stream=None, process_group=None) -> None:
         """Enqueue `clip` (a grad_clip() of this optimizer) and the step with the grads as it leaves
-        them; the process group's ranks join their norms where each holds a shard."""
+        them; the process group's ranks join their norms where each holds a shard.  norm_buf, which
+        finish_step() and a loss scale's launch_update() read, gets the clip's result over all."""
         if clip.shard is not self.grad:
             raise ValueError("the clip is not over this optimizer's grad buffer (grad_clip())")
         clip.launch(stream=stream, process_group=process_group if self._shard_grads else None)
         self._norm_ready = False
-        self.launch_step(stream=stream, norm_result=clip.result)
+        with torch.cuda.stream(torch_stream(stream, self.device)):
+            self.norm_buf.copy_(clip.result)
+        self.launch_step(stream=stream, norm_result=self.norm_buf)
 
     def step(self, extra_sqnorm: float = 0.0, stream=None, process_group=None, clip=None) -> zs.NormResult:
         """One optimizer step.  With a torch.distributed process group of more than

@@ -68,3 +68,27 @@ def test_reduce_needs_a_shards_buffer_on_every_rank(gathers, rank):
         o.reduce(chunks, accumulate=False, scale=0.5)
     pkg.FlatShardAdamW([5, 3], world_size=2, rank=rank, device="cpu").reduce(chunks, accumulate=False, scale=0.5)
     pkg.FlatShardAdamW([5, 3], grad_range="full", device="cpu").reduce(torch.zeros(1, 8), accumulate=False, scale=1.0)
+
+
+# --------------------------------------------- the result that a step leaves
+def test_a_step_with_a_clip_leaves_the_clips_result(gathers, monkeypatch):
+    """norm_buf is what finish_step() and a loss scale's update read, after a step of either kind."""
+    o = pkg.FlatShardAdamW([5, 3], device="cpu")
+    c = o.grad_clip(group_of=[0, 1], max_norm=[1.0, 2.0])
+    used = []
+    monkeypatch.setattr(zs, "zero_adamw_step", lambda *a: used.append(bytes(a[11].numpy())))
+
+    def launch(norm, finite):
+        r = zs.zero_norm_result(norm * norm, norm, 1.0, finite)
+        c.launch = lambda **kw: c.result.copy_(torch.frombuffer(bytearray(bytes(r)), dtype=torch.uint8))
+        o.launch_clip(c)
+        return bytes(r)
+
+    want = launch(3.0, 1)
+    assert used[-1] == want and bytes(o.norm_buf.numpy()) == want
+    assert o.finish_step() == (9.0, 3.0, 1.0, True) and o.t == 1
+    want = launch(float("inf"), 0)
+    assert used[-1] == want and bytes(o.norm_buf.numpy()) == want
+    assert not o.finish_step().finite and o.t == 1
+    launch(2.0, 1)
+    assert o.finish_step().norm == 2.0 and o.t == 2
