@@ -10,7 +10,7 @@ waits for the host, so a whole step can be captured in a graph.
 from __future__ import annotations
 
 import math
-from typing import NamedTuple, Optional, Sequence, Union
+from typing import List, NamedTuple, Optional, Sequence, Union
 
 import numpy as np
 import torch
@@ -27,6 +27,17 @@ class ClipResult(NamedTuple):
     group_norms: np.ndarray
     coefs: np.ndarray
     whole: zs.NormResult
+
+
+class GradEntries(NamedTuple):
+    """A list of grads prepared for launches: the list, its table's stream, whether its grads may be
+    written; for a registered one the tensors that launches read and write, which it keeps alive,
+    and the streams besides the table's that their memory was recorded on."""
+    list: zs.GradList
+    table: GradTable
+    write: bool
+    tensors: tuple
+    streams: set
 
 
 class GradClip(GradTables):
@@ -70,7 +81,7 @@ class GradClip(GradTables):
         self.found_nonfinite = self.buffers.found
         self._home = self._current()  # the stream whose order the buffers' memory follows
         self.shard: Optional[torch.Tensor] = None
-        self._kept: tuple = ()
+        self._replayed: List[GradEntries] = []  # what captured graphs read and write
 
     @classmethod
     def of_shard(cls, numels: Sequence[int], grad: torch.Tensor, start: int, **kw) -> "GradClip":
@@ -89,7 +100,7 @@ class GradClip(GradTables):
         local = np.maximum(0, hi - lo)
         clip = cls(local.tolist(), **{"device": grad.device, **kw})
         gl = zs.flat_grad_list(clip.plan, grad, lo - start)
-        clip._registered, clip.shard = (gl, GradTable(gl.entries, clip._current()), True), grad
+        clip._registered, clip.shard = clip._prepared(gl, True, (grad,)), grad
         return clip
 
     # ------------------------------------------------------------ limits
@@ -112,20 +123,23 @@ class GradClip(GradTables):
         out: other buffers for the clipped grads (None for a tensor: it is not written; a
         tensor without a grad gets zeros); without it they are clipped in place.  A launch
         without grads then does no work per tensor on the host, and can be captured.  The
-        tensors are kept alive until others are registered.
+        tensors are kept alive until others are registered, and as long as this object where a
+        launch of them was captured.
         write=False: for norms only; a tensor may then be listed twice."""
-        self._registered = self._entries(grads, out, write)
-        self._kept = (list(grads), None if out is None else list(out))
+        tensors = tuple(t for t in (*grads, *(out or ())) if t is not None)
+        self._registered = self._entries(grads, out, write, tensors)
 
-    def _entries(self, grads, out, write, wait=True):
+    def _entries(self, grads, out, write, tensors=(), wait=True) -> GradEntries:
         not_in_capture(self._index)
-        gl = zs.grad_list(self.plan, grads, out, write, wait)
-        return gl, GradTable(gl.entries, self._current()), write
+        return self._prepared(zs.grad_list(self.plan, grads, out, write, wait), write, tensors)
+
+    def _prepared(self, gl, write, tensors) -> GradEntries:
+        return GradEntries(gl, GradTable(gl.entries, self._current()), write, tensors, set())
 
     def _current(self) -> int:
         return 0 if self._index is None else self._handle(None)  # host: only to be refused at a launch
 
-    def _list(self, grads, out, write, stream):
+    def _list(self, grads, out, write, stream) -> GradEntries:
         if grads is not None:
             here = self._index is not None and self._handle(stream) == self._current()
             return self._entries(grads, out, write, wait=not here)
@@ -133,22 +147,34 @@ class GradClip(GradTables):
             raise ValueError("out needs grads")
         if self._registered is None:
             raise ValueError("no grads given and none registered")
-        if write and not self._registered[2]:
+        if write and not self._registered.write:
             raise ValueError("the registered grads are for norms only (write=False)")
         return self._registered
 
-    def _on(self, stream, table: GradTable) -> int:
-        """The handle of the stream to launch on, its use of the object's memory noted."""
+    def _on(self, stream, of: GradEntries) -> int:
+        """The handle of the stream to launch on, its use of the memory of this object and of the
+        registered tensors noted."""
         if self._index is None:
             return 0
         raw = self._handle(stream)
-        if raw == self._home == table.stream and not torch.cuda.is_current_stream_capturing():
+        capturing = torch.cuda.is_current_stream_capturing()
+        if raw == self._home == of.table.stream and not capturing:
             return raw
-        self._read_on(table, raw)
-        if raw != self._home and not torch.cuda.is_current_stream_capturing():
+        self._read_on(of.table, raw)
+        if capturing:
+            if not any(r is of for r in self._replayed):
+                self._replayed.append(of)
+            return raw
+        if raw != self._home:
             st = torch_stream(raw, self.device)
             for t in (self.plan.ints, *self.buffers[1:8]):
                 t.record_stream(st)
+        if raw != of.table.stream and raw not in of.streams:
+            # once: whatever was launched there until their memory is freed is waited for
+            st = torch_stream(raw, self.device)
+            for t in of.tensors:
+                t.record_stream(st)
+            of.streams.add(raw)
         return raw
 
     def _used_on(self, raw: int, *lists) -> None:
@@ -169,8 +195,8 @@ class GradClip(GradTables):
             with torch.cuda.device(self._index):
                 return self.launch_sums(grads, scale=scale, loss_scale=loss_scale, stream=stream)
         sc, dsc, _ = self._scale_args(scale, loss_scale)
-        gl, table, _ = self._list(grads, None, False, stream)
-        raw = self._on(stream, table)
+        of = self._list(grads, None, False, stream)
+        gl, raw = of.list, self._on(stream, of)
         self._used_on(raw, grads)
         zs.zero_list_sums(gl, sc, self.buffers, raw, d_scale=dsc)
 
@@ -205,8 +231,8 @@ class GradClip(GradTables):
         if gathered is not None and (gathered.numel() == 0 or gathered.numel() % n or gathered.device != dev
                                      or (gathered.dim() > 1 and gathered.shape[-1] != n)):
             raise ValueError(f"gathered_sums must be [ranks, {n}] on {dev}")
-        gl, table, _ = self._list(grads, out, clip, stream)
-        raw = self._on(stream, table)
+        of = self._list(grads, out, clip, stream)
+        gl, raw = of.list, self._on(stream, of)
         if grads is not None or gathered is not None:
             self._used_on(raw, grads, out, None if gathered is None else [gathered])
         sc, dsc, flag = self._scale_args(scale, loss_scale)
