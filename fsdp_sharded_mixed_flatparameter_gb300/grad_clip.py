@@ -80,6 +80,7 @@ class GradClip(GradTables):
         self.result = self.results[g * zs.NORM_RESULT_BYTES:]
         self.found_nonfinite = self.buffers.found
         self._home = self._current()  # the stream whose order the buffers' memory follows
+        self._last: Optional[int] = None  # the stream of the last launch that was not captured
         self.shard: Optional[torch.Tensor] = None
         self._replayed: List[GradEntries] = []  # what captured graphs read and write
 
@@ -112,9 +113,23 @@ class GradClip(GradTables):
             raise ValueError("max_norm must be >= 0")
         return torch.tensor([float(v) for v in values], dtype=torch.float64)
 
-    def set_max_norm(self, max_norm: Union[float, Sequence[float]]) -> None:
-        """Change the limits (also for the next replay of a captured graph)."""
-        self.max_norms.copy_(self._limits(max_norm))
+    def set_max_norm(self, max_norm: Union[float, Sequence[float]], stream=None) -> None:
+        """Change the limits for every later launch (also for the next replay of a captured graph),
+        and for none before.  They are written on `stream` (default: the current one), behind what
+        was enqueued there and behind the last launch, whichever its stream; this waits for that.
+        Replays that may still run on another stream have to be waited for, or that stream given."""
+        limits = self._limits(max_norm)
+        if self._index is None:
+            self.max_norms.copy_(limits)
+            return
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("change the limits outside the capture: the graph's replays follow them")
+        raw = self._handle(stream)
+        st = torch_stream(raw, self.device)
+        if self._last is not None and self._last != raw:
+            st.wait_stream(torch_stream(self._last, self.device))
+        with torch.cuda.stream(st):
+            self.max_norms.copy_(limits)  # waits, as the limits are not in pinned memory: any stream may launch then
 
     # ------------------------------------------------------------- grads
     def register_grads(self, grads: Sequence[Optional[torch.Tensor]],
@@ -158,6 +173,8 @@ class GradClip(GradTables):
             return 0
         raw = self._handle(stream)
         capturing = torch.cuda.is_current_stream_capturing()
+        if not capturing:
+            self._last = raw
         if raw == self._home == of.table.stream and not capturing:
             return raw
         self._read_on(of.table, raw)

@@ -1,0 +1,88 @@
+"""Limits changed between launches, without a GPU: streams are stand-ins that note what is enqueued on them and what they wait for."""
+import contextlib
+
+import pytest
+import torch
+
+import fsdp_sharded_mixed_flatparameter_gb300 as pkg
+from fsdp_sharded_mixed_flatparameter_gb300 import grad_clip as G
+from fsdp_sharded_mixed_flatparameter_gb300 import zero_shard as zs
+
+OWN, SIDE = 11, 22
+
+
+class World:
+    def __init__(self):
+        self.current, self.log, self.capturing = [OWN], [], False
+
+    @contextlib.contextmanager
+    def stream(self, s):
+        self.current.append(s.handle)
+        yield
+        self.current.pop()
+
+
+class Stream:
+    def __init__(self, world, handle):
+        self.world, self.handle = world, handle
+
+    def wait_stream(self, other):
+        self.world.log.append((self.handle, "waits for", other.handle))
+
+
+@pytest.fixture
+def world(monkeypatch):
+    w = World()
+    monkeypatch.setattr(zs, "_current_handle", lambda index: w.current[-1])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "stream", w.stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: w.capturing)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None, raising=False)
+    monkeypatch.setattr(G, "torch_stream", lambda s, device: Stream(w, w.current[-1] if s is None else s))
+    monkeypatch.setattr(G.GradClip, "_read_on", lambda *a: None)
+    monkeypatch.setattr(zs, "zero_list_norms", lambda gl, sc, clip, b, flag, raw, **k: w.log.append((raw, "launch")))
+    copy = torch.Tensor.copy_
+
+    def noted(t, *a, **k):
+        if t.dtype == torch.float64:
+            w.log.append((w.current[-1], "limits"))
+        return copy(t, *a, **k)
+
+    monkeypatch.setattr(torch.Tensor, "copy_", noted)
+    return w
+
+
+def clip():
+    c = pkg.GradClip([5, 3], device="cpu", group_of=[0, 1], max_norm=[1.0, 2.0])
+    c._index, c._home = 0, OWN
+    c.register_grads([torch.zeros(5), torch.zeros(3)])
+    return c
+
+
+def test_limits_are_written_behind_the_last_launch(world):
+    c = clip()
+    c.set_max_norm(3.0)  # nothing to wait for yet
+    c.launch(stream=SIDE)
+    c.set_max_norm([4.0, 5.0])
+    c.launch(stream=SIDE)
+    c.set_max_norm(6.0, stream=SIDE)
+    c.launch()
+    c.set_max_norm(7.0)
+    c.set_max_norm(8.0, stream=SIDE)
+    assert world.log == [(OWN, "limits"), (SIDE, "launch"), (OWN, "waits for", SIDE), (OWN, "limits"), (SIDE, "launch"), (SIDE, "limits"),
+                         (OWN, "launch"), (OWN, "limits"), (SIDE, "waits for", OWN), (SIDE, "limits")]
+    assert c.max_norms.tolist() == [8.0, 8.0]
+
+
+def test_limits_are_not_changed_in_a_capture(world):
+    c = clip()
+    world.capturing = True
+    c.launch(stream=SIDE)  # captured: nothing runs there yet
+    with pytest.raises(RuntimeError, match="outside the capture"):
+        c.set_max_norm(1.0)
+    world.capturing = False
+    with pytest.raises(ValueError, match="max_norm"):
+        c.set_max_norm([1.0, -1.0])
+    assert c.max_norms.tolist() == [1.0, 2.0]
+    c.set_max_norm(3.0)
+    assert world.log == [(SIDE, "launch"), (OWN, "limits")]
