@@ -436,8 +436,10 @@ __device__ __forceinline__ double join_parts(const FinishArgs& a, int i) {
 // Roots and quotients: binary32 ones corrected by Newton's method with binary64
 // residuals, where the chain of binary64 operations of __dsqrt_rn and __ddiv_rn
 // is much of the time that one thread takes for a result (a small list's norms 8.4
-// against 7.8 us).  The root of s: y + (s - y y) / 2y twice; after the first step the
-// error is (2^-24)^2 / 2 of it, after the second what the last addition rounds.
+// against 7.8 us).  The root of s: y + (s - y y) / 2y twice.  With u = 2^-24, y is
+// 1.5 u off at first (s and the root rounded) and the factor 1 / 2y u more, which leaves
+// 1.125 u^2 + 1.5 u^2 after the first step and, after the second, what the last
+// addition rounds.
 __device__ __forceinline__ bool in_float_range(float f) { return f > 0x1p-100f && f < 0x1p100f; }
 __device__ __forceinline__ double root(double s) {
   const float f = __double2float_rn(s);
@@ -448,7 +450,8 @@ __device__ __forceinline__ double root(double s) {
   y = fma(fma(-y, y, s), half, y);
   return fma(fma(-y, y, s), half, y);
 }
-// A tensor's norm in binary32, at most 2^-24 (1 + 2^-22) off.
+// A tensor's norm in binary32, at most u (1 + 2^-21) off: one such step, its residual and
+// quotient rounded by u each, leaves 1.125 u^2 + 2 u x 1.5 u before the last rounding.
 template <int P>
 __device__ __forceinline__ float tensor_norm(double s) {
   const float f = __double2float_rn(s);
@@ -458,7 +461,9 @@ __device__ __forceinline__ float tensor_norm(double s) {
   const float rest = __double2float_rn(fma(-static_cast<double>(y), static_cast<double>(y), s));
   return __fadd_rn(y, __fdiv_rn(rest, 2.0f * y));
 }
-// min(1, limit / d) in binary32, at most 2^-24 (1 + 2^-22) off.
+// min(1, limit / d) in binary32, at most u (1 + 2^-20) off where it is above 2^-100: the
+// first quotient is 3 u off (limit, d and itself rounded); residual, d and the second
+// quotient, rounded by u each, leave 3 u x 3 u before the last rounding.
 __device__ __forceinline__ float clip_coefficient(double limit, double d) {
   if (!(limit < d)) return 1.0f;  // a NaN too
   const float fd = __double2float_rn(d), fl = __double2float_rn(limit);
