@@ -42,8 +42,8 @@ class GradEntries(NamedTuple):
 
 class GradClip(GradTables):
     """The clip over tensors of the sizes `numels`.  max_norm: the limit, or one per group (inf:
-    not clipped); group_of: each tensor's group (default: all in group 0), with
-    range(len(numels)) each tensor is clipped by its own norm; norm_type: 1, 2 or inf.
+    not clipped); group_of: each tensor's group (with one limit by default 0 for all; several
+    limits need it), with range(len(numels)) each tensor is clipped by its own norm; norm_type: 1, 2 or inf.
 
     After a launch, on the device: ``tensor_norms``, ``group_norms`` (float32), ``norm`` (0-d),
     ``tensor_sums`` (float64, this rank's; ``joined_sums``: of gathered ones, all ranks'),
@@ -64,6 +64,7 @@ class GradClip(GradTables):
             n_groups = 1 if group_of is None or len(group_of) == 0 else int(max(group_of)) + 1
         else:
             n_groups = len(max_norm)
+            need_groups(max_norm, group_of)
         self.norm_type, self.n_groups = float(norm_type), n_groups
         if not self.numels:
             raise ValueError("an empty tensor list")
@@ -301,6 +302,12 @@ def clip_grad_norm_(grads: Sequence[Optional[torch.Tensor]], max_norm: float, no
 def one_limit(max_norm) -> bool:
     """Whether max_norm is a number and not one for each group."""
     return not hasattr(max_norm, "__len__") or getattr(max_norm, "ndim", 1) == 0
+
+
+def need_groups(max_norm, group_of) -> None:
+    """Several limits without groups would all but the first belong to no tensor."""
+    if len(max_norm) > 1 and group_of is None:
+        raise ValueError(f"max_norm has {len(max_norm)} limits: group_of has to say which tensors each is for")
 
 
 def not_in_capture(index) -> None:

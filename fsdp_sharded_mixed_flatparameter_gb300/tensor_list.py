@@ -17,7 +17,7 @@ import numpy as np
 import torch
 
 from . import zero_shard as zs
-from .grad_clip import GradClip, not_in_capture, one_limit
+from .grad_clip import GradClip, need_groups, not_in_capture, one_limit
 from .optimizer import GradTables, torch_stream
 
 _DEFAULTS = ("lr", "betas", "eps", "weight_decay")
@@ -32,8 +32,8 @@ class TensorListAdamW(GradTables):
     do not follow their recurrences over a run (optimizer.py).  Lists that share a seed take
     rounding_streams that are further apart than they have tensors.
 
-    max_norm: the limit of the norm over all grads, or a limit for each group (inf: not clipped):
-    then every group's grads are clipped by the group's own norm (``clip``, a GradClip, has the
+    max_norm: the limit of the norm over all grads, or a limit for each group (inf: not clipped;
+    several need group_of): then every group's grads are clipped by the group's own norm (``clip``, a GradClip, has the
     norms, and its set_max_norm() changes the limits; the grads themselves stay as they are), the step is skipped where the norm
     over all is not finite, and step() gives that norm with a coefficient of 1.
 
@@ -69,6 +69,8 @@ class TensorListAdamW(GradTables):
         per_group = not one_limit(max_norm)
         if per_group and len(max_norm) != len(self._groups):
             raise ValueError(f"{len(max_norm)} limits for {len(self._groups)} groups")
+        if per_group:
+            need_groups(max_norm, group_of)
         columns, numels, lowp_dtype = zs.list_masters(self.masters, self.lowp, group_of)
         self._init_tables(numels, self.device)
         blocks = np.cumsum([0] + [zs.state8_blocks(n) for n in numels])  # each tensor starts on a block's border

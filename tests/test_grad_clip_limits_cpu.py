@@ -86,3 +86,20 @@ def test_limits_are_not_changed_in_a_capture(world):
     assert c.max_norms.tolist() == [1.0, 2.0]
     c.set_max_norm(3.0)
     assert world.log == [(SIDE, "launch"), (OWN, "limits")]
+
+
+# ------------------------------------------------- limits and their groups
+def test_several_limits_need_groups():
+    """Without them every tensor would be clipped by the first."""
+    for many in ([1.0, 0.5], (1.0, 0.5), torch.tensor([1.0, 0.5])):
+        with pytest.raises(ValueError, match="2 limits: group_of"):
+            pkg.GradClip([5, 3], device="cpu", max_norm=many)
+        with pytest.raises(ValueError, match="2 limits: group_of"):
+            pkg.GradClip.of_shard([5, 3], torch.zeros(8), 0, max_norm=many)
+        with pytest.raises(ValueError, match="2 limits: group_of"):
+            pkg.FlatShardAdamW([5, 3], device="cpu").grad_clip(max_norm=many)
+        with pytest.raises(ValueError, match="2 limits: group_of"):
+            pkg.TensorListAdamW([torch.zeros(5), torch.zeros(3)], groups=[{}, {}], max_norm=many)
+    assert pkg.GradClip([5, 3], device="cpu", max_norm=[0.5]).max_norms.tolist() == [0.5]  # one for all
+    assert pkg.GradClip([5, 3], device="cpu", max_norm=[1.0, 0.5], group_of=[0, 0]).n_groups == 2  # an empty group that was asked for
+    assert pkg.GradClip([5, 3], device="cpu", max_norm=0.5).n_groups == 1
