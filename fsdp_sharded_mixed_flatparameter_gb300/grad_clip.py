@@ -144,6 +144,7 @@ class GradClip(GradTables):
         write=False: for norms only; a tensor may then be listed twice."""
         tensors = tuple(t for t in (*grads, *(out or ())) if t is not None)
         self._registered = self._entries(grads, out, write, tensors)
+        self.shard = None  # no longer the clip over a flat buffer, which that buffer's step takes
 
     def _entries(self, grads, out, write, tensors=(), wait=True) -> GradEntries:
         not_in_capture(self._index)

@@ -92,3 +92,15 @@ def test_a_step_with_a_clip_leaves_the_clips_result(gathers, monkeypatch):
     assert not o.finish_step().finite and o.t == 1
     launch(2.0, 1)
     assert o.finish_step().norm == 2.0 and o.t == 2
+
+
+def test_a_step_refuses_a_clip_that_other_grads_were_registered_with(gathers):
+    """It would clip those and step with its own grads as they are."""
+    o = pkg.FlatShardAdamW([5, 3], device="cpu")
+    c = o.grad_clip(max_norm=1.0)
+    with pytest.raises(ValueError):
+        c.register_grads([torch.zeros(5)])
+    assert c.shard is o.grad  # nothing was registered
+    c.register_grads([torch.zeros(5), torch.zeros(3)])
+    with pytest.raises(ValueError, match="not over this optimizer's grad buffer"):
+        o.step(clip=c)
