@@ -148,16 +148,22 @@ class TensorListAdamW(GradTables):
 
     # -------------------------------------------------------------- step
     def register_grads(self, grads: Sequence[Optional[torch.Tensor]]) -> None:
-        """Fix the grads once (see GradTables); with a limit for each group needed before a capture."""
+        """Fix the grads once (see GradTables); with a limit for each group needed before a capture,
+        and on this list's device."""
+        before = self._registered
         super().register_grads(grads)
         if self.clip is not None:
-            self.clip.register_grads(grads, write=False)
+            try:
+                self.clip.register_grads(grads, write=False)
+            except Exception:  # the step's grads and those of its norms are the same ones
+                self._registered = before
+                raise
 
     def launch_step(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None, *, scale: float = 1.0, stream=None,
                     loss_scale=None, norm_result: Optional[torch.Tensor] = None) -> None:
         """Enqueue the grad norm over the whole list and the update for step t + 1 without
-        waiting.  grads: a grad or None (reads as zeros) per tensor, any alignment, one dtype;
-        None: the registered ones.  loss_scale: a DeviceLossScale, whose unscale factor
+        waiting.  grads: a grad or None (reads as zeros) per tensor, any alignment, one dtype (in
+        pinned host memory only with one limit); None: the registered ones.  loss_scale: a DeviceLossScale, whose unscale factor
         replaces `scale`.  norm_result: a zero_norm_result computed elsewhere (one clip over
         several optimizers): used as is, no norm is computed."""
         if grads is not None and norm_result is None and self.clip is not None:

@@ -103,3 +103,25 @@ def test_several_limits_need_groups():
     assert pkg.GradClip([5, 3], device="cpu", max_norm=[0.5]).max_norms.tolist() == [0.5]  # one for all
     assert pkg.GradClip([5, 3], device="cpu", max_norm=[1.0, 0.5], group_of=[0, 0]).n_groups == 2  # an empty group that was asked for
     assert pkg.GradClip([5, 3], device="cpu", max_norm=0.5).n_groups == 1
+
+
+def test_grads_that_the_clip_refuses_are_not_registered_for_the_step_either(monkeypatch):
+    """Else the step would go by the norms of the grads registered before."""
+    made = []
+    monkeypatch.setattr(zs, "zero_tensor_table", lambda grads, numels=None: (None, sum(g.numel() for g in grads)))
+    monkeypatch.setattr(zs, "device_table", lambda table, n, device: made.append(torch.zeros(1)) or made[-1])
+    monkeypatch.setattr(zs, "_stream", lambda s: OWN)
+    o = pkg.TensorListAdamW.__new__(pkg.TensorListAdamW)  # host memory: without the parts that only a launch reads
+    o._init_tables([5, 3], "cpu")
+    o.clip = pkg.GradClip([5, 3], device="cpu", group_of=[0, 1], max_norm=[1.0, 2.0])
+    with pytest.raises(ValueError, match="must be a tensor on"):  # as pinned host memory would be
+        o.register_grads([torch.zeros(5, device="meta"), torch.zeros(3)])
+    assert o._registered is None and o.clip._registered is None
+    x = [torch.zeros(5), torch.zeros(3)]
+    o.register_grads(x)
+    first, norms = o._registered, o.clip._registered
+    with pytest.raises(ValueError, match="must be a tensor on"):
+        o.register_grads([torch.zeros(5), torch.zeros(3, device="meta")])
+    assert o._registered is first and o.clip._registered is norms and norms.tensors[0] is x[0]
+    o.register_grads([torch.zeros(5), torch.zeros(3)])
+    assert o._registered is not first and o.clip._registered is not norms
