@@ -146,6 +146,13 @@ class GradClip(GradTables):
         self._registered = self._entries(grads, out, write, tensors)
         self.shard = None  # no longer the clip over a flat buffer, which that buffer's step takes
 
+    def device_table(self, grads: Sequence[Optional[torch.Tensor]]):
+        """The FlatParameter table of a grads list (see GradTables).  A clip's launches read tables of
+        their own kind, so the registered grads have none."""
+        if grads is None:
+            raise ValueError("device_table() of a GradClip needs the grads: its registered ones have no FlatParameter table")
+        return super().device_table(grads)
+
     def _entries(self, grads, out, write, tensors=(), wait=True) -> GradEntries:
         not_in_capture(self._index)
         return self._prepared(zs.grad_list(self.plan, grads, out, write, wait), write, tensors)

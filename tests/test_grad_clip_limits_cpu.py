@@ -125,3 +125,17 @@ def test_grads_that_the_clip_refuses_are_not_registered_for_the_step_either(monk
     assert o._registered is first and o.clip._registered is norms and norms.tensors[0] is x[0]
     o.register_grads([torch.zeros(5), torch.zeros(3)])
     assert o._registered is not first and o.clip._registered is not norms
+
+
+def test_a_clips_registered_grads_have_no_flat_parameter_table(monkeypatch):
+    c = pkg.GradClip([5, 3], device="cpu")
+    x = [torch.zeros(5), torch.zeros(3)]
+    for _ in range(2):
+        with pytest.raises(ValueError, match="needs the grads"):
+            c.device_table(None)
+        c.register_grads(x)
+    table = torch.zeros(1)
+    monkeypatch.setattr(zs, "zero_tensor_table", lambda grads, numels=None: (None, sum(g.numel() for g in grads)))
+    monkeypatch.setattr(zs, "device_table", lambda *a: table)
+    monkeypatch.setattr(zs, "_stream", lambda s: OWN)
+    assert c.device_table(x) == (table, 2, torch.float32)
