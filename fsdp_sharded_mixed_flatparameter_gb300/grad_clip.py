@@ -246,13 +246,20 @@ class GradClip(GradTables):
         ranks' tensor_sums in rank order, [ranks, tensors] (launch_sums() has run, its row is this
         rank's); process_group: the sums are gathered here, ordered on `stream`.
 
-        y = scale * coefficient * x, written where the norm over all tensors is finite."""
+        y = scale * coefficient * x, written where the norm over all tensors is finite.  Autograd
+        counts that as a change in place of tensors given here (so that a graph that has saved one
+        refuses to use it), not of registered ones."""
         self._launch(True, grads, out, scale, loss_scale, gathered_sums, process_group, stream)
 
     def _launch(self, clip, grads, out, scale, loss_scale, gathered, process_group, stream) -> None:
         if self._elsewhere():
             with torch.cuda.device(self._index):
                 return self._launch(clip, grads, out, scale, loss_scale, gathered, process_group, stream)
+        self._enqueue(clip, grads, out, scale, loss_scale, gathered, process_group, stream)
+        if clip and grads is not None:  # 55 ns a tensor, which a registered list is spared
+            torch.autograd.graph.increment_version([t for t in (grads if out is None else out) if t is not None])
+
+    def _enqueue(self, clip, grads, out, scale, loss_scale, gathered, process_group, stream) -> None:
         n, dev = len(self.numels), self.plan.ints.device
         if gathered is not None and (gathered.numel() == 0 or gathered.numel() % n or gathered.device != dev
                                      or (gathered.dim() > 1 and gathered.shape[-1] != n)):
