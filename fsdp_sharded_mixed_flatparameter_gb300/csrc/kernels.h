@@ -128,7 +128,8 @@ inline int grad_chunk_size(int64_t total) {
                                        : kMaxGradChunk;
 }
 // Elements up to which a tensor is narrow, a warp's work: a chunk, but no more
-// than 16384 (the 20,000 ragged tensors: 460 us with 4096, 450 with 16384).
+// than 16384 (the 20,000 ragged tensors: 460 us with 4096, 450 with 16384; not
+// measured where thousands of tensors have a few million elements in all).
 inline int grad_narrow_size(int chunk) { return chunk < 16384 ? chunk : 16384; }
 
 // The norms of a grads list and its clipping (arguments checked; plan: zero_grad_plan's ints).

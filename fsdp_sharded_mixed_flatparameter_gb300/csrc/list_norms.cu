@@ -36,9 +36,9 @@ namespace cg = cooperative_groups;
 
 // ------------------------------------------------------------ 1: chunks
 // Threads of a block, vectors of 8 that a thread has in flight, and blocks on
-// an SM (72 registers).  Llama-7B's four layers in bf16, us: 304; with 8 blocks
-// (64 registers, some spilled) 313, with 6 and 3 vectors 310, with blocks of
-// 64 or 192 323 and 309.
+// an SM (72 registers, of which p = 2 spills 4 bytes and infinity 20).
+// Llama-7B's four layers in bf16, us: 304; with 8 blocks (64 registers, more
+// spilled) 313, with 6 and 3 vectors 310, with blocks of 64 or 192 323 and 309.
 constexpr int kSumThreads = 128, kAhead16 = 8, kAhead32 = 4, kSumBlocks = 7;
 
 // What a thread gathers of its elements: the sums, and in `bits` the elements'

@@ -460,7 +460,9 @@ class FlatShardAdamW(GradTables):
         not used then): its groups are clipped in the grad buffer, by their norms over the process
         group's ranks (without one: over this rank's buffer alone), the step is skipped where
         its norm over all tensors is not finite, and the result is that norm's, with a
-        coefficient of 1 (clip.finish() gives the groups')."""
+        coefficient of 1 (clip.finish() gives the groups').  That norm is finite for any finite
+        grads, where the one clip's squares end at 2^64: a group without a limit takes grads of
+        that size, whose squares exp_avg_sq cannot hold."""
         if clip is not None:
             if extra_sqnorm != 0.0:
                 raise ValueError("a clip takes the other ranks' sums from the process group, not extra_sqnorm")

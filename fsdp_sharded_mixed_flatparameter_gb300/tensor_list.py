@@ -34,8 +34,11 @@ class TensorListAdamW(GradTables):
 
     max_norm: the limit of the norm over all grads, or a limit for each group (inf: not clipped;
     several need group_of): then every group's grads are clipped by the group's own norm (``clip``, a GradClip, has the
-    norms, and its set_max_norm() changes the limits; the grads themselves stay as they are), the step is skipped where the norm
-    over all is not finite, and step() gives that norm with a coefficient of 1.
+    norms, and its set_max_norm() changes the limits; the grads themselves stay as they are), the
+    step is skipped where the norm over all is not finite, and step() gives that norm with a
+    coefficient of 1.  Those norms are finite for any finite grads, where the one norm's squares
+    end at 2^64: a group without a limit takes grads of that size, whose squares exp_avg_sq cannot
+    hold, and so does any group of grads whose scaled values leave binary32.
 
     The moments live in storages of this object, tensor i's at elements offsets[i] ..
     offsets[i] + numels[i]: ``exp_avg`` and ``exp_avg_sq`` (fp32), or ``state8`` (8 bits:
