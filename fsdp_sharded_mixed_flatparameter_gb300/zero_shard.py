@@ -977,6 +977,8 @@ def _addresses_of(tensors: Sequence[Optional[torch.Tensor]], sizes: List[int], d
         if not t.is_contiguous() and not _dense(t):
             raise ValueError(f"{name}[{i}] does not fill one run of memory (strides {t.stride()})")
         ptrs[i], dts[i] = t.data_ptr(), dt
+        if ptrs[i] == 0 and sizes[i]:  # NULL would read as no grad
+            raise ValueError(f"{name}[{i}] has no memory (its storage was freed)")
     return ptrs, dts
 
 
@@ -1013,6 +1015,8 @@ def flat_grad_list(plan: GradPlan, flat: torch.Tensor, starts: np.ndarray) -> Gr
     """The list of a flat grad's pieces, clipped in place: tensor i's plan.numels[i] elements from starts[i]."""
     if flat.device != plan.ints.device or flat.dtype not in _DT or flat.dim() != 1 or not flat.is_contiguous():
         raise ValueError(f"the flat grad must be 1-D, contiguous, f32, bf16 or f16, on {plan.ints.device}")
+    if flat.untyped_storage().nbytes() < (flat.storage_offset() + flat.numel()) * flat.element_size():
+        raise ValueError("the flat grad has no memory (its storage was freed)")
     some = plan.numels > 0
     if np.any(some & ((starts < 0) | (starts + plan.numels > flat.numel()))):
         raise ValueError("a piece lies outside the flat grad")

@@ -139,3 +139,32 @@ def test_a_clips_registered_grads_have_no_flat_parameter_table(monkeypatch):
     monkeypatch.setattr(zs, "device_table", lambda *a: table)
     monkeypatch.setattr(zs, "_stream", lambda s: OWN)
     assert c.device_table(x) == (table, 2, torch.float32)
+
+
+# ---------------------------------------------------------- freed storages
+def freed(n):
+    """A tensor whose storage was given back, as sharded loops do with whole parameters between uses."""
+    t = torch.zeros(n)
+    t.untyped_storage().resize_(0)
+    return t
+
+
+def test_tensors_without_memory_are_refused():
+    """Their address is NULL, which stands for a tensor without a grad."""
+    plan = zs.zero_grad_plan([5, 0], None, 1, 2, "cpu")
+    empty = torch.zeros(0)
+    zs.grad_list(plan, [torch.zeros(5), empty])
+    for kw in (dict(), dict(write=False), dict(out=[torch.zeros(5), None])):
+        with pytest.raises(ValueError, match=r"grads\[0\] has no memory"):
+            zs.grad_list(plan, [freed(5), empty], **kw)
+    with pytest.raises(ValueError, match=r"out\[0\] has no memory"):
+        zs.grad_list(plan, [torch.zeros(5), empty], [freed(5), empty])
+    with pytest.raises(ValueError, match="flat grad has no memory"):
+        pkg.GradClip.of_shard([5, 3], freed(8), 0)
+    whole = torch.zeros(10)
+    part = whole[2:]
+    pkg.GradClip.of_shard([5, 3], part, 0)
+    whole.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="flat grad has no memory"):
+        pkg.GradClip.of_shard([5, 3], part, 0)
+    pkg.GradClip.of_shard([5, 3], empty, 8)  # a rank without elements
